@@ -329,6 +329,75 @@ kvq_status extend_prefixes(const ExtendPlan& ep, const void* q, const void* pool
   return KVQ_OK;
 }
 
+// Workspace of a fork or a resize of n list entries: the status word, the entries, the free pages' bitmap with
+// its prefixes, and the parents' rows.
+struct PagesPlan {
+  int32_t chunks;
+  size_t entries, chunk_free, word_prefix, bits, rows, total;
+};
+
+bool plan_pages(const kvq_layout& L, int32_t n, int32_t max_pages, PagesPlan* pp) {
+  if (n < 0 || max_pages <= 0) return false;
+  const int64_t chunks = (L.num_pages + kPagesChunk - 1) / kPagesChunk;
+  if (chunks > kMaxPagesChunks) return false;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t words = static_cast<size_t>(chunks) * (kPagesChunk / 32);
+  pp->chunks = static_cast<int32_t>(chunks);
+  pp->entries = kWorkspaceHeader;
+  pp->chunk_free = pp->entries + up(static_cast<size_t>(n) * sizeof(PagesEntry));
+  pp->word_prefix = pp->chunk_free + up(static_cast<size_t>(chunks) * sizeof(int32_t));
+  pp->bits = pp->word_prefix + up(words * sizeof(int32_t));
+  pp->rows = pp->bits + up(words * sizeof(uint32_t));
+  pp->total = pp->rows + up(static_cast<size_t>(n) * max_pages * sizeof(int32_t));
+  return true;
+}
+
+// Checks and arguments that fork and resize share; KVQ_OK with a->n = 0 when there is nothing to do.
+kvq_status pages_common(int32_t* block_table, int32_t max_pages, int32_t* seq_lens, int32_t batch, int32_t* page_refs,
+                        const int32_t* dst, int32_t n, void* workspace, size_t workspace_bytes,
+                        const kvq_layout* layout, PagesArgs* a) {
+  kvq_status st = check_layout(layout);
+  if (st != KVQ_OK) return st;
+  if (batch < 0 || n < 0 || max_pages <= 0) return KVQ_EINVAL;
+  if (static_cast<int64_t>(max_pages) * layout->page_size > std::numeric_limits<int32_t>::max()) return KVQ_EINVAL;
+  PagesPlan pp;
+  if (!plan_pages(*layout, n, max_pages, &pp)) return KVQ_EUNSUPPORTED;
+  a->n = 0;
+  if (n > 0 && (!block_table || !seq_lens || (!page_refs && layout->num_pages > 0) || !dst)) return KVQ_EINVAL;
+  if (!workspace) return KVQ_EINVAL;
+  if (workspace_bytes < pp.total) return KVQ_EWORKSPACE;
+  if (!aligned(workspace)) return KVQ_EALIGN;
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(page_refs), static_cast<const void*>(dst)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a->block_table = block_table;
+  a->seq_lens = seq_lens;
+  a->page_refs = page_refs;
+  a->src = nullptr;
+  a->dst = dst;
+  a->new_lens = nullptr;
+  a->copy_src = a->copy_dst = nullptr;
+  a->batch = batch;
+  a->max_pages = max_pages;
+  a->n = n;
+  a->page_size = layout->page_size;
+  a->chunks = pp.chunks;
+  a->num_pages = layout->num_pages;
+  a->status = reinterpret_cast<uint32_t*>(ws);
+  a->entries = reinterpret_cast<PagesEntry*>(ws + pp.entries);
+  a->chunk_free = reinterpret_cast<int32_t*>(ws + pp.chunk_free);
+  a->word_prefix = reinterpret_cast<int32_t*>(ws + pp.word_prefix);
+  a->bits = reinterpret_cast<uint32_t*>(ws + pp.bits);
+  a->rows = reinterpret_cast<int32_t*>(ws + pp.rows);
+  return KVQ_OK;
+}
+
+// The status word of a page call with an empty list.
+kvq_status clear_status(void* workspace, cudaStream_t s) {
+  return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+}
+
 }  // namespace
 
 
@@ -350,6 +419,7 @@ const char* kvq_strerror(kvq_status s) {
     case KVQ_ECUDA: return "a CUDA call or kernel launch failed";
     case KVQ_EUNSUPPORTED: return "no decode kernel for this page size / head_dim / path";
     case KVQ_ETIMEOUT: return "a kernel gave up a bounded wait; its output is not valid";
+    case KVQ_ENOPAGES: return "not enough free pages; the call changed nothing";
   }
   return "unknown status";
 }
@@ -612,6 +682,116 @@ kvq_status kvq_extend_ex(const void* q, const void* pool, const void* scales, co
   return launch_extend_tc(a, s);
 }
 
+size_t kvq_pages_workspace_bytes(const kvq_layout* layout, int32_t n, int32_t max_pages_per_seq) {
+  PagesPlan pp;
+  if (check_layout(layout) != KVQ_OK || !plan_pages(*layout, n, max_pages_per_seq, &pp)) return 0;
+  return pp.total;
+}
+
+kvq_status kvq_pages_copy(void* pool, void* scales, const int32_t* src, const int32_t* dst, int32_t n,
+                          const kvq_layout* layout, kvq_kind kind, void* stream) {
+  kvq_status st = check_layout(layout);
+  if (st != KVQ_OK) return st;
+  if (!kind_read_ok(kind)) return KVQ_EKIND;
+  if (!has_scales(kind)) scales = nullptr;
+  if (n < 0) return KVQ_EINVAL;
+  const int64_t page_bytes =
+      static_cast<int64_t>(n_kv_of(*layout)) * layout->num_kv_heads * layout->page_size * layout->head_dim;
+  const int64_t scale_bytes = has_scales(kind) ? page_bytes / 16 : 0;
+  if (scale_bytes % 16 != 0 || page_bytes > (1LL << 34)) return KVQ_EUNSUPPORTED;  // whole 16-byte pieces, 32-bit counts
+  if (n == 0) return KVQ_OK;
+  if (!pool || (has_scales(kind) && !scales) || !src || !dst) return KVQ_EINVAL;
+  if (!aligned(pool) || !aligned(scales) || (reinterpret_cast<uintptr_t>(src) % 4) != 0 ||
+      (reinterpret_cast<uintptr_t>(dst) % 4) != 0)
+    return KVQ_EALIGN;
+  st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  return launch_copy_pages(pool, scales, src, dst, n, layout->num_pages, static_cast<uint32_t>(page_bytes / 16),
+                           static_cast<uint32_t>(scale_bytes / 16), static_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_pages_fork(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,
+                          int32_t* page_refs, const int32_t* src, const int32_t* dst, int32_t n, int32_t* copy_src,
+                          int32_t* copy_dst, void* workspace, size_t workspace_bytes, const kvq_layout* layout,
+                          void* stream) {
+  PagesArgs a;
+  kvq_status st = pages_common(block_table, max_pages_per_seq, seq_lens, batch, page_refs, dst, n, workspace,
+                               workspace_bytes, layout, &a);
+  if (st != KVQ_OK) return st;
+  if (n > 0 && (!src || !copy_src || !copy_dst)) return KVQ_EINVAL;
+  for (const void* p : {static_cast<const void*>(src), static_cast<const void*>(copy_src),
+                        static_cast<const void*>(copy_dst)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  if (n == 0) return clear_status(workspace, static_cast<cudaStream_t>(stream));
+  a.src = src;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  return launch_fork_pages(a, static_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_pages_resize(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,
+                            int32_t* page_refs, const int32_t* seqs, const int32_t* new_lens, int32_t n,
+                            void* workspace, size_t workspace_bytes, const kvq_layout* layout, void* stream) {
+  PagesArgs a;
+  kvq_status st = pages_common(block_table, max_pages_per_seq, seq_lens, batch, page_refs, seqs, n, workspace,
+                               workspace_bytes, layout, &a);
+  if (st != KVQ_OK) return st;
+  if (n > 0 && !new_lens) return KVQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(new_lens) % 4 != 0) return KVQ_EALIGN;
+  st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  if (n == 0) return clear_status(workspace, static_cast<cudaStream_t>(stream));
+  a.new_lens = new_lens;
+  return launch_resize_pages(a, static_cast<cudaStream_t>(stream));
+}
+
+kvq_status kvq_pages_compact(void* pool, void* scales, const int32_t* block_table, int32_t max_pages_per_seq,
+                             const int32_t* seq_lens, const int32_t* q_start, const int64_t* keep, int32_t mask_words,
+                             int32_t batch, int32_t* new_lens, const int32_t* page_refs, void* workspace,
+                             size_t workspace_bytes, const kvq_layout* layout, kvq_kind kind, void* stream) {
+  kvq_status st = check_layout(layout);
+  if (st != KVQ_OK) return st;
+  if (!kind_read_ok(kind)) return KVQ_EKIND;
+  if (!has_scales(kind)) scales = nullptr;
+  if (batch < 0 || max_pages_per_seq <= 0 || mask_words <= 0) return KVQ_EINVAL;
+  if (mask_words > kMaxMaskWords) return KVQ_EUNSUPPORTED;
+  if (!workspace) return KVQ_EINVAL;
+  if (workspace_bytes < kWorkspaceHeader) return KVQ_EWORKSPACE;
+  const int64_t kv_rows = static_cast<int64_t>(n_kv_of(*layout)) * layout->num_kv_heads;
+  if (kv_rows > 65535) return KVQ_EUNSUPPORTED;  // a grid dimension
+  if (batch > 0 && (!pool || (has_scales(kind) && !scales) || !block_table || !seq_lens || !q_start || !keep || !new_lens))
+    return KVQ_EINVAL;
+  if (!aligned(workspace) || !aligned(pool) || !aligned(scales) || (reinterpret_cast<uintptr_t>(keep) % 8) != 0)
+    return KVQ_EALIGN;
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(q_start), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(page_refs)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  if (batch == 0) return clear_status(workspace, static_cast<cudaStream_t>(stream));
+  CompactArgs a;
+  a.codes = static_cast<uint8_t*>(pool);
+  a.scales = static_cast<uint16_t*>(scales);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.keep = keep;
+  a.page_refs = page_refs;
+  a.new_lens = new_lens;
+  a.status = static_cast<uint32_t*>(workspace);
+  a.num_pages = layout->num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch;
+  a.mask_words = mask_words;
+  a.page_size = layout->page_size;
+  a.kv_rows = static_cast<int32_t>(kv_rows);
+  a.head_dim = layout->head_dim;
+  return launch_compact(a, static_cast<cudaStream_t>(stream));
+}
+
 kvq_status kvq_workspace_status(const void* workspace, void* stream) {
   if (!workspace) return KVQ_EINVAL;
   uint32_t word = 0;
@@ -619,6 +799,7 @@ kvq_status kvq_workspace_status(const void* workspace, void* stream) {
   if (cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess) return KVQ_ECUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return KVQ_ECUDA;
   if (word == 0) return KVQ_OK;
+  if (word == kStatusNoPagesWord) return KVQ_ENOPAGES;
   return word == kStatusTimeoutWord ? KVQ_ETIMEOUT : KVQ_EINVAL;
 }
 

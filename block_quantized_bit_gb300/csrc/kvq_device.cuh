@@ -28,6 +28,8 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded waits give up after
 constexpr uint32_t kStatusTimeout = 0x7100u;
 constexpr uint32_t kStatusBadPage = 0x7200u;
 constexpr uint32_t kStatusBadExtend = 0x7300u;  // q_start inconsistent with seq_lens or total_q
+constexpr uint32_t kStatusBadPages = 0x7400u;   // a page call's list, table or counts are inconsistent
+constexpr uint32_t kStatusNoPages = kStatusNoPagesWord;  // too few free pages
 
 // ------------------------------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -49,6 +49,7 @@ struct DecodeArgs {
 // Tokens per page the decode kernels support, and the workspace's leading status block.
 constexpr int kPageTokens = 16;
 constexpr size_t kWorkspaceHeader = 256;
+constexpr uint32_t kStatusNoPagesWord = 0x7500u;  // status word of a page call that found too few free pages
 
 // Work-item planning constants shared by the host (workspace bound) and the kernels.
 constexpr int kTargetItems = 1216;  // items when the host sets no target; also the SM count assumed without a device
@@ -130,4 +131,59 @@ kvq_status launch_exp2_probe(const float* x, float* y, int64_t n, cudaStream_t s
 // are left as they are and flagged in the status word).
 kvq_status launch_extend_expand(const int32_t* q_start, const int32_t* seq_lens, int32_t batch, int32_t total_q,
                                 int32_t* vlens, int32_t* vrow, uint32_t* status, cudaStream_t stream);
+
+// Pages of the cache (kvq_pages_*).
+constexpr int32_t kPagesChunk = 8192;       // pages whose counts one CTA of the plan reads
+constexpr int32_t kMaxPagesChunks = 8192;   // chunks whose prefixes fit the apply kernel's shared memory
+constexpr int32_t kMaxMaskWords = 4;        // 64-bit words of a drafted token's mask: 256 drafted tokens
+
+// What the plan finds for one list entry of a fork or a resize.
+struct PagesEntry {
+  int32_t row;       // block-table row that changes, -1: a bad entry
+  int32_t used_old;  // pages it holds
+  int32_t used_new;  // pages it will hold
+  int32_t new_len;   // tokens it will hold
+  int32_t tail;      // (fork) the parent's partly filled last page, or -1
+  int32_t need;      // free pages it takes
+};
+
+struct PagesArgs {
+  int32_t* block_table;      // [batch][max_pages]
+  int32_t* seq_lens;         // [batch]
+  int32_t* page_refs;        // [num_pages]
+  const int32_t* src;        // [n] (fork) parents
+  const int32_t* dst;        // [n] rows that change
+  const int32_t* new_lens;   // [n] (resize)
+  int32_t* copy_src;         // [n] (fork)
+  int32_t* copy_dst;         // [n] (fork)
+  int32_t batch, max_pages, n, page_size, chunks;
+  int64_t num_pages;
+  // workspace carve-up
+  uint32_t* status;
+  PagesEntry* entries;       // [n]
+  int32_t* chunk_free;       // [chunks] free pages of each chunk
+  int32_t* word_prefix;      // [chunks][kPagesChunk / 32] free pages of the chunk before each word
+  uint32_t* bits;            // [chunks][kPagesChunk / 32] free pages
+  int32_t* rows;             // [n][max_pages] the parents' rows (fork)
+};
+
+struct CompactArgs {
+  uint8_t* codes;
+  uint16_t* scales;          // null: an unscaled pool
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* q_start;    // [batch + 1]
+  const int64_t* keep;       // [batch][mask_words]
+  const int32_t* page_refs;  // [num_pages] or null
+  int32_t* new_lens;         // [batch]
+  uint32_t* status;
+  int64_t num_pages;
+  int32_t max_pages, batch, mask_words, page_size, kv_rows, head_dim;
+};
+
+kvq_status launch_copy_pages(void* codes, void* scales, const int32_t* src, const int32_t* dst, int32_t n,
+                             int64_t num_pages, uint32_t code_vecs, uint32_t scale_vecs, cudaStream_t stream);
+kvq_status launch_fork_pages(const PagesArgs& a, cudaStream_t stream);
+kvq_status launch_resize_pages(const PagesArgs& a, cudaStream_t stream);
+kvq_status launch_compact(const CompactArgs& a, cudaStream_t stream);
 }  // namespace kvq

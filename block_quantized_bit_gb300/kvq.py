@@ -8,6 +8,7 @@ in libkvq's CUDA kernels.  If the library has not been built, importing works bu
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -27,7 +28,8 @@ KVQ_OUT_BF16 = 0
 KVQ_OUT_F32 = 1
 
 STATUS = {0: "KVQ_OK", -1: "KVQ_EINVAL", -2: "KVQ_EKIND", -3: "KVQ_EHEADDIM", -4: "KVQ_EALIGN",
-          -5: "KVQ_EWORKSPACE", -6: "KVQ_EARCH", -7: "KVQ_ECUDA", -8: "KVQ_EUNSUPPORTED", -9: "KVQ_ETIMEOUT"}
+          -5: "KVQ_EWORKSPACE", -6: "KVQ_EARCH", -7: "KVQ_ECUDA", -8: "KVQ_EUNSUPPORTED", -9: "KVQ_ETIMEOUT",
+          -10: "KVQ_ENOPAGES"}
 
 EXPORTS = ["kvq_pool_bytes", "kvq_scale_bytes", "kvq_bytes_per_token", "kvq_num_pages", "kvq_store",
            "kvq_decode_workspace_bytes", "kvq_decode_workspace_bytes_ex", "kvq_decode_path",
@@ -36,7 +38,8 @@ EXPORTS = ["kvq_pool_bytes", "kvq_scale_bytes", "kvq_bytes_per_token", "kvq_num_
            "kvq_device_check", "kvq_version", "kvq_decode_noalloc", "kvq_noalloc_status", "kvq_wait_probe",
            "kvq_extend_workspace_bytes", "kvq_extend", "kvq_store_act_quant", "kvq_store_unscaled",
            "kvq_bytes_per_token_ex", "kvq_num_pages_ex", "kvq_exp2_probe", "kvq_extend_workspace_bytes_ex",
-           "kvq_extend_ex", "kvq_extend_path"]
+           "kvq_extend_ex", "kvq_extend_path", "kvq_pages_workspace_bytes", "kvq_pages_copy", "kvq_pages_fork",
+           "kvq_pages_resize", "kvq_pages_compact"]
 
 
 class kvq_layout(ctypes.Structure):
@@ -107,6 +110,11 @@ def lib():
             "kvq_extend_path": (i32, [LP, i32, i32, i32, EP]),
             "kvq_extend_ex": (i32, [P, P, P, P, i32, P, P, i32, i32, i32, ctypes.c_float, P, i32, P, sz, LP, i32,
                                     EP, P]),
+            "kvq_pages_workspace_bytes": (sz, [LP, i32, i32]),
+            "kvq_pages_copy": (i32, [P, P, P, P, i32, LP, i32, P]),
+            "kvq_pages_fork": (i32, [P, i32, P, i32, P, P, P, i32, P, P, P, sz, LP, P]),
+            "kvq_pages_resize": (i32, [P, i32, P, i32, P, P, P, i32, P, sz, LP, P]),
+            "kvq_pages_compact": (i32, [P, P, P, i32, P, P, P, i32, i32, P, P, P, sz, LP, i32, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -358,6 +366,146 @@ def kvq_extend(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
         _check(lib().kvq_extend(*args, _stream(stream)), "kvq_extend")
     else:
         _check(lib().kvq_extend_ex(*args, opts, _stream(stream)), "kvq_extend_ex")
+
+
+# ---------------------------------------------------------------------------- pages
+# The calls below belong to loops of short GPU work, so what they marshal is checked and passed as plain
+# integers, and a layout's C struct is built once.
+_I32, _I64, _U8, _I16, _BF16 = torch.int32, torch.int64, torch.uint8, torch.int16, torch.bfloat16
+_layout_refs: dict = {}
+
+
+def _layout_ref(L: Layout):
+    key = (L.num_pages, L.page_size, L.num_kv_heads, L.head_dim, L.v_dim, L.mla)
+    ref = _layout_refs.get(key)
+    if ref is None:
+        if len(_layout_refs) >= 1024:
+            _layout_refs.clear()
+        ref = _layout_refs[key] = ctypes.byref(L.c())
+    return ref
+
+
+def _check_args(*args):
+    """(name, tensor, type) triples: tensors of that type, dense, all on the current CUDA device."""
+    for name, t, dtype in args:
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    if not all([t.is_cuda for _, t, _ in args]):
+        raise ValueError("every tensor must be on the current CUDA device")
+    device = torch.cuda.current_device()
+    for name, t, _ in args:
+        if t.get_device() != device:
+            raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _pool_args(pool, scales, layout: Layout, kind):
+    """The kind's number and the pool's (name, tensor, type) triples; a block-scaled kind needs scales."""
+    k = _kind(kind)
+    if pool.numel() < math.prod(layout.codes_shape()):
+        raise ValueError("pool must have the layout's %s codes" % (layout.codes_shape(),))
+    if k not in (KVQ_FP8_E4M3, KVQ_Q8_0):
+        return k, (("pool", pool, _U8),), None
+    if scales is None or scales.numel() < math.prod(layout.scales_shape()):
+        raise ValueError("scales must have the layout's %s scales" % (layout.scales_shape(),))
+    return k, (("pool", pool, _U8), ("scales", scales, scales.dtype if scales.dtype.itemsize == 2 else _I16)), scales
+
+
+def alloc_pages_workspace(layout: Layout, n: int, max_pages_per_seq: int, device="cuda"):
+    """Workspace of kvq_pages_fork and kvq_pages_resize for n list entries (kvq_pages_compact takes it too)."""
+    b = lib().kvq_pages_workspace_bytes(ctypes.byref(layout.c()), int(n), int(max_pages_per_seq))
+    if b == 0:
+        raise KvqError(-1, "kvq_pages_workspace_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+def kvq_pages_copy(pool: torch.Tensor, scales: Optional[torch.Tensor], src: torch.Tensor, dst: torch.Tensor,
+                   layout: Layout, kind, stream=None):
+    """Page dst[i] of the pool becomes a copy of page src[i] (int32 lists; pairs with -1 are skipped)."""
+    n = src.numel()
+    if dst.numel() != n:
+        raise ValueError("src and dst must have one entry per copy")
+    k, checked, scales = _pool_args(pool, scales, layout, kind)
+    _check_args(*checked, ("src", src, _I32), ("dst", dst, _I32))
+    st = lib().kvq_pages_copy(pool.data_ptr(), None if scales is None else scales.data_ptr(), src.data_ptr(),
+                              dst.data_ptr(), n, _layout_ref(layout), k, _raw_stream(stream))
+    if st:
+        raise KvqError(st, "kvq_pages_copy")
+
+
+def _check_tables(block_table, seq_lens, page_refs, layout: Layout):
+    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [batch, max_pages] and seq_lens [batch]")
+    if page_refs is not None and page_refs.numel() < layout.num_pages:
+        raise ValueError("page_refs needs one count per page")
+
+
+def kvq_pages_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, src: torch.Tensor,
+                   dst: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor, workspace: torch.Tensor,
+                   layout: Layout, stream=None):
+    """Rows dst continue rows src (int32 lists, parents read as before the call); the copies of partly filled
+    last pages that kvq_pages_copy must then make in every layer are written to copy_src / copy_dst."""
+    n = src.numel()
+    if dst.numel() != n or copy_src.numel() != n or copy_dst.numel() != n:
+        raise ValueError("src, dst, copy_src and copy_dst must have the same length")
+    _check_tables(block_table, seq_lens, page_refs, layout)
+    _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
+                ("src", src, _I32), ("dst", dst, _I32), ("copy_src", copy_src, _I32), ("copy_dst", copy_dst, _I32),
+                ("workspace", workspace, _U8))
+    batch, max_pages = block_table.shape
+    st = lib().kvq_pages_fork(block_table.data_ptr(), max_pages, seq_lens.data_ptr(), batch, page_refs.data_ptr(),
+                              src.data_ptr(), dst.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
+                              workspace.data_ptr(), workspace.numel(), _layout_ref(layout), _raw_stream(stream))
+    if st:
+        raise KvqError(st, "kvq_pages_fork")
+
+
+def kvq_pages_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, seqs: torch.Tensor,
+                     new_lens: torch.Tensor, workspace: torch.Tensor, layout: Layout, stream=None):
+    """Rows seqs get room for new_lens tokens (int32 lists): pages are taken or released; 0 frees a row."""
+    n = seqs.numel()
+    if new_lens.numel() != n:
+        raise ValueError("seqs and new_lens must have the same length")
+    _check_tables(block_table, seq_lens, page_refs, layout)
+    _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
+                ("seqs", seqs, _I32), ("new_lens", new_lens, _I32), ("workspace", workspace, _U8))
+    batch, max_pages = block_table.shape
+    st = lib().kvq_pages_resize(block_table.data_ptr(), max_pages, seq_lens.data_ptr(), batch, page_refs.data_ptr(),
+                                seqs.data_ptr(), new_lens.data_ptr(), n, workspace.data_ptr(), workspace.numel(),
+                                _layout_ref(layout), _raw_stream(stream))
+    if st:
+        raise KvqError(st, "kvq_pages_resize")
+
+
+def kvq_pages_compact(pool: torch.Tensor, scales: Optional[torch.Tensor], block_table: torch.Tensor,
+                      seq_lens: torch.Tensor, q_start: torch.Tensor, keep: torch.Tensor, new_lens: torch.Tensor,
+                      workspace: torch.Tensor, layout: Layout, kind, page_refs: Optional[torch.Tensor] = None,
+                      stream=None):
+    """Of the last q_start[b+1] - q_start[b] tokens of sequence b, those whose bit is set in keep ([B, words]
+    int64) move together; new_lens ([B] int32) receives the tokens that remain."""
+    B = seq_lens.numel()
+    if keep.dim() != 2 or keep.shape[0] != B or q_start.numel() != B + 1 or new_lens.numel() != B:
+        raise ValueError("keep must be [batch, words], q_start [batch + 1] and new_lens [batch]")
+    _check_tables(block_table, seq_lens, page_refs, layout)
+    k, checked, scales = _pool_args(pool, scales, layout, kind)
+    if page_refs is not None:
+        checked += (("page_refs", page_refs, _I32),)
+    _check_args(*checked, ("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("q_start", q_start, _I32),
+                ("keep", keep, _I64), ("new_lens", new_lens, _I32), ("workspace", workspace, _U8))
+    st = lib().kvq_pages_compact(pool.data_ptr(), None if scales is None else scales.data_ptr(), block_table.data_ptr(),
+                                 block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(), keep.data_ptr(),
+                                 keep.shape[1], B, new_lens.data_ptr(),
+                                 None if page_refs is None else page_refs.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), _layout_ref(layout), k, _raw_stream(stream))
+    if st:
+        raise KvqError(st, "kvq_pages_compact")
 
 
 def kvq_workspace_status(workspace: torch.Tensor, stream=None) -> int:

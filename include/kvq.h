@@ -63,7 +63,8 @@ typedef enum {
     KVQ_EARCH = -6,        /* current device is not compute capability 10.3 */
     KVQ_ECUDA = -7,        /* a CUDA call or launch failed */
     KVQ_EUNSUPPORTED = -8, /* valid, but no kernel for this shape (see kvq_decode) */
-    KVQ_ETIMEOUT = -9      /* a kernel gave up a bounded wait (reported by kvq_workspace_status) */
+    KVQ_ETIMEOUT = -9,     /* a kernel gave up a bounded wait (reported by kvq_workspace_status) */
+    KVQ_ENOPAGES = -10     /* too few free pages; nothing was changed (reported by kvq_workspace_status) */
 } kvq_status;
 
 /*
@@ -332,6 +333,72 @@ kvq_status kvq_noalloc_status(void* stream);
  * Synchronizes `stream`.
  */
 kvq_status kvq_workspace_status(const void* workspace, void* stream);
+
+/* ---------------------------------------------------------------- pages of the cache */
+/*
+ * Copies, forks, growth, release and compaction of cache pages.  The upstream pages have no counterpart: they
+ * leave pages to the engine around the cache.  These calls let that engine keep its tables on the GPU, with no
+ * host synchronization, in captured graphs too.
+ *
+ * Beside the pool the caller keeps one int32 per page, page_refs (device, [layout->num_pages]): the number of
+ * block-table rows that hold the page; 0 = free.  Row b of block_table holds the pages of its first
+ * ceil(seq_lens[b] / page_size) entries; -1 entries hold nothing.  Tables of one cache serve every layer:
+ * fork and resize change tables and counts once, and copy and compact move the rows of one layer's pool.
+ *
+ * Calls that need pages take the lowest-numbered free ones, in list order and, within a row, in column order.
+ * Pages that a call releases are free from the next call on.  A call whose list is bad (an index outside
+ * [0, batch), the same row twice among those that change, a length outside [0, max_pages_per_seq * page_size])
+ * changes nothing and makes kvq_workspace_status report KVQ_EINVAL; one that finds too few free pages changes
+ * nothing and makes it report KVQ_ENOPAGES.  A count that would fall below 0 stays 0 and is reported as
+ * KVQ_EINVAL.  Entries >= num_pages are kept in the rows but never counted.
+ * workspace: at least kvq_pages_workspace_bytes for n list entries (0 if invalid; pools of more than 2^26 pages
+ * are KVQ_EUNSUPPORTED), 16-byte aligned; its content on entry is irrelevant.  All arrays int32, 4-byte aligned.
+ */
+size_t kvq_pages_workspace_bytes(const kvq_layout* layout, int32_t n, int32_t max_pages_per_seq);
+/*
+ * Page dst[i] of one layer's pool becomes a copy of page src[i] (codes and scales), i = 0 .. n-1.  A pair with a
+ * negative or too large page is skipped.  Destinations must be distinct, and no destination may be a source of
+ * the same call; a page may be the source of many.  For the block-scaled kinds a page's scales must be a
+ * multiple of 16 bytes (else KVQ_EUNSUPPORTED), as they are with page_size 16.
+ */
+kvq_status kvq_pages_copy(void* pool, void* scales, const int32_t* src, const int32_t* dst, int32_t n,
+                          const kvq_layout* layout, kvq_kind kind, void* stream);
+/*
+ * Row dst[i] becomes a continuation of row src[i], all at once: parents are read as they were before the call,
+ * so src = the parent of every beam and dst = 0 .. n-1 re-orders beams.  dst[i]'s own pages are released.  The
+ * child shares the parent's full pages.  A partly filled last page goes on with one row: the parent's, or, where
+ * the parent's row is itself among dst, the first child in the list; every other child gets a free page, and
+ * (copy_src[i], copy_dst[i]) (device, [n]) name the copy that kvq_pages_copy must then make in each layer; they
+ * are -1 where no copy is due.  A masked (-1) last page stays masked.  Entries of row dst[i] behind its last page
+ * become -1, and seq_lens[dst[i]] the parent's length.
+ */
+kvq_status kvq_pages_fork(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,
+                          int32_t* page_refs, const int32_t* src, const int32_t* dst, int32_t n, int32_t* copy_src,
+                          int32_t* copy_dst, void* workspace, size_t workspace_bytes, const kvq_layout* layout,
+                          void* stream);
+/*
+ * Row seqs[i] gets room for new_lens[i] tokens: missing pages are taken, surplus pages released and their
+ * entries set to -1; seq_lens[seqs[i]] = new_lens[i].  A new length of 0 frees the row.  The pages taken hold
+ * whatever they held before; store the new tokens before an attention reads them.
+ */
+kvq_status kvq_pages_resize(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,
+                            int32_t* page_refs, const int32_t* seqs, const int32_t* new_lens, int32_t n,
+                            void* workspace, size_t workspace_bytes, const kvq_layout* layout, void* stream);
+/*
+ * Keeps some of each sequence's last n_b = q_start[b + 1] - q_start[b] stored tokens (n_b <= 64 * mask_words,
+ * mask_words <= 4) and moves their rows together, in order, behind the token before them: bit j % 64 of
+ * keep[b][j / 64] (device int64, [batch][mask_words], 8-byte aligned) keeps token seq_lens[b] - n_b + j.  With
+ * the tree mask of the last accepted token as keep, the accepted path of a drafted tree stays.  new_lens[b]
+ * (device) = the tokens that remain; block_table, seq_lens and counts are not changed: kvq_pages_resize with
+ * new_lens releases the surplus pages, once all layers are compacted.  A sequence is left as it is, with
+ * new_lens[b] = seq_lens[b] and KVQ_EINVAL reported by kvq_workspace_status, when its numbers are inconsistent,
+ * a page of its last n_b tokens is masked or past the pool, or, with page_refs not NULL, a page that rows would
+ * move to is held by another row too.  workspace: at least 256 bytes, 16-byte aligned.
+ */
+kvq_status kvq_pages_compact(void* pool, void* scales, const int32_t* block_table, int32_t max_pages_per_seq,
+                             const int32_t* seq_lens, const int32_t* q_start, const int64_t* keep, int32_t mask_words,
+                             int32_t batch, int32_t* new_lens, const int32_t* page_refs, void* workspace,
+                             size_t workspace_bytes, const kvq_layout* layout, kvq_kind kind, void* stream);
 
 /* ---------------------------------------------------------------- rounding probes */
 /*
