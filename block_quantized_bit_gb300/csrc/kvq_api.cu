@@ -147,12 +147,19 @@ using namespace kvq;
 
 namespace {
 
+// Masks of the decode's sequences when they are the rows of drafted trees (kvq_tree).
+struct TreeRows {
+  const int64_t* mask;
+  const int32_t* base;
+  int32_t words;
+};
+
 kvq_status decode_common(const void* q, const void* pool, const void* scales, const int32_t* block_table,
                          int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
                          float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace,
                          size_t workspace_bytes, const kvq_layout* layout, kvq_kind kind,
                          const kvq_decode_options* options, void* stream, bool clear_status,
-                         const int32_t* bt_row = nullptr) {
+                         const int32_t* bt_row = nullptr, const TreeRows* tree = nullptr) {
   kvq_status st = check_layout(layout);
   if (st != KVQ_OK) return st;
   if (!kind_read_ok(kind)) return KVQ_EKIND;
@@ -187,6 +194,9 @@ kvq_status decode_common(const void* q, const void* pool, const void* scales, co
   a.num_pages = layout->num_pages;
   a.max_pages = max_pages_per_seq;
   a.seq_lens = seq_lens;
+  a.tree_mask = tree ? tree->mask : nullptr;
+  a.tree_base = tree ? tree->base : nullptr;
+  a.tree_words = tree ? tree->words : 0;
   a.batch = batch;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = layout->num_kv_heads;
@@ -327,6 +337,52 @@ kvq_status extend_prefixes(const ExtendPlan& ep, const void* q, const void* pool
     if (st != KVQ_OK) return st;
   }
   return KVQ_OK;
+}
+
+// Attention of drafted tokens: the split-K flash kernel (GQA, head_dim 128 and 256), else every drafted token is
+// a sequence of its own to the decode kernels, in chunks, with its mask.
+struct TreePlan {
+  bool flash;
+  kvq_decode_options dec;
+  int32_t chunk, grid;
+  size_t tab_offset, acc_offset, ml_offset;                          // flash
+  size_t dense_bytes, lens_offset, rows_offset, base_offset, total;  // rows through the decode kernels
+};
+
+bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t max_pages, int32_t path,
+               TreePlan* tp) {
+  if (path < 0 || path > 2 || batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages <= 0) return false;
+  if (num_q_heads % L.num_kv_heads != 0) return false;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int64_t G = num_q_heads / L.num_kv_heads;
+  // units (tiles of at least 64 keys, for blocks of 128 rows) and merge CTAs are counted in 32 bits
+  const double units = (static_cast<double>(total_q) * G / 128 + batch) * L.num_kv_heads *
+                       (static_cast<double>(max_pages) * L.page_size / 64 + 1);
+  const bool flash_ok = tree_tc_supported(L.head_dim, L.v_dim, L.mla, batch) && units < 2.0e9 &&
+                        static_cast<double>(total_q) * num_q_heads < 2.0e9;
+  tp->flash = !L.mla && path != 1 && flash_ok;
+  if (!L.mla && path == 2 && !flash_ok) return false;
+  if (tp->flash) {
+    tp->grid = sm_count();
+    const size_t slots = 2 * static_cast<size_t>(tp->grid) * 128;
+    tp->tab_offset = kWorkspaceHeader;
+    tp->ml_offset = tp->tab_offset + up((static_cast<size_t>(batch) + 2) * sizeof(int32_t));
+    tp->acc_offset = tp->ml_offset + up(slots * 2 * sizeof(float));
+    tp->total = tp->acc_offset + up(slots * L.head_dim * sizeof(float));
+    return true;
+  }
+  tp->dec.pages_per_split = 0;
+  tp->dec.path = L.mla ? path : 1;  // (the GQA tensor-core decode has no masks)
+  tp->chunk = std::max<int32_t>(1, std::min<int32_t>(total_q, kExtendChunk));
+  WorkspacePlan w;
+  if (!plan_workspace(L, tp->chunk, num_q_heads, max_pages, &tp->dec, &w) || w.path < 0) return false;
+  const size_t n = static_cast<size_t>(std::max<int32_t>(total_q, 1)) * sizeof(int32_t);
+  tp->dense_bytes = up(w.total);
+  tp->lens_offset = tp->dense_bytes;
+  tp->base_offset = tp->lens_offset + up(n);
+  tp->rows_offset = tp->base_offset + up(n);
+  tp->total = tp->rows_offset + up(n);
+  return true;
 }
 
 // Workspace of a fork or a resize of n list entries: the status word, the entries, the free pages' bitmap with
@@ -680,6 +736,100 @@ kvq_status kvq_extend_ex(const void* q, const void* pool, const void* scales, co
   a.kind = kind;
   a.split_p = ep.split ? 1 : 0;
   return launch_extend_tc(a, s);
+}
+
+size_t kvq_tree_workspace_bytes(const kvq_layout* layout, int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                int32_t max_pages_per_seq, int32_t path) {
+  TreePlan tp;
+  if (check_layout(layout) != KVQ_OK || layout->page_size != kPageTokens) return 0;
+  if (!plan_tree(*layout, batch, total_q, num_q_heads, max_pages_per_seq, path, &tp)) return 0;
+  return tp.total;
+}
+
+kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const int32_t* block_table,
+                    int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* q_start, const int64_t* tree_mask,
+                    int32_t mask_words, int32_t total_q, int32_t batch, int32_t num_q_heads, float sm_scale, void* out,
+                    kvq_out_dtype out_dtype, void* workspace, size_t workspace_bytes, const kvq_layout* layout,
+                    kvq_kind kind, int32_t path, void* stream) {
+  kvq_status st = check_layout(layout);
+  if (st != KVQ_OK) return st;
+  if (!kind_read_ok(kind)) return KVQ_EKIND;
+  if (!has_scales(kind)) scales = nullptr;
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_F32) return KVQ_EINVAL;
+  if (batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages_per_seq <= 0 || mask_words <= 0) return KVQ_EINVAL;
+  if (num_q_heads % layout->num_kv_heads != 0 || path < 0 || path > 2) return KVQ_EINVAL;
+  if (!(sm_scale > 0.0f) || sm_scale > std::numeric_limits<float>::max()) return KVQ_EINVAL;  // finite, > 0
+  if (layout->page_size != kPageTokens || mask_words > kMaxMaskWords) return KVQ_EUNSUPPORTED;
+  if (static_cast<int64_t>(max_pages_per_seq) * kPageTokens > std::numeric_limits<int32_t>::max()) return KVQ_EINVAL;
+  TreePlan tp;
+  if (!plan_tree(*layout, batch, total_q, num_q_heads, max_pages_per_seq, path, &tp)) return KVQ_EUNSUPPORTED;
+  if (!workspace) return KVQ_EINVAL;
+  if (workspace_bytes < tp.total) return KVQ_EWORKSPACE;
+  const bool empty = batch == 0 || total_q == 0;
+  if (!empty && (!q || !pool || (has_scales(kind) && !scales) || !block_table || !seq_lens || !q_start || !tree_mask || !out))
+    return KVQ_EINVAL;
+  if (!aligned(workspace) || !aligned(q) || !aligned(pool) || !aligned(scales) || !aligned(out) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) % 8) != 0)
+    return KVQ_EALIGN;
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(q_start)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return KVQ_ECUDA;
+  if (empty) return KVQ_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (!tp.flash) {
+    int32_t* vlens = reinterpret_cast<int32_t*>(ws + tp.lens_offset);
+    int32_t* vbase = reinterpret_cast<int32_t*>(ws + tp.base_offset);
+    int32_t* vrow = reinterpret_cast<int32_t*>(ws + tp.rows_offset);
+    // rows that no sequence covers keep length 0 and row -1: they are left as they are
+    if (cudaMemsetAsync(vlens, 0, tp.rows_offset - tp.lens_offset, s) != cudaSuccess ||
+        cudaMemsetAsync(vrow, 0xFF, tp.total - tp.rows_offset, s) != cudaSuccess)
+      return KVQ_ECUDA;
+    st = launch_tree_expand(q_start, seq_lens, batch, total_q, mask_words,
+                            static_cast<int64_t>(max_pages_per_seq) * kPageTokens, vlens, vrow, vbase,
+                            reinterpret_cast<uint32_t*>(ws), s);
+    if (st != KVQ_OK) return st;
+    const size_t q_row = static_cast<size_t>(num_q_heads) * layout->head_dim * 2;
+    const size_t o_row = static_cast<size_t>(num_q_heads) * layout->v_dim * (out_dtype == KVQ_OUT_F32 ? 4 : 2);
+    for (int32_t c0 = 0; c0 < total_q; c0 += tp.chunk) {
+      const int32_t n = std::min<int32_t>(tp.chunk, total_q - c0);
+      const TreeRows rows = {tree_mask + static_cast<int64_t>(c0) * mask_words, vbase + c0, mask_words};
+      st = decode_common(static_cast<const uint8_t*>(q) + c0 * q_row, pool, scales, block_table, max_pages_per_seq,
+                         vlens + c0, n, num_q_heads, sm_scale, static_cast<uint8_t*>(out) + c0 * o_row, out_dtype,
+                         workspace, tp.dense_bytes, layout, kind, &tp.dec, s, false, vrow + c0, &rows);
+      if (st != KVQ_OK) return st;
+    }
+    return KVQ_OK;
+  }
+  TreeArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.codes = static_cast<const uint8_t*>(pool);
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.mask = tree_mask;
+  a.out = out;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.tab = reinterpret_cast<int32_t*>(ws + tp.tab_offset);
+  a.part_acc = reinterpret_cast<float*>(ws + tp.acc_offset);
+  a.part_ml = reinterpret_cast<float*>(ws + tp.ml_offset);
+  a.num_pages = layout->num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = layout->num_kv_heads;
+  a.head_dim = layout->head_dim;
+  a.mask_words = mask_words;
+  a.grid = tp.grid;
+  a.score_scale = sm_scale * 1.4426950408889634f;  // log2(e)
+  a.out_dtype = out_dtype;
+  a.kind = kind;
+  return launch_tree_tc(a, s);
 }
 
 size_t kvq_pages_workspace_bytes(const kvq_layout* layout, int32_t n, int32_t max_pages_per_seq) {

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) decode_cc_kernel(KParams p) 
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t b = plan.b;
+  if (uncovered(p, b)) return;
   const int32_t local = static_cast<int32_t>(blockIdx.x) - plan.base;
   const int32_t qg = local / plan.nsplit;
   const int32_t split = local - qg * plan.nsplit;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) decode_cc_kernel(KParams p) 
       const uint8_t* vc = MLA ? kc : kc + Cfg::CODE_BYTES;
       const uint16_t* ks = reinterpret_cast<const uint16_t*>(kc + Cfg::NKV * Cfg::CODE_BYTES);
       const uint16_t* vs = MLA ? ks : ks + kPage * NB;
+      const uint32_t vis = page_vis(p, b, pg, L);
 
       // ---- scores of this lane's head for its tokens of the page
       float sc[ITERS];
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) decode_cc_kernel(KParams p) 
 #pragma unroll
         for (int h = 0; h < GT; ++h) v[h] = part[h][0] + part[h][1];
         const float dot = reduce_heads<LPT, GT>(v, lane);
-        sc[it] = (pg * kPage + t < L) ? dot * p.score_scale : -INFINITY;
+        sc[it] = ((vis >> t) & 1u) ? dot * p.score_scale : -INFINITY;
       }
       // ---- online softmax for this lane's head; the page max is uniform over the head's lanes
       float mx = -INFINITY;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) decode_cc_kernel(KParams p) 
         float ph[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) ph[h] = __shfl_sync(0xffffffffu, sc[it], tg * LPT + head_lane<LPT, GT>(h));
-        if (pg * kPage + t >= L) continue;  // never touch rows past the sequence end
+        if (!((vis >> t) & 1u)) continue;  // never touch rows past the sequence end
 #pragma unroll
         for (int k = 0; k < CPL_V; ++k) {
           const int c = c0 + 32 * k;
@@ -509,6 +511,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(KParams p, OutT* _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int sub = lane >> 3, q = lane & 7;  // split of the four, float4 of the slice
   const int32_t b = blockIdx.x / units_per_seq;
+  if (uncovered(p, b)) return;
   const int32_t u = blockIdx.x - b * units_per_seq;
   const int32_t slices = DV / 32;
   const int32_t slice = u % slices;

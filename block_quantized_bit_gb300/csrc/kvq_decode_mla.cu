@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
     mla_first(t, sTab, p, C, n_items);
     uint32_t n = 0;
     while (ok && t.live) {
-      int32_t phys = -1, nvalid = 0;
+      int32_t phys = -1, vis = 0;  // vis: the page's tokens that are attended to
       if (lane < kPagesPerTile) {
         const int32_t pg = t.pg0 + t.i * kPagesPerTile + lane;
         if (pg < t.pg1) {
@@ -350,13 +350,13 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
             set_status(p.status, kStatusBadPage);
             phys = -1;
           }
-          if (phys >= 0) nvalid = min(kPage, t.L - pg * kPage);  // >= 1: pg < the sequence's page count
+          if (phys >= 0) vis = static_cast<int32_t>(page_vis(p, t.b, pg, t.L));
         }
       }
       const uint32_t npg = __reduce_add_sync(0xffffffffu, phys >= 0 ? 1u : 0u);
       int32_t nv[kPagesPerTile];
 #pragma unroll
-      for (int i = 0; i < kPagesPerTile; ++i) nv[i] = __shfl_sync(0xffffffffu, nvalid, i);
+      for (int i = 0; i < kPagesPerTile; ++i) nv[i] = __shfl_sync(0xffffffffu, vis, i);
       // the scale buffer of this tile parity was last read by the K warps two tiles ago
       if (n >= 2 && !mbar_wait_bounded(&bar_sc_free[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
 #pragma unroll 1
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
         const int rs = u % kRing, ks = u & 1;
         if (!mbar_wait_bounded(&bar_full[rs], (u / kRing) & 1)) { ok = false; break; }
         if (j == 0) {
-          v_ok = off < sMeta[rs * kPagesPerTile + pi];
+          v_ok = (sMeta[rs * kPagesPerTile + pi] >> off) & 1;
           // the validity slot of this tile parity was last read by the softmax of tile n - 2
           if (n >= 2 && !mbar_wait_bounded(&bar_p_full[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
           if (part == 0) sValid[(n & 1) * kTile + tt] = v_ok ? 1 : 0;  // published with sc_free (last slab)

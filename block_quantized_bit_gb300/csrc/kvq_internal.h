@@ -18,6 +18,9 @@ struct DecodeArgs {
   int64_t num_pages;
   int32_t max_pages;
   const int32_t* seq_lens;
+  const int64_t* tree_mask;  // per sequence, the drafted tokens it sees, or null; set by kvq_tree (with bt_row)
+  const int32_t* tree_base;
+  int32_t tree_words;
   int32_t batch;
   int32_t num_q_heads;
   int32_t num_kv_heads;
@@ -131,6 +134,42 @@ kvq_status launch_exp2_probe(const float* x, float* y, int64_t n, cudaStream_t s
 // are left as they are and flagged in the status word).
 kvq_status launch_extend_expand(const int32_t* q_start, const int32_t* seq_lens, int32_t batch, int32_t total_q,
                                 int32_t* vlens, int32_t* vrow, uint32_t* status, cudaStream_t stream);
+
+// Attention of drafted tokens over the cache (kvq_tree): the split-K flash kernel.
+struct TreeArgs {
+  const uint16_t* q;          // [total_q][num_q_heads][head_dim] bf16
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const int32_t* block_table; // [batch][max_pages]
+  const int32_t* seq_lens;    // [batch]
+  const int32_t* q_start;     // [batch + 1]
+  const int64_t* mask;        // [total_q][mask_words]
+  void* out;                  // [total_q][num_q_heads][head_dim]
+  uint32_t* status;
+  int32_t* tab;               // [batch + 1] work units before each sequence, then [1] CTAs that share them
+  float* part_acc;            // [2 * CTAs][128][head_dim]
+  float* part_ml;             // [2 * CTAs][128][2]
+  int64_t num_pages;
+  int32_t max_pages;
+  int32_t batch;
+  int32_t total_q;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t mask_words;
+  int32_t grid;               // CTAs launched
+  float score_scale;          // sm_scale * log2(e)
+  kvq_out_dtype out_dtype;
+  kvq_kind kind;
+};
+constexpr int32_t kMaxTreeBatch = 2048;  // sequences whose unit prefixes fit the kernel's shared table
+bool tree_tc_supported(int32_t head_dim, int32_t v_dim, int32_t mla, int32_t batch);
+kvq_status launch_tree_tc(const TreeArgs& a, cudaStream_t stream);
+// Per query row: stored tokens, block-table row and first drafted position of its sequence; rows that no
+// (consistent) sequence covers get length 0 and row -1.
+kvq_status launch_tree_expand(const int32_t* q_start, const int32_t* seq_lens, int32_t batch, int32_t total_q,
+                              int32_t mask_words, int64_t max_tokens, int32_t* vlens, int32_t* vrow, int32_t* vbase,
+                              uint32_t* status, cudaStream_t stream);
 
 // Pages of the cache (kvq_pages_*).
 constexpr int32_t kPagesChunk = 8192;       // pages whose counts one CTA of the plan reads

@@ -31,6 +31,9 @@ struct KParams {
   const int32_t* block_table;
   const int32_t* bt_row;  // block-table row of each sequence, or null: row b (the extend's per-token prefixes)
   const int32_t* seq_lens;
+  const int64_t* tree_mask;  // [batch][tree_words] drafted tokens each row sees (kvq_tree), or null
+  const int32_t* tree_base;  // [batch] position of the first drafted token
+  int32_t tree_words;
   float* part_acc;
   float* part_ml;
   int32_t* plan_tab;      // [batch][2] first item, splits per query group; CTA 0 of the decode writes it
@@ -58,6 +61,36 @@ struct KParams {
 __device__ __forceinline__ int32_t bt_entry(const KParams& p, int32_t b, int32_t pg) {
   const int64_t row = p.bt_row ? __ldg(p.bt_row + b) : b;
   return __ldg(p.block_table + row * p.max_pages + pg);
+}
+
+// Bits j0 .. j0 + 63 of a drafted token's mask (kvq_tree): bit i says whether it sees drafted token j0 + i;
+// what lies before the drafted tokens (j0 + i < 0) is seen.
+__device__ __forceinline__ uint64_t tree_window(const int64_t* mask, int32_t words, int32_t j0) {
+  if (j0 <= -64) return ~0ull;
+  auto word = [&](int32_t w) -> uint64_t {
+    return w < words ? static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(mask) + w)) : 0ull;
+  };
+  if (j0 < 0) return (word(0) << -j0) | ((1ull << -j0) - 1ull);
+  const int32_t w = j0 >> 6, s = j0 & 63;
+  return s == 0 ? word(w) : (word(w) >> s) | (word(w + 1) << (64 - s));
+}
+
+// Tokens of page pg that sequence b attends to (bit t = token t of the page): those before its end, and of
+// the drafted tokens those in its mask.
+__device__ __forceinline__ uint32_t page_vis(const KParams& p, int32_t b, int32_t pg, int32_t L) {
+  const int32_t left = L - pg * kPage;
+  uint32_t v = left >= kPage ? 0xFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+  if (p.tree_mask != nullptr) {
+    const int32_t j0 = pg * kPage - __ldg(p.tree_base + b);
+    if (j0 > -kPage)
+      v &= static_cast<uint32_t>(tree_window(p.tree_mask + static_cast<int64_t>(b) * p.tree_words, p.tree_words, j0));
+  }
+  return v;
+}
+
+// A query row that no sequence covers (kvq_tree): its output is left as it was.
+__device__ __forceinline__ bool uncovered(const KParams& p, int32_t b) {
+  return p.tree_mask != nullptr && __ldg(p.bt_row + b) < 0;
 }
 
 __device__ __forceinline__ int32_t seq_pages(const KParams& p, int32_t b) {
@@ -163,6 +196,9 @@ inline KParams make_kparams(const DecodeArgs& a) {
   p.block_table = a.block_table;
   p.bt_row = a.bt_row;
   p.seq_lens = a.seq_lens;
+  p.tree_mask = a.tree_mask;
+  p.tree_base = a.tree_base;
+  p.tree_words = a.tree_words;
   p.part_acc = a.part_acc;
   p.part_ml = a.part_ml;
   p.plan_tab = a.plan_tab;

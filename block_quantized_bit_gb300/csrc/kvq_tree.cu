@@ -1,0 +1,849 @@
+// kvq_tree.cu -- attention of drafted tokens over the 8-bit pool: split-K, flash-shaped, on the tcgen05 tensor cores.
+//
+// The last n_b stored tokens of sequence b are drafted; query row (i, h) sees every token before them and those
+// drafted tokens whose bit is set in its mask:
+//   out[i][h] = sum_t softmax_t(sm_scale q[i][h].K[t]) V[t]   over t < L - n, and t = L - n + j with bit j set.
+// Rows are few (n_b times the heads of a kv head) and contexts long, so the work is reading K and V once:
+// 2 * Hkv * D * 17/16 bytes per token.  A block of 128 rows of one (sequence, kv head) shares every dequantized
+// tile, in the extend kernel's arrangement (rows are the MMA's M; S and O in tensor memory; the same tile
+// layouts, dequant and softmax), with three differences.
+//
+// Work split.  A unit is one tile of T keys for one block of rows; units are numbered by (sequence, row block,
+// kv head, tile), and CTA c of C takes the units [c U / C, (c + 1) U / C): every CTA gets the same number of tiles to
+// within one, whatever the lengths, and reads a contiguous run of each sequence.  The run is cut into segments, one
+// per (sequence, row block, kv head); only a CTA's first and last segment can be parts of a block, so two partial
+// slots per CTA suffice.  A segment that is a whole block writes its output; the others write (m, l, O) and
+// the merge kernel (a programmatic dependent) joins the segments of each row.
+//
+// Masks.  Visibility of a half tile's keys is one 64-bit word per row: ones before the drafted tokens, the
+// row's mask bits among them, zeros behind the end, and zeros for masked pages.  A warp whose words are all ones
+// takes the unmasked pass.
+//
+// Row blocks that are not full.  Lane quarters without a row skip the softmax (an MMA row depends on its own P row
+// only); their warps just keep the barriers' counts.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "kvq_device.cuh"
+#include "kvq_flash.cuh"
+#include "kvq_internal.h"
+#include "kvq_plan.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kM = 128;  // query rows per block (the MMA M)
+constexpr int kSmWarps = 8;  // two per tensor-memory lane quarter, each on half of a tile's keys
+constexpr int kDwWarps = 8;
+constexpr int kMmaWarp = kSmWarps + kDwWarps;   // warp 16
+constexpr int kProdWarp = kMmaWarp + 1;         // warps 17 (K ring) and 18 (V ring)
+constexpr int kThreads = (kProdWarp + 2) * 32;  // 19 warps
+constexpr int kDwThreads = kDwWarps * 32;
+constexpr int kTmemCols = 512;
+constexpr int kBox = kPage * 128;      // one TMA box: 16 tokens x 128 code bytes
+constexpr float kLazyRescale = 8.0f;   // log2 headroom before the running max must move
+constexpr int kMinUnits = 2;           // tiles per CTA below which fewer CTAs share the work
+
+template <int D>
+struct TCfg {
+  static constexpr int T = (D == 128) ? 128 : 64;  // keys per tile
+  static constexpr int PPT = T / kPage;            // pages per tile
+  static constexpr int RS = D * 16;                // bytes between 8-row groups of a tile
+  static constexpr int KV_TILE = T * D * 2;        // one bf16 K or V tile
+  static constexpr int Q_BYTES = kM * D * 2;
+  static constexpr int PARTS = kDwThreads / T;     // dequant threads per token row
+  static constexpr int SPAN = D / PARTS;           // codes per dequant thread (of K, and of V)
+  static constexpr int NCH = SPAN / 16;            // 16-code chunks per dequant thread
+  static constexpr int NBT = SPAN / 32;            // scale blocks per dequant thread
+  static constexpr int NB = D / 32;
+  static constexpr int NSL = D / 128;              // 128-byte slices of a code row
+  static constexpr int SC_KV = kPage * NB * 2;     // scale bytes of one page of K or of V
+  // a ring slot (of the K ring or of the V ring): codes [page][slice] boxes as TMA wrote them, then the
+  // scales [page].  The K ring is freed as soon as K is dequantized, the V ring only after the previous PV,
+  // so the two rings run at their own pace and the K ring runs deeper.
+  static constexpr int CODE_BYTES = PPT * NSL * kBox;
+  static constexpr int SLOT_BYTES = CODE_BYTES + PPT * SC_KV;
+  static constexpr int KSTAGES = 3;
+  static constexpr int VSTAGES = (D == 128) ? 3 : 2;
+  static constexpr int NSLOTS = KSTAGES + VSTAGES;  // K ring slots, then V ring slots
+  static constexpr int RING_OFF = 0;  // 1024-byte aligned: swizzle atoms
+  static constexpr int K_OFF = RING_OFF + NSLOTS * SLOT_BYTES;
+  static constexpr int V_OFF = K_OFF + KV_TILE;
+  static constexpr int Q_OFF = V_OFF + KV_TILE;
+  static constexpr int META_OFF = Q_OFF + Q_BYTES;              // [NSLOTS][PPT] valid tokens per page
+  static constexpr int RED_OFF = META_OFF + NSLOTS * PPT * 4;   // [2 parities][2 halves][128 rows] row maxima
+  static constexpr int SUM_OFF = RED_OFF + 2 * 2 * kM * 4;      // [2 item parities][2 halves][128 rows] row sums
+  static constexpr int TAB_OFF = SUM_OFF + 2 * 2 * kM * 4;      // [batch + 1] units before each sequence
+  static constexpr int NBARS = 2 * NSLOTS + 10 + 12;
+  static constexpr int BAR_OFF = (TAB_OFF + (kMaxTreeBatch + 1) * 4 + 15) / 16 * 16;  // mbarriers: 8-byte aligned
+  static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
+  // tensor-memory columns: O [0, D); S buffer b [D + b T, D + (b + 1) T); P buffer b [384 + b T / 2, ...)
+  static constexpr int S_COL = D;
+  static constexpr int P_COL = 384;
+  static_assert(D == 128 || D == 256, "the tree kernel needs head_dim 128 or 256");
+  static_assert(D + 2 * T <= P_COL && P_COL + T <= kTmemCols, "tensor-memory columns");
+  static_assert(PARTS * T == kDwThreads && NCH % 2 == 0 && NBT == 2, "dequant split");
+  static_assert(SLOT_BYTES % 1024 == 0, "slots keep the boxes 1024-byte aligned");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  static_assert(K_OFF % 16 == 0 && V_OFF % 16 == 0 && Q_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
+};
+
+// Drafted tokens of sequence b after validation; 0 for an inconsistent one (reported in the status word).
+__device__ __forceinline__ int32_t drafted(const TreeArgs& a, int32_t b, bool report) {
+  const int32_t q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1), L = __ldg(a.seq_lens + b);
+  const int32_t n = q1 - q0;
+  if (q0 < 0 || n < 0 || q1 > a.total_q || n > L || n > 64 * a.mask_words ||
+      L > static_cast<int64_t>(a.max_pages) * kPage) {
+    if (report) set_status(a.status, kStatusBadExtend);
+    return 0;
+  }
+  return n;
+}
+
+__device__ __forceinline__ int32_t row_blocks(int32_t n, int32_t G) { return (n * G + kM - 1) / kM; }
+
+// A segment: the tiles [t0, t1) of row block blk of (sequence b, kv head g); slot: where its partial goes, or -1
+// when the segment is the whole block.
+struct Seg {
+  int32_t b, g, blk, n, L, q0, rows, t0, t1, slot;
+};
+
+struct Range {
+  int32_t u0, u1;  // units of this CTA
+};
+
+// The units of CTA c when C CTAs share U.
+__device__ __forceinline__ int32_t range_start(int32_t U, int32_t C, int32_t c) {
+  return static_cast<int32_t>(static_cast<int64_t>(U) * c / C);
+}
+
+template <int D>
+__device__ __forceinline__ Seg locate(const int32_t* tab, const TreeArgs& a, int32_t G, const Range& r, int32_t u) {
+  using Cfg = TCfg<D>;
+  int lo = 0, hi = a.batch;  // first b with tab[b] > u
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (tab[mid] <= u) lo = mid + 1;
+    else hi = mid;
+  }
+  Seg s;
+  s.b = lo - 1;
+  s.L = __ldg(a.seq_lens + s.b);
+  s.q0 = __ldg(a.q_start + s.b);
+  s.n = drafted(a, s.b, false);
+  const int32_t nt = (s.L + Cfg::T - 1) / Cfg::T;
+  const int32_t local = u - tab[s.b];
+  const int32_t item = local / nt;
+  s.blk = item / a.num_kv_heads;
+  s.g = item - s.blk * a.num_kv_heads;
+  s.rows = min(kM, s.n * G - s.blk * kM);
+  s.t0 = local - item * nt;
+  s.t1 = min(nt, s.t0 + (r.u1 - u));
+  const bool whole = s.t0 == 0 && s.t1 == nt;
+  s.slot = whole ? -1 : 2 * static_cast<int32_t>(blockIdx.x) + (u == r.u0 ? 0 : 1);
+  return s;
+}
+
+// The (segment, tile) pairs of this CTA, in order.
+template <int D>
+struct TreeIter {
+  Seg s;
+  Range r;
+  int32_t u, t;  // first unit of the segment; tile
+  bool live;
+  __device__ __forceinline__ void first(const int32_t* tab, const TreeArgs& a, int32_t G, const Range& range) {
+    r = range;
+    u = r.u0;
+    live = u < r.u1;
+    if (live) {
+      s = locate<D>(tab, a, G, r, u);
+      t = s.t0;
+    }
+  }
+  __device__ __forceinline__ bool last_tile() const { return t == s.t1 - 1; }
+  __device__ __forceinline__ void next_segment(const int32_t* tab, const TreeArgs& a, int32_t G) {
+    u += s.t1 - s.t0;
+    live = u < r.u1;
+    if (live) {
+      s = locate<D>(tab, a, G, r, u);
+      t = s.t0;
+    }
+  }
+  __device__ __forceinline__ void next(const int32_t* tab, const TreeArgs& a, int32_t G) {
+    if (!live) return;
+    if (++t < s.t1) return;
+    next_segment(tab, a, G);
+  }
+};
+
+// 16 ones for each set bit of a 4-bit page mask.
+__device__ __forceinline__ uint64_t spread_pages(uint32_t m) {
+  uint64_t v = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v |= ((m >> i) & 1u) ? (0xFFFFull << (16 * i)) : 0ull;
+  return v;
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap) {
+  using Cfg = TCfg<D>;
+  constexpr int T = Cfg::T;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms are 1024 B
+  uint8_t* sRing = smem + Cfg::RING_OFF;
+  uint8_t* sK = smem + Cfg::K_OFF;
+  uint8_t* sV = smem + Cfg::V_OFF;
+  uint8_t* sQ = smem + Cfg::Q_OFF;
+  int32_t* sMeta = reinterpret_cast<int32_t*>(smem + Cfg::META_OFF);
+  int32_t* sTab = reinterpret_cast<int32_t*>(smem + Cfg::TAB_OFF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
+  // Every barrier completes once per use of its buffer, so a waiter names an unambiguous phase.
+  uint64_t* bar_full = bars;                      // [NSLOTS] ring slot landed (producer arrival + bytes)
+  uint64_t* bar_empty = bars + Cfg::NSLOTS;       // [NSLOTS] ring slot read by every dequant warp
+  uint64_t* bar_k_full = bars + 2 * Cfg::NSLOTS;  // K tile written (dequant warps), once per tile
+  uint64_t* bar_v_full = bar_k_full + 1;          // V tile written (dequant warps), once per tile
+  uint64_t* bar_qk_done = bar_k_full + 2;         // [2] QK into S buffer b completed (commit)
+  uint64_t* bar_pv_done = bar_k_full + 4;         // [2] PV that read P buffer b completed (commit)
+  uint64_t* bar_p_full = bar_k_full + 6;          // [2] P buffer b written, S buffer b read (softmax warps)
+  uint64_t* bar_q_full = bar_k_full + 8;          // an item's Q rows written (softmax warps), once per item
+  uint64_t* bar_o_free = bar_k_full + 9;          // an item's O read out (softmax warps), once per item
+  uint64_t* bar_pair = bar_k_full + 10;           // [4 quarters][2 parities] both half-tile maxima written
+  uint64_t* bar_sum = bar_k_full + 18;            // [4 quarters] both half row sums written, once per item
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t G = a.num_q_heads / a.num_kv_heads;
+
+  // ---- plan: units before every sequence
+  for (int32_t b = tid; b < a.batch; b += kThreads) {
+    const int32_t n = drafted(a, b, blockIdx.x == 0);
+    sTab[b + 1] = n == 0 ? 0 : row_blocks(n, G) * a.num_kv_heads * ((__ldg(a.seq_lens + b) + T - 1) / T);
+  }
+  if (tid == 0) {
+    sTab[0] = 0;
+    for (int s = 0; s < Cfg::NSLOTS; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], kDwWarps);
+    }
+    mbar_init(bar_k_full, kDwWarps);
+    mbar_init(bar_v_full, kDwWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar_qk_done[b], 1);
+      mbar_init(&bar_pv_done[b], 1);
+      mbar_init(&bar_p_full[b], kSmWarps);
+    }
+    mbar_init(bar_q_full, kSmWarps);
+    mbar_init(bar_o_free, kSmWarps);
+    for (int i = 0; i < 12; ++i) mbar_init(&bar_pair[i], 2);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == 0) {  // inclusive prefix, 32 sequences at a time
+    int32_t run = 0;
+    for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {
+      const int32_t b = b0 + lane;
+      int32_t x = b < a.batch ? sTab[b + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < a.batch) sTab[b + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sTmem;
+  // the merge kernel may launch now; it waits for this grid to complete before it reads
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int32_t U = sTab[a.batch];
+  const int32_t C = max(1, min(a.grid, U / kMinUnits));  // CTAs that share the units
+  Range range;
+  range.u0 = static_cast<int32_t>(blockIdx.x) < C ? range_start(U, C, blockIdx.x) : 0;
+  range.u1 = static_cast<int32_t>(blockIdx.x) < C ? range_start(U, C, blockIdx.x + 1) : 0;
+  if (blockIdx.x == 0) {  // the plan, for the merge
+    for (int32_t b = tid; b <= a.batch; b += kThreads) a.tab[b] = sTab[b];
+    if (tid == 0) a.tab[a.batch + 1] = C;
+  }
+  bool ok = true;
+
+  if (warp >= kProdWarp) {
+    // ===================================================================== producers
+    // Warp 13 fills the K ring, warp 14 the V ring.  Lane pi (< PPT) owns page pi of a tile: its block-table
+    // entry (read one tile ahead), valid tokens and copies.
+    const int kv = warp - kProdWarp;
+    const int stages = kv ? Cfg::VSTAGES : Cfg::KSTAGES;
+    const int base = kv ? Cfg::KSTAGES : 0;
+    auto page_entry = [&](const TreeIter<D>& ti) -> int32_t {
+      if (!ti.live || lane >= Cfg::PPT) return -1;
+      const int32_t pg = ti.t * Cfg::PPT + lane;
+      if (pg >= a.max_pages || pg * kPage >= ti.s.L) return -1;
+      return __ldg(a.block_table + static_cast<int64_t>(ti.s.b) * a.max_pages + pg);
+    };
+    TreeIter<D> t;
+    t.first(sTab, a, G, range);
+    int32_t bt = page_entry(t);
+    uint32_t n = 0;  // tiles issued
+    while (ok && t.live) {
+      int32_t phys = bt, nvalid = 0;
+      if (phys >= a.num_pages) {  // never dereferenced; reported in the status word
+        set_status(a.status, kStatusBadPage);
+        phys = -1;
+      }
+      if (phys >= 0) nvalid = min(kPage, t.s.L - (t.t * Cfg::PPT + lane) * kPage);
+      TreeIter<D> nx = t;
+      nx.next(sTab, a, G);
+      bt = page_entry(nx);
+      const int sl = base + static_cast<int>(n % stages);
+      const uint32_t use = n / stages;
+      if (use > 0 && !warp_wait(&bar_empty[sl], (use - 1) & 1)) { ok = false; break; }
+      constexpr uint32_t kPageBytes = Cfg::NSL * kBox + (KindTraits<KIND>::kScaled ? Cfg::SC_KV : 0);
+      const uint32_t bytes = __reduce_add_sync(0xffffffffu, phys >= 0 ? kPageBytes : 0u);
+      int32_t nv[Cfg::PPT];
+#pragma unroll
+      for (int i = 0; i < Cfg::PPT; ++i) nv[i] = __shfl_sync(0xffffffffu, nvalid, i);
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < Cfg::PPT; ++i) sMeta[sl * Cfg::PPT + i] = nv[i];
+        mbar_arrive_expect_tx(&bar_full[sl], bytes);  // releases the page counts with the slot
+      }
+      __syncwarp();
+      if (phys >= 0) {
+        uint8_t* slot = sRing + sl * Cfg::SLOT_BYTES;
+#pragma unroll
+        for (int c = 0; c < Cfg::NSL; ++c)
+          tma_load_codes(smem_u32(slot + (lane * Cfg::NSL + c) * kBox), &tmap, c, t.s.g * kPage, kv, phys,
+                         &bar_full[sl]);
+        if (KindTraits<KIND>::kScaled) {  // an unscaled pool has codes only
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(a.scales) +
+                               ((static_cast<int64_t>(phys) * 2 + kv) * a.num_kv_heads + t.s.g) * Cfg::SC_KV;
+          bulk_g2s(slot + Cfg::CODE_BYTES + lane * Cfg::SC_KV, src, Cfg::SC_KV, &bar_full[sl]);
+        }
+      }
+      t = nx;
+      ++n;
+    }
+    // no copy may still be in flight when the CTA exits
+    for (uint32_t j = 1; j <= n && j <= static_cast<uint32_t>(stages); ++j) {
+      const uint32_t m = n - j;
+      (void)mbar_wait_bounded(&bar_full[base + m % stages], (m / stages) & 1);
+    }
+  } else if (warp >= kSmWarps && warp < kMmaWarp) {
+    // ===================================================================== dequant warps
+    const int dw = tid - kSmWarps * 32;
+    const int tt = dw % T;     // key of the tile (consecutive threads: consecutive keys)
+    const int part = dw / T;   // which SPAN of the row
+    const int pi = tt / kPage, off = tt % kPage;
+    const int swz = off & 7;   // 128-byte swizzle phase of this token's staging rows
+    const uint32_t toff = (tt % 8) * 16 + (tt / 8) * Cfg::RS;
+    // dequantize this thread's codes of K or V from a ring slot into a bf16 tile
+    auto write_tile = [&](uint8_t* dst, const uint8_t* slot, bool v_ok) {
+      const uint8_t* rows = slot + pi * Cfg::NSL * kBox + off * 128;
+      const uint32_t sc = KindTraits<KIND>::kScaled ? *reinterpret_cast<const uint32_t*>(
+          slot + Cfg::CODE_BYTES + pi * Cfg::SC_KV + (off * Cfg::NB + part * Cfg::NBT) * 2) : 0u;
+#pragma unroll
+      for (int k = 0; k < Cfg::NCH; ++k) {
+        uint32_t w[8];
+        if (v_ok) {
+          const int c = part * Cfg::NCH + k;  // 16-code chunk along the row
+          const uint4 codes = *reinterpret_cast<const uint4*>(rows + (c / 8) * kBox + (((c % 8) ^ swz) * 16));
+          dequant16<KIND>(codes, static_cast<uint16_t>(sc >> (16 * (k >> 1))), w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = 0u;
+        }
+        const int d8 = part * (Cfg::SPAN / 8) + 2 * k;
+        *reinterpret_cast<uint4*>(dst + toff + d8 * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + toff + (d8 + 1) * 128) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
+    uint32_t nk = 0, nv = 0;                     // tiles whose K / V have been written
+    while (ok && nv < total) {
+      if (nk < total) {
+        const int ring = nk % Cfg::KSTAGES;
+        if (!warp_wait(&bar_full[ring], (nk / Cfg::KSTAGES) & 1)) { ok = false; break; }
+        const uint8_t* slot = sRing + ring * Cfg::SLOT_BYTES;
+        const bool v_ok = off < sMeta[ring * Cfg::PPT + pi];
+        // the K tile was last read by the QK of tile nk - 1
+        if (nk >= 1 && !warp_wait(&bar_qk_done[(nk - 1) & 1], ((nk - 1) >> 1) & 1)) { ok = false; break; }
+        write_tile(sK, slot, v_ok);
+        if (lane == 0) {
+          bar_arrive(bar_k_full);
+          bar_arrive(&bar_empty[ring]);
+        }
+        ++nk;
+        if (nk == 1 && nk < total) continue;  // K runs one tile ahead of V
+      }
+      {
+        const int ring = Cfg::KSTAGES + nv % Cfg::VSTAGES;
+        if (!warp_wait(&bar_full[ring], (nv / Cfg::VSTAGES) & 1)) { ok = false; break; }
+        const uint8_t* slot = sRing + ring * Cfg::SLOT_BYTES;
+        const bool v_ok = off < sMeta[ring * Cfg::PPT + pi];
+        // the V tile was last read by the PV of tile nv - 1
+        if (nv >= 1 && !warp_wait(&bar_pv_done[(nv - 1) & 1], ((nv - 1) >> 1) & 1)) { ok = false; break; }
+        write_tile(sV, slot, v_ok);
+        if (lane == 0) {
+          bar_arrive(bar_v_full);
+          bar_arrive(&bar_empty[ring]);
+        }
+        ++nv;
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ===================================================================== MMA issue (elected lane)
+    const uint32_t idesc_qk = x_idesc(T, false);
+    const uint32_t idesc_pv = x_idesc(D, true);
+    // descriptors of the first K-step; later steps add their byte offset >> 4 to the address field
+    const uint64_t dQ = smem_desc(smem_u32(sQ), 128, Cfg::RS);
+    const uint64_t dK = smem_desc(smem_u32(sK), 128, Cfg::RS);
+    const uint64_t dV = smem_desc(smem_u32(sV), Cfg::RS, 128);
+    const uint32_t tS = tmem + Cfg::S_COL, tO = tmem, tP = tmem + Cfg::P_COL;
+    uint32_t n = 0, items = 0;  // tiles QK'd; items finished
+    // PV of tile m; the first tile of an item overwrites O, once the previous item's O has been read out
+    auto pv = [&](uint32_t m, bool first) -> bool {
+      const int bp = m & 1;
+      if (!warp_wait(bar_v_full, m & 1)) return false;
+      if (!warp_wait(&bar_p_full[bp], (m >> 1) & 1)) return false;
+      if (first && items >= 1 && !warp_wait(bar_o_free, (items - 1) & 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < T / 16; ++ks)
+        mma_bf16_tmem_a(tO, tP + bp * (T / 2) + ks * 8, dV + static_cast<uint64_t>((ks * 2 * Cfg::RS) >> 4),
+                        idesc_pv, (!first || ks > 0) ? 1u : 0u);
+      mma_commit(&bar_pv_done[bp]);
+      __syncwarp();
+      return true;
+    };
+    TreeIter<D> t;
+    for (t.first(sTab, a, G, range); ok && t.live; t.next_segment(sTab, a, G)) {
+      const int32_t ntiles = t.s.t1 - t.s.t0;
+      if (!warp_wait(bar_q_full, items & 1)) { ok = false; break; }
+      for (int32_t i = 0; i < ntiles; ++i, ++n) {
+        const int b = n & 1;
+        if (!warp_wait(bar_k_full, n & 1)) { ok = false; break; }
+        // S buffer b was read by the softmax of tile n - 2
+        if (n >= 2 && !warp_wait(&bar_p_full[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_bf16(tS + b * T, dQ + static_cast<uint64_t>((ks * 256) >> 4), dK + static_cast<uint64_t>((ks * 256) >> 4),
+                   idesc_qk, ks > 0 ? 1u : 0u);
+        mma_commit(&bar_qk_done[b]);
+        __syncwarp();
+        if (i > 0 && !pv(n - 1, i == 1)) { ok = false; break; }
+      }
+      if (!ok) break;
+      if (!pv(n - 1, ntiles == 1)) { ok = false; break; }
+      ++items;
+    }
+    // before tensor memory is freed, every MMA issued must have completed (the last commit implies all)
+    if (n > 0) (void)mbar_wait_bounded(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+    if (n > 0) (void)mbar_wait_bounded(&bar_qk_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+  } else {
+    // ===================================================================== softmax warps
+    const int quarter = warp & 3, hf = warp >> 2;  // lane quarter; which half of the keys and of O
+    const int r = quarter * 32 + lane;             // query row = tensor-memory lane
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + Cfg::S_COL + lane_base + hf * (T / 2);
+    const uint32_t tO = tmem + lane_base + hf * (D / 2);
+    const uint32_t tP = tmem + Cfg::P_COL + lane_base + hf * (T / 4);
+    float* sRed = reinterpret_cast<float*>(smem + Cfg::RED_OFF);
+    float* sSum = reinterpret_cast<float*>(smem + Cfg::SUM_OFF);
+    // this warp's half of the segment's Q rows into the shared tile (rows past the block's are zero)
+    auto write_q = [&](const Seg& s) {
+      if (quarter * 32 < s.rows) {
+        const bool valid = r < s.rows;
+        const int32_t row = s.blk * kM + (valid ? r : 0);
+        const int32_t tok = row / G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + s.g * G + (row - tok * G)) * D);
+        uint8_t* dst = sQ + (r % 8) * 16 + (r / 8) * Cfg::RS;
+#pragma unroll 4
+        for (int j = hf * (D / 16); j < (hf + 1) * (D / 16); ++j)
+          *reinterpret_cast<uint4*>(dst + j * 128) = valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar_q_full);
+    };
+    // the two warps of a lane quarter meet on mbarriers (bounded waits: a warp that gave up cannot strand
+    // the other)
+    auto pair_meet = [&](uint64_t* bar, uint32_t parity) -> bool {
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar);
+      return warp_wait(bar, parity);
+    };
+    // tiles processed; segments; row sums exchanged and phases of the maxima's barriers (both only of segments in
+    // which this lane quarter holds rows)
+    uint32_t n = 0, items = 0, sums = 0, pair_phase = 0;
+    TreeIter<D> cur;
+    cur.first(sTab, a, G, range);
+    if (cur.live) write_q(cur.s);
+    while (ok && cur.live) {
+      const Seg s = cur.s;
+      const bool active = quarter * 32 < s.rows;  // (warp-uniform) this lane quarter holds rows
+      const bool row_ok = r < s.rows;
+      const int32_t row = s.blk * kM + (row_ok ? r : 0);
+      const int32_t tok = row / G;
+      const int64_t* mask = a.mask + static_cast<int64_t>(s.q0 + tok) * a.mask_words;
+      float m_used = -INFINITY, l = 0.0f;
+      // lane pi (< PPT) holds the block-table entry of page pi of a tile, read one tile ahead of its use
+      auto fetch = [&](int32_t t) -> int32_t {
+        const int32_t pg = t * Cfg::PPT + lane;
+        if (lane >= Cfg::PPT || t >= s.t1 || pg >= a.max_pages || pg * kPage >= s.L) return -1;
+        return __ldg(a.block_table + static_cast<int64_t>(s.b) * a.max_pages + pg);
+      };
+      int32_t ent = active ? fetch(s.t0) : -1;
+      for (int32_t t = s.t0; t < s.t1; ++t, ++n) {
+        const int b = n & 1;
+        if (!active) {  // only keep the count of the tile's barrier
+          if (!warp_wait(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
+          if (lane == 0) bar_arrive(&bar_p_full[b]);
+          continue;
+        }
+        // mapped pages of the tile (chunk c of 16 keys is page c of the tile)
+        const uint32_t pmask = __ballot_sync(0xffffffffu, ent >= 0 && ent < a.num_pages) & ((1u << Cfg::PPT) - 1u);
+        ent = fetch(t + 1);
+        // keys of this warp's half that this row sees
+        const int32_t k0 = t * T + hf * (T / 2);
+        uint64_t vis = spread_pages(pmask >> (hf * Cfg::PPT / 2));
+        if (k0 + T / 2 > s.L - s.n) {  // (warp-uniform) drafted tokens, or keys behind the end
+          vis &= tree_window(mask, a.mask_words, k0 - (s.L - s.n));
+          const int32_t left = s.L - k0;
+          vis &= left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1ull : 0ull;
+        }
+        constexpr uint64_t kAll = T / 2 == 64 ? ~0ull : (1ull << (T / 2)) - 1ull;
+        vis = row_ok ? vis & kAll : kAll;  // (rows past the block's are zeros that nobody reads)
+        if (!warp_wait(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        // every row of the warp sees every key of its half: no masking.  The two variants of each pass are
+        // separate straight-line loops behind one warp-uniform branch.
+        const bool full = __all_sync(0xffffffffu, vis == kAll);
+        // pass 1: the row's max over the visible keys of this half (sm_scale > 0: scaling commutes with it)
+        float mh = -INFINITY;
+        auto pass1 = [&](auto masked) {
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = 0; h < T / 64; ++h) {
+            uint32_t v[32];
+            tmem_ld32(tS + b * T + h * 32, v);
+            const uint32_t vw = static_cast<uint32_t>(vis >> (32 * h));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x = __uint_as_float(v[e]);
+              if constexpr (decltype(masked)::value) x = ((vw >> e) & 1u) ? x : -INFINITY;
+              m[e & 3] = fmaxf(m[e & 3], x);
+            }
+          }
+          mh = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        };
+        if (full) pass1(std::false_type{});
+        else pass1(std::true_type{});
+        // the row's max over the whole tile: exchange halves with the other warp of the lane quarter
+        // (double-buffered by tile parity, so one barrier per tile suffices)
+        sRed[(b * 2 + hf) * kM + r] = mh;
+        if (!pair_meet(&bar_pair[quarter * 2 + b], (pair_phase >> b) & 1u)) { ok = false; break; }
+        pair_phase ^= 1u << b;
+        float mx = fmaxf(sRed[(b * 2) * kM + r], sRed[(b * 2 + 1) * kM + r]);
+        if (mx > -INFINITY) mx *= a.score_scale;
+        float alpha = 1.0f;
+        bool resc = false;
+        if (mx > -INFINITY && (m_used == -INFINITY || mx > m_used + kLazyRescale)) {
+          if (m_used != -INFINITY) {
+            alpha = ex2(m_used - mx);
+            resc = true;
+          }
+          m_used = mx;
+        }
+        // P buffer b is free once the PV two tiles back has read it
+        if (n >= 2 && !warp_wait(&bar_pv_done[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
+        if (__any_sync(0xffffffffu, resc)) {  // (only from the second tile of an item on)
+          // O must hold the PV of the previous tile before it is scaled; this warp scales its half of O
+          if (!warp_wait(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          l *= alpha;
+        }
+        // pass 2: P = 2^(s * scale - m) of this half as bf16 into tensor memory; the row sum in fp32
+        auto pass2 = [&](auto masked) {
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+          for (int h = 0; h < T / 64; ++h) {
+            uint32_t v[32];
+            tmem_ld32(tS + b * T + h * 32, v);
+            uint32_t w[16];
+            const uint32_t vw = static_cast<uint32_t>(vis >> (32 * h));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x0 = fmaf(__uint_as_float(v[2 * e]), a.score_scale, -m_used);
+              const float x1 = fmaf(__uint_as_float(v[2 * e + 1]), a.score_scale, -m_used);
+              // every fourth pair on the FMA pipe, the rest on the MUFU unit
+              const bool fma_pipe = (e & 3) == 3;
+              float p0 = fma_pipe ? ex2_fma(x0) : ex2(x0);
+              float p1 = fma_pipe ? ex2_fma(x1) : ex2(x1);
+              if constexpr (decltype(masked)::value) {
+                p0 = ((vw >> (2 * e)) & 1u) ? p0 : 0.0f;
+                p1 = ((vw >> (2 * e + 1)) & 1u) ? p1 : 0.0f;
+              }
+              ls[(2 * e) & 3] += p0;
+              ls[(2 * e + 1) & 3] += p1;
+              w[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16u(tP + b * (T / 2) + h * 16, w);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        };
+        if (full) pass2(std::false_type{});
+        else pass2(std::true_type{});
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar_p_full[b]);
+      }
+      if (!ok) break;
+      // the next segment's Q rows (every QK of this segment has completed: its last S was read above)
+      cur.next_segment(sTab, a, G);
+      if (cur.live) write_q(cur.s);
+      if (active) {
+        // the row sum over both halves (double-buffered by the parity of the quarter's meetings)
+        float* sum = sSum + (sums & 1) * 2 * kM;
+        sum[hf * kM + r] = l;
+        if (!pair_meet(&bar_sum[quarter], sums & 1)) { ok = false; break; }
+        ++sums;
+        const float lt = sum[r] + sum[kM + r];
+        // this warp's half of O, once the segment's last PV has completed: normalised into the output when the
+        // segment is the whole block, else as a partial
+        if (!warp_wait(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const bool whole = s.slot < 0;
+        const float scale = whole ? (lt > 0.0f ? 1.0f / lt : 0.0f) : 1.0f;
+        const int64_t orow =
+            (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + s.g * G + (row - tok * G)) * D + hf * (D / 2);
+        const int64_t prow = static_cast<int64_t>(max(s.slot, 0)) * kM + r;
+        if (!whole && row_ok && hf == 0)
+          *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m_used, lt);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          if (row_ok) {
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * scale;
+            if (!whole || a.out_dtype == KVQ_OUT_F32) {
+              float* base = whole ? static_cast<float*>(a.out) + orow : a.part_acc + prow * D + hf * (D / 2);
+              float4* dst = reinterpret_cast<float4*>(base + c * 32);
+#pragma unroll
+              for (int q4 = 0; q4 < 8; ++q4)
+                dst[q4] = make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow + c * 32);
+#pragma unroll
+              for (int h8 = 0; h8 < 4; ++h8)
+                dst[h8] = make_uint4(pack_bf16x2(o[8 * h8], o[8 * h8 + 1]), pack_bf16x2(o[8 * h8 + 2], o[8 * h8 + 3]),
+                                     pack_bf16x2(o[8 * h8 + 4], o[8 * h8 + 5]),
+                                     pack_bf16x2(o[8 * h8 + 6], o[8 * h8 + 7]));
+            }
+          }
+        }
+      } else if (!warp_wait(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) {
+        // (that PV was issued after o_free of the segment before had completed: no arrival below can be
+        // counted for that one)
+        ok = false;
+        break;
+      }
+      ++items;
+      tc_fence_before();  // the reads are ordered before the arrival that lets the next PV overwrite O
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar_o_free);
+    }
+  }
+  if (!ok) set_status(a.status, kStatusTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// One CTA per output row: joins the partials of the segments that its block was cut into,
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s with M = max_s m_s.  Rows of blocks that one segment covered
+// whole are final already.  A row without a visible key has l = 0 everywhere and gives zeros.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = kMergeThreads / 32;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
+  constexpr int DPL = D / 32;  // dims per lane
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float s_a[kMergeWarps][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int32_t G = a.num_q_heads / a.num_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t tokrow = blockIdx.x / a.num_q_heads, head = blockIdx.x - tokrow * a.num_q_heads;
+  int lo = 0, hi = a.batch;  // first b with q_start[b] > tokrow
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.q_start + mid) <= tokrow) lo = mid + 1;
+    else hi = mid;
+  }
+  const int32_t b = lo - 1;
+  if (b < 0) return;
+  const int32_t q0 = __ldg(a.q_start + b), n = drafted(a, b, false);
+  if (tokrow < q0 || tokrow >= q0 + n) return;  // behind the last sequence, or a skipped one
+  const int32_t U = a.tab[a.batch], C = a.tab[a.batch + 1];
+  const int32_t nt = (__ldg(a.seq_lens + b) + TCfg<D>::T - 1) / TCfg<D>::T;
+  const int32_t g = head / G, row = (tokrow - q0) * G + (head - g * G);
+  const int32_t blk = row / kM, r = row - blk * kM;
+  const int32_t u0 = a.tab[b] + (blk * a.num_kv_heads + g) * nt, u1 = u0 + nt;
+  // CTAs whose ranges hold units of the block: start(c) <= u < start(c + 1), start(c) = floor(U c / C)
+  const int32_t c0 = static_cast<int32_t>((static_cast<int64_t>(u0) * C + C - 1) / U);
+  const int32_t c1 = static_cast<int32_t>((static_cast<int64_t>(u1 - 1) * C + C - 1) / U);
+  auto owner = [&](int32_t c, int32_t u) -> int32_t {  // c, corrected to the CTA whose range holds unit u
+    while (c > 0 && range_start(U, C, c) > u) --c;
+    while (c + 1 < C && range_start(U, C, c + 1) <= u) ++c;
+    return c;
+  };
+  const int32_t first = owner(min(c0, C - 1), u0), last = owner(min(c1, C - 1), u1 - 1);
+  if (first == last) return;
+  auto prow = [&](int32_t c) -> int64_t {  // this row's partial in CTA c: its first segment, or its last
+    return static_cast<int64_t>(2 * c + (range_start(U, C, c) >= u0 ? 0 : 1)) * kM + r;
+  };
+  float M = -INFINITY;
+  for (int32_t c = first + tid; c <= last; c += kMergeThreads) M = fmaxf(M, a.part_ml[prow(c) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w]);
+  float acc[DPL], l = 0.0f;
+#pragma unroll
+  for (int j = 0; j < DPL; ++j) acc[j] = 0.0f;
+#pragma unroll 2
+  for (int32_t c = first + warp; c <= last; c += kMergeWarps) {
+    const int64_t p = prow(c);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + p * 2);
+    const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+    l = fmaf(ml.y, w, l);
+#pragma unroll
+    for (int j = 0; j < DPL / 4; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part_acc + p * D + j * 128 + lane * 4);
+      acc[4 * j] = fmaf(v.x, w, acc[4 * j]);
+      acc[4 * j + 1] = fmaf(v.y, w, acc[4 * j + 1]);
+      acc[4 * j + 2] = fmaf(v.z, w, acc[4 * j + 2]);
+      acc[4 * j + 3] = fmaf(v.w, w, acc[4 * j + 3]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < DPL / 4; ++j)
+    *reinterpret_cast<float4*>(&s_a[warp][j * 128 + lane * 4]) =
+        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  float lt = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) lt += s_l[w];
+  for (int d = tid; d < D; d += kMergeThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) v += s_a[w][d];
+    const float o = lt > 0.0f ? v / lt : 0.0f;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * D + d;
+    if (a.out_dtype == KVQ_OUT_F32) static_cast<float*>(a.out)[at] = o;
+    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
+  }
+}
+
+template <int D>
+kvq_status launch_tree_d(const TreeArgs& a, cudaStream_t stream) {
+  using Cfg = TCfg<D>;
+  decltype(&tree_tc_kernel<D, KVQ_FP8_E4M3>) kern = nullptr;
+  switch (a.kind) {
+    case KVQ_FP8_E4M3: kern = tree_tc_kernel<D, KVQ_FP8_E4M3>; break;
+    case KVQ_Q8_0: kern = tree_tc_kernel<D, KVQ_Q8_0>; break;
+    case KVQ_FP8_E4M3_UNSCALED: kern = tree_tc_kernel<D, KVQ_FP8_E4M3_UNSCALED>; break;
+    case KVQ_FP8_E5M2_UNSCALED: kern = tree_tc_kernel<D, KVQ_FP8_E5M2_UNSCALED>; break;
+  }
+  if (kern == nullptr) return KVQ_EKIND;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess)
+    return KVQ_ECUDA;
+  CUtensorMap map;
+  if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
+  kern<<<static_cast<unsigned>(a.grid), kThreads, Cfg::SMEM_BYTES, stream>>>(a, map);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.total_q) * a.num_q_heads));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? KVQ_OK : KVQ_ECUDA;
+}
+
+// One CTA per sequence: each of its query rows is a sequence of its own to the decode kernels, with the
+// sequence's tokens and pages and the row's mask.
+__global__ void tree_expand_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict__ seq_lens,
+                                   int32_t total_q, int32_t mask_words, int64_t max_tokens, int32_t* __restrict__ vlens,
+                                   int32_t* __restrict__ vrow, int32_t* __restrict__ vbase, uint32_t* status) {
+  const int32_t b = blockIdx.x;
+  const int32_t q0 = __ldg(q_start + b), q1 = __ldg(q_start + b + 1), L = __ldg(seq_lens + b);
+  const int32_t n = q1 - q0;
+  if (q0 < 0 || n < 0 || n > L || q1 > total_q || n > 64 * mask_words || L > max_tokens) {
+    if (threadIdx.x == 0) set_status(status, kStatusBadExtend);
+    return;
+  }
+  for (int32_t i = threadIdx.x; i < n; i += blockDim.x) {
+    vlens[q0 + i] = L;
+    vrow[q0 + i] = b;
+    vbase[q0 + i] = L - n;
+  }
+}
+
+}  // namespace
+
+bool tree_tc_supported(int32_t head_dim, int32_t v_dim, int32_t mla, int32_t batch) {
+  return !mla && v_dim == head_dim && (head_dim == 128 || head_dim == 256) && batch <= kMaxTreeBatch;
+}
+
+kvq_status launch_tree_expand(const int32_t* q_start, const int32_t* seq_lens, int32_t batch, int32_t total_q,
+                              int32_t mask_words, int64_t max_tokens, int32_t* vlens, int32_t* vrow, int32_t* vbase,
+                              uint32_t* status, cudaStream_t stream) {
+  tree_expand_kernel<<<static_cast<unsigned>(batch), 64, 0, stream>>>(q_start, seq_lens, total_q, mask_words, max_tokens,
+                                                                       vlens, vrow, vbase, status);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+}
+
+kvq_status launch_tree_tc(const TreeArgs& a, cudaStream_t stream) {
+  if (a.head_dim == 128) return launch_tree_d<128>(a, stream);
+  if (a.head_dim == 256) return launch_tree_d<256>(a, stream);
+  return KVQ_EUNSUPPORTED;
+}
+
+}  // namespace kvq

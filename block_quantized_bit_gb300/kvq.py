@@ -39,7 +39,7 @@ EXPORTS = ["kvq_pool_bytes", "kvq_scale_bytes", "kvq_bytes_per_token", "kvq_num_
            "kvq_extend_workspace_bytes", "kvq_extend", "kvq_store_act_quant", "kvq_store_unscaled",
            "kvq_bytes_per_token_ex", "kvq_num_pages_ex", "kvq_exp2_probe", "kvq_extend_workspace_bytes_ex",
            "kvq_extend_ex", "kvq_extend_path", "kvq_pages_workspace_bytes", "kvq_pages_copy", "kvq_pages_fork",
-           "kvq_pages_resize", "kvq_pages_compact"]
+           "kvq_pages_resize", "kvq_pages_compact", "kvq_tree_workspace_bytes", "kvq_tree"]
 
 
 class kvq_layout(ctypes.Structure):
@@ -110,6 +110,9 @@ def lib():
             "kvq_extend_path": (i32, [LP, i32, i32, i32, EP]),
             "kvq_extend_ex": (i32, [P, P, P, P, i32, P, P, i32, i32, i32, ctypes.c_float, P, i32, P, sz, LP, i32,
                                     EP, P]),
+            "kvq_tree_workspace_bytes": (sz, [LP, i32, i32, i32, i32, i32]),
+            "kvq_tree": (i32, [P, P, P, P, i32, P, P, P, i32, i32, i32, i32, ctypes.c_float, P, i32, P, sz, LP, i32, i32,
+                               P]),
             "kvq_pages_workspace_bytes": (sz, [LP, i32, i32]),
             "kvq_pages_copy": (i32, [P, P, P, P, i32, LP, i32, P]),
             "kvq_pages_fork": (i32, [P, i32, P, i32, P, P, P, i32, P, P, P, sz, LP, P]),
@@ -368,7 +371,7 @@ def kvq_extend(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
         _check(lib().kvq_extend_ex(*args, opts, _stream(stream)), "kvq_extend_ex")
 
 
-# ---------------------------------------------------------------------------- pages
+# ---------------------------------------------------------------------------- checked marshalling
 # The calls below belong to loops of short GPU work, so what they marshal is checked and passed as plain
 # integers, and a layout's C struct is built once.
 _I32, _I64, _U8, _I16, _BF16 = torch.int32, torch.int64, torch.uint8, torch.int16, torch.bfloat16
@@ -386,23 +389,27 @@ def _layout_ref(L: Layout):
 
 
 def _check_args(*args):
-    """(name, tensor, type) triples: tensors of that type, dense, all on the current CUDA device."""
+    """(name, tensor, type) triples: tensors of that type, dense, all on the current CUDA device, whose index is
+    returned."""
+    device = args[0][1].get_device()
+    for _, t, dtype in args:
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+            break
+    else:
+        if device >= 0 and device == torch.cuda.current_device():
+            return device
     for name, t, dtype in args:
         if t.dtype is not dtype:
             raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-    if not all([t.is_cuda for _, t, _ in args]):
-        raise ValueError("every tensor must be on the current CUDA device")
-    device = torch.cuda.current_device()
-    for name, t, _ in args:
-        if t.get_device() != device:
-            raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
+    raise ValueError("every tensor must be on the current CUDA device, got " +
+                     ", ".join("%s on %s" % (name, t.device) for name, t, _ in args))
 
 
-def _raw_stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+def _raw_stream(stream, device):
+    if stream is None:  # (torch.cuda.current_stream() builds an object, 3 us)
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -418,6 +425,52 @@ def _pool_args(pool, scales, layout: Layout, kind):
     return k, (("pool", pool, _U8), ("scales", scales, scales.dtype if scales.dtype.itemsize == 2 else _I16)), scales
 
 
+def _out_dtype(out):
+    if out.dtype is torch.bfloat16:
+        return KVQ_OUT_BF16
+    if out.dtype is torch.float32:
+        return KVQ_OUT_F32
+    raise TypeError("out must be bfloat16 or float32")
+
+
+# ---------------------------------------------------------------------------- drafted tokens
+def alloc_tree_workspace(layout: Layout, batch: int, total_q: int, num_q_heads: int, max_pages_per_seq: int,
+                         path: int = 0, device="cuda"):
+    n = lib().kvq_tree_workspace_bytes(ctypes.byref(layout.c()), int(batch), int(total_q), int(num_q_heads),
+                                       int(max_pages_per_seq), int(path))
+    if n == 0:
+        raise KvqError(-1, "kvq_tree_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kvq_tree(q: torch.Tensor, pool: torch.Tensor, scales: Optional[torch.Tensor], block_table: torch.Tensor,
+             seq_lens: torch.Tensor, q_start: torch.Tensor, tree_mask: torch.Tensor, out: torch.Tensor,
+             workspace: torch.Tensor, layout: Layout, kind, sm_scale: float = 1.0, path: int = 0, stream=None):
+    """Attention of drafted tokens: the q rows q_start[b] .. q_start[b+1]-1 ([total_q, Hq, D] bf16) are the last
+    stored tokens of sequence b; each sees the tokens before them and the drafted ones in its row of tree_mask
+    ([total_q, words] int64).  Writes out ([total_q, Hq, v_dim], bf16 or float32).  path: 0 automatic, 1 CUDA cores
+    with P in fp32, 2 tensor cores."""
+    B = seq_lens.numel()
+    if q.dim() != 3 or q.shape[2] != layout.head_dim or out.shape != (q.shape[0], q.shape[1], layout.v_dim):
+        raise ValueError("q must be [total_q, heads, head_dim] and out [total_q, heads, v_dim]")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] or q_start.numel() != B + 1:
+        raise ValueError("tree_mask must be [total_q, words] and q_start [batch + 1]")
+    _check_tables(block_table, seq_lens, None, layout)
+    od = _out_dtype(out)
+    k, checked, scales = _pool_args(pool, scales, layout, kind)
+    device = _check_args(*checked, ("q", q, _BF16), ("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32),
+                         ("q_start", q_start, _I32), ("tree_mask", tree_mask, _I64), ("out", out, out.dtype),
+                         ("workspace", workspace, _U8))
+    st = lib().kvq_tree(q.data_ptr(), pool.data_ptr(), None if scales is None else scales.data_ptr(),
+                        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(),
+                        tree_mask.data_ptr(), tree_mask.shape[1], q.shape[0], B, q.shape[1], sm_scale, out.data_ptr(), od,
+                        workspace.data_ptr(), workspace.numel(), _layout_ref(layout), k, path,
+                        _raw_stream(stream, device))
+    if st:
+        raise KvqError(st, "kvq_tree")
+
+
+# ---------------------------------------------------------------------------- pages
 def alloc_pages_workspace(layout: Layout, n: int, max_pages_per_seq: int, device="cuda"):
     """Workspace of kvq_pages_fork and kvq_pages_resize for n list entries (kvq_pages_compact takes it too)."""
     b = lib().kvq_pages_workspace_bytes(ctypes.byref(layout.c()), int(n), int(max_pages_per_seq))
@@ -433,9 +486,9 @@ def kvq_pages_copy(pool: torch.Tensor, scales: Optional[torch.Tensor], src: torc
     if dst.numel() != n:
         raise ValueError("src and dst must have one entry per copy")
     k, checked, scales = _pool_args(pool, scales, layout, kind)
-    _check_args(*checked, ("src", src, _I32), ("dst", dst, _I32))
+    device = _check_args(*checked, ("src", src, _I32), ("dst", dst, _I32))
     st = lib().kvq_pages_copy(pool.data_ptr(), None if scales is None else scales.data_ptr(), src.data_ptr(),
-                              dst.data_ptr(), n, _layout_ref(layout), k, _raw_stream(stream))
+                              dst.data_ptr(), n, _layout_ref(layout), k, _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_copy")
 
@@ -456,13 +509,13 @@ def kvq_pages_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, page_refs:
     if dst.numel() != n or copy_src.numel() != n or copy_dst.numel() != n:
         raise ValueError("src, dst, copy_src and copy_dst must have the same length")
     _check_tables(block_table, seq_lens, page_refs, layout)
-    _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
-                ("src", src, _I32), ("dst", dst, _I32), ("copy_src", copy_src, _I32), ("copy_dst", copy_dst, _I32),
-                ("workspace", workspace, _U8))
+    device = _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
+                         ("src", src, _I32), ("dst", dst, _I32), ("copy_src", copy_src, _I32),
+                         ("copy_dst", copy_dst, _I32), ("workspace", workspace, _U8))
     batch, max_pages = block_table.shape
     st = lib().kvq_pages_fork(block_table.data_ptr(), max_pages, seq_lens.data_ptr(), batch, page_refs.data_ptr(),
                               src.data_ptr(), dst.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _layout_ref(layout), _raw_stream(stream))
+                              workspace.data_ptr(), workspace.numel(), _layout_ref(layout), _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_fork")
 
@@ -474,12 +527,12 @@ def kvq_pages_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, page_ref
     if new_lens.numel() != n:
         raise ValueError("seqs and new_lens must have the same length")
     _check_tables(block_table, seq_lens, page_refs, layout)
-    _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
-                ("seqs", seqs, _I32), ("new_lens", new_lens, _I32), ("workspace", workspace, _U8))
+    device = _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
+                         ("seqs", seqs, _I32), ("new_lens", new_lens, _I32), ("workspace", workspace, _U8))
     batch, max_pages = block_table.shape
     st = lib().kvq_pages_resize(block_table.data_ptr(), max_pages, seq_lens.data_ptr(), batch, page_refs.data_ptr(),
                                 seqs.data_ptr(), new_lens.data_ptr(), n, workspace.data_ptr(), workspace.numel(),
-                                _layout_ref(layout), _raw_stream(stream))
+                                _layout_ref(layout), _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_resize")
 
@@ -497,13 +550,14 @@ def kvq_pages_compact(pool: torch.Tensor, scales: Optional[torch.Tensor], block_
     k, checked, scales = _pool_args(pool, scales, layout, kind)
     if page_refs is not None:
         checked += (("page_refs", page_refs, _I32),)
-    _check_args(*checked, ("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("q_start", q_start, _I32),
-                ("keep", keep, _I64), ("new_lens", new_lens, _I32), ("workspace", workspace, _U8))
+    device = _check_args(*checked, ("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32),
+                         ("q_start", q_start, _I32), ("keep", keep, _I64), ("new_lens", new_lens, _I32),
+                         ("workspace", workspace, _U8))
     st = lib().kvq_pages_compact(pool.data_ptr(), None if scales is None else scales.data_ptr(), block_table.data_ptr(),
                                  block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(), keep.data_ptr(),
                                  keep.shape[1], B, new_lens.data_ptr(),
                                  None if page_refs is None else page_refs.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel(), _layout_ref(layout), k, _raw_stream(stream))
+                                 workspace.numel(), _layout_ref(layout), k, _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_compact")
 

@@ -334,6 +334,39 @@ kvq_status kvq_noalloc_status(void* stream);
  */
 kvq_status kvq_workspace_status(const void* workspace, void* stream);
 
+/* ---------------------------------------------------------------- drafted tokens */
+/*
+ * Attention of drafted tokens over the cache, as a speculative step verifies them.  The upstream pages have no
+ * counterpart; it is kvq_extend with the causal rule among the new tokens replaced by a mask.  Store the drafted
+ * tokens' K/V rows first (kvq_store): the last n_b = q_start[b + 1] - q_start[b] tokens of sequence b are drafted.
+ *   tree_mask    [total_q, mask_words] int64, device, 8-byte aligned: bit j % 64 of word j / 64 of row
+ *                q_start[b] + i says whether drafted token i sees drafted token j (itself included, or not: only the
+ *                bits count).  For a tree of drafts, a token's row is its parent's row and its own bit.  Bits from
+ *                n_b on are ignored.  n_b <= 64 * mask_words, mask_words <= 4 (else KVQ_EUNSUPPORTED).
+ *   workspace    at least kvq_tree_workspace_bytes() for the same sizes and path (0 if invalid or unsupported)
+ *   path         0 = automatic; 1 = CUDA cores, P in fp32; 2 = tensor cores
+ * Query row (b, i, h) gets softmax(sm_scale * q.K^T) V over the positions before seq_lens[b] - n_b and the drafted
+ * ones of its mask, as far as their pages are not masked, with K and V dequantized to bf16 and fp32 accumulation;
+ * no such position gives zeros.  sm_scale must be finite and > 0.  Other arguments as kvq_extend.
+ * Kernels.  GQA with head_dim 128 or 256, any number of query heads per kv head: a split-K flash kernel on the
+ * tensor cores (paths 0 and 2; P enters the MMA as bf16, error about 2^-9 of sum p|V|) and its merge, two
+ * launches.  Other shapes, the MLA row, and path 1: each drafted token is decoded as a sequence of its own with
+ * the decode kernels and the mask, reading its context once per drafted token (mostly from L2).
+ * Supported: page_size 16 and every kvq_decode shape (path 2: GQA with head_dim 128 or 256, or the MLA row with the
+ * tensor-core decode's query heads); the flash kernel takes batch <= 2048.  q_start and seq_lens are read on the
+ * device: a sequence with n_b < 0, n_b > seq_lens[b], n_b > 64 * mask_words, q_start[b + 1] > total_q or
+ * seq_lens[b] > max_pages_per_seq * 16 is skipped and makes kvq_workspace_status report KVQ_EINVAL, as does a
+ * block-table entry >= layout->num_pages (that page is skipped).  Output rows of skipped sequences and behind the
+ * last one are left as they are.
+ */
+size_t kvq_tree_workspace_bytes(const kvq_layout* layout, int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                int32_t max_pages_per_seq, int32_t path);
+kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const int32_t* block_table,
+                    int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* q_start, const int64_t* tree_mask,
+                    int32_t mask_words, int32_t total_q, int32_t batch, int32_t num_q_heads, float sm_scale, void* out,
+                    kvq_out_dtype out_dtype, void* workspace, size_t workspace_bytes, const kvq_layout* layout,
+                    kvq_kind kind, int32_t path, void* stream);
+
 /* ---------------------------------------------------------------- pages of the cache */
 /*
  * Copies, forks, growth, release and compaction of cache pages.  The upstream pages have no counterpart: they
