@@ -832,6 +832,70 @@ kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const i
   return launch_tree_tc(a, s);
 }
 
+size_t kvq_prompt_workspace_bytes(void) { return kWorkspaceHeader; }
+
+kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t* q_start, int32_t total, int32_t batch,
+                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float sm_scale, void* out,
+                      kvq_out_dtype out_dtype, const kvq_prompt_strides* strides, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_F32) return KVQ_EINVAL;
+  if (total < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+    return KVQ_EINVAL;
+  if (head_dim <= 0 || head_dim % 32 != 0) return KVQ_EHEADDIM;
+  if (!(sm_scale > 0.0f) || sm_scale > std::numeric_limits<float>::max()) return KVQ_EINVAL;  // finite, > 0
+  if (!prompt_supported(head_dim, batch)) return KVQ_EUNSUPPORTED;
+  // rows of tiles, and the items of the longest sequence, are counted in 32 bits
+  if (static_cast<int64_t>(total) + 128 > std::numeric_limits<int32_t>::max() ||
+      (static_cast<int64_t>(total) / 128 + 1) * num_q_heads > std::numeric_limits<int32_t>::max() / 2)
+    return KVQ_EUNSUPPORTED;
+  PromptArgs a;
+  const int64_t d = head_dim;
+  a.q_head = a.k_head = a.v_head = a.out_head = d;
+  a.q_token = a.out_token = num_q_heads * d;
+  a.k_token = a.v_token = num_kv_heads * d;
+  if (strides != nullptr) {
+    // 16-byte rows; a stride says nothing along a dimension of one
+    auto take = [&](int64_t token, int64_t head, int32_t heads, int64_t* t, int64_t* h) {
+      if (heads > 1) *h = head;
+      if (total > 1) *t = token;
+      return *t > 0 && *h > 0 && *t % 8 == 0 && *h % 8 == 0 && *t < (1LL << 39) && *h < (1LL << 39);
+    };
+    if (!take(strides->q_token, strides->q_head, num_q_heads, &a.q_token, &a.q_head) ||
+        !take(strides->k_token, strides->k_head, num_kv_heads, &a.k_token, &a.k_head) ||
+        !take(strides->v_token, strides->v_head, num_kv_heads, &a.v_token, &a.v_head) ||
+        !take(strides->out_token, strides->out_head, num_q_heads, &a.out_token, &a.out_head))
+      return KVQ_EINVAL;
+  }
+  if (!workspace) return KVQ_EINVAL;
+  if (workspace_bytes < kWorkspaceHeader) return KVQ_EWORKSPACE;
+  const bool empty = batch == 0 || total == 0;
+  if (!empty && (!q || !k || !v || !q_start || !out)) return KVQ_EINVAL;
+  if (!aligned(workspace) || !aligned(q) || !aligned(k) || !aligned(v) || !aligned(out) ||
+      (reinterpret_cast<uintptr_t>(q_start) % 4) != 0)
+    return KVQ_EALIGN;
+  const kvq_status st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(workspace, 0, 2 * sizeof(uint32_t), s) != cudaSuccess) return KVQ_ECUDA;
+  if (empty) return KVQ_OK;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_start = q_start;
+  a.out = out;
+  a.status = static_cast<uint32_t*>(workspace);
+  a.counter = a.status + 1;
+  a.total = total;
+  a.batch = batch;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.sms = sm_count();
+  a.score_scale = sm_scale * 1.4426950408889634f;  // log2(e)
+  a.out_dtype = out_dtype;
+  return launch_prompt(a, s);
+}
+
 size_t kvq_pages_workspace_bytes(const kvq_layout* layout, int32_t n, int32_t max_pages_per_seq) {
   PagesPlan pp;
   if (check_layout(layout) != KVQ_OK || !plan_pages(*layout, n, max_pages_per_seq, &pp)) return 0;

@@ -171,6 +171,29 @@ kvq_status launch_tree_expand(const int32_t* q_start, const int32_t* seq_lens, i
                               int32_t mask_words, int64_t max_tokens, int32_t* vlens, int32_t* vrow, int32_t* vbase,
                               uint32_t* status, cudaStream_t stream);
 
+// Causal attention over packed prompts (kvq_prompt).  Strides in elements.
+struct PromptArgs {
+  const void* q;              // [total][num_q_heads][head_dim] bf16
+  const void* k;              // [total][num_kv_heads][head_dim] bf16
+  const void* v;
+  const int32_t* q_start;     // [batch + 1]
+  void* out;                  // [total][num_q_heads][head_dim]
+  uint32_t* status;
+  uint32_t* counter;          // items handed out, zeroed per call
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+  int32_t total;
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t sms;
+  float score_scale;          // sm_scale * log2(e)
+  kvq_out_dtype out_dtype;
+};
+constexpr int32_t kMaxPromptBatch = 2048;  // sequences whose tile counts fit the kernel's shared table
+bool prompt_supported(int32_t head_dim, int32_t batch);
+kvq_status launch_prompt(const PromptArgs& a, cudaStream_t stream);
+
 // Pages of the cache (kvq_pages_*).
 constexpr int32_t kPagesChunk = 8192;       // pages whose counts one CTA of the plan reads
 constexpr int32_t kMaxPagesChunks = 8192;   // chunks whose prefixes fit the apply kernel's shared memory

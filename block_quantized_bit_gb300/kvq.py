@@ -39,7 +39,8 @@ EXPORTS = ["kvq_pool_bytes", "kvq_scale_bytes", "kvq_bytes_per_token", "kvq_num_
            "kvq_extend_workspace_bytes", "kvq_extend", "kvq_store_act_quant", "kvq_store_unscaled",
            "kvq_bytes_per_token_ex", "kvq_num_pages_ex", "kvq_exp2_probe", "kvq_extend_workspace_bytes_ex",
            "kvq_extend_ex", "kvq_extend_path", "kvq_pages_workspace_bytes", "kvq_pages_copy", "kvq_pages_fork",
-           "kvq_pages_resize", "kvq_pages_compact", "kvq_tree_workspace_bytes", "kvq_tree"]
+           "kvq_pages_resize", "kvq_pages_compact", "kvq_tree_workspace_bytes", "kvq_tree",
+           "kvq_prompt_workspace_bytes", "kvq_prompt"]
 
 
 class kvq_layout(ctypes.Structure):
@@ -53,6 +54,10 @@ class kvq_decode_options(ctypes.Structure):
 
 class kvq_extend_options(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int32), ("precise_p", ctypes.c_int32)]
+
+
+class kvq_prompt_strides(ctypes.Structure):
+    _fields_ = [(x + "_" + y, ctypes.c_int64) for x in ("q", "k", "v", "out") for y in ("token", "head")]
 
 
 class KvqError(RuntimeError):
@@ -110,6 +115,9 @@ def lib():
             "kvq_extend_path": (i32, [LP, i32, i32, i32, EP]),
             "kvq_extend_ex": (i32, [P, P, P, P, i32, P, P, i32, i32, i32, ctypes.c_float, P, i32, P, sz, LP, i32,
                                     EP, P]),
+            "kvq_prompt_workspace_bytes": (sz, []),
+            "kvq_prompt": (i32, [P, P, P, P, i32, i32, i32, i32, i32, ctypes.c_float, P, i32,
+                                 ctypes.POINTER(kvq_prompt_strides), P, sz, P]),
             "kvq_tree_workspace_bytes": (sz, [LP, i32, i32, i32, i32, i32]),
             "kvq_tree": (i32, [P, P, P, P, i32, P, P, P, i32, i32, i32, i32, ctypes.c_float, P, i32, P, sz, LP, i32, i32,
                                P]),
@@ -431,6 +439,40 @@ def _out_dtype(out):
     if out.dtype is torch.float32:
         return KVQ_OUT_F32
     raise TypeError("out must be bfloat16 or float32")
+
+
+# ---------------------------------------------------------------------------- whole prompts
+def alloc_prompt_workspace(device="cuda"):
+    return torch.empty(lib().kvq_prompt_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def kvq_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, out: torch.Tensor,
+               workspace: torch.Tensor, sm_scale: float = 1.0, stream=None):
+    """Causal attention over packed prompts: rows q_start[b] .. q_start[b+1]-1 of q ([total, Hq, D] bf16) and k / v
+    ([total, Hkv, D] bf16) are sequence b.  Writes out ([total, Hq, D], bf16 or float32).  q, k, v and out may be
+    strided between tokens and heads (slices of one projection)."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [total, Hq, D], k and v [total, Hkv, D]")
+    if out.shape != q.shape or q_start.numel() < 1:
+        raise ValueError("out must have q's shape and q_start batch + 1 entries")
+    od = _out_dtype(out)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
+        st = [t.stride() for t in (q, k, v, out)]
+        if q.shape[2] > 1 and any(s[2] != 1 for s in st):
+            raise ValueError("the last dimension of q, k, v and out must be dense")
+        strides = ctypes.byref(kvq_prompt_strides(*[x for s in st for x in s[:2]]))
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype is not _BF16:
+            raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
+    device = _check_args(("q_start", q_start, _I32), ("workspace", workspace, _U8))
+    if not (q.get_device() == k.get_device() == v.get_device() == out.get_device() == device):
+        raise ValueError("every tensor must be on the current CUDA device")
+    status = lib().kvq_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_start.data_ptr(), q.shape[0],
+                              q_start.numel() - 1, q.shape[1], k.shape[1], q.shape[2], sm_scale, out.data_ptr(), od,
+                              strides, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, device))
+    if status:
+        raise KvqError(status, "kvq_prompt")
 
 
 # ---------------------------------------------------------------------------- drafted tokens

@@ -334,6 +334,36 @@ kvq_status kvq_noalloc_status(void* stream);
  */
 kvq_status kvq_workspace_status(const void* workspace, void* stream);
 
+/* ---------------------------------------------------------------- whole prompts */
+/*
+ * Causal attention over whole prompts, packed one behind the other, before or beside their kvq_store: keys and
+ * values are the step's own bf16 rows, not the 8-bit pool (kvq_extend attends over the pool, and is what continues a
+ * stored sequence).  The upstream pages leave the first prefill to the engine's bf16 kernel.
+ *   q            [total, num_q_heads, head_dim] bf16, device
+ *   k, v         [total, num_kv_heads, head_dim] bf16, device
+ *   q_start      [batch + 1] int32, device: rows q_start[b] .. q_start[b + 1] - 1 are sequence b
+ *   out          [total, num_q_heads, head_dim], bf16 or f32 (out_dtype), device
+ *   strides      NULL: dense.  Else elements between tokens and between heads of each tensor, multiples of 8 (the
+ *                last dimension is dense), so that q, k and v may be slices of one projection; ignored along a
+ *                dimension of one.  Tensors are 16-byte aligned.
+ *   workspace    at least kvq_prompt_workspace_bytes(), 16-byte aligned, device
+ * Row i of a sequence, query head h gets softmax(sm_scale * q.k^T) v over rows 0 .. i of that sequence and kv head
+ * h / (num_q_heads / num_kv_heads), with fp32 accumulation and P as bf16 (error about 2^-9 of sum p|v|).  sm_scale must
+ * be finite and > 0.  What lies in rows that belong to no sequence, or to others, does not matter, NaN included;
+ * within a sequence v must be finite (a non-finite row also spoils up to 127 rows before it).
+ * Supported: head_dim 64 and 128, any number of query heads per kv head, batch <= 2048.  q_start is read on
+ * the device: a sequence with q_start[b] < 0, q_start[b + 1] < q_start[b] or q_start[b + 1] > total is skipped
+ * and makes kvq_workspace_status report KVQ_EINVAL.  Output rows that no sequence covers are left as they are.
+ */
+typedef struct kvq_prompt_strides {
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+} kvq_prompt_strides;
+size_t kvq_prompt_workspace_bytes(void);
+kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t* q_start, int32_t total, int32_t batch,
+                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float sm_scale, void* out,
+                      kvq_out_dtype out_dtype, const kvq_prompt_strides* strides, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- drafted tokens */
 /*
  * Attention of drafted tokens over the cache, as a speculative step verifies them.  The upstream pages have no
