@@ -193,6 +193,7 @@ struct PromptArgs {
 constexpr int32_t kMaxPromptBatch = 2048;  // sequences whose tile counts fit the kernel's shared table
 bool prompt_supported(int32_t head_dim, int32_t batch);
 kvq_status launch_prompt(const PromptArgs& a, cudaStream_t stream);
+kvq_status launch_prompt_wide(const PromptArgs& a, cudaStream_t stream);
 
 // Pages of the cache (kvq_pages_*).
 constexpr int32_t kPagesChunk = 8192;       // pages whose counts one CTA of the plan reads

@@ -351,7 +351,7 @@ kvq_status kvq_workspace_status(const void* workspace, void* stream);
  * h / (num_q_heads / num_kv_heads), with fp32 accumulation and P as bf16 (error about 2^-9 of sum p|v|).  sm_scale must
  * be finite and > 0.  What lies in rows that belong to no sequence, or to others, does not matter, NaN included;
  * within a sequence v must be finite (a non-finite row also spoils up to 127 rows before it).
- * Supported: head_dim 64 and 128, any number of query heads per kv head, batch <= 2048.  q_start is read on
+ * Supported: head_dim 64, 128 and 256, any number of query heads per kv head, batch <= 2048.  q_start is read on
  * the device: a sequence with q_start[b] < 0, q_start[b + 1] < q_start[b] or q_start[b + 1] > total is skipped
  * and makes kvq_workspace_status report KVQ_EINVAL.  Output rows that no sequence covers are left as they are.
  */

@@ -66,7 +66,8 @@ def check(out, q, k, v, start, dtype=torch.float32, skipped=(), extra=1.0):
     assert err.numel() == 0 or err.mean() <= mean, (float(err.mean()), float(mean))
 
 
-HEADS = [(8, 2, 128), (16, 8, 128), (5, 5, 128), (3, 1, 128), (12, 2, 64), (7, 7, 64), (9, 3, 64)]
+HEADS = [(8, 2, 128), (16, 8, 128), (5, 5, 128), (3, 1, 128), (12, 2, 64), (7, 7, 64), (9, 3, 64), (16, 2, 256),
+         (3, 3, 256)]
 
 
 @pytest.mark.parametrize("hq,hkv,d", HEADS)
@@ -78,7 +79,7 @@ def test_packed_prompts(lens, hq, hkv, d):
     check(out, q, k, v, start)
 
 
-@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 1, 64)])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 1, 64), (16, 2, 256)])
 @pytest.mark.parametrize("lens", [[5000], [2048, 1500, 3000, 17], [40] * 300])
 def test_more_items_than_multiprocessors(lens, hq, hkv, d):
     q, k, v, start = inputs(lens, hq, hkv, d, seed=7)
@@ -88,7 +89,7 @@ def test_more_items_than_multiprocessors(lens, hq, hkv, d):
         check(out, q, k, v, start, dtype)
 
 
-@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (6, 2, 64)])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (6, 2, 64), (4, 1, 256)])
 def test_what_lies_outside_a_sequence_does_not_matter(hq, hkv, d):
     """NaN and infinities in rows behind the last sequence, between sequences and in other sequences."""
     lens = [100, 77, 300, 30]
@@ -128,8 +129,9 @@ def test_strides_of_one_projection():
     assert torch.equal(got, want)
 
 
-def test_large_scores_and_a_late_maximum():
-    q, k, v, start = inputs([900, 260], 8, 2, 128, seed=5, scale=8.0)
+@pytest.mark.parametrize("d", [128, 256])
+def test_large_scores_and_a_late_maximum(d):
+    q, k, v, start = inputs([900, 260], 8, 2, d, seed=5, scale=8.0)
     k[850] *= 4.0
     out, ws = run(q, k, v, start)
     assert kvq.kvq_workspace_status(ws) == 0
