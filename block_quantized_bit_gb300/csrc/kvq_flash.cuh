@@ -91,6 +91,23 @@ __device__ __forceinline__ float ex2_fma(float x) {
   return __int_as_float(__float_as_int(p) + (j << 23));
 }
 
+// Four MMAs from a single elect.sync, A in tensor memory (a_step in columns); as mma8_bf16_tmem_a.
+__device__ __forceinline__ void mma4_bf16_tmem_a(uint32_t d_tmem, uint32_t a, uint32_t a_step, uint64_t b,
+                                                 uint64_t b_step, uint32_t idesc, uint32_t acc_first) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 a1, %1, %5;\n\tadd.u32 a2, a1, %5;\n\tadd.u32 a3, a2, %5;\n\t"
+      "add.u64 b1, %2, %6;\n\tadd.u64 b2, b1, %6;\n\tadd.u64 b3, b2, %6;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc_first), "r"(a_step), "l"(b_step)
+      : "memory");
+}
+
 // A bounded wait that the whole warp agrees on: no lane runs ahead into a warp-collective tcgen05 instruction
 // while another gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {

@@ -38,10 +38,11 @@ namespace {
 
 constexpr int kM = 128;  // query rows per block (the MMA M)
 constexpr int kSmWarps = 8;  // two per tensor-memory lane quarter, each on half of a tile's keys
-constexpr int kDwWarps = 8;
-constexpr int kMmaWarp = kSmWarps + kDwWarps;   // warp 16
-constexpr int kProdWarp = kMmaWarp + 1;         // warps 17 (K ring) and 18 (V ring)
-constexpr int kThreads = (kProdWarp + 2) * 32;  // 19 warps
+constexpr int kDwWarps = 8;  // of K, and of V
+constexpr int kVWarp = kSmWarps + kDwWarps;     // warp 16: first of V
+constexpr int kMmaWarp = kVWarp + kDwWarps;     // warp 24
+constexpr int kProdWarp = kMmaWarp + 1;         // warps 25 (K ring) and 26 (V ring)
+constexpr int kThreads = (kProdWarp + 2) * 32;  // 27 warps
 constexpr int kDwThreads = kDwWarps * 32;
 constexpr int kTmemCols = 512;
 constexpr int kBox = kPage * 128;      // one TMA box: 16 tokens x 128 code bytes
@@ -67,18 +68,19 @@ struct TCfg {
   // so the two rings run at their own pace and the K ring runs deeper.
   static constexpr int CODE_BYTES = PPT * NSL * kBox;
   static constexpr int SLOT_BYTES = CODE_BYTES + PPT * SC_KV;
-  static constexpr int KSTAGES = 3;
+  static constexpr int KB = (D == 128) ? 2 : 1;    // bf16 K tiles (the shared memory that is left decides)
+  static constexpr int KSTAGES = (D == 128) ? 2 : 3;
   static constexpr int VSTAGES = (D == 128) ? 3 : 2;
   static constexpr int NSLOTS = KSTAGES + VSTAGES;  // K ring slots, then V ring slots
   static constexpr int RING_OFF = 0;  // 1024-byte aligned: swizzle atoms
   static constexpr int K_OFF = RING_OFF + NSLOTS * SLOT_BYTES;
-  static constexpr int V_OFF = K_OFF + KV_TILE;
+  static constexpr int V_OFF = K_OFF + KB * KV_TILE;
   static constexpr int Q_OFF = V_OFF + KV_TILE;
   static constexpr int META_OFF = Q_OFF + Q_BYTES;              // [NSLOTS][PPT] valid tokens per page
   static constexpr int RED_OFF = META_OFF + NSLOTS * PPT * 4;   // [2 parities][2 halves][128 rows] row maxima
   static constexpr int SUM_OFF = RED_OFF + 2 * 2 * kM * 4;      // [2 item parities][2 halves][128 rows] row sums
   static constexpr int TAB_OFF = SUM_OFF + 2 * 2 * kM * 4;      // [batch + 1] units before each sequence
-  static constexpr int NBARS = 2 * NSLOTS + 10 + 12;
+  static constexpr int NBARS = 2 * NSLOTS + 11 + 12;
   static constexpr int BAR_OFF = (TAB_OFF + (kMaxTreeBatch + 1) * 4 + 15) / 16 * 16;  // mbarriers: 8-byte aligned
   static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
   // tensor-memory columns: O [0, D); S buffer b [D + b T, D + (b + 1) T); P buffer b [384 + b T / 2, ...)
@@ -86,7 +88,7 @@ struct TCfg {
   static constexpr int P_COL = 384;
   static_assert(D == 128 || D == 256, "the tree kernel needs head_dim 128 or 256");
   static_assert(D + 2 * T <= P_COL && P_COL + T <= kTmemCols, "tensor-memory columns");
-  static_assert(PARTS * T == kDwThreads && NCH % 2 == 0 && NBT == 2, "dequant split");
+  static_assert(PARTS * T == kDwThreads && NBT == 2, "dequant split");
   static_assert(SLOT_BYTES % 1024 == 0, "slots keep the boxes 1024-byte aligned");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(K_OFF % 16 == 0 && V_OFF % 16 == 0 && Q_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
@@ -204,15 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
   // Every barrier completes once per use of its buffer, so a waiter names an unambiguous phase.
   uint64_t* bar_full = bars;                      // [NSLOTS] ring slot landed (producer arrival + bytes)
   uint64_t* bar_empty = bars + Cfg::NSLOTS;       // [NSLOTS] ring slot read by every dequant warp
-  uint64_t* bar_k_full = bars + 2 * Cfg::NSLOTS;  // K tile written (dequant warps), once per tile
-  uint64_t* bar_v_full = bar_k_full + 1;          // V tile written (dequant warps), once per tile
-  uint64_t* bar_qk_done = bar_k_full + 2;         // [2] QK into S buffer b completed (commit)
-  uint64_t* bar_pv_done = bar_k_full + 4;         // [2] PV that read P buffer b completed (commit)
-  uint64_t* bar_p_full = bar_k_full + 6;          // [2] P buffer b written, S buffer b read (softmax warps)
-  uint64_t* bar_q_full = bar_k_full + 8;          // an item's Q rows written (softmax warps), once per item
-  uint64_t* bar_o_free = bar_k_full + 9;          // an item's O read out (softmax warps), once per item
-  uint64_t* bar_pair = bar_k_full + 10;           // [4 quarters][2 parities] both half-tile maxima written
-  uint64_t* bar_sum = bar_k_full + 18;            // [4 quarters] both half row sums written, once per item
+  uint64_t* bar_k_full = bars + 2 * Cfg::NSLOTS;  // [2] K tile b written (K warps)
+  uint64_t* bar_v_full = bar_k_full + 2;          // V tile written (V warps), once per tile
+  uint64_t* bar_qk_done = bar_k_full + 3;         // [2] QK into S buffer b completed (commit)
+  uint64_t* bar_pv_done = bar_k_full + 5;         // [2] PV that read P buffer b completed (commit)
+  uint64_t* bar_p_full = bar_k_full + 7;          // [2] P buffer b written, S buffer b read (softmax warps)
+  uint64_t* bar_q_full = bar_k_full + 9;          // a segment's Q rows written (softmax warps), once per segment
+  uint64_t* bar_o_free = bar_k_full + 10;         // a segment's O read out (softmax warps), once per segment
+  uint64_t* bar_pair = bar_k_full + 11;           // [4 quarters][2 parities] both half-tile maxima written
+  uint64_t* bar_sum = bar_k_full + 19;            // [4 quarters] both half row sums written, once per segment
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -229,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], kDwWarps);
     }
-    mbar_init(bar_k_full, kDwWarps);
+    mbar_init(&bar_k_full[0], kDwWarps);
+    mbar_init(&bar_k_full[1], kDwWarps);
     mbar_init(bar_v_full, kDwWarps);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bar_qk_done[b], 1);
@@ -341,66 +344,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     }
   } else if (warp >= kSmWarps && warp < kMmaWarp) {
     // ===================================================================== dequant warps
-    const int dw = tid - kSmWarps * 32;
+    // Eight for K and eight for V, one copy of the code for both (with five roles on an SM, instruction-cache
+    // misses cost more than the selects).  Each pays its waits and the fence to the async proxy, some 800 clocks
+    // a tile, under the other's work.
+    const int kv = warp >= kVWarp ? 1 : 0;
+    const int dw = tid - (kv ? kVWarp : kSmWarps) * 32;
     const int tt = dw % T;     // key of the tile (consecutive threads: consecutive keys)
     const int part = dw / T;   // which SPAN of the row
     const int pi = tt / kPage, off = tt % kPage;
     const int swz = off & 7;   // 128-byte swizzle phase of this token's staging rows
-    const uint32_t toff = (tt % 8) * 16 + (tt / 8) * Cfg::RS;
-    // dequantize this thread's codes of K or V from a ring slot into a bf16 tile
-    auto write_tile = [&](uint8_t* dst, const uint8_t* slot, bool v_ok) {
+    const uint32_t toff = (tt % 8) * 16 + (tt / 8) * Cfg::RS + part * (Cfg::SPAN / 8) * 128;
+    const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
+    const uint32_t stages = kv ? Cfg::VSTAGES : Cfg::KSTAGES;
+    const uint32_t bufs = kv ? 1 : Cfg::KB;
+    uint64_t* done = kv ? bar_pv_done : bar_qk_done;
+    uint32_t ring = kv ? Cfg::KSTAGES : 0, ring_phase = 0;
+    for (uint32_t i = 0; i < total; ++i) {
+      if (!warp_wait(&bar_full[ring], ring_phase)) { ok = false; break; }
+      const uint8_t* slot = sRing + ring * Cfg::SLOT_BYTES;
+      const bool v_ok = off < sMeta[ring * Cfg::PPT + pi];
+      // the tile was last read by the QK (PV) of the tile `bufs` before
+      if (i >= bufs && !warp_wait(&done[(i - bufs) & 1], ((i - bufs) >> 1) & 1)) { ok = false; break; }
       const uint8_t* rows = slot + pi * Cfg::NSL * kBox + off * 128;
-      const uint32_t sc = KindTraits<KIND>::kScaled ? *reinterpret_cast<const uint32_t*>(
-          slot + Cfg::CODE_BYTES + pi * Cfg::SC_KV + (off * Cfg::NB + part * Cfg::NBT) * 2) : 0u;
-#pragma unroll
+      uint32_t sc = 0u;  // (zero codes times a zero scale: what lies in unwritten or masked rows does not matter)
+      if (KindTraits<KIND>::kScaled && v_ok)
+        sc = *reinterpret_cast<const uint32_t*>(slot + Cfg::CODE_BYTES + pi * Cfg::SC_KV +
+                                                (off * Cfg::NB + part * Cfg::NBT) * 2);
+      uint8_t* dst = (kv ? sV : sK + (i % Cfg::KB) * Cfg::KV_TILE) + toff;
+#pragma unroll 2
       for (int k = 0; k < Cfg::NCH; ++k) {
+        const int c = part * Cfg::NCH + k;  // 16-code chunk along the row
+        uint4 codes = make_uint4(0u, 0u, 0u, 0u);
+        if (v_ok) codes = *reinterpret_cast<const uint4*>(rows + (c / 8) * kBox + (((c % 8) ^ swz) * 16));
         uint32_t w[8];
-        if (v_ok) {
-          const int c = part * Cfg::NCH + k;  // 16-code chunk along the row
-          const uint4 codes = *reinterpret_cast<const uint4*>(rows + (c / 8) * kBox + (((c % 8) ^ swz) * 16));
-          dequant16<KIND>(codes, static_cast<uint16_t>(sc >> (16 * (k >> 1))), w);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 0u;
-        }
-        const int d8 = part * (Cfg::SPAN / 8) + 2 * k;
-        *reinterpret_cast<uint4*>(dst + toff + d8 * 128) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dst + toff + (d8 + 1) * 128) = make_uint4(w[4], w[5], w[6], w[7]);
+        dequant16<KIND>(codes, static_cast<uint16_t>(sc >> (16 * (k >> 1))), w);
+        *reinterpret_cast<uint4*>(dst + 2 * k * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + (2 * k + 1) * 128) = make_uint4(w[4], w[5], w[6], w[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-    };
-    const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
-    uint32_t nk = 0, nv = 0;                     // tiles whose K / V have been written
-    while (ok && nv < total) {
-      if (nk < total) {
-        const int ring = nk % Cfg::KSTAGES;
-        if (!warp_wait(&bar_full[ring], (nk / Cfg::KSTAGES) & 1)) { ok = false; break; }
-        const uint8_t* slot = sRing + ring * Cfg::SLOT_BYTES;
-        const bool v_ok = off < sMeta[ring * Cfg::PPT + pi];
-        // the K tile was last read by the QK of tile nk - 1
-        if (nk >= 1 && !warp_wait(&bar_qk_done[(nk - 1) & 1], ((nk - 1) >> 1) & 1)) { ok = false; break; }
-        write_tile(sK, slot, v_ok);
-        if (lane == 0) {
-          bar_arrive(bar_k_full);
-          bar_arrive(&bar_empty[ring]);
-        }
-        ++nk;
-        if (nk == 1 && nk < total) continue;  // K runs one tile ahead of V
+      if (lane == 0) {
+        bar_arrive(kv ? bar_v_full : &bar_k_full[i % Cfg::KB]);
+        bar_arrive(&bar_empty[ring]);
       }
-      {
-        const int ring = Cfg::KSTAGES + nv % Cfg::VSTAGES;
-        if (!warp_wait(&bar_full[ring], (nv / Cfg::VSTAGES) & 1)) { ok = false; break; }
-        const uint8_t* slot = sRing + ring * Cfg::SLOT_BYTES;
-        const bool v_ok = off < sMeta[ring * Cfg::PPT + pi];
-        // the V tile was last read by the PV of tile nv - 1
-        if (nv >= 1 && !warp_wait(&bar_pv_done[(nv - 1) & 1], ((nv - 1) >> 1) & 1)) { ok = false; break; }
-        write_tile(sV, slot, v_ok);
-        if (lane == 0) {
-          bar_arrive(bar_v_full);
-          bar_arrive(&bar_empty[ring]);
-        }
-        ++nv;
+      if (++ring == (kv ? Cfg::KSTAGES : 0) + stages) {
+        ring = kv ? Cfg::KSTAGES : 0;
+        ring_phase ^= 1;
       }
     }
   } else if (warp == kMmaWarp) {
@@ -420,10 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
       if (!warp_wait(&bar_p_full[bp], (m >> 1) & 1)) return false;
       if (first && items >= 1 && !warp_wait(bar_o_free, (items - 1) & 1)) return false;
       tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < T / 16; ++ks)
-        mma_bf16_tmem_a(tO, tP + bp * (T / 2) + ks * 8, dV + static_cast<uint64_t>((ks * 2 * Cfg::RS) >> 4),
-                        idesc_pv, (!first || ks > 0) ? 1u : 0u);
+      if constexpr (T == 128)
+        mma8_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, dV, static_cast<uint64_t>((2 * Cfg::RS) >> 4), idesc_pv, first ? 0u : 1u);
+      else
+        mma4_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, dV, static_cast<uint64_t>((2 * Cfg::RS) >> 4), idesc_pv, first ? 0u : 1u);
       mma_commit(&bar_pv_done[bp]);
       __syncwarp();
       return true;
@@ -434,14 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
       if (!warp_wait(bar_q_full, items & 1)) { ok = false; break; }
       for (int32_t i = 0; i < ntiles; ++i, ++n) {
         const int b = n & 1;
-        if (!warp_wait(bar_k_full, n & 1)) { ok = false; break; }
+        const uint32_t kb = n % Cfg::KB;
+        if (!warp_wait(&bar_k_full[kb], (n / Cfg::KB) & 1)) { ok = false; break; }
         // S buffer b was read by the softmax of tile n - 2
         if (n >= 2 && !warp_wait(&bar_p_full[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_bf16(tS + b * T, dQ + static_cast<uint64_t>((ks * 256) >> 4), dK + static_cast<uint64_t>((ks * 256) >> 4),
-                   idesc_qk, ks > 0 ? 1u : 0u);
+        for (int k8 = 0; k8 < D / 128; ++k8)
+          mma8_bf16(tS + b * T, dQ + static_cast<uint64_t>((k8 * 8 * 256) >> 4), 256 >> 4,
+                    dK + kb * static_cast<uint64_t>(Cfg::KV_TILE >> 4) + static_cast<uint64_t>((k8 * 8 * 256) >> 4), 256 >> 4, idesc_qk, k8 > 0 ? 1u : 0u);
         mma_commit(&bar_qk_done[b]);
         __syncwarp();
         if (i > 0 && !pv(n - 1, i == 1)) { ok = false; break; }
@@ -530,32 +520,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
         vis = row_ok ? vis & kAll : kAll;  // (rows past the block's are zeros that nobody reads)
         if (!warp_wait(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
-        // every row of the warp sees every key of its half: no masking.  The two variants of each pass are
-        // separate straight-line loops behind one warp-uniform branch.
-        const bool full = __all_sync(0xffffffffu, vis == kAll);
-        // pass 1: the row's max over the visible keys of this half (sm_scale > 0: scaling commutes with it)
-        float mh = -INFINITY;
-        auto pass1 = [&](auto masked) {
-          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // Keys that some row of the warp does not see: their scores become -inf in tensor memory first, so that the
+        // passes below need one variant only.
+        if (!__all_sync(0xffffffffu, vis == kAll)) {
 #pragma unroll 1
           for (int h = 0; h < T / 64; ++h) {
             uint32_t v[32];
             tmem_ld32(tS + b * T + h * 32, v);
             const uint32_t vw = static_cast<uint32_t>(vis >> (32 * h));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float x = __uint_as_float(v[e]);
-              if constexpr (decltype(masked)::value) x = ((vw >> e) & 1u) ? x : -INFINITY;
-              m[e & 3] = fmaxf(m[e & 3], x);
-            }
+            for (int e = 0; e < 32; ++e) v[e] = ((vw >> e) & 1u) ? v[e] : 0xFF800000u;
+            tmem_st32(tS + b * T + h * 32, v);
           }
-          mh = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        };
-        if (full) pass1(std::false_type{});
-        else pass1(std::true_type{});
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        // pass 1: the row's max over this half (sm_scale > 0: scaling commutes with it)
+        float mh[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < T / 64; ++h) {
+          uint32_t v[32];
+          tmem_ld32(tS + b * T + h * 32, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mh[e & 3] = fmaxf(mh[e & 3], __uint_as_float(v[e]));
+        }
         // the row's max over the whole tile: exchange halves with the other warp of the lane quarter
         // (double-buffered by tile parity, so one barrier per tile suffices)
-        sRed[(b * 2 + hf) * kM + r] = mh;
+        sRed[(b * 2 + hf) * kM + r] = fmaxf(fmaxf(mh[0], mh[1]), fmaxf(mh[2], mh[3]));
         if (!pair_meet(&bar_pair[quarter * 2 + b], (pair_phase >> b) & 1u)) { ok = false; break; }
         pair_phase ^= 1u << b;
         float mx = fmaxf(sRed[(b * 2) * kM + r], sRed[(b * 2 + 1) * kM + r]);
@@ -586,37 +576,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           l *= alpha;
         }
-        // pass 2: P = 2^(s * scale - m) of this half as bf16 into tensor memory; the row sum in fp32
-        auto pass2 = [&](auto masked) {
-          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // pass 2: P = 2^(s * scale - m) of this half as bf16 into tensor memory; the row sum in fp32.  (A row without
+        // a visible key so far has only scores of -inf: any finite m gives zeros.)
+        const float m_fin = m_used == -INFINITY ? 0.0f : m_used;
+        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-          for (int h = 0; h < T / 64; ++h) {
-            uint32_t v[32];
-            tmem_ld32(tS + b * T + h * 32, v);
-            uint32_t w[16];
-            const uint32_t vw = static_cast<uint32_t>(vis >> (32 * h));
+        for (int h = 0; h < T / 64; ++h) {
+          uint32_t v[32];
+          tmem_ld32(tS + b * T + h * 32, v);
+          uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x0 = fmaf(__uint_as_float(v[2 * e]), a.score_scale, -m_used);
-              const float x1 = fmaf(__uint_as_float(v[2 * e + 1]), a.score_scale, -m_used);
-              // every fourth pair on the FMA pipe, the rest on the MUFU unit
-              const bool fma_pipe = (e & 3) == 3;
-              float p0 = fma_pipe ? ex2_fma(x0) : ex2(x0);
-              float p1 = fma_pipe ? ex2_fma(x1) : ex2(x1);
-              if constexpr (decltype(masked)::value) {
-                p0 = ((vw >> (2 * e)) & 1u) ? p0 : 0.0f;
-                p1 = ((vw >> (2 * e + 1)) & 1u) ? p1 : 0.0f;
-              }
-              ls[(2 * e) & 3] += p0;
-              ls[(2 * e + 1) & 3] += p1;
-              w[e] = pack_bf16x2(p0, p1);
-            }
-            tmem_st16u(tP + b * (T / 2) + h * 16, w);
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), a.score_scale, -m_fin));
+            const float p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), a.score_scale, -m_fin));
+            ls[(2 * e) & 3] += p0;
+            ls[(2 * e + 1) & 3] += p1;
+            w[e] = pack_bf16x2(p0, p1);
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        };
-        if (full) pass2(std::false_type{});
-        else pass2(std::true_type{});
+          tmem_st16u(tP + b * (T / 2) + h * 16, w);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
