@@ -345,7 +345,7 @@ struct TreePlan {
   bool flash;
   kvq_decode_options dec;
   int32_t chunk, grid;
-  size_t tab_offset, acc_offset, ml_offset;                          // flash
+  size_t tab_offset, seq_offset, st_offset, acc_offset, ml_offset;   // flash
   size_t dense_bytes, lens_offset, rows_offset, base_offset, total;  // rows through the decode kernels
 };
 
@@ -366,7 +366,9 @@ bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
     tp->grid = sm_count();
     const size_t slots = 2 * static_cast<size_t>(tp->grid) * 128;
     tp->tab_offset = kWorkspaceHeader;
-    tp->ml_offset = tp->tab_offset + up((static_cast<size_t>(batch) + 2) * sizeof(int32_t));
+    tp->seq_offset = tp->tab_offset + up((static_cast<size_t>(batch) + 2) * sizeof(int32_t));
+    tp->st_offset = tp->seq_offset + up(static_cast<size_t>(total_q) * sizeof(int32_t));
+    tp->ml_offset = tp->st_offset + up(static_cast<size_t>(tp->grid) * sizeof(uint32_t));
     tp->acc_offset = tp->ml_offset + up(slots * 2 * sizeof(float));
     tp->total = tp->acc_offset + up(slots * L.head_dim * sizeof(float));
     return true;
@@ -777,10 +779,11 @@ kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const i
   st = kvq_device_check();
   if (st != KVQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return KVQ_ECUDA;
-  if (empty) return KVQ_OK;
+  if (empty) return clear_status(workspace, s);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (!tp.flash) {
+    st = clear_status(workspace, s);
+    if (st != KVQ_OK) return st;
     int32_t* vlens = reinterpret_cast<int32_t*>(ws + tp.lens_offset);
     int32_t* vbase = reinterpret_cast<int32_t*>(ws + tp.base_offset);
     int32_t* vrow = reinterpret_cast<int32_t*>(ws + tp.rows_offset);
@@ -815,6 +818,8 @@ kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const i
   a.out = out;
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.tab = reinterpret_cast<int32_t*>(ws + tp.tab_offset);
+  a.row_seq = reinterpret_cast<int32_t*>(ws + tp.seq_offset);
+  a.cta_status = reinterpret_cast<uint32_t*>(ws + tp.st_offset);
   a.part_acc = reinterpret_cast<float*>(ws + tp.acc_offset);
   a.part_ml = reinterpret_cast<float*>(ws + tp.ml_offset);
   a.num_pages = layout->num_pages;

@@ -147,6 +147,8 @@ struct TreeArgs {
   void* out;                  // [total_q][num_q_heads][head_dim]
   uint32_t* status;
   int32_t* tab;               // [batch + 1] work units before each sequence, then [1] CTAs that share them
+  int32_t* row_seq;           // [total_q] sequence of each query row, or -1
+  uint32_t* cta_status;       // [CTAs]
   float* part_acc;            // [2 * CTAs][128][head_dim]
   float* part_ml;             // [2 * CTAs][128][2]
   int64_t num_pages;

@@ -94,13 +94,13 @@ struct TCfg {
   static_assert(K_OFF % 16 == 0 && V_OFF % 16 == 0 && Q_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
-// Drafted tokens of sequence b after validation; 0 for an inconsistent one (reported in the status word).
-__device__ __forceinline__ int32_t drafted(const TreeArgs& a, int32_t b, bool report) {
+// Drafted tokens of sequence b after validation; 0 for an inconsistent one (reported in `report`, if given).
+__device__ __forceinline__ int32_t drafted(const TreeArgs& a, int32_t b, uint32_t* report) {
   const int32_t q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1), L = __ldg(a.seq_lens + b);
   const int32_t n = q1 - q0;
   if (q0 < 0 || n < 0 || q1 > a.total_q || n > L || n > 64 * a.mask_words ||
       L > static_cast<int64_t>(a.max_pages) * kPage) {
-    if (report) set_status(a.status, kStatusBadExtend);
+    set_status(report, kStatusBadExtend);
     return 0;
   }
   return n;
@@ -136,7 +136,7 @@ __device__ __forceinline__ Seg locate(const int32_t* tab, const TreeArgs& a, int
   s.b = lo - 1;
   s.L = __ldg(a.seq_lens + s.b);
   s.q0 = __ldg(a.q_start + s.b);
-  s.n = drafted(a, s.b, false);
+  s.n = drafted(a, s.b, nullptr);
   const int32_t nt = (s.L + Cfg::T - 1) / Cfg::T;
   const int32_t local = u - tab[s.b];
   const int32_t item = local / nt;
@@ -220,9 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t G = a.num_q_heads / a.num_kv_heads;
 
+  // Each CTA has a status word of its own, which the merge kernel sums up: no clearing launch before this one.
+  uint32_t* my_status = a.cta_status + blockIdx.x;
+  if (tid == 0) *my_status = 0;
+  __syncthreads();
+
   // ---- plan: units before every sequence
   for (int32_t b = tid; b < a.batch; b += kThreads) {
-    const int32_t n = drafted(a, b, blockIdx.x == 0);
+    const int32_t n = drafted(a, b, blockIdx.x == 0 ? my_status : nullptr);
     sTab[b + 1] = n == 0 ? 0 : row_blocks(n, G) * a.num_kv_heads * ((__ldg(a.seq_lens + b) + T - 1) / T);
   }
   if (tid == 0) {
@@ -279,6 +284,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     for (int32_t b = tid; b <= a.batch; b += kThreads) a.tab[b] = sTab[b];
     if (tid == 0) a.tab[a.batch + 1] = C;
   }
+  // ... and the sequence of each query row, the CTAs taking rows in turn (the last sequence whose rows begin at or
+  // before it; -1 where that one does not reach it)
+  for (int32_t i = blockIdx.x * kThreads + tid; i < a.total_q; i += gridDim.x * kThreads) {
+    int lo = 0, hi = a.batch;  // first b with q_start[b] > i
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.q_start + mid) <= i) lo = mid + 1;
+      else hi = mid;
+    }
+    const int32_t b = lo - 1;
+    a.row_seq[i] = b >= 0 && i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr) ? b : -1;
+  }
   bool ok = true;
 
   if (warp >= kProdWarp) {
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     while (ok && t.live) {
       int32_t phys = bt, nvalid = 0;
       if (phys >= a.num_pages) {  // never dereferenced; reported in the status word
-        set_status(a.status, kStatusBadPage);
+        set_status(my_status, kStatusBadPage);
         phys = -1;
       }
       if (phys >= 0) nvalid = min(kPage, t.s.L - (t.t * Cfg::PPT + lane) * kPage);
@@ -659,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
       if (lane == 0) bar_arrive(bar_o_free);
     }
   }
-  if (!ok) set_status(a.status, kStatusTimeout);
+  if (!ok) set_status(my_status, kStatusTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -667,92 +684,123 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-// One CTA per output row: joins the partials of the segments that its block was cut into,
+// Joins the partials of the segments that a row's block was cut into, WPR warps per row:
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s with M = max_s m_s.  Rows of blocks that one segment covered
 // whole are final already.  A row without a visible key has l = 0 everywhere and gives zeros.
 constexpr int kMergeThreads = 128;
 constexpr int kMergeWarps = kMergeThreads / 32;
 
-template <int D>
+template <int D, int WPR>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
   constexpr int DPL = D / 32;  // dims per lane
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
-  __shared__ float s_a[kMergeWarps][D];
+  __shared__ float s_a[WPR > 1 ? kMergeWarps : 1][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int32_t G = a.num_q_heads / a.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t tokrow = blockIdx.x / a.num_q_heads, head = blockIdx.x - tokrow * a.num_q_heads;
-  int lo = 0, hi = a.batch;  // first b with q_start[b] > tokrow
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.q_start + mid) <= tokrow) lo = mid + 1;
-    else hi = mid;
+  if (blockIdx.x == 0) {  // the call's status: any CTA's
+    uint32_t st = 0;
+    for (int32_t i = tid; i < a.grid; i += kMergeThreads) st = max(st, a.cta_status[i]);
+    st = __reduce_max_sync(0xffffffffu, st);
+    if (lane == 0) s_m[warp] = __uint_as_float(st);
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kMergeWarps; ++w) st = max(st, __float_as_uint(s_m[w]));
+      *a.status = st;
+    }
+    __syncthreads();
   }
-  const int32_t b = lo - 1;
-  if (b < 0) return;
-  const int32_t q0 = __ldg(a.q_start + b), n = drafted(a, b, false);
-  if (tokrow < q0 || tokrow >= q0 + n) return;  // behind the last sequence, or a skipped one
-  const int32_t U = a.tab[a.batch], C = a.tab[a.batch + 1];
-  const int32_t nt = (__ldg(a.seq_lens + b) + TCfg<D>::T - 1) / TCfg<D>::T;
-  const int32_t g = head / G, row = (tokrow - q0) * G + (head - g * G);
-  const int32_t blk = row / kM, r = row - blk * kM;
-  const int32_t u0 = a.tab[b] + (blk * a.num_kv_heads + g) * nt, u1 = u0 + nt;
-  // CTAs whose ranges hold units of the block: start(c) <= u < start(c + 1), start(c) = floor(U c / C)
-  const int32_t c0 = static_cast<int32_t>((static_cast<int64_t>(u0) * C + C - 1) / U);
-  const int32_t c1 = static_cast<int32_t>((static_cast<int64_t>(u1 - 1) * C + C - 1) / U);
-  auto owner = [&](int32_t c, int32_t u) -> int32_t {  // c, corrected to the CTA whose range holds unit u
-    while (c > 0 && range_start(U, C, c) > u) --c;
-    while (c + 1 < C && range_start(U, C, c + 1) <= u) ++c;
-    return c;
-  };
-  const int32_t first = owner(min(c0, C - 1), u0), last = owner(min(c1, C - 1), u1 - 1);
-  if (first == last) return;
+  const int64_t out_row = (static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp) / WPR;
+  const int sub = warp % WPR;
+  const bool live = out_row < static_cast<int64_t>(a.total_q) * a.num_q_heads;
+  const int32_t G = a.num_q_heads / a.num_kv_heads;
+  const int32_t tokrow = live ? static_cast<int32_t>(out_row / a.num_q_heads) : 0;
+  const int32_t head = static_cast<int32_t>(out_row - static_cast<int64_t>(tokrow) * a.num_q_heads);
+  const int32_t b = live ? a.row_seq[tokrow] : -1;  // -1: no sequence covers the row
+  int32_t first = 0, last = 0, u0 = 0, U = 0, C = 1, r = 0;
+  if (b >= 0) {
+    U = a.tab[a.batch];
+    C = a.tab[a.batch + 1];
+    const int32_t nt = (__ldg(a.seq_lens + b) + TCfg<D>::T - 1) / TCfg<D>::T;
+    const int32_t g = head / G, row = (tokrow - __ldg(a.q_start + b)) * G + (head - g * G);
+    const int32_t blk = row / kM;
+    r = row - blk * kM;
+    u0 = a.tab[b] + (blk * a.num_kv_heads + g) * nt;
+    // the CTAs whose ranges hold the block's first and last unit: start(c) = floor(U c / C) <= u < start(c + 1)
+    auto owner = [&](int32_t u) -> int32_t {
+      int32_t c = min(static_cast<int32_t>((static_cast<int64_t>(u) * C + C - 1) / U), C - 1);
+      while (c > 0 && range_start(U, C, c) > u) --c;
+      while (c + 1 < C && range_start(U, C, c + 1) <= u) ++c;
+      return c;
+    };
+    first = owner(u0);
+    last = owner(u0 + nt - 1);
+  }
+  if (WPR == 1 && first == last) return;  // (the block was one segment, or there is no row)
   auto prow = [&](int32_t c) -> int64_t {  // this row's partial in CTA c: its first segment, or its last
     return static_cast<int64_t>(2 * c + (range_start(U, C, c) >= u0 ? 0 : 1)) * kM + r;
   };
+  const bool split = first != last;
   float M = -INFINITY;
-  for (int32_t c = first + tid; c <= last; c += kMergeThreads) M = fmaxf(M, a.part_ml[prow(c) * 2]);
+  if (split)
+    for (int32_t c = first + lane; c <= last; c += 32) M = fmaxf(M, a.part_ml[prow(c) * 2]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w]);
   float acc[DPL], l = 0.0f;
 #pragma unroll
   for (int j = 0; j < DPL; ++j) acc[j] = 0.0f;
-#pragma unroll 2
-  for (int32_t c = first + warp; c <= last; c += kMergeWarps) {
-    const int64_t p = prow(c);
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + p * 2);
-    const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
-    l = fmaf(ml.y, w, l);
+  if (split) {
+#pragma unroll 4
+    for (int32_t c = first + sub; c <= last; c += WPR) {
+      const int64_t p = prow(c);
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + p * 2);
+      const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+      l = fmaf(ml.y, w, l);
 #pragma unroll
-    for (int j = 0; j < DPL / 4; ++j) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part_acc + p * D + j * 128 + lane * 4);
-      acc[4 * j] = fmaf(v.x, w, acc[4 * j]);
-      acc[4 * j + 1] = fmaf(v.y, w, acc[4 * j + 1]);
-      acc[4 * j + 2] = fmaf(v.z, w, acc[4 * j + 2]);
-      acc[4 * j + 3] = fmaf(v.w, w, acc[4 * j + 3]);
+      for (int j = 0; j < DPL / 4; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part_acc + p * D + j * 128 + lane * 4);
+        acc[4 * j] = fmaf(v.x, w, acc[4 * j]);
+        acc[4 * j + 1] = fmaf(v.y, w, acc[4 * j + 1]);
+        acc[4 * j + 2] = fmaf(v.z, w, acc[4 * j + 2]);
+        acc[4 * j + 3] = fmaf(v.w, w, acc[4 * j + 3]);
+      }
     }
   }
+  if constexpr (WPR > 1) {  // the row's warps are this CTA's
+    static_assert(WPR == kMergeWarps, "one row per CTA");
 #pragma unroll
-  for (int j = 0; j < DPL / 4; ++j)
-    *reinterpret_cast<float4*>(&s_a[warp][j * 128 + lane * 4]) =
-        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  float lt = 0.0f;
+    for (int j = 0; j < DPL / 4; ++j)
+      *reinterpret_cast<float4*>(&s_a[warp][j * 128 + lane * 4]) =
+          make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (!split || warp != 0) return;
+    l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) lt += s_l[w];
-  for (int d = tid; d < D; d += kMergeThreads) {
-    float v = 0.0f;
+    for (int w = 0; w < WPR; ++w) l += s_l[w];
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) v += s_a[w][d];
-    const float o = lt > 0.0f ? v / lt : 0.0f;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * D + d;
-    if (a.out_dtype == KVQ_OUT_F32) static_cast<float*>(a.out)[at] = o;
-    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
+    for (int j = 0; j < DPL / 4; ++j) {
+      float4 v = *reinterpret_cast<const float4*>(&s_a[0][j * 128 + lane * 4]);
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&s_a[w][j * 128 + lane * 4]);
+        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+      }
+      acc[4 * j] = v.x;
+      acc[4 * j + 1] = v.y;
+      acc[4 * j + 2] = v.z;
+      acc[4 * j + 3] = v.w;
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int j = 0; j < DPL / 4; ++j) {
+    const int64_t at = out_row * D + j * 128 + lane * 4;
+    const float4 o = make_float4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv, acc[4 * j + 3] * inv);
+    if (a.out_dtype == KVQ_OUT_F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   }
 }
 
@@ -773,8 +821,12 @@ kvq_status launch_tree_d(const TreeArgs& a, cudaStream_t stream) {
   if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
   kern<<<static_cast<unsigned>(a.grid), kThreads, Cfg::SMEM_BYTES, stream>>>(a, map);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
+  // Few rows: a CTA for each (their blocks are cut into many segments); else a warp for each (64 rows 5.7 us, 9600
+  // rows 23 us with a CTA each).
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.num_q_heads;
+  const bool few = rows <= 2048;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.total_q) * a.num_q_heads));
+  cfg.gridDim = dim3(static_cast<unsigned>(few ? rows : (rows + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -782,7 +834,8 @@ kvq_status launch_tree_d(const TreeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kMergeWarps>, a)
+                            : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 1>, a);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? KVQ_OK : KVQ_ECUDA;
 }
 
