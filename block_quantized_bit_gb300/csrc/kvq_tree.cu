@@ -47,7 +47,6 @@ constexpr int kDwThreads = kDwWarps * 32;
 constexpr int kTmemCols = 512;
 constexpr int kBox = kPage * 128;      // one TMA box: 16 tokens x 128 code bytes
 constexpr float kLazyRescale = 8.0f;   // log2 headroom before the running max must move
-constexpr int kMinUnits = 2;           // tiles per CTA below which fewer CTAs share the work
 
 template <int D>
 struct TCfg {
@@ -276,25 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
   // the merge kernel may launch now; it waits for this grid to complete before it reads
   asm volatile("griddepcontrol.launch_dependents;");
   const int32_t U = sTab[a.batch];
-  const int32_t C = max(1, min(a.grid, U / kMinUnits));  // CTAs that share the units
+  const int32_t C = max(1, min(a.grid, U));  // CTAs that share the units
   Range range;
   range.u0 = static_cast<int32_t>(blockIdx.x) < C ? range_start(U, C, blockIdx.x) : 0;
   range.u1 = static_cast<int32_t>(blockIdx.x) < C ? range_start(U, C, blockIdx.x + 1) : 0;
   if (blockIdx.x == 0) {  // the plan, for the merge
     for (int32_t b = tid; b <= a.batch; b += kThreads) a.tab[b] = sTab[b];
     if (tid == 0) a.tab[a.batch + 1] = C;
-  }
-  // ... and the sequence of each query row, the CTAs taking rows in turn (the last sequence whose rows begin at or
-  // before it; -1 where that one does not reach it)
-  for (int32_t i = blockIdx.x * kThreads + tid; i < a.total_q; i += gridDim.x * kThreads) {
-    int lo = 0, hi = a.batch;  // first b with q_start[b] > i
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.q_start + mid) <= i) lo = mid + 1;
-      else hi = mid;
-    }
-    const int32_t b = lo - 1;
-    a.row_seq[i] = b >= 0 && i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr) ? b : -1;
   }
   bool ok = true;
 
@@ -371,6 +358,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     const int pi = tt / kPage, off = tt % kPage;
     const int swz = off & 7;   // 128-byte swizzle phase of this token's staging rows
     const uint32_t toff = (tt % 8) * 16 + (tt / 8) * Cfg::RS + part * (Cfg::SPAN / 8) * 128;
+    // While the first tile is on its way, the V warps write down the sequence of each query row for the merge, the
+    // CTAs taking rows in turn: the last sequence whose rows begin at or before it, -1 where that one does not reach it.
+    if (kv == 1)
+      for (int32_t i = blockIdx.x * kDwThreads + dw; i < a.total_q; i += gridDim.x * kDwThreads) {
+        int lo = 0, hi = a.batch;  // first b with q_start[b] > i
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(a.q_start + mid) <= i) lo = mid + 1;
+          else hi = mid;
+        }
+        const int32_t b = lo - 1;
+        a.row_seq[i] = b >= 0 && i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr) ? b : -1;
+      }
     const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
     const uint32_t stages = kv ? Cfg::VSTAGES : Cfg::KSTAGES;
     const uint32_t bufs = kv ? 1 : Cfg::KB;
