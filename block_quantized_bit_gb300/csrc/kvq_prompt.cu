@@ -338,19 +338,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
         if (!warp_wait(&bar_s_full[w], nt & 1)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[kM];
+        float top;
+        if (j < n - 1) {
+          uint32_t mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + 32 * c, s + 32 * c);
+          for (int c = 0; c < 4; ++c) tmem_ld32_max_issue(tS + 32 * c, s + 32 * c, mx[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
-        if (j == n - 1) {
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld32(s + 32 * c);
+            tmem_wait_max(mx[c]);
+          }
+          top = fmaxf(fmaxf(__uint_as_float(mx[0]), __uint_as_float(mx[1])),
+                      fmaxf(__uint_as_float(mx[2]), __uint_as_float(mx[3])));
+        } else {
 #pragma unroll
-          for (int e = 0; e < kM; ++e) s[e] = e <= r ? s[e] : 0xFF800000u;
+          for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + 32 * c, s + 32 * c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kM; ++e) {
+            s[e] = e <= r ? s[e] : 0xFF800000u;
+            mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+          }
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < kM; e += 2)
-          mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.score_scale;
+        top *= a.score_scale;
         update_max(top, j);
         const float2 sc2 = make_float2(a.score_scale, a.score_scale), m2 = make_float2(-m, -m);
 #pragma unroll

@@ -19,10 +19,6 @@ struct Item {
 };
 static_assert(sizeof(Item) == 32, "item slots");
 
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return smem_desc(addr, lbo, sbo) | (static_cast<uint64_t>(2) << 61);  // 128-byte swizzle
-}
-
 // One box: 64 elements (128 bytes) of `head`, the map's number of rows from `row`.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint64_t* bar) {
   asm volatile(
@@ -30,16 +26,6 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(row), "r"(smem_u32(bar))
       : "memory");
-}
-
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  uint64_t A, B, C;
-  memcpy(&A, &a, 8);
-  memcpy(&B, &b, 8);
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(C) : "l"(A), "l"(B));
-  float2 c;
-  memcpy(&c, &C, 8);
-  return c;
 }
 
 // Items of a sequence of len tokens: ceil(len / 128) token blocks of G heads, TILES of them at a time.

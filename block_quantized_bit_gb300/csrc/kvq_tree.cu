@@ -40,46 +40,37 @@ constexpr int kM = 128;  // query rows per block (the MMA M)
 constexpr int kSmWarps = 8;  // two per tensor-memory lane quarter, each on half of a tile's keys
 constexpr int kDwWarps = 8;  // of K, and of V
 constexpr int kVWarp = kSmWarps + kDwWarps;     // warp 16: first of V
-constexpr int kMmaWarp = kVWarp + kDwWarps;     // warp 24
-constexpr int kProdWarp = kMmaWarp + 1;         // warps 25 (K ring) and 26 (V ring)
-constexpr int kThreads = (kProdWarp + 2) * 32;  // 27 warps
+constexpr int kPlanWarp = kVWarp + kDwWarps;    // warp 24: pages of the tiles to come
+constexpr int kMmaWarp = kPlanWarp + 1;         // warp 25
+constexpr int kThreads = (kMmaWarp + 1) * 32;   // 26 warps
 constexpr int kDwThreads = kDwWarps * 32;
 constexpr int kTmemCols = 512;
-constexpr int kBox = kPage * 128;      // one TMA box: 16 tokens x 128 code bytes
+constexpr int kMeta = 8;               // tiles whose pages are looked up ahead
 constexpr float kLazyRescale = 8.0f;   // log2 headroom before the running max must move
 
 template <int D>
 struct TCfg {
   static constexpr int T = (D == 128) ? 128 : 64;  // keys per tile
   static constexpr int PPT = T / kPage;            // pages per tile
-  static constexpr int RS = D * 16;                // bytes between 8-row groups of a tile
+  static constexpr int RS = D * 16;                // bytes between 8-row groups of the Q tile
+  static constexpr int CHUNK = T * 128;            // bytes of a 64-column chunk of a K or V tile
   static constexpr int KV_TILE = T * D * 2;        // one bf16 K or V tile
   static constexpr int Q_BYTES = kM * D * 2;
-  static constexpr int PARTS = kDwThreads / T;     // dequant threads per token row
-  static constexpr int SPAN = D / PARTS;           // codes per dequant thread (of K, and of V)
-  static constexpr int NCH = SPAN / 16;            // 16-code chunks per dequant thread
-  static constexpr int NBT = SPAN / 32;            // scale blocks per dequant thread
-  static constexpr int NB = D / 32;
-  static constexpr int NSL = D / 128;              // 128-byte slices of a code row
-  static constexpr int SC_KV = kPage * NB * 2;     // scale bytes of one page of K or of V
-  // a ring slot (of the K ring or of the V ring): codes [page][slice] boxes as TMA wrote them, then the
-  // scales [page].  The K ring is freed as soon as K is dequantized, the V ring only after the previous PV,
-  // so the two rings run at their own pace and the K ring runs deeper.
-  static constexpr int CODE_BYTES = PPT * NSL * kBox;
-  static constexpr int SLOT_BYTES = CODE_BYTES + PPT * SC_KV;
-  static constexpr int KB = (D == 128) ? 2 : 1;    // bf16 K tiles (the shared memory that is left decides)
-  static constexpr int KSTAGES = (D == 128) ? 2 : 3;
-  static constexpr int VSTAGES = (D == 128) ? 3 : 2;
-  static constexpr int NSLOTS = KSTAGES + VSTAGES;  // K ring slots, then V ring slots
-  static constexpr int RING_OFF = 0;  // 1024-byte aligned: swizzle atoms
-  static constexpr int K_OFF = RING_OFF + NSLOTS * SLOT_BYTES;
-  static constexpr int V_OFF = K_OFF + KB * KV_TILE;
-  static constexpr int Q_OFF = V_OFF + KV_TILE;
-  static constexpr int META_OFF = Q_OFF + Q_BYTES;              // [NSLOTS][PPT] valid tokens per page
-  static constexpr int RED_OFF = META_OFF + NSLOTS * PPT * 4;   // [2 parities][2 halves][128 rows] row maxima
+  static constexpr int NB = D / 32;                // scale blocks of a row
+  // A dequant warp converts 2 KB of codes of K or V per tile: four 16-byte pieces per lane, consecutive lanes
+  // consecutive pieces of a row.
+  static constexpr int CPR = D / 16;               // pieces of a row
+  static constexpr int RPI = 32 / CPR;             // rows per load
+  static constexpr int RPW = 4 * RPI;              // rows per warp
+  static constexpr int K_OFF = 0;                  // [2] bf16 K tiles; 1024-byte aligned: swizzle atoms
+  static constexpr int V_OFF = K_OFF + 2 * KV_TILE;  // [2] bf16 V tiles
+  static constexpr int Q_OFF = V_OFF + 2 * KV_TILE;
+  static constexpr int BASE_OFF = Q_OFF + Q_BYTES;              // [kMeta][PPT] pool row group of each page, or -1
+  static constexpr int NVAL_OFF = BASE_OFF + kMeta * PPT * 8;   // [kMeta][PPT] valid tokens
+  static constexpr int RED_OFF = NVAL_OFF + kMeta * PPT * 4;    // [2 parities][2 halves][128 rows] row maxima
   static constexpr int SUM_OFF = RED_OFF + 2 * 2 * kM * 4;      // [2 item parities][2 halves][128 rows] row sums
   static constexpr int TAB_OFF = SUM_OFF + 2 * 2 * kM * 4;      // [batch + 1] units before each sequence
-  static constexpr int NBARS = 2 * NSLOTS + 11 + 12;
+  static constexpr int NBARS = 2 * kMeta + 14 + 12;
   static constexpr int BAR_OFF = (TAB_OFF + (kMaxTreeBatch + 1) * 4 + 15) / 16 * 16;  // mbarriers: 8-byte aligned
   static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
   // tensor-memory columns: O [0, D); S buffer b [D + b T, D + (b + 1) T); P buffer b [384 + b T / 2, ...)
@@ -87,10 +78,8 @@ struct TCfg {
   static constexpr int P_COL = 384;
   static_assert(D == 128 || D == 256, "the tree kernel needs head_dim 128 or 256");
   static_assert(D + 2 * T <= P_COL && P_COL + T <= kTmemCols, "tensor-memory columns");
-  static_assert(PARTS * T == kDwThreads && NBT == 2, "dequant split");
-  static_assert(SLOT_BYTES % 1024 == 0, "slots keep the boxes 1024-byte aligned");
+  static_assert(kDwWarps * RPW == T && kPage % RPW == 0, "dequant split");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(K_OFF % 16 == 0 && V_OFF % 16 == 0 && Q_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
 // Drafted tokens of sequence b after validation; 0 for an inconsistent one (reported in `report`, if given).
@@ -190,30 +179,30 @@ __device__ __forceinline__ uint64_t spread_pages(uint32_t m) {
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap) {
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) {
   using Cfg = TCfg<D>;
   constexpr int T = Cfg::T;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms are 1024 B
-  uint8_t* sRing = smem + Cfg::RING_OFF;
   uint8_t* sK = smem + Cfg::K_OFF;
   uint8_t* sV = smem + Cfg::V_OFF;
   uint8_t* sQ = smem + Cfg::Q_OFF;
-  int32_t* sMeta = reinterpret_cast<int32_t*>(smem + Cfg::META_OFF);
+  int64_t* sBase = reinterpret_cast<int64_t*>(smem + Cfg::BASE_OFF);
+  int32_t* sNval = reinterpret_cast<int32_t*>(smem + Cfg::NVAL_OFF);
   int32_t* sTab = reinterpret_cast<int32_t*>(smem + Cfg::TAB_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
   // Every barrier completes once per use of its buffer, so a waiter names an unambiguous phase.
-  uint64_t* bar_full = bars;                      // [NSLOTS] ring slot landed (producer arrival + bytes)
-  uint64_t* bar_empty = bars + Cfg::NSLOTS;       // [NSLOTS] ring slot read by every dequant warp
-  uint64_t* bar_k_full = bars + 2 * Cfg::NSLOTS;  // [2] K tile b written (K warps)
-  uint64_t* bar_v_full = bar_k_full + 2;          // V tile written (V warps), once per tile
-  uint64_t* bar_qk_done = bar_k_full + 3;         // [2] QK into S buffer b completed (commit)
-  uint64_t* bar_pv_done = bar_k_full + 5;         // [2] PV that read P buffer b completed (commit)
-  uint64_t* bar_p_full = bar_k_full + 7;          // [2] P buffer b written, S buffer b read (softmax warps)
-  uint64_t* bar_q_full = bar_k_full + 9;          // a segment's Q rows written (softmax warps), once per segment
-  uint64_t* bar_o_free = bar_k_full + 10;         // a segment's O read out (softmax warps), once per segment
-  uint64_t* bar_pair = bar_k_full + 11;           // [4 quarters][2 parities] both half-tile maxima written
-  uint64_t* bar_sum = bar_k_full + 19;            // [4 quarters] both half row sums written, once per segment
+  uint64_t* bar_meta = bars;                      // [kMeta] a tile's pages written
+  uint64_t* bar_meta_free = bars + kMeta;         // [kMeta] ... read by every dequant warp
+  uint64_t* bar_k_full = bars + 2 * kMeta;        // [2] K tile b written (K warps)
+  uint64_t* bar_v_full = bar_k_full + 2;          // [2] V tile b written (V warps)
+  uint64_t* bar_qk_done = bar_k_full + 4;         // [2] QK into S buffer b completed (commit)
+  uint64_t* bar_pv_done = bar_k_full + 6;         // [2] PV that read P buffer b completed (commit)
+  uint64_t* bar_p_full = bar_k_full + 8;          // [2] P buffer b written, S buffer b read (softmax warps)
+  uint64_t* bar_q_full = bar_k_full + 10;         // a segment's Q rows written (softmax warps), once per segment
+  uint64_t* bar_o_free = bar_k_full + 11;         // a segment's O read out (softmax warps), once per segment
+  uint64_t* bar_pair = bar_k_full + 14;           // [4 quarters][2 parities] both half-tile maxima written
+  uint64_t* bar_sum = bar_k_full + 22;            // [4 quarters] both half row sums written, once per segment
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -231,14 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
   }
   if (tid == 0) {
     sTab[0] = 0;
-    for (int s = 0; s < Cfg::NSLOTS; ++s) {
-      mbar_init(&bar_full[s], 1);
-      mbar_init(&bar_empty[s], kDwWarps);
+    for (int s = 0; s < kMeta; ++s) {
+      mbar_init(&bar_meta[s], 1);
+      mbar_init(&bar_meta_free[s], 2 * kDwWarps);
     }
-    mbar_init(&bar_k_full[0], kDwWarps);
-    mbar_init(&bar_k_full[1], kDwWarps);
-    mbar_init(bar_v_full, kDwWarps);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar_k_full[b], kDwWarps);
+      mbar_init(&bar_v_full[b], kDwWarps);
       mbar_init(&bar_qk_done[b], 1);
       mbar_init(&bar_pv_done[b], 1);
       mbar_init(&bar_p_full[b], kSmWarps);
@@ -285,13 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
   }
   bool ok = true;
 
-  if (warp >= kProdWarp) {
-    // ===================================================================== producers
-    // Warp 13 fills the K ring, warp 14 the V ring.  Lane pi (< PPT) owns page pi of a tile: its block-table
-    // entry (read one tile ahead), valid tokens and copies.
-    const int kv = warp - kProdWarp;
-    const int stages = kv ? Cfg::VSTAGES : Cfg::KSTAGES;
-    const int base = kv ? Cfg::KSTAGES : 0;
+  if (warp == kPlanWarp) {
+    // ===================================================================== pages of the tiles to come
+    // Lane pi (< PPT) owns page pi of a tile: its block-table entry (read one tile ahead) and valid tokens.
     auto page_entry = [&](const TreeIter<D>& ti) -> int32_t {
       if (!ti.live || lane >= Cfg::PPT) return -1;
       const int32_t pg = ti.t * Cfg::PPT + lane;
@@ -301,67 +285,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     TreeIter<D> t;
     t.first(sTab, a, G, range);
     int32_t bt = page_entry(t);
-    uint32_t n = 0;  // tiles issued
-    while (ok && t.live) {
-      int32_t phys = bt, nvalid = 0;
+    for (uint32_t n = 0; t.live; ++n) {
+      int32_t phys = bt;
       if (phys >= a.num_pages) {  // never dereferenced; reported in the status word
         set_status(my_status, kStatusBadPage);
         phys = -1;
       }
-      if (phys >= 0) nvalid = min(kPage, t.s.L - (t.t * Cfg::PPT + lane) * kPage);
-      TreeIter<D> nx = t;
-      nx.next(sTab, a, G);
-      bt = page_entry(nx);
-      const int sl = base + static_cast<int>(n % stages);
-      const uint32_t use = n / stages;
-      if (use > 0 && !warp_wait(&bar_empty[sl], (use - 1) & 1)) { ok = false; break; }
-      constexpr uint32_t kPageBytes = Cfg::NSL * kBox + (KindTraits<KIND>::kScaled ? Cfg::SC_KV : 0);
-      const uint32_t bytes = __reduce_add_sync(0xffffffffu, phys >= 0 ? kPageBytes : 0u);
-      int32_t nv[Cfg::PPT];
-#pragma unroll
-      for (int i = 0; i < Cfg::PPT; ++i) nv[i] = __shfl_sync(0xffffffffu, nvalid, i);
-      if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < Cfg::PPT; ++i) sMeta[sl * Cfg::PPT + i] = nv[i];
-        mbar_arrive_expect_tx(&bar_full[sl], bytes);  // releases the page counts with the slot
+      const int32_t nval = phys >= 0 ? min(kPage, t.s.L - (t.t * Cfg::PPT + lane) * kPage) : 0;
+      const int32_t g = t.s.g;
+      t.next(sTab, a, G);
+      bt = page_entry(t);
+      const uint32_t sl = n % kMeta;
+      if (n >= kMeta && !warp_wait(&bar_meta_free[sl], (n / kMeta - 1) & 1)) { ok = false; break; }
+      if (lane < Cfg::PPT) {
+        sBase[sl * Cfg::PPT + lane] = phys >= 0 ? static_cast<int64_t>(phys) * 2 * a.num_kv_heads + g : -1;
+        sNval[sl * Cfg::PPT + lane] = nval;
       }
       __syncwarp();
-      if (phys >= 0) {
-        uint8_t* slot = sRing + sl * Cfg::SLOT_BYTES;
-#pragma unroll
-        for (int c = 0; c < Cfg::NSL; ++c)
-          tma_load_codes(smem_u32(slot + (lane * Cfg::NSL + c) * kBox), &tmap, c, t.s.g * kPage, kv, phys,
-                         &bar_full[sl]);
-        if (KindTraits<KIND>::kScaled) {  // an unscaled pool has codes only
-          const uint8_t* src = reinterpret_cast<const uint8_t*>(a.scales) +
-                               ((static_cast<int64_t>(phys) * 2 + kv) * a.num_kv_heads + t.s.g) * Cfg::SC_KV;
-          bulk_g2s(slot + Cfg::CODE_BYTES + lane * Cfg::SC_KV, src, Cfg::SC_KV, &bar_full[sl]);
-        }
-      }
-      t = nx;
-      ++n;
+      if (lane == 0) bar_arrive(&bar_meta[sl]);
     }
-    // no copy may still be in flight when the CTA exits
-    for (uint32_t j = 1; j <= n && j <= static_cast<uint32_t>(stages); ++j) {
-      const uint32_t m = n - j;
-      (void)mbar_wait_bounded(&bar_full[base + m % stages], (m / stages) & 1);
-    }
-  } else if (warp >= kSmWarps && warp < kMmaWarp) {
+  } else if (warp >= kSmWarps && warp < kPlanWarp) {
     // ===================================================================== dequant warps
-    // Eight for K and eight for V, one copy of the code for both (with five roles on an SM, instruction-cache
-    // misses cost more than the selects).  Each pays its waits and the fence to the async proxy, some 800 clocks
-    // a tile, under the other's work.
+    // Eight for K and eight for V, one copy of the code for both (with four roles on an SM, instruction-cache
+    // misses cost more than the selects).  A warp's codes and scales come straight from the pool into registers, two
+    // tiles ahead (a staging ring would cost their bytes twice more in shared-memory bandwidth, which two bf16 tiles of K
+    // and V and the MMAs' reads of them already use), and leave as bf16 in 128-byte swizzled rows.
     const int kv = warp >= kVWarp ? 1 : 0;
-    const int dw = tid - (kv ? kVWarp : kSmWarps) * 32;
-    const int tt = dw % T;     // key of the tile (consecutive threads: consecutive keys)
-    const int part = dw / T;   // which SPAN of the row
-    const int pi = tt / kPage, off = tt % kPage;
-    const int swz = off & 7;   // 128-byte swizzle phase of this token's staging rows
-    const uint32_t toff = (tt % 8) * 16 + (tt / 8) * Cfg::RS + part * (Cfg::SPAN / 8) * 128;
+    const int wi = warp - (kv ? kVWarp : kSmWarps);
+    const int c = lane % Cfg::CPR, r0 = wi * Cfg::RPW + lane / Cfg::CPR;  // piece of a row; first row (token) of the tile
+    const int page = wi * Cfg::RPW / kPage, off0 = r0 % kPage;
+    const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
     // While the first tile is on its way, the V warps write down the sequence of each query row for the merge, the
     // CTAs taking rows in turn: the last sequence whose rows begin at or before it, -1 where that one does not reach it.
-    if (kv == 1)
-      for (int32_t i = blockIdx.x * kDwThreads + dw; i < a.total_q; i += gridDim.x * kDwThreads) {
+    auto write_row_seq = [&]() {
+      for (int32_t i = blockIdx.x * kDwThreads + wi * 32 + lane; i < a.total_q; i += gridDim.x * kDwThreads) {
         int lo = 0, hi = a.batch;  // first b with q_start[b] > i
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
@@ -371,65 +328,87 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
         const int32_t b = lo - 1;
         a.row_seq[i] = b >= 0 && i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr) ? b : -1;
       }
-    const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
-    const uint32_t stages = kv ? Cfg::VSTAGES : Cfg::KSTAGES;
-    const uint32_t bufs = kv ? 1 : Cfg::KB;
+    };
+    struct Pieces {
+      uint4 codes[4];
+      uint16_t sc[4];
+    };
+    // (what lies in unwritten or masked rows does not matter: zero codes times a zero scale)
+    auto fetch = [&](uint32_t i, Pieces& p) -> bool {
+      const uint32_t sl = i % kMeta;
+      if (!warp_wait(&bar_meta[sl], (i / kMeta) & 1)) return false;
+      const int64_t base = sBase[sl * Cfg::PPT + page];
+      const int32_t nval = sNval[sl * Cfg::PPT + page];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bar_meta_free[sl]);
+      const int64_t row = (base + (kv ? a.num_kv_heads : 0)) * kPage + off0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p.codes[j] = make_uint4(0u, 0u, 0u, 0u);
+        p.sc[j] = 0;
+        if (off0 + j * Cfg::RPI < nval) {
+          p.codes[j] = ldg_stream(a.codes + (row + j * Cfg::RPI) * D + c * 16);
+          if (KindTraits<KIND>::kScaled) p.sc[j] = __ldg(a.scales + (row + j * Cfg::RPI) * Cfg::NB + c / 2);
+        }
+      }
+      return true;
+    };
     uint64_t* done = kv ? bar_pv_done : bar_qk_done;
-    uint32_t ring = kv ? Cfg::KSTAGES : 0, ring_phase = 0;
-    for (uint32_t i = 0; i < total; ++i) {
-      if (!warp_wait(&bar_full[ring], ring_phase)) { ok = false; break; }
-      const uint8_t* slot = sRing + ring * Cfg::SLOT_BYTES;
-      const bool v_ok = off < sMeta[ring * Cfg::PPT + pi];
-      // the tile was last read by the QK (PV) of the tile `bufs` before
-      if (i >= bufs && !warp_wait(&done[(i - bufs) & 1], ((i - bufs) >> 1) & 1)) { ok = false; break; }
-      const uint8_t* rows = slot + pi * Cfg::NSL * kBox + off * 128;
-      uint32_t sc = 0u;  // (zero codes times a zero scale: what lies in unwritten or masked rows does not matter)
-      if (KindTraits<KIND>::kScaled && v_ok)
-        sc = *reinterpret_cast<const uint32_t*>(slot + Cfg::CODE_BYTES + pi * Cfg::SC_KV +
-                                                (off * Cfg::NB + part * Cfg::NBT) * 2);
-      uint8_t* dst = (kv ? sV : sK + (i % Cfg::KB) * Cfg::KV_TILE) + toff;
-#pragma unroll 2
-      for (int k = 0; k < Cfg::NCH; ++k) {
-        const int c = part * Cfg::NCH + k;  // 16-code chunk along the row
-        uint4 codes = make_uint4(0u, 0u, 0u, 0u);
-        if (v_ok) codes = *reinterpret_cast<const uint4*>(rows + (c / 8) * kBox + (((c % 8) ^ swz) * 16));
+    uint64_t* full = kv ? bar_v_full : bar_k_full;
+    // 64-column chunk of this lane's piece, and its two 16-byte halves there: odd chunks store the second half first,
+    // so that eight lanes' stores fall into eight different banks
+    uint8_t* tiles = (kv ? sV : sK) + (c / 4) * Cfg::CHUNK + r0 * 128;
+    const int flip = (c / 4) & 1, h0 = 2 * (c % 4) + flip, h1 = h0 ^ 1;
+    // tile i out of its registers, which then take tile i + 2
+    auto step = [&](uint32_t i, Pieces& p) -> bool {
+      // the buffer was last read by the QK (PV) two tiles back
+      if (i >= 2 && !warp_wait(&done[i & 1], ((i >> 1) - 1) & 1)) return false;
+      uint8_t* dst = tiles + (i & 1) * Cfg::KV_TILE;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
         uint32_t w[8];
-        dequant16<KIND>(codes, static_cast<uint16_t>(sc >> (16 * (k >> 1))), w);
-        *reinterpret_cast<uint4*>(dst + 2 * k * 128) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dst + (2 * k + 1) * 128) = make_uint4(w[4], w[5], w[6], w[7]);
+        dequant16<KIND>(p.codes[j], p.sc[j], w);
+        const int swz = (r0 + j * Cfg::RPI) & 7;
+        uint8_t* d = dst + j * Cfg::RPI * 128;
+        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(d + ((h0 ^ swz) * 16)) = flip ? hi : lo;
+        *reinterpret_cast<uint4*>(d + ((h1 ^ swz) * 16)) = flip ? lo : hi;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        bar_arrive(kv ? bar_v_full : &bar_k_full[i % Cfg::KB]);
-        bar_arrive(&bar_empty[ring]);
-      }
-      if (++ring == (kv ? Cfg::KSTAGES : 0) + stages) {
-        ring = kv ? Cfg::KSTAGES : 0;
-        ring_phase ^= 1;
-      }
+      if (lane == 0) bar_arrive(&full[i & 1]);
+      return i + 2 >= total || fetch(i + 2, p);
+    };
+    Pieces even, odd;
+    ok = (total < 1 || fetch(0, even)) && (total < 2 || fetch(1, odd));
+    if (kv == 1) write_row_seq();
+    for (uint32_t i = 0; ok && i < total; i += 2) {
+      ok = step(i, even);
+      if (ok && i + 1 < total) ok = step(i + 1, odd);
     }
   } else if (warp == kMmaWarp) {
     // ===================================================================== MMA issue (elected lane)
     const uint32_t idesc_qk = x_idesc(T, false);
     const uint32_t idesc_pv = x_idesc(D, true);
-    // descriptors of the first K-step; later steps add their byte offset >> 4 to the address field
+    // Q: the no-swizzle core-matrix layout, a k-step is 256 bytes.  K: K-major with the 128-byte swizzle, a k-step is 32
+    // bytes along a 64-column chunk.  V: MN-major with the same swizzle, a k-step is 16 rows of 128 bytes.
     const uint64_t dQ = smem_desc(smem_u32(sQ), 128, Cfg::RS);
-    const uint64_t dK = smem_desc(smem_u32(sK), 128, Cfg::RS);
-    const uint64_t dV = smem_desc(smem_u32(sV), Cfg::RS, 128);
+    const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
+    const uint64_t dV = sw128_desc(smem_u32(sV), Cfg::CHUNK, 1024);
     const uint32_t tS = tmem + Cfg::S_COL, tO = tmem, tP = tmem + Cfg::P_COL;
     uint32_t n = 0, items = 0;  // tiles QK'd; items finished
     // PV of tile m; the first tile of an item overwrites O, once the previous item's O has been read out
     auto pv = [&](uint32_t m, bool first) -> bool {
       const int bp = m & 1;
-      if (!warp_wait(bar_v_full, m & 1)) return false;
+      if (!warp_wait(&bar_v_full[bp], (m >> 1) & 1)) return false;
       if (!warp_wait(&bar_p_full[bp], (m >> 1) & 1)) return false;
       if (first && items >= 1 && !warp_wait(bar_o_free, (items - 1) & 1)) return false;
       tc_fence_after();
+      const uint64_t v = dV + bp * static_cast<uint64_t>(Cfg::KV_TILE >> 4);
       if constexpr (T == 128)
-        mma8_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, dV, static_cast<uint64_t>((2 * Cfg::RS) >> 4), idesc_pv, first ? 0u : 1u);
+        mma8_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, v, (16 * 128) >> 4, idesc_pv, first ? 0u : 1u);
       else
-        mma4_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, dV, static_cast<uint64_t>((2 * Cfg::RS) >> 4), idesc_pv, first ? 0u : 1u);
+        mma4_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, v, (16 * 128) >> 4, idesc_pv, first ? 0u : 1u);
       mma_commit(&bar_pv_done[bp]);
       __syncwarp();
       return true;
@@ -440,15 +419,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
       if (!warp_wait(bar_q_full, items & 1)) { ok = false; break; }
       for (int32_t i = 0; i < ntiles; ++i, ++n) {
         const int b = n & 1;
-        const uint32_t kb = n % Cfg::KB;
-        if (!warp_wait(&bar_k_full[kb], (n / Cfg::KB) & 1)) { ok = false; break; }
+        if (!warp_wait(&bar_k_full[b], (n >> 1) & 1)) { ok = false; break; }
         // S buffer b was read by the softmax of tile n - 2
         if (n >= 2 && !warp_wait(&bar_p_full[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
-        for (int k8 = 0; k8 < D / 128; ++k8)
-          mma8_bf16(tS + b * T, dQ + static_cast<uint64_t>((k8 * 8 * 256) >> 4), 256 >> 4,
-                    dK + kb * static_cast<uint64_t>(Cfg::KV_TILE >> 4) + static_cast<uint64_t>((k8 * 8 * 256) >> 4), 256 >> 4, idesc_qk, k8 > 0 ? 1u : 0u);
+        for (int q = 0; q < D / 64; ++q)
+          mma4_bf16(tS + b * T, dQ + static_cast<uint64_t>((q * 4 * 256) >> 4), 256 >> 4,
+                    dK + b * static_cast<uint64_t>(Cfg::KV_TILE >> 4) + static_cast<uint64_t>((q * Cfg::CHUNK) >> 4), 32 >> 4,
+                    idesc_qk, q > 0 ? 1u : 0u);
         mma_commit(&bar_qk_done[b]);
         __syncwarp();
         if (i > 0 && !pv(n - 1, i == 1)) { ok = false; break; }
@@ -552,17 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
         // pass 1: the row's max over this half (sm_scale > 0: scaling commutes with it)
-        float mh[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mh = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < T / 64; ++h) {
-          uint32_t v[32];
-          tmem_ld32(tS + b * T + h * 32, v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mh[e & 3] = fmaxf(mh[e & 3], __uint_as_float(v[e]));
+          uint32_t v[32], top;
+          tmem_ld32_max_issue(tS + b * T + h * 32, v, top);
+          tmem_wait_max(top);
+          mh = fmaxf(mh, __uint_as_float(top));
         }
         // the row's max over the whole tile: exchange halves with the other warp of the lane quarter
         // (double-buffered by tile parity, so one barrier per tile suffices)
-        sRed[(b * 2 + hf) * kM + r] = fmaxf(fmaxf(mh[0], mh[1]), fmaxf(mh[2], mh[3]));
+        sRed[(b * 2 + hf) * kM + r] = mh;
         if (!pair_meet(&bar_pair[quarter * 2 + b], (pair_phase >> b) & 1u)) { ok = false; break; }
         pair_phase ^= 1u << b;
         float mx = fmaxf(sRed[(b * 2) * kM + r], sRed[(b * 2 + 1) * kM + r]);
@@ -596,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
         // pass 2: P = 2^(s * scale - m) of this half as bf16 into tensor memory; the row sum in fp32.  (A row without
         // a visible key so far has only scores of -inf: any finite m gives zeros.)
         const float m_fin = m_used == -INFINITY ? 0.0f : m_used;
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 sc2 = make_float2(a.score_scale, a.score_scale), m2 = make_float2(-m_fin, -m_fin);
+        float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
         for (int h = 0; h < T / 64; ++h) {
           uint32_t v[32];
@@ -604,15 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), a.score_scale, -m_fin));
-            const float p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), a.score_scale, -m_fin));
-            ls[(2 * e) & 3] += p0;
-            ls[(2 * e + 1) & 3] += p1;
-            w[e] = pack_bf16x2(p0, p1);
+            const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, m2);
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            ls[e & 1] = fadd2(ls[e & 1], p);
+            w[e] = pack_bf16x2(p.x, p.y);
           }
           tmem_st16u(tP + b * (T / 2) + h * 16, w);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -817,9 +796,7 @@ kvq_status launch_tree_d(const TreeArgs& a, cudaStream_t stream) {
   if (kern == nullptr) return KVQ_EKIND;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess)
     return KVQ_ECUDA;
-  CUtensorMap map;
-  if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
-  kern<<<static_cast<unsigned>(a.grid), kThreads, Cfg::SMEM_BYTES, stream>>>(a, map);
+  kern<<<static_cast<unsigned>(a.grid), kThreads, Cfg::SMEM_BYTES, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
   // Few rows: a CTA for each (their blocks are cut into many segments); else a warp for each (64 rows 5.7 us, 9600
   // rows 23 us with a CTA each).
