@@ -131,6 +131,10 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // 16 bytes that are read once: no line is kept in L1.
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
   uint4 v;
@@ -178,6 +182,16 @@ __device__ __forceinline__ void mma4_bf16_tmem_a(uint32_t d_tmem, uint32_t a, ui
 // while another gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+// The same with everything behind the first try out of line: where several roles share an SM's instruction cache,
+// each wait's unlikely part costs the others misses (prompt 16384 x 32 heads 1455 -> 1405 us, tree at head_dim 128
+// 139 -> 132 us; the tree kernel at 256, whose registers spill around the call, keeps the other: 180 against 256 us).
+__device__ __noinline__ bool mbar_wait_rest(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+
+__device__ __forceinline__ bool warp_wait_far(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_rest(bar, parity));
 }
 
 }  // namespace

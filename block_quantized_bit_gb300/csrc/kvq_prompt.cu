@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
 
   // the item in slot k & 1 (k-th of this CTA), for a consumer warp
   auto take_item = [&](uint32_t k, Item& it) -> bool {
-    if (!warp_wait(&bar_item[k & 1], (k >> 1) & 1)) return false;
+    if (!warp_wait_far(&bar_item[k & 1], (k >> 1) & 1)) return false;
     it = sItem[k & 1];
     __syncwarp();
     if (lane == 0) bar_arrive(&bar_item_free[k & 1]);
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
     uint32_t nq[2] = {0, 0};
     while (ok) {
       const Item it = source.get(idx);
-      if (k >= 2 && !warp_wait(&bar_item_free[k & 1], ((k >> 1) - 1) & 1)) { ok = false; break; }
+      if (k >= 2 && !warp_wait_far(&bar_item_free[k & 1], ((k >> 1) - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
         sItem[k & 1] = it;
         bar_arrive(&bar_item[k & 1]);
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(a.counter, 1u);
       // Q tiles, once the previous item's QKs have read theirs
-      if (k >= 1 && !warp_wait(bar_q_empty, (k - 1) & 1)) { ok = false; break; }
+      if (k >= 1 && !warp_wait_far(bar_q_empty, (k - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
       const int32_t n = max(it.blk[0], it.blk[1]) + 1;
       for (int32_t j = 0; j < n; ++j, ++kv) {
         const int s = kv % STAGES;
-        if (kv >= STAGES && !warp_wait(&bar_empty[s], (kv / STAGES - 1) & 1)) { ok = false; break; }
+        if (kv >= STAGES && !warp_wait_far(&bar_empty[s], (kv / STAGES - 1) & 1)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_full[s], 2 * Cfg::TILE);
           uint8_t* dst = sKV + s * 2 * Cfg::TILE;
@@ -241,15 +241,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
     Item it;
     auto qk = [&](int w, uint32_t stage) -> bool {
       // P of the tile's last PV lies in the columns that this QK writes
-      if (nt[w] > 0 && !warp_wait(&bar_pv_done[w], (nt[w] - 1) & 1)) return false;
+      if (nt[w] > 0 && !warp_wait_far(&bar_pv_done[w], (nt[w] - 1) & 1)) return false;
       tc_fence_after();
       mma_chunks<Cfg::CH>(tmem + Cfg::S_COL + w * kM, dq + ((w * Cfg::TILE) >> 4), dk0 + stage * kStageStep, idesc_qk);
       mma_commit(&bar_s_full[w]);
       return true;
     };
     auto pv = [&](int w, uint32_t stage, bool first) -> bool {
-      if (first && ni[w] > 1 && !warp_wait(&bar_o_free[w], (ni[w] - 2) & 1)) return false;
-      if (!warp_wait(&bar_p_full[w], nt[w] & 1)) return false;
+      if (first && ni[w] > 1 && !warp_wait_far(&bar_o_free[w], (ni[w] - 2) & 1)) return false;
+      if (!warp_wait_far(&bar_p_full[w], nt[w] & 1)) return false;
       tc_fence_after();
       // a k-step is 16 keys: 8 columns of P, 16 rows of V
       mma8_bf16_tmem_a(tmem + Cfg::O_COL + w * kM, tmem + Cfg::S_COL + w * kM, 8u, dv0 + stage * kStageStep,
@@ -262,14 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
       if (!take_item(k, it)) { ok = false; break; }
       if (!it.live) break;
       const int32_t nA = it.blk[0] + 1, nB = it.blk[1] + 1, n = max(nA, nB);
-      if (nA > 0 && !warp_wait(&bar_q_full[0], ni[0]++ & 1)) { ok = false; break; }
-      if (nB > 0 && !warp_wait(&bar_q_full[1], ni[1]++ & 1)) { ok = false; break; }
+      if (nA > 0 && !warp_wait_far(&bar_q_full[0], ni[0]++ & 1)) { ok = false; break; }
+      if (nB > 0 && !warp_wait_far(&bar_q_full[1], ni[1]++ & 1)) { ok = false; break; }
       uint32_t stage = 0, before = 0;
       for (int32_t j = 0; j <= n; ++j) {
         before = stage;
         if (j < n) {
           stage = kv % STAGES;
-          if (!warp_wait(&bar_full[stage], (kv / STAGES) & 1)) { ok = false; break; }
+          if (!warp_wait_far(&bar_full[stage], (kv / STAGES) & 1)) { ok = false; break; }
           ++kv;
           const int32_t from = it.len - j * kM;
           if (from < kM) {  // the V rows of keys behind the sequence's end
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
         l2.y *= alpha;
       };
       for (int32_t j = 0; j < n; ++j, ++nt) {
-        if (!warp_wait(&bar_s_full[w], nt & 1)) { ok = false; break; }
+        if (!warp_wait_far(&bar_s_full[w], nt & 1)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[kM];
         float top;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
       }
       if (!ok) break;
       // O / l of this row, once the item's last PV has completed
-      if (!warp_wait(&bar_pv_done[w], (nt - 1) & 1)) { ok = false; break; }
+      if (!warp_wait_far(&bar_pv_done[w], (nt - 1) & 1)) { ok = false; break; }
       tc_fence_after();
       const float inv = 1.0f / (l2.x + l2.y);
       const int32_t tok = it.blk[w] * kM + r;

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
 
   // the item in slot k & 1 (k-th of this CTA), for a consumer warp
   auto take_item = [&](uint32_t k, Item& it) -> bool {
-    if (!warp_wait(&bar_item[k & 1], (k >> 1) & 1)) return false;
+    if (!warp_wait_far(&bar_item[k & 1], (k >> 1) & 1)) return false;
     it = sItem[k & 1];
     __syncwarp();
     if (lane == 0) bar_arrive(&bar_item_free[k & 1]);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
     int64_t idx = blockIdx.x;
     while (ok) {
       const Item it = source.get(idx);
-      if (k >= 2 && !warp_wait(&bar_item_free[k & 1], ((k >> 1) - 1) & 1)) { ok = false; break; }
+      if (k >= 2 && !warp_wait_far(&bar_item_free[k & 1], ((k >> 1) - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
         sItem[k & 1] = it;
         bar_arrive(&bar_item[k & 1]);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(a.counter, 1u);
       // the Q tile, once the previous item's QKs have read theirs
-      if (k >= 1 && !warp_wait(bar_q_empty, (k - 1) & 1)) { ok = false; break; }
+      if (k >= 1 && !warp_wait_far(bar_q_empty, (k - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
         mbar_arrive_expect_tx(bar_q_full, kQTile);
 #pragma unroll
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
       const int32_t n = key_tiles(it);
       for (int32_t i = 0; i < 2 * n; ++i, ++kv) {  // K of key tile i / 2, then its V
         const int s = kv % kSlots;
-        if (kv >= kSlots && !warp_wait(&bar_empty[s], (kv / kSlots - 1) & 1)) { ok = false; break; }
+        if (kv >= kSlots && !warp_wait_far(&bar_empty[s], (kv / kSlots - 1) & 1)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_full[s], kKvTile);
 #pragma unroll
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
       if (!take_item(k, it)) { ok = false; break; }
       if (!it.live) break;
       const int32_t n = key_tiles(it);
-      if (!warp_wait(bar_q_full, k & 1)) { ok = false; break; }
-      auto landed = [&](uint32_t u) -> bool { return warp_wait(&bar_full[u % kSlots], (u / kSlots) & 1); };
+      if (!warp_wait_far(bar_q_full, k & 1)) { ok = false; break; }
+      auto landed = [&](uint32_t u) -> bool { return warp_wait_far(&bar_full[u % kSlots], (u / kSlots) & 1); };
       // QK of key tile j.  Its S buffer was read by the softmax two tiles back, whose P the PV issued last has waited for.
       auto qk = [&](int32_t j) -> bool {
         const uint32_t u = kv + 2 * j;
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (j == 0 && k > 0 && !warp_wait(bar_o_free, (k - 1) & 1)) { ok = false; break; }
-        if (!warp_wait(&bar_p_full[npv & 1], (npv >> 1) & 1)) { ok = false; break; }
+        if (j == 0 && k > 0 && !warp_wait_far(bar_o_free, (k - 1) & 1)) { ok = false; break; }
+        if (!warp_wait_far(&bar_p_full[npv & 1], (npv >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         mma_pv(tmem + kOCol, tmem + kPCol + (npv & 1) * (kKeys / 2),
                dv0 + static_cast<uint64_t>((u % kSlots) * (kKvTile >> 4)), idesc_pv, j > 0 ? 1u : 0u);
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
       for (int32_t j = 0; j < n; ++j, ++nt) {
         const uint32_t b = nt & 1;
         const uint32_t tS = tmem + kSCol + b * kKeys + lane_base, tP = tmem + kPCol + b * (kKeys / 2) + lane_base;
-        if (!warp_wait(&bar_s_full[b], (nt >> 1) & 1)) { ok = false; break; }
+        if (!warp_wait_far(&bar_s_full[b], (nt >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[kKeys];
         tmem_ld32_issue(tS, s);
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
             const float alpha = moved ? ex2(m - top) : 1.0f;
             m = moved ? top : m;
             // O must hold the PV of the tile before
-            if (!warp_wait(&bar_pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1)) { ok = false; break; }
+            if (!warp_wait_far(&bar_pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kD / 16; ++c) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
           pw[e] = pack_bf16x2(p.x, p.y);
         }
         // the P buffer was last read by the PV two tiles back
-        if (nt >= 2 && !warp_wait(&bar_pv_done[b], ((nt >> 1) - 1) & 1)) { ok = false; break; }
+        if (nt >= 2 && !warp_wait_far(&bar_pv_done[b], ((nt >> 1) - 1) & 1)) { ok = false; break; }
         tc_fence_after();
         tmem_st32(tP, pw);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
       }
       if (!ok) break;
       // O / l of this row, once the item's last PV has completed
-      if (!warp_wait(&bar_pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1)) { ok = false; break; }
+      if (!warp_wait_far(&bar_pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       const float inv = 1.0f / (l2.x + l2.y);
       const int64_t orow = static_cast<int64_t>(it.q0 + tok) * a.out_token + static_cast<int64_t>(it.head[0]) * a.out_head;

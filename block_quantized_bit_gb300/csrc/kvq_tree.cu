@@ -170,6 +170,12 @@ struct TreeIter {
   }
 };
 
+template <int D>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  if constexpr (D == 128) return warp_wait_far(bar, parity);
+  else return warp_wait(bar, parity);
+}
+
 // 16 ones for each set bit of a 4-bit page mask.
 __device__ __forceinline__ uint64_t spread_pages(uint32_t m) {
   uint64_t v = 0;
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
       t.next(sTab, a, G);
       bt = page_entry(t);
       const uint32_t sl = n % kMeta;
-      if (n >= kMeta && !warp_wait(&bar_meta_free[sl], (n / kMeta - 1) & 1)) { ok = false; break; }
+      if (n >= kMeta && !wait<D>(&bar_meta_free[sl], (n / kMeta - 1) & 1)) { ok = false; break; }
       if (lane < Cfg::PPT) {
         sBase[sl * Cfg::PPT + lane] = phys >= 0 ? static_cast<int64_t>(phys) * 2 * a.num_kv_heads + g : -1;
         sNval[sl * Cfg::PPT + lane] = nval;
@@ -312,7 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     // and V and the MMAs' reads of them already use), and leave as bf16 in 128-byte swizzled rows.
     const int kv = warp >= kVWarp ? 1 : 0;
     const int wi = warp - (kv ? kVWarp : kSmWarps);
-    const int c = lane % Cfg::CPR, r0 = wi * Cfg::RPW + lane / Cfg::CPR;  // piece of a row; first row (token) of the tile
+    // piece c of a row and first row (token) of the tile: four lanes take neighbouring pieces, the next four the same
+    // pieces of the next row, whose swizzle differs in the lowest bit; so eight lanes' stores fall into eight banks
+    const int c = (lane & 3) | ((lane >> 3) % (Cfg::CPR / 4)) << 2;
+    const int r0 = wi * Cfg::RPW + ((lane >> 2) & 1) + 2 * (lane / (2 * Cfg::CPR));
     const int page = wi * Cfg::RPW / kPage, off0 = r0 % kPage;
     const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
     // While the first tile is on its way, the V warps write down the sequence of each query row for the merge, the
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     // (what lies in unwritten or masked rows does not matter: zero codes times a zero scale)
     auto fetch = [&](uint32_t i, Pieces& p) -> bool {
       const uint32_t sl = i % kMeta;
-      if (!warp_wait(&bar_meta[sl], (i / kMeta) & 1)) return false;
+      if (!wait<D>(&bar_meta[sl], (i / kMeta) & 1)) return false;
       const int64_t base = sBase[sl * Cfg::PPT + page];
       const int32_t nval = sNval[sl * Cfg::PPT + page];
       __syncwarp();
@@ -355,24 +364,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     };
     uint64_t* done = kv ? bar_pv_done : bar_qk_done;
     uint64_t* full = kv ? bar_v_full : bar_k_full;
-    // 64-column chunk of this lane's piece, and its two 16-byte halves there: odd chunks store the second half first,
-    // so that eight lanes' stores fall into eight different banks
-    uint8_t* tiles = (kv ? sV : sK) + (c / 4) * Cfg::CHUNK + r0 * 128;
-    const int flip = (c / 4) & 1, h0 = 2 * (c % 4) + flip, h1 = h0 ^ 1;
+    // where this lane's first piece goes in a tile: its 64-column chunk, its row, its two 16-byte halves swizzled
+    // by the row; rows 8 apart share the swizzle, so later pieces are a constant xor and sum away
+    const uint32_t at = smem_u32(kv ? sV : sK) + (c / 4) * Cfg::CHUNK + r0 * 128 + (((2 * (c % 4)) ^ (r0 & 7)) * 16);
     // tile i out of its registers, which then take tile i + 2
     auto step = [&](uint32_t i, Pieces& p) -> bool {
       // the buffer was last read by the QK (PV) two tiles back
-      if (i >= 2 && !warp_wait(&done[i & 1], ((i >> 1) - 1) & 1)) return false;
-      uint8_t* dst = tiles + (i & 1) * Cfg::KV_TILE;
+      if (i >= 2 && !wait<D>(&done[i & 1], ((i >> 1) - 1) & 1)) return false;
+      const uint32_t dst = at + (i & 1) * Cfg::KV_TILE;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t w[8];
         dequant16<KIND>(p.codes[j], p.sc[j], w);
-        const int swz = (r0 + j * Cfg::RPI) & 7;
-        uint8_t* d = dst + j * Cfg::RPI * 128;
-        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
-        *reinterpret_cast<uint4*>(d + ((h0 ^ swz) * 16)) = flip ? hi : lo;
-        *reinterpret_cast<uint4*>(d + ((h1 ^ swz) * 16)) = flip ? lo : hi;
+        const uint32_t d = (dst ^ ((j * Cfg::RPI & 7) * 16)) + j * Cfg::RPI * 128;
+        sts16(d, w[0], w[1], w[2], w[3]);
+        sts16(d ^ 16, w[4], w[5], w[6], w[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -400,9 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     // PV of tile m; the first tile of an item overwrites O, once the previous item's O has been read out
     auto pv = [&](uint32_t m, bool first) -> bool {
       const int bp = m & 1;
-      if (!warp_wait(&bar_v_full[bp], (m >> 1) & 1)) return false;
-      if (!warp_wait(&bar_p_full[bp], (m >> 1) & 1)) return false;
-      if (first && items >= 1 && !warp_wait(bar_o_free, (items - 1) & 1)) return false;
+      if (!wait<D>(&bar_v_full[bp], (m >> 1) & 1)) return false;
+      if (!wait<D>(&bar_p_full[bp], (m >> 1) & 1)) return false;
+      if (first && items >= 1 && !wait<D>(bar_o_free, (items - 1) & 1)) return false;
       tc_fence_after();
       const uint64_t v = dV + bp * static_cast<uint64_t>(Cfg::KV_TILE >> 4);
       if constexpr (T == 128)
@@ -416,12 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     TreeIter<D> t;
     for (t.first(sTab, a, G, range); ok && t.live; t.next_segment(sTab, a, G)) {
       const int32_t ntiles = t.s.t1 - t.s.t0;
-      if (!warp_wait(bar_q_full, items & 1)) { ok = false; break; }
+      if (!wait<D>(bar_q_full, items & 1)) { ok = false; break; }
       for (int32_t i = 0; i < ntiles; ++i, ++n) {
         const int b = n & 1;
-        if (!warp_wait(&bar_k_full[b], (n >> 1) & 1)) { ok = false; break; }
+        if (!wait<D>(&bar_k_full[b], (n >> 1) & 1)) { ok = false; break; }
         // S buffer b was read by the softmax of tile n - 2
-        if (n >= 2 && !warp_wait(&bar_p_full[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
+        if (n >= 2 && !wait<D>(&bar_p_full[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
         for (int q = 0; q < D / 64; ++q)
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     auto pair_meet = [&](uint64_t* bar, uint32_t parity) -> bool {
       __syncwarp();
       if (lane == 0) bar_arrive(bar);
-      return warp_wait(bar, parity);
+      return wait<D>(bar, parity);
     };
     // tiles processed; segments; row sums exchanged and phases of the maxima's barriers (both only of segments in
     // which this lane quarter holds rows)
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
       for (int32_t t = s.t0; t < s.t1; ++t, ++n) {
         const int b = n & 1;
         if (!active) {  // only keep the count of the tile's barrier
-          if (!warp_wait(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
+          if (!wait<D>(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
           if (lane == 0) bar_arrive(&bar_p_full[b]);
           continue;
         }
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
         }
         constexpr uint64_t kAll = T / 2 == 64 ? ~0ull : (1ull << (T / 2)) - 1ull;
         vis = row_ok ? vis & kAll : kAll;  // (rows past the block's are zeros that nobody reads)
-        if (!warp_wait(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
+        if (!wait<D>(&bar_qk_done[b], (n >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         // Keys that some row of the warp does not see: their scores become -inf in tensor memory first, so that the
         // passes below need one variant only.
@@ -556,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
           m_used = mx;
         }
         // P buffer b is free once the PV two tiles back has read it
-        if (n >= 2 && !warp_wait(&bar_pv_done[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
+        if (n >= 2 && !wait<D>(&bar_pv_done[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
         if (__any_sync(0xffffffffu, resc)) {  // (only from the second tile of an item on)
           // O must hold the PV of the previous tile before it is scaled; this warp scales its half of O
-          if (!warp_wait(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
+          if (!wait<D>(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
         const float lt = sum[r] + sum[kM + r];
         // this warp's half of O, once the segment's last PV has completed: normalised into the output when the
         // segment is the whole block, else as a partial
-        if (!warp_wait(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
+        if (!wait<D>(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         const bool whole = s.slot < 0;
         const float scale = whole ? (lt > 0.0f ? 1.0f / lt : 0.0f) : 1.0f;
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
             }
           }
         }
-      } else if (!warp_wait(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) {
+      } else if (!wait<D>(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) {
         // (that PV was issued after o_free of the segment before had completed: no arrival below can be
         // counted for that one)
         ok = false;
