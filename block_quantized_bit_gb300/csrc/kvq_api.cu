@@ -356,7 +356,8 @@ bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int64_t G = num_q_heads / L.num_kv_heads;
   // units (tiles of at least 64 keys, for blocks of 128 rows) and merge CTAs are counted in 32 bits
-  const double units = (static_cast<double>(total_q) * G / 128 + batch) * L.num_kv_heads *
+  // (for any q_start, consistent or not: at most 64 * kMaxMaskWords drafted tokens a sequence)
+  const double units = static_cast<double>(batch) * (64.0 * kMaxMaskWords * G / 128 + 1) * L.num_kv_heads *
                        (static_cast<double>(max_pages) * L.page_size / 64 + 1);
   const bool flash_ok = tree_tc_supported(L.head_dim, L.v_dim, L.mla, batch) && units < 2.0e9 &&
                         static_cast<double>(total_q) * num_q_heads < 2.0e9;

@@ -138,6 +138,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(PagesArgs a) {
     earlier = __syncthreads_or(earlier);
   }
   ok = ok && !dup;
+  if (!FORK && ok && new_len > old_len && old_len % a.page_size != 0) {
+    // the new tokens' first rows would go into a page that another row reads
+    const int32_t p = a.block_table[static_cast<int64_t>(d) * a.max_pages + old_len / a.page_size];
+    ok = !(p >= 0 && p < a.num_pages && a.page_refs[p] > 1);
+  }
   const int32_t used_new = ok ? pages_of(new_len, a.page_size) : 0;
   const int32_t used_old = ok ? pages_of(old_len, a.page_size) : 0;
   const int32_t* row = a.block_table + static_cast<int64_t>(ok ? s : 0) * a.max_pages;
@@ -145,11 +150,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(PagesArgs a) {
     int32_t need = max(used_new - used_old, 0), tail = -1;
     if (FORK) {
       // the partly filled last page of the parent goes on with one row: the parent's own, or where that is
-      // replaced the first child in the list; every other child gets a copy
+      // replaced the first child in the list; every other child gets a copy, and so does that one when a row
+      // besides the parent holds the page (a row cut back into a page that it had shared when it was full)
       need = 0;
       if (ok && new_len % a.page_size != 0) {
         tail = row[used_new - 1];
-        need = tail >= 0 && tail < a.num_pages && (!gone || earlier);
+        need = tail >= 0 && tail < a.num_pages && (!gone || earlier || a.page_refs[tail] > 1);
       }
     }
     PagesEntry e;

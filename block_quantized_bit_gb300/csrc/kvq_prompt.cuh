@@ -62,9 +62,11 @@ struct ItemSource {
   }
   // items of levels > p
   __device__ __forceinline__ int64_t above(int32_t p) const {
-    int32_t s = 0;
+    int64_t s = 0;
     for (int32_t b = threadIdx.x & 31; b < a.batch; b += 32) s += max(tab[b] - p - 1, 0);
-    return static_cast<int64_t>(__reduce_add_sync(0xffffffffu, s)) * a.num_kv_heads;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s * a.num_kv_heads;
   }
   __device__ __forceinline__ Item get(int64_t idx) const {
     Item it;
@@ -78,9 +80,10 @@ struct ItemSource {
       if (above(mid) <= idx) hi = mid;
       else lo = mid + 1;
     }
-    const int32_t p = lo, q = static_cast<int32_t>(idx - above(p));
-    int32_t rank = q / a.num_kv_heads, b = 0;
-    it.g = q - rank * a.num_kv_heads;
+    const int32_t p = lo;
+    const int64_t q = idx - above(p);  // below batch * kv heads
+    int32_t rank = static_cast<int32_t>(q / a.num_kv_heads), b = 0;
+    it.g = static_cast<int32_t>(q - static_cast<int64_t>(rank) * a.num_kv_heads);
     for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {  // the rank-th sequence with more than p items
       const uint32_t m = __ballot_sync(0xffffffffu, b0 + lane < a.batch && tab[b0 + lane] > p);
       const int32_t c = __popc(m);

@@ -432,8 +432,9 @@ kvq_status kvq_pages_copy(void* pool, void* scales, const int32_t* src, const in
  * child shares the parent's full pages.  A partly filled last page goes on with one row: the parent's, or, where
  * the parent's row is itself among dst, the first child in the list; every other child gets a free page, and
  * (copy_src[i], copy_dst[i]) (device, [n]) name the copy that kvq_pages_copy must then make in each layer; they
- * are -1 where no copy is due.  A masked (-1) last page stays masked.  Entries of row dst[i] behind its last page
- * become -1, and seq_lens[dst[i]] the parent's length.
+ * are -1 where no copy is due.  (A page that a row besides the parent holds too never goes on: the child gets a
+ * copy.  So a fork of a row onto itself gives it a last page of its own.)  A masked (-1) last page stays masked.
+ * Entries of row dst[i] behind its last page become -1, and seq_lens[dst[i]] the parent's length.
  */
 kvq_status kvq_pages_fork(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,
                           int32_t* page_refs, const int32_t* src, const int32_t* dst, int32_t n, int32_t* copy_src,
@@ -442,7 +443,9 @@ kvq_status kvq_pages_fork(int32_t* block_table, int32_t max_pages_per_seq, int32
 /*
  * Row seqs[i] gets room for new_lens[i] tokens: missing pages are taken, surplus pages released and their
  * entries set to -1; seq_lens[seqs[i]] = new_lens[i].  A new length of 0 frees the row.  The pages taken hold
- * whatever they held before; store the new tokens before an attention reads them.
+ * whatever they held before; store the new tokens before an attention reads them.  A row that grows while
+ * another row holds its partly filled last page (it was cut back into a page shared when full) is a bad entry:
+ * fork the row onto itself first.
  */
 kvq_status kvq_pages_resize(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,
                             int32_t* page_refs, const int32_t* seqs, const int32_t* new_lens, int32_t n,

@@ -29,9 +29,9 @@ class Model:
             row = np.full(self.table.shape[1], -1, self.table.dtype)
             u = pages(lens[s])
             row[:u] = table[s][:u]
-            keeps = s in dst and s not in src[:i]
             a = b = -1
-            if lens[s] % PAGE and 0 <= row[u - 1] < len(self.refs) and not keeps:
+            if lens[s] % PAGE and 0 <= row[u - 1] < len(self.refs) and not (
+                    s in dst and s not in src[:i] and self.refs[row[u - 1]] == 1):
                 if not free:
                     return None
                 a, b = int(row[u - 1]), free.pop(0)

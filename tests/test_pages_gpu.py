@@ -187,6 +187,36 @@ def test_too_few_free_pages_and_bad_lists_change_nothing():
     assert kvq.kvq_workspace_status(ws) == -1 and int(dr.abs().sum()) == 0
 
 
+def test_a_row_cut_back_into_a_shared_page_gets_its_own_before_it_grows():
+    """Two full pages shared by a fork, one row cut back to 20 tokens: growing it would write into the other row's
+    page and is refused; a fork onto itself copies that page, and then it grows."""
+    L = layout("d32", 12)
+    t, refs = tables(random.Random(1), 12, [32, 0], 8)
+    codes, scales = pool(L, "q8_0", 5)
+    m = Model(t, [32, 0], refs, [codes.cpu().numpy(), scales.cpu().numpy()])
+    table, dl, dr = dev(t), dev([32, 0]), dev(refs)
+    ws = kvq.alloc_pages_workspace(L, 2, 8)
+    cs, cd = _fork(m, L, [0], [1], table, dl, dr, ws)
+    assert (cs.cpu().tolist(), cd.cpu().tolist()) == m.fork([0], [1]) == ([-1], [-1])
+    kvq.kvq_pages_resize(table, dl, dr, dev([0]), dev([20]), ws, L)
+    assert kvq.kvq_workspace_status(ws) == 0 and m.resize([0], [20])
+    same(m, table, dl, dr)
+    for grown in (21, 40):
+        kvq.kvq_pages_resize(table, dl, dr, dev([0]), dev([grown]), ws, L)
+        assert kvq.kvq_workspace_status(ws) == -1
+        same(m, table, dl, dr)
+    cs, cd = _fork(m, L, [0], [0], table, dl, dr, ws)
+    want = m.fork([0], [0])
+    assert (cs.cpu().tolist(), cd.cpu().tolist()) == want and want[0][0] >= 0
+    kvq.kvq_pages_copy(codes, scales, cs, cd, L, "q8_0")
+    m.copy(*want)
+    same(m, table, dl, dr)
+    assert np.array_equal(codes.cpu().numpy(), m.pools[0]) and np.array_equal(scales.cpu().numpy(), m.pools[1])
+    kvq.kvq_pages_resize(table, dl, dr, dev([0]), dev([40]), ws, L)
+    assert kvq.kvq_workspace_status(ws) == 0 and m.resize([0], [40])
+    same(m, table, dl, dr)
+
+
 def test_new_lengths_may_be_the_lengths_themselves():
     L = layout("d32", 10)
     t, refs = tables(random.Random(1), 10, [40, 50], 8)
