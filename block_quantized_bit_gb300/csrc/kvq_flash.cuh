@@ -110,6 +110,23 @@ __device__ __forceinline__ float ex2_fma(float x) {
   return __int_as_float(__float_as_int(p) + (j << 23));
 }
 
+// Four MMAs of which two read A at a0 and two at a1 (8 columns apart each).
+__device__ __forceinline__ void mma2x2_bf16_tmem_a(uint32_t d_tmem, uint32_t a0, uint32_t a1, uint64_t b, uint64_t b_step,
+                                                   uint32_t idesc, uint32_t acc_first) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 a2, %1, 8;\n\tadd.u32 a3, %5, 8;\n\t"
+      "add.u64 b1, %2, %6;\n\tadd.u64 b2, b1, %6;\n\tadd.u64 b3, b2, %6;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d_tmem),
+      "r"(a0), "l"(b), "r"(idesc), "r"(acc_first), "r"(a1), "l"(b_step)
+      : "memory");
+}
+
 // Shared-memory descriptor of an operand in 128-byte swizzled rows (1024-byte aligned groups of eight).
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
   return smem_desc(addr, lbo, sbo) | (static_cast<uint64_t>(2) << 61);  // 128-byte swizzle

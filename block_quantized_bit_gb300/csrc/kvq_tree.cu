@@ -52,10 +52,8 @@ template <int D>
 struct TCfg {
   static constexpr int T = (D == 128) ? 128 : 64;  // keys per tile
   static constexpr int PPT = T / kPage;            // pages per tile
-  static constexpr int RS = D * 16;                // bytes between 8-row groups of the Q tile
   static constexpr int CHUNK = T * 128;            // bytes of a 64-column chunk of a K or V tile
   static constexpr int KV_TILE = T * D * 2;        // one bf16 K or V tile
-  static constexpr int Q_BYTES = kM * D * 2;
   static constexpr int NB = D / 32;                // scale blocks of a row
   // A dequant warp converts 2 KB of codes of K or V per tile: four 16-byte pieces per lane, consecutive lanes
   // consecutive pieces of a row.
@@ -64,8 +62,7 @@ struct TCfg {
   static constexpr int RPW = 4 * RPI;              // rows per warp
   static constexpr int K_OFF = 0;                  // [2] bf16 K tiles; 1024-byte aligned: swizzle atoms
   static constexpr int V_OFF = K_OFF + 2 * KV_TILE;  // [2] bf16 V tiles
-  static constexpr int Q_OFF = V_OFF + 2 * KV_TILE;
-  static constexpr int BASE_OFF = Q_OFF + Q_BYTES;              // [kMeta][PPT] pool row group of each page, or -1
+  static constexpr int BASE_OFF = V_OFF + 2 * KV_TILE;              // [kMeta][PPT] pool row group of each page, or -1
   static constexpr int NVAL_OFF = BASE_OFF + kMeta * PPT * 8;   // [kMeta][PPT] valid tokens
   static constexpr int RED_OFF = NVAL_OFF + kMeta * PPT * 4;    // [2 parities][2 halves][128 rows] row maxima
   static constexpr int SUM_OFF = RED_OFF + 2 * 2 * kM * 4;      // [2 item parities][2 halves][128 rows] row sums
@@ -73,11 +70,12 @@ struct TCfg {
   static constexpr int NBARS = 2 * kMeta + 14 + 12;
   static constexpr int BAR_OFF = (TAB_OFF + (kMaxTreeBatch + 1) * 4 + 15) / 16 * 16;  // mbarriers: 8-byte aligned
   static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
-  // tensor-memory columns: O [0, D); S buffer b [D + b T, D + (b + 1) T); P buffer b [384 + b T / 2, ...)
-  static constexpr int S_COL = D;
-  static constexpr int P_COL = 384;
+  // tensor-memory columns: O [0, D); Q (bf16, two per column) [D, D + D / 2); S buffer b [S_COL + b T, + T).  P replaces
+  // the S it was made from: half hf of the keys takes the first T / 4 columns of its own T / 2.
+  static constexpr int Q_COL = D;
+  static constexpr int S_COL = D + D / 2;
   static_assert(D == 128 || D == 256, "the tree kernel needs head_dim 128 or 256");
-  static_assert(D + 2 * T <= P_COL && P_COL + T <= kTmemCols, "tensor-memory columns");
+  static_assert(S_COL + 2 * T <= kTmemCols, "tensor-memory columns");
   static_assert(kDwWarps * RPW == T && kPage % RPW == 0, "dequant split");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
@@ -192,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms are 1024 B
   uint8_t* sK = smem + Cfg::K_OFF;
   uint8_t* sV = smem + Cfg::V_OFF;
-  uint8_t* sQ = smem + Cfg::Q_OFF;
   int64_t* sBase = reinterpret_cast<int64_t*>(smem + Cfg::BASE_OFF);
   int32_t* sNval = reinterpret_cast<int32_t*>(smem + Cfg::NVAL_OFF);
   int32_t* sTab = reinterpret_cast<int32_t*>(smem + Cfg::TAB_OFF);
@@ -396,12 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     // ===================================================================== MMA issue (elected lane)
     const uint32_t idesc_qk = x_idesc(T, false);
     const uint32_t idesc_pv = x_idesc(D, true);
-    // Q: the no-swizzle core-matrix layout, a k-step is 256 bytes.  K: K-major with the 128-byte swizzle, a k-step is 32
-    // bytes along a 64-column chunk.  V: MN-major with the same swizzle, a k-step is 16 rows of 128 bytes.
-    const uint64_t dQ = smem_desc(smem_u32(sQ), 128, Cfg::RS);
+    // K: K-major in 128-byte swizzled rows, a k-step is 32 bytes along a 64-column chunk.  V: MN-major in the same rows, a
+    // k-step is 16 of them.  Q and P in tensor memory, a k-step is 8 columns.
     const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
     const uint64_t dV = sw128_desc(smem_u32(sV), Cfg::CHUNK, 1024);
-    const uint32_t tS = tmem + Cfg::S_COL, tO = tmem, tP = tmem + Cfg::P_COL;
+    const uint32_t tQ = tmem + Cfg::Q_COL, tS = tmem + Cfg::S_COL, tO = tmem;
     uint32_t n = 0, items = 0;  // tiles QK'd; items finished
     // PV of tile m; the first tile of an item overwrites O, once the previous item's O has been read out
     auto pv = [&](uint32_t m, bool first) -> bool {
@@ -411,10 +407,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
       if (first && items >= 1 && !wait<D>(bar_o_free, (items - 1) & 1)) return false;
       tc_fence_after();
       const uint64_t v = dV + bp * static_cast<uint64_t>(Cfg::KV_TILE >> 4);
-      if constexpr (T == 128)
-        mma8_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, v, (16 * 128) >> 4, idesc_pv, first ? 0u : 1u);
-      else
-        mma4_bf16_tmem_a(tO, tP + bp * (T / 2), 8u, v, (16 * 128) >> 4, idesc_pv, first ? 0u : 1u);
+      const uint32_t p = tS + bp * T;
+      constexpr uint64_t step = (16 * 128) >> 4;
+      if constexpr (T == 128) {
+        mma4_bf16_tmem_a(tO, p, 8u, v, step, idesc_pv, first ? 0u : 1u);
+        mma4_bf16_tmem_a(tO, p + T / 2, 8u, v + 4 * step, step, idesc_pv, 1u);
+      } else {
+        mma2x2_bf16_tmem_a(tO, p, p + T / 2, v, step, idesc_pv, first ? 0u : 1u);
+      }
       mma_commit(&bar_pv_done[bp]);
       __syncwarp();
       return true;
@@ -426,14 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
       for (int32_t i = 0; i < ntiles; ++i, ++n) {
         const int b = n & 1;
         if (!wait<D>(&bar_k_full[b], (n >> 1) & 1)) { ok = false; break; }
-        // S buffer b was read by the softmax of tile n - 2
-        if (n >= 2 && !wait<D>(&bar_p_full[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
+        // S buffer b holds P of tile n - 2: its PV, whose P came after the softmax had read S, must have completed
+        if (n >= 2 && !wait<D>(&bar_pv_done[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
         for (int q = 0; q < D / 64; ++q)
-          mma4_bf16(tS + b * T, dQ + static_cast<uint64_t>((q * 4 * 256) >> 4), 256 >> 4,
-                    dK + b * static_cast<uint64_t>(Cfg::KV_TILE >> 4) + static_cast<uint64_t>((q * Cfg::CHUNK) >> 4), 32 >> 4,
-                    idesc_qk, q > 0 ? 1u : 0u);
+          mma4_bf16_tmem_a(tS + b * T, tQ + q * 32, 8u,
+                           dK + b * static_cast<uint64_t>(Cfg::KV_TILE >> 4) + static_cast<uint64_t>((q * Cfg::CHUNK) >> 4),
+                           32 >> 4, idesc_qk, q > 0 ? 1u : 0u);
         mma_commit(&bar_qk_done[b]);
         __syncwarp();
         if (i > 0 && !pv(n - 1, i == 1)) { ok = false; break; }
@@ -452,22 +452,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + Cfg::S_COL + lane_base + hf * (T / 2);
     const uint32_t tO = tmem + lane_base + hf * (D / 2);
-    const uint32_t tP = tmem + Cfg::P_COL + lane_base + hf * (T / 4);
     float* sRed = reinterpret_cast<float*>(smem + Cfg::RED_OFF);
     float* sSum = reinterpret_cast<float*>(smem + Cfg::SUM_OFF);
-    // this warp's half of the segment's Q rows into the shared tile (rows past the block's are zero)
+    // this warp's half of the segment's Q rows into tensor memory (rows past the block's are zero): as the A operand of
+    // every tile's QK they would otherwise cost 2 * 128 * D bytes of shared-memory reads a tile
     auto write_q = [&](const Seg& s) {
       if (quarter * 32 < s.rows) {
         const bool valid = r < s.rows;
         const int32_t row = s.blk * kM + (valid ? r : 0);
         const int32_t tok = row / G;
         const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + s.g * G + (row - tok * G)) * D);
-        uint8_t* dst = sQ + (r % 8) * 16 + (r / 8) * Cfg::RS;
-#pragma unroll 4
-        for (int j = hf * (D / 16); j < (hf + 1) * (D / 16); ++j)
-          *reinterpret_cast<uint4*>(dst + j * 128) = valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+            a.q + (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + s.g * G + (row - tok * G)) * D + hf * (D / 2));
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 x = valid ? __ldg(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
+            w[4 * j] = x.x;
+            w[4 * j + 1] = x.y;
+            w[4 * j + 2] = x.z;
+            w[4 * j + 3] = x.w;
+          }
+          tmem_st16u(tmem + Cfg::Q_COL + lane_base + hf * (D / 4) + c * 16, w);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) bar_arrive(bar_q_full);
@@ -561,8 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
           }
           m_used = mx;
         }
-        // P buffer b is free once the PV two tiles back has read it
-        if (n >= 2 && !wait<D>(&bar_pv_done[b], ((n >> 1) - 1) & 1)) { ok = false; break; }
         if (__any_sync(0xffffffffu, resc)) {  // (only from the second tile of an item on)
           // O must hold the PV of the previous tile before it is scaled; this warp scales its half of O
           if (!wait<D>(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
@@ -595,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
             ls[e & 1] = fadd2(ls[e & 1], p);
             w[e] = pack_bf16x2(p.x, p.y);
           }
-          tmem_st16u(tP + b * (T / 2) + h * 16, w);
+          tmem_st16u(tS + b * T + h * 16, w);  // (over scores that have been read)
         }
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
