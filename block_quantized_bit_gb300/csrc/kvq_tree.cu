@@ -4,9 +4,11 @@
 // drafted tokens whose bit is set in its mask:
 //   out[i][h] = sum_t softmax_t(sm_scale q[i][h].K[t]) V[t]   over t < L - n, and t = L - n + j with bit j set.
 // Rows are few (n_b times the heads of a kv head) and contexts long, so the work is reading K and V once:
-// 2 * Hkv * D * 17/16 bytes per token.  A block of 128 rows of one (sequence, kv head) shares every dequantized
-// tile, in the extend kernel's arrangement (rows are the MMA's M; S and O in tensor memory; the same tile
-// layouts, dequant and softmax), with three differences.
+// 2 * Hkv * D * 17/16 bytes per token.  Blocks of 128 rows of one (sequence, kv head) share every dequantized tile:
+//   S[128 rows][T keys] = Q . Kd^T,   O[128 rows][D] += P . Vd      (T = 128 at D = 128, 64 at D = 256)
+// Q, S, P (over the S it was made from) and O are in tensor memory, one row per lane; K and V are bf16 tiles in 128-byte
+// swizzled shared memory, two of each.  MMAs of different accumulators are not ordered among themselves, so the QK
+// that next writes an S buffer waits for the PV that reads the P in it.
 //
 // Work split.  A unit is one tile of T keys for one block of rows; units are numbered by (sequence, row block,
 // kv head, tile), and CTA c of C takes the units [c U / C, (c + 1) U / C): every CTA gets the same number of tiles to
@@ -16,12 +18,21 @@
 // the merge kernel (a programmatic dependent) joins the segments of each row.
 //
 // Masks.  Visibility of a half tile's keys is one 64-bit word per row: ones before the drafted tokens, the
-// row's mask bits among them, zeros behind the end, and zeros for masked pages.  A warp whose words are all ones
-// takes the unmasked pass.
+// row's mask bits among them, zeros behind the end, and zeros for masked pages.  Where a row of a warp does not see a
+// key, its score is set to -inf first; the passes of the softmax have one variant.
 //
-// Row blocks that are not full.  Lane quarters without a row skip the softmax (an MMA row depends on its own P row
-// only); their warps just keep the barriers' counts.
-#include <cuda.h>
+// Roles of a CTA's 28 warps: 0-7 softmax (two per lane quarter, each on half of a tile's keys; quarters without a row
+// only keep the barriers' counts), 8-15 dequantize K and 16-23 V, 26 looks up pages, 27 issues the MMAs.
+//
+// Measured: 32 sequences of 3..16 drafted tokens over 0.7k..8k, 4 heads per kv head (q8_0): 117 us, 2.8 TB/s; 4 x 32 over
+// 64k at head_dim 256, 8 heads per kv head (two blocks): 166 us, 829 TFLOP/s.  What bounds it: instruction issue.  A
+// tile costs a sub-partition about 2300 instructions (16 warps converting 64 codes each, the softmax, waits of some
+// 100 clocks), against 1480 clocks that its bytes take at the memory's rate.  What the steps were worth, first case / second:
+// one copy of the dequant code for K and V, one masked pass, eight MMAs per elect 183 -> 159 / 218; K and V by warps of
+// their own 157 / 204; the merge by a warp per row and without a clearing launch 146 / 201; loads straight into registers
+// instead of a staging ring, conflict-free stores without selects, waits' unlikely parts out of line 131 / 178; Q and P in
+// tensor memory 124 / 168.  Measured slower, and not kept: sixteen warps each taking K and then V (166), rows repeated in idle
+// lane quarters with the keys divided among them (137 / 183), one register set per warp rotated by moves (147).
 #include <math.h>
 
 #include <algorithm>
@@ -40,9 +51,11 @@ constexpr int kM = 128;  // query rows per block (the MMA M)
 constexpr int kSmWarps = 8;  // two per tensor-memory lane quarter, each on half of a tile's keys
 constexpr int kDwWarps = 8;  // of K, and of V
 constexpr int kVWarp = kSmWarps + kDwWarps;     // warp 16: first of V
-constexpr int kPlanWarp = kVWarp + kDwWarps;    // warp 24: pages of the tiles to come
-constexpr int kMmaWarp = kPlanWarp + 1;         // warp 25
-constexpr int kThreads = (kMmaWarp + 1) * 32;   // 26 warps
+// Warps 24 and 25 only fill up: a lane quarter's softmax runs on the SM sub-partition of its number, blocks that are not
+// full use the first quarters, and so the two other roles belong on the last sub-partitions (123 -> 117 us at 12..64 rows).
+constexpr int kPlanWarp = kVWarp + kDwWarps + 2;  // warp 26: pages of the tiles to come
+constexpr int kMmaWarp = kPlanWarp + 1;           // warp 27
+constexpr int kThreads = (kMmaWarp + 1) * 32;     // 28 warps
 constexpr int kDwThreads = kDwWarps * 32;
 constexpr int kTmemCols = 512;
 constexpr int kMeta = 8;               // tiles whose pages are looked up ahead
@@ -307,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
       __syncwarp();
       if (lane == 0) bar_arrive(&bar_meta[sl]);
     }
-  } else if (warp >= kSmWarps && warp < kPlanWarp) {
+  } else if (warp >= kSmWarps && warp < kVWarp + kDwWarps) {
     // ===================================================================== dequant warps
     // Eight for K and eight for V, one copy of the code for both (with four roles on an SM, instruction-cache
     // misses cost more than the selects).  A warp's codes and scales come straight from the pool into registers, two
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     // before tensor memory is freed, every MMA issued must have completed (the last commit implies all)
     if (n > 0) (void)mbar_wait_bounded(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
     if (n > 0) (void)mbar_wait_bounded(&bar_qk_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
-  } else {
+  } else if (warp < kSmWarps) {
     // ===================================================================== softmax warps
     const int quarter = warp & 3, hf = warp >> 2;  // lane quarter; which half of the keys and of O
     const int r = quarter * 32 + lane;             // query row = tensor-memory lane
