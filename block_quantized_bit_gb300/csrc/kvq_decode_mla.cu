@@ -292,12 +292,23 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
   const int32_t n_items = plan.n_items;
   const int32_t groups = p.num_kv_heads * p.head_tiles;
   const int32_t HP = p.group / p.head_tiles;  // query heads per item, <= kHG (the rest of N is padding)
-  if (tid == 0) {
+  for (int32_t b = tid; b < p.batch; b += kThreads) sTab[b] = groups * ((seq_pages(p, b) + C - 1) / C);
+  __syncthreads();
+  if (warp == 0) {  // exclusive prefix, 32 sequences at a time
     int32_t run = 0;
-    for (int32_t b = 0; b < p.batch; ++b) {
-      sTab[b] = run;
-      run += groups * ((seq_pages(p, b) + C - 1) / C);
+    for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
+      const int32_t x = b0 + lane < p.batch ? sTab[b0 + lane] : 0;
+      int32_t incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (b0 + lane < p.batch) sTab[b0 + lane] = run + incl - x;
+      run += __shfl_sync(0xffffffffu, incl, 31);
     }
+  }
+  if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bar_k_full[b], 8);
       mbar_init(&bar_k_free[b], 1);
@@ -753,6 +764,48 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
       // ---- item end: O^T -> partials (thread = dim within each 128-dim block); (m, l) per head
       if (!mbar_wait_bounded(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
       mla_fence_after();
+      if (p.tree_mask != nullptr && t.pg0 == 0 && t.pg1 == seq_pages(p, t.b)) {
+        // A drafted token's only split (kvq_tree): its output, no partial.  (1024 drafted tokens of 64: the partials
+        // alone were half a gigabyte each way.)
+#pragma unroll
+        for (int h = 0; h < kHS; ++h) {
+          float v = l_t[h];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) sRed[warp * kHS + h] = v;
+        }
+        mla_named_sync(1, kSmWarps * 32);
+        if (tid < kHG) {
+          const int half = tid / kHS, idx = tid % kHS;
+          float lsum = 0.0f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) lsum += sRed[(half * 4 + w) * kHS + idx];
+          sA[tid] = lsum > 0.0f ? 1.0f / lsum : 0.0f;
+          sM[tid] = tid < HP ? kNoMax : INFINITY;  // the next item starts afresh
+        }
+        mla_named_sync(1, kSmWarps * 32);
+        const int64_t row = static_cast<int64_t>(t.b) * p.num_q_heads + t.hg * HP;
+#pragma unroll 1
+        for (int c = 0; c < kVBlocks; ++c) {
+#pragma unroll 1
+          for (int g = 0; g < kHS / 16; ++g) {
+            float o[16];
+            mla_ld16(tO + c * 64 + h0 + g * 16 + lane_base, o);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+              const int hd = h0 + g * 16 + h;
+              if (hd >= HP) continue;
+              const int64_t at = (row + hd) * kDV + c * 128 + tt;
+              const float v = o[h] * sA[hd];
+              if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+              else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+            }
+          }
+        }
+        mla_fence_before();
+        mla_named_sync(1, kSmWarps * 32);
+        continue;
+      }
       float* acc = p.part_acc + static_cast<int64_t>(item) * HP * kDV;
 #pragma unroll 1
       for (int c = 0; c < kVBlocks; ++c) {
