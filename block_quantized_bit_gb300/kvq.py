@@ -382,37 +382,37 @@ def kvq_extend(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
 # ---------------------------------------------------------------------------- checked marshalling
 # The calls below belong to loops of short GPU work, so what they marshal is checked and passed as plain
 # integers, and a layout's C struct is built once.
-_I32, _I64, _U8, _I16, _BF16 = torch.int32, torch.int64, torch.uint8, torch.int16, torch.bfloat16
-_layout_refs: dict = {}
+_I32, _I64, _U8, _BF16 = torch.int32, torch.int64, torch.uint8, torch.bfloat16
+_layouts: dict = {}
 
 
-def _layout_ref(L: Layout):
+def _layout_info(L: Layout):
+    """(pointer to the C struct, code bytes, scales) of a layout."""
     key = (L.num_pages, L.page_size, L.num_kv_heads, L.head_dim, L.v_dim, L.mla)
-    ref = _layout_refs.get(key)
-    if ref is None:
-        if len(_layout_refs) >= 1024:
-            _layout_refs.clear()
-        ref = _layout_refs[key] = ctypes.byref(L.c())
-    return ref
+    info = _layouts.get(key)
+    if info is None:
+        if len(_layouts) >= 1024:
+            _layouts.clear()
+        info = _layouts[key] = (ctypes.byref(L.c()), math.prod(L.codes_shape()), math.prod(L.scales_shape()))
+    return info
 
 
-def _check_args(*args):
-    """(name, tensor, type) triples: tensors of that type, dense, all on the current CUDA device, whose index is
-    returned."""
-    device = args[0][1].get_device()
-    for _, t, dtype in args:
+def _check_args(names, types, *tensors):
+    """The tensors (named, of these types) must be dense and on the current CUDA device, whose index is returned."""
+    device = tensors[0].get_device()
+    for t, dtype in zip(tensors, types):
         if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
             break
     else:
         if device >= 0 and device == torch.cuda.current_device():
             return device
-    for name, t, dtype in args:
+    for name, t, dtype in zip(names, tensors, types):
         if t.dtype is not dtype:
             raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
     raise ValueError("every tensor must be on the current CUDA device, got " +
-                     ", ".join("%s on %s" % (name, t.device) for name, t, _ in args))
+                     ", ".join("%s on %s" % (name, t.device) for name, t in zip(names, tensors)))
 
 
 def _raw_stream(stream, device):
@@ -421,16 +421,24 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _pool_args(pool, scales, layout: Layout, kind):
-    """The kind's number and the pool's (name, tensor, type) triples; a block-scaled kind needs scales."""
+def _check_pool(pool, scales, info, kind, device):
+    """The kind's number and the scales' address (None for the unscaled kinds); pool and scales must hold the layout's
+    pages."""
     k = _kind(kind)
-    if pool.numel() < math.prod(layout.codes_shape()):
-        raise ValueError("pool must have the layout's %s codes" % (layout.codes_shape(),))
-    if k not in (KVQ_FP8_E4M3, KVQ_Q8_0):
-        return k, (("pool", pool, _U8),), None
-    if scales is None or scales.numel() < math.prod(layout.scales_shape()):
-        raise ValueError("scales must have the layout's %s scales" % (layout.scales_shape(),))
-    return k, (("pool", pool, _U8), ("scales", scales, scales.dtype if scales.dtype.itemsize == 2 else _I16)), scales
+    if pool.dtype is not _U8:
+        raise TypeError("pool must be torch.uint8, got %s" % pool.dtype)
+    if pool.numel() < info[1] or not pool.is_contiguous():
+        raise ValueError("pool must be contiguous and hold the layout's %d codes" % info[1])
+    if k == KVQ_FP8_E4M3 or k == KVQ_Q8_0:
+        if scales is None or scales.numel() < info[2] or scales.dtype.itemsize != 2 or not scales.is_contiguous():
+            raise ValueError("scales must be contiguous and hold the layout's %d scales of 16 bits" % info[2])
+        if scales.get_device() != device:
+            raise ValueError("scales is on %s, not on the current CUDA device" % scales.device)
+    else:
+        scales = None
+    if pool.get_device() != device:
+        raise ValueError("pool is on %s, not on the current CUDA device" % pool.device)
+    return k, None if scales is None else scales.data_ptr()
 
 
 def _out_dtype(out):
@@ -465,7 +473,7 @@ def kvq_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t.dtype is not _BF16:
             raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
-    device = _check_args(("q_start", q_start, _I32), ("workspace", workspace, _U8))
+    device = _check_args(("q_start", "workspace"), (_I32, _U8), q_start, workspace)
     if not (q.get_device() == k.get_device() == v.get_device() == out.get_device() == device):
         raise ValueError("every tensor must be on the current CUDA device")
     status = lib().kvq_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_start.data_ptr(), q.shape[0],
@@ -476,6 +484,9 @@ def kvq_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
 
 
 # ---------------------------------------------------------------------------- drafted tokens
+_TREE_NAMES = ("q", "block_table", "seq_lens", "q_start", "tree_mask", "out", "workspace")
+
+
 def alloc_tree_workspace(layout: Layout, batch: int, total_q: int, num_q_heads: int, max_pages_per_seq: int,
                          path: int = 0, device="cuda"):
     n = lib().kvq_tree_workspace_bytes(ctypes.byref(layout.c()), int(batch), int(total_q), int(num_q_heads),
@@ -499,20 +510,28 @@ def kvq_tree(q: torch.Tensor, pool: torch.Tensor, scales: Optional[torch.Tensor]
         raise ValueError("tree_mask must be [total_q, words] and q_start [batch + 1]")
     _check_tables(block_table, seq_lens, None, layout)
     od = _out_dtype(out)
-    k, checked, scales = _pool_args(pool, scales, layout, kind)
-    device = _check_args(*checked, ("q", q, _BF16), ("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32),
-                         ("q_start", q_start, _I32), ("tree_mask", tree_mask, _I64), ("out", out, out.dtype),
-                         ("workspace", workspace, _U8))
-    st = lib().kvq_tree(q.data_ptr(), pool.data_ptr(), None if scales is None else scales.data_ptr(),
+    info = _layout_info(layout)
+    device = _check_args(_TREE_NAMES, (_BF16, _I32, _I32, _I32, _I64, out.dtype, _U8), q, block_table, seq_lens, q_start,
+                         tree_mask, out, workspace)
+    k, sc = _check_pool(pool, scales, info, kind, device)
+    st = lib().kvq_tree(q.data_ptr(), pool.data_ptr(), sc,
                         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(),
                         tree_mask.data_ptr(), tree_mask.shape[1], q.shape[0], B, q.shape[1], sm_scale, out.data_ptr(), od,
-                        workspace.data_ptr(), workspace.numel(), _layout_ref(layout), k, path,
+                        workspace.data_ptr(), workspace.numel(), info[0], k, path,
                         _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_tree")
 
 
 # ---------------------------------------------------------------------------- pages
+_FORK_NAMES = ("block_table", "seq_lens", "page_refs", "src", "dst", "copy_src", "copy_dst", "workspace")
+_FORK_TYPES = (_I32,) * 7 + (_U8,)
+_RESIZE_NAMES = ("block_table", "seq_lens", "page_refs", "seqs", "new_lens", "workspace")
+_RESIZE_TYPES = (_I32,) * 5 + (_U8,)
+_COMPACT_NAMES = ("block_table", "seq_lens", "q_start", "keep", "new_lens", "workspace", "page_refs")
+_COMPACT_TYPES = (_I32, _I32, _I32, _I64, _I32, _U8, _I32)
+
+
 def alloc_pages_workspace(layout: Layout, n: int, max_pages_per_seq: int, device="cuda"):
     """Workspace of kvq_pages_fork and kvq_pages_resize for n list entries (kvq_pages_compact takes it too)."""
     b = lib().kvq_pages_workspace_bytes(ctypes.byref(layout.c()), int(n), int(max_pages_per_seq))
@@ -527,10 +546,11 @@ def kvq_pages_copy(pool: torch.Tensor, scales: Optional[torch.Tensor], src: torc
     n = src.numel()
     if dst.numel() != n:
         raise ValueError("src and dst must have one entry per copy")
-    k, checked, scales = _pool_args(pool, scales, layout, kind)
-    device = _check_args(*checked, ("src", src, _I32), ("dst", dst, _I32))
-    st = lib().kvq_pages_copy(pool.data_ptr(), None if scales is None else scales.data_ptr(), src.data_ptr(),
-                              dst.data_ptr(), n, _layout_ref(layout), k, _raw_stream(stream, device))
+    info = _layout_info(layout)
+    device = _check_args(("src", "dst"), (_I32, _I32), src, dst)
+    k, sc = _check_pool(pool, scales, info, kind, device)
+    st = lib().kvq_pages_copy(pool.data_ptr(), sc, src.data_ptr(), dst.data_ptr(), n, info[0], k,
+                              _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_copy")
 
@@ -551,13 +571,12 @@ def kvq_pages_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, page_refs:
     if dst.numel() != n or copy_src.numel() != n or copy_dst.numel() != n:
         raise ValueError("src, dst, copy_src and copy_dst must have the same length")
     _check_tables(block_table, seq_lens, page_refs, layout)
-    device = _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
-                         ("src", src, _I32), ("dst", dst, _I32), ("copy_src", copy_src, _I32),
-                         ("copy_dst", copy_dst, _I32), ("workspace", workspace, _U8))
+    device = _check_args(_FORK_NAMES, _FORK_TYPES, block_table, seq_lens, page_refs, src, dst, copy_src, copy_dst,
+                         workspace)
     batch, max_pages = block_table.shape
     st = lib().kvq_pages_fork(block_table.data_ptr(), max_pages, seq_lens.data_ptr(), batch, page_refs.data_ptr(),
                               src.data_ptr(), dst.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _layout_ref(layout), _raw_stream(stream, device))
+                              workspace.data_ptr(), workspace.numel(), _layout_info(layout)[0], _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_fork")
 
@@ -569,12 +588,11 @@ def kvq_pages_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, page_ref
     if new_lens.numel() != n:
         raise ValueError("seqs and new_lens must have the same length")
     _check_tables(block_table, seq_lens, page_refs, layout)
-    device = _check_args(("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32), ("page_refs", page_refs, _I32),
-                         ("seqs", seqs, _I32), ("new_lens", new_lens, _I32), ("workspace", workspace, _U8))
+    device = _check_args(_RESIZE_NAMES, _RESIZE_TYPES, block_table, seq_lens, page_refs, seqs, new_lens, workspace)
     batch, max_pages = block_table.shape
     st = lib().kvq_pages_resize(block_table.data_ptr(), max_pages, seq_lens.data_ptr(), batch, page_refs.data_ptr(),
                                 seqs.data_ptr(), new_lens.data_ptr(), n, workspace.data_ptr(), workspace.numel(),
-                                _layout_ref(layout), _raw_stream(stream, device))
+                                _layout_info(layout)[0], _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_resize")
 
@@ -589,17 +607,15 @@ def kvq_pages_compact(pool: torch.Tensor, scales: Optional[torch.Tensor], block_
     if keep.dim() != 2 or keep.shape[0] != B or q_start.numel() != B + 1 or new_lens.numel() != B:
         raise ValueError("keep must be [batch, words], q_start [batch + 1] and new_lens [batch]")
     _check_tables(block_table, seq_lens, page_refs, layout)
-    k, checked, scales = _pool_args(pool, scales, layout, kind)
-    if page_refs is not None:
-        checked += (("page_refs", page_refs, _I32),)
-    device = _check_args(*checked, ("block_table", block_table, _I32), ("seq_lens", seq_lens, _I32),
-                         ("q_start", q_start, _I32), ("keep", keep, _I64), ("new_lens", new_lens, _I32),
-                         ("workspace", workspace, _U8))
-    st = lib().kvq_pages_compact(pool.data_ptr(), None if scales is None else scales.data_ptr(), block_table.data_ptr(),
+    info = _layout_info(layout)
+    device = _check_args(_COMPACT_NAMES, _COMPACT_TYPES, block_table, seq_lens, q_start, keep, new_lens, workspace,
+                         *(() if page_refs is None else (page_refs,)))
+    k, sc = _check_pool(pool, scales, info, kind, device)
+    st = lib().kvq_pages_compact(pool.data_ptr(), sc, block_table.data_ptr(),
                                  block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(), keep.data_ptr(),
                                  keep.shape[1], B, new_lens.data_ptr(),
                                  None if page_refs is None else page_refs.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel(), _layout_ref(layout), k, _raw_stream(stream, device))
+                                 workspace.numel(), info[0], k, _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_pages_compact")
 
