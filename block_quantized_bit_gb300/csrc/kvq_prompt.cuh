@@ -52,19 +52,22 @@ struct ItemSource {
   const PromptArgs& a;
   const int32_t* tab;
   int32_t top;      // items of the longest sequence
+  bool narrow;      // sums over the sequences fit 32 bits
   int64_t n_items;
   __device__ __forceinline__ ItemSource(const PromptArgs& args, const int32_t* table) : a(args), tab(table) {
     const int lane = threadIdx.x & 31;
     top = 0;
     for (int32_t b = lane; b < a.batch; b += 32) top = max(top, tab[b]);
     top = __reduce_max_sync(0xffffffffu, top);
+    narrow = static_cast<int64_t>(top) * a.batch < (1LL << 31);
     n_items = above(-1);
   }
   // items of levels > p
   __device__ __forceinline__ int64_t above(int32_t p) const {
     int64_t s = 0;
     for (int32_t b = threadIdx.x & 31; b < a.batch; b += 32) s += max(tab[b] - p - 1, 0);
-#pragma unroll
+    if (narrow) return static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<int32_t>(s))) * a.num_kv_heads;
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s * a.num_kv_heads;
   }
@@ -87,8 +90,9 @@ struct ItemSource {
     for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {  // the rank-th sequence with more than p items
       const uint32_t m = __ballot_sync(0xffffffffu, b0 + lane < a.batch && tab[b0 + lane] > p);
       const int32_t c = __popc(m);
-      if (rank < c) {
-        b = b0 + __fns(m, 0, rank + 1);
+      if (rank < c) {  // the lane whose bit is the rank-th of the mask (from 0)
+        const bool hit = ((m >> lane) & 1u) && __popc(m & ((1u << lane) - 1u)) == rank;
+        b = b0 + __ffs(__ballot_sync(0xffffffffu, hit)) - 1;
         break;
       }
       rank -= c;
