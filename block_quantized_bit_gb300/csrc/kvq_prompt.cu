@@ -271,15 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
           stage = kv % STAGES;
           if (!warp_wait_far(&bar_full[stage], (kv / STAGES) & 1)) { ok = false; break; }
           ++kv;
-          const int32_t from = it.len - j * kM;
-          if (from < kM) {  // the V rows of keys behind the sequence's end
-            uint8_t* v = sKV + stage * 2 * Cfg::TILE + Cfg::TILE;
-#pragma unroll 1
-            for (int32_t o = lane * 16; o < Cfg::TILE; o += 512)
-              if ((o & (Cfg::CHUNK - 1)) >= from * 128) *reinterpret_cast<uint4*>(v + o) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
           if (j < nA && !qk(0, stage)) { ok = false; break; }
         }
         if (j >= 1) {
@@ -289,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
         if (j < n) {
           if (j < nB && !qk(1, stage)) { ok = false; break; }
           if (j == n - 1) mma_commit(bar_q_empty);
+          if (it.len - j * kM < kM)  // (before the first PV that reads the tile)
+            clear_rows<Cfg::CH, kM>(sKV + stage * 2 * Cfg::TILE + Cfg::TILE, it.len - j * kM);
           if (j < nA && !pv(0, stage, j == 0)) { ok = false; break; }
         }
       }

@@ -84,9 +84,9 @@ struct ItemSource {
       else lo = mid + 1;
     }
     const int32_t p = lo;
-    const int64_t q = idx - above(p);  // below batch * kv heads
-    int32_t rank = static_cast<int32_t>(q / a.num_kv_heads), b = 0;
-    it.g = static_cast<int32_t>(q - static_cast<int64_t>(rank) * a.num_kv_heads);
+    const int32_t q = static_cast<int32_t>(idx - above(p));  // below batch * kv heads
+    int32_t rank = q / a.num_kv_heads, b = 0;
+    it.g = q - rank * a.num_kv_heads;
     for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {  // the rank-th sequence with more than p items
       const uint32_t m = __ballot_sync(0xffffffffu, b0 + lane < a.batch && tab[b0 + lane] > p);
       const int32_t c = __popc(m);
@@ -109,6 +109,19 @@ struct ItemSource {
     return it;
   }
 };
+
+// Clears the rows from `from` on of a tile of CHUNKS column chunks of ROWS rows: the V rows of keys behind the
+// sequence's end, which no probability but 0 meets.
+template <int CHUNKS, int ROWS>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int32_t from) {
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll 4
+    for (int32_t o = from * 128 + (threadIdx.x & 31) * 16; o < ROWS * 128; o += 512)
+      *reinterpret_cast<uint4*>(tile + c * ROWS * 128 + o) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
 
 // One row's 32 output columns o * scale, at element `at` of the output.
 __device__ __forceinline__ void store_row32(const PromptArgs& a, int64_t at, const uint32_t (&ov)[32], float scale) {

@@ -226,15 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
         if (j + 1 < n && !qk(j + 1)) { ok = false; break; }
         const uint32_t u = kv + 2 * j + 1;
         if (!landed(u)) { ok = false; break; }
-        const int32_t from = it.len - j * kKeys;
-        if (from < kKeys) {  // the V rows of keys behind the sequence's end
-          uint8_t* v = sKV + (u % kSlots) * kKvTile;
-#pragma unroll 1
-          for (int32_t o = lane * 16; o < kKvTile; o += 512)
-            if ((o & (kKvChunk - 1)) >= from * 128) *reinterpret_cast<uint4*>(v + o) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+        if (it.len - j * kKeys < kKeys)
+          clear_rows<kChunks, kKeys>(sKV + (u % kSlots) * kKvTile, it.len - j * kKeys);
         if (j == 0 && k > 0 && !warp_wait_far(bar_o_free, (k - 1) & 1)) { ok = false; break; }
         if (!warp_wait_far(&bar_p_full[npv & 1], (npv >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
