@@ -882,8 +882,7 @@ kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t
   const kvq_status st = kvq_device_check();
   if (st != KVQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 2 * sizeof(uint32_t), s) != cudaSuccess) return KVQ_ECUDA;
-  if (empty) return KVQ_OK;
+  if (empty) return cudaMemsetAsync(workspace, 0, 2 * sizeof(uint32_t), s) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
   a.q = q;
   a.k = k;
   a.v = v;

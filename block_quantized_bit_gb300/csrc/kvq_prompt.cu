@@ -62,7 +62,8 @@ struct PCfg {
   static constexpr int ITEM_OFF = TAB_OFF + kMaxPromptBatch * 4;         // [2] published items
   static constexpr int NBARS = 2 * STAGES + 15;
   static constexpr int BAR_OFF = ITEM_OFF + 2 * 32;
-  static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;     // + slack to align the base
+  static constexpr int STG_OFF = BAR_OFF + (NBARS * 8 + 16 + 15) / 16 * 16;  // [8 softmax warps] 2 KB of output
+  static constexpr int SMEM_BYTES = STG_OFF + kSmWarps * 2048 + 1024;    // + slack to align the base
   static constexpr int S_COL = 0, O_COL = 256;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
@@ -105,6 +106,13 @@ __device__ __forceinline__ void mma_chunks(uint32_t d_tmem, uint64_t a, uint64_t
   }
 }
 
+// A value that the compiler takes for a new one at each use: branches on it stay apart (merged, they would index the row's
+// scores by it, in local memory).
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap,
                                                              const __grid_constant__ CUtensorMap kmap,
@@ -131,8 +139,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
   uint64_t* bar_item_free = bar_q_full + 13;   // [2] item slot read by the MMA warp and every softmax warp
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
 
+  uint8_t* sStage = smem + Cfg::STG_OFF;
+
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  if (tid == kLoadWarp * 32) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   prompt_table<2>(a, sTab);
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
@@ -185,9 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
         bar_arrive(&bar_item[k & 1]);
       }
       __syncwarp();
+      if (k == 0) wait_cleared();
       if (!it.live) break;
-      uint32_t next = 0;
-      if (lane == 0) next = atomicAdd(a.counter, 1u);
       // Q tiles, once the previous item's QKs have read theirs
       if (k >= 1 && !warp_wait_far(bar_q_empty, (k - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
@@ -202,6 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
           }
       }
       __syncwarp();
+      uint32_t next = 0;
+      if (lane == 0) next = atomicAdd(a.counter, 1u);
 #pragma unroll
       for (int w = 0; w < 2; ++w) nq[w] += it.blk[w] >= 0;
       const int32_t n = max(it.blk[0], it.blk[1]) + 1;
@@ -292,17 +308,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
   } else {
     // ===================================================================== softmax warps
     const int w = warp >> 2;                   // tile
-    const int r = tid & (kM - 1);              // row = tensor-memory lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + Cfg::S_COL + w * kM + lane_base;
     const uint32_t tO = tmem + Cfg::O_COL + w * kM + lane_base;
     uint32_t nt = 0;  // key tiles processed
-    Item it;
-    for (uint32_t k = 0; ok; ++k) {
-      if (!take_item(k, it)) { ok = false; break; }
-      if (!it.live) break;
-      const int32_t n = it.blk[w] + 1;  // key tiles; 0: no such tile
-      if (n == 0) continue;
+    Item it, next;
+    ok = take_item(0, it);
+    for (uint32_t k = 0; ok && it.live; ++k, it = next) {
+      const int32_t blk = w == 0 ? it.blk[0] : it.blk[1], head = w == 0 ? it.head[0] : it.head[1];
+      const int32_t n = blk + 1;  // key tiles; 0: no such tile
+      if (n == 0) {
+        ok = take_item(k + 1, next);
+        continue;
+      }
       float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
       // the running max moves only when some row's passes it by more than 2^8; O and l are then rescaled (O holds
@@ -331,9 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
         if (!warp_wait_far(&bar_s_full[w], nt & 1)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[kM];
-        float top;
+        uint32_t mx[4];
         if (j < n - 1) {
-          uint32_t mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32_max_issue(tS + 32 * c, s + 32 * c, mx[c]);
 #pragma unroll
@@ -341,22 +358,39 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
             tmem_wait_ld32(s + 32 * c);
             tmem_wait_max(mx[c]);
           }
-          top = fmaxf(fmaxf(__uint_as_float(mx[0]), __uint_as_float(mx[1])),
-                      fmaxf(__uint_as_float(mx[2]), __uint_as_float(mx[3])));
         } else {
+          // on the diagonal the warp's rows see the 32-key chunks before their own whole, their own up to the row,
+          // and none behind it
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + 32 * c, s + 32 * c);
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = 0xFF800000u;
+            const int own = opaque(warp & 3);
+            if (c < own) {
+              tmem_ld32_max_issue(tS + 32 * c, s + 32 * c, mx[c]);
+            } else if (c == own) {
+              tmem_ld32_issue(tS + 32 * c, s + 32 * c);
+            } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < kM; ++e) {
-            s[e] = e <= r ? s[e] : 0xFF800000u;
-            mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+              for (int e = 0; e < 32; ++e) s[32 * c + e] = 0xFF800000u;
+            }
           }
-          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld32(s + 32 * c);
+            tmem_wait_max(mx[c]);
+            if (c == opaque(warp & 3)) {
+              float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                s[32 * c + e] = e <= lane ? s[32 * c + e] : 0xFF800000u;
+                x[e & 3] = fmaxf(x[e & 3], __uint_as_float(s[32 * c + e]));
+              }
+              mx[c] = __float_as_uint(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+            }
+          }
         }
-        top *= a.score_scale;
+        const float top = a.score_scale * fmaxf(fmaxf(__uint_as_float(mx[0]), __uint_as_float(mx[1])),
+                                                fmaxf(__uint_as_float(mx[2]), __uint_as_float(mx[3])));
         update_max(top, j);
         const float2 sc2 = make_float2(a.score_scale, a.score_scale), m2 = make_float2(-m, -m);
 #pragma unroll
@@ -377,25 +411,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
         __syncwarp();
         if (lane == 0) bar_arrive(&bar_p_full[w]);
       }
-      if (!ok) break;
+      if (!ok || !take_item(k + 1, next)) { ok = false; break; }
       // O / l of this row, once the item's last PV has completed
       if (!warp_wait_far(&bar_pv_done[w], (nt - 1) & 1)) { ok = false; break; }
       tc_fence_after();
       const float inv = 1.0f / (l2.x + l2.y);
-      const int32_t tok = it.blk[w] * kM + r;
-      const int64_t orow = static_cast<int64_t>(it.q0 + tok) * a.out_token + static_cast<int64_t>(it.head[w]) * a.out_head;
+      const int32_t tok = blk * kM + (warp & 3) * 32;  // the warp's first row
+      const int64_t orow = static_cast<int64_t>(it.q0 + tok) * a.out_token + head * a.out_head;
+      auto read_out = [&] {  // the reads are ordered before the arrival that lets the next PV overwrite O
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar_o_free[w]);
+      };
+      if (a.out_dtype == KVQ_OUT_F32) {
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t ov[32];
-        tmem_ld32(tO + c * 32, ov);
-        if (tok < it.len) store_row32(a, orow + c * 32, ov, inv);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          store_rows32<true>(a, sStage + warp * 2048, orow + c * 32, it.len - tok, ov, inv);
+        }
+        read_out();
+      } else {
+        uint32_t ov[D / 32][32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld32_issue(tO + c * 32, ov[c]);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_wait_ld32(ov[c]);
+        read_out();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          store_rows32<false>(a, sStage + warp * 2048, orow + c * 32, it.len - tok, ov[c], inv);
       }
-      tc_fence_before();  // the reads are ordered before the arrival that lets the next PV overwrite O
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bar_o_free[w]);
     }
   }
-  if (!ok) set_status(a.status, kStatusTimeout);
+  if (!ok) prompt_report(a, kStatusTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -418,8 +467,7 @@ kvq_status launch_prompt_d(const PromptArgs& a, cudaStream_t stream) {
   const int64_t blocks = static_cast<int64_t>(a.total) / kM + std::min<int64_t>(a.batch, a.total);  // at most
   const int64_t bound = (blocks * G / 2 + a.batch) * a.num_kv_heads;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(bound, a.sms));
-  kern<<<static_cast<unsigned>(grid), kThreads, Cfg::SMEM_BYTES, stream>>>(a, qm, km, vm);
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  return launch_cleared(kern, a, grid, kThreads, Cfg::SMEM_BYTES, qm, km, vm, stream);
 }
 
 }  // namespace

@@ -41,7 +41,8 @@ constexpr int kTabOff = kKvOff + kSlots * kKvTile;            // [batch] items p
 constexpr int kItemOff = kTabOff + kMaxPromptBatch * 4;       // [2] published items
 constexpr int kBarOff = kItemOff + 2 * 32;
 constexpr int kBars = 2 * kSlots + 13;
-constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;        // + slack to align the base
+constexpr int kStgOff = kBarOff + (kBars * 8 + 16 + 15) / 16 * 16;  // [4 softmax warps] 2 KB of output
+constexpr int kSmem = kStgOff + kSmWarps * 2048 + 1024;       // + slack to align the base
 constexpr int kOCol = 0, kSCol = 256, kPCol = 384;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -105,8 +106,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
   uint64_t* bar_item_free = bar_q_full + 11;   // [2] item slot read by the MMA warp and every softmax warp
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + kBarOff + kBars * 8);
 
+  uint8_t* sStage = smem + kStgOff;
+
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  if (tid == kLoadWarp * 32) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   prompt_table<1>(a, sTab);
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -158,9 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
         bar_arrive(&bar_item[k & 1]);
       }
       __syncwarp();
+      if (k == 0) wait_cleared();
       if (!it.live) break;
-      uint32_t next = 0;
-      if (lane == 0) next = atomicAdd(a.counter, 1u);
       // the Q tile, once the previous item's QKs have read theirs
       if (k >= 1 && !warp_wait_far(bar_q_empty, (k - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
@@ -170,6 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
           tma_rows(smem_u32(sQ + c * kQChunk), &qmap, c * 64, it.head[0], it.q0 + it.blk[0] * kM, bar_q_full);
       }
       __syncwarp();
+      uint32_t next = 0;
+      if (lane == 0) next = atomicAdd(a.counter, 1u);
       ++k;
       const int32_t n = key_tiles(it);
       for (int32_t i = 0; i < 2 * n; ++i, ++kv) {  // K of key tile i / 2, then its V
@@ -321,19 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
       if (!warp_wait_far(&bar_pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       const float inv = 1.0f / (l2.x + l2.y);
-      const int64_t orow = static_cast<int64_t>(it.q0 + tok) * a.out_token + static_cast<int64_t>(it.head[0]) * a.out_head;
+      const int32_t tok0 = it.blk[0] * kM + warp * 32;  // the warp's first row
+      const int64_t orow = static_cast<int64_t>(it.q0 + tok0) * a.out_token + static_cast<int64_t>(it.head[0]) * a.out_head;
 #pragma unroll 1
       for (int c = 0; c < kD / 32; ++c) {
         uint32_t ov[32];
         tmem_ld32(tO + c * 32, ov);
-        if (tok < it.len) store_row32(a, orow + c * 32, ov, inv);
+        if (a.out_dtype == KVQ_OUT_F32) store_rows32<true>(a, sStage + warp * 2048, orow + c * 32, it.len - tok0, ov, inv);
+        else store_rows32<false>(a, sStage + warp * 2048, orow + c * 32, it.len - tok0, ov, inv);
       }
       tc_fence_before();  // the reads are ordered before the arrival that lets the next PV overwrite O
       __syncwarp();
       if (lane == 0) bar_arrive(bar_o_free);
     }
   }
-  if (!ok) set_status(a.status, kStatusTimeout);
+  if (!ok) prompt_report(a, kStatusTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -353,8 +364,7 @@ kvq_status launch_prompt_wide(const PromptArgs& a, cudaStream_t stream) {
     return KVQ_ECUDA;
   const int64_t blocks = static_cast<int64_t>(a.total) / kM + std::min<int64_t>(a.batch, a.total);  // at most
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(blocks * a.num_q_heads, a.sms));
-  prompt_wide_kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, stream>>>(a, qm, km, vm);
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  return launch_cleared(prompt_wide_kernel, a, grid, kThreads, kSmem, qm, km, vm, stream);
 }
 
 }  // namespace kvq

@@ -16,6 +16,10 @@
  *               GQA pools keep separate K and V rows; MLA pools keep one latent row per token that
  *               serves as both (same page, "What this adds").
  *
+ * Around these two: extend attention over stored tokens (kvq_extend), causal attention over whole prompts before
+ * their rows are quantized (kvq_prompt), attention of a drafted token tree (kvq_tree), and the pages of the cache
+ * themselves: copies, forks, growth, release and the compaction of accepted drafts (kvq_pages_*).
+ *
  * Conventions for every entry point:
  *   - Pointers named as device pointers must point to device memory of the current device; host
  *     pointers (kvq_layout) are read during the call only.  The caller owns every buffer; the
