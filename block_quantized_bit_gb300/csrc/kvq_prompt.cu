@@ -280,6 +280,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptArgs a,
       const int32_t nA = it.blk[0] + 1, nB = it.blk[1] + 1, n = max(nA, nB);
       if (nA > 0 && !warp_wait_far(&bar_q_full[0], ni[0]++ & 1)) { ok = false; break; }
       if (nB > 0 && !warp_wait_far(&bar_q_full[1], ni[1]++ & 1)) { ok = false; break; }
+      auto clear = [&](int32_t j, uint32_t stage) {  // before the first PV that reads the tile
+        if (it.len - j * kM < kM)
+          clear_rows<Cfg::CH, kM>(sKV + stage * 2 * Cfg::TILE + Cfg::TILE, it.len - j * kM);
+      };
+      if (nA == nB) {  // (the usual item: its loop has no more branches than it needs)
+        uint32_t stage = kv % STAGES;
+        if (!warp_wait_far(&bar_full[stage], (kv / STAGES) & 1) || !qk(0, stage) || !qk(1, stage)) { ok = false; break; }
+        if (n == 1) mma_commit(bar_q_empty);
+        clear(0, stage);
+        if (!pv(0, stage, true)) { ok = false; break; }
+        for (int32_t j = 1; j < n; ++j) {
+          const uint32_t before = stage;
+          stage = ++kv % STAGES;
+          if (!warp_wait_far(&bar_full[stage], (kv / STAGES) & 1) || !qk(0, stage) || !pv(1, before, j == 1)) {
+            ok = false;
+            break;
+          }
+          mma_commit(&bar_empty[before]);
+          if (!qk(1, stage)) { ok = false; break; }
+          if (j == n - 1) {
+            mma_commit(bar_q_empty);
+            clear(j, stage);
+          }
+          if (!pv(0, stage, false)) { ok = false; break; }
+        }
+        if (!ok || !pv(1, stage, n == 1)) { ok = false; break; }
+        mma_commit(&bar_empty[stage]);
+        ++kv;
+        continue;
+      }
       uint32_t stage = 0, before = 0;
       for (int32_t j = 0; j <= n; ++j) {
         before = stage;
