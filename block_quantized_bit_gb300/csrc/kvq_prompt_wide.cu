@@ -226,26 +226,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
                     c > 0 ? 1u : 0u);
         mma_commit(&bar_s_full[nqk & 1]);
         mma_commit(&bar_empty[u % kSlots]);
-        if (j == n - 1) mma_commit(bar_q_empty);
         ++nqk;
         return true;
       };
-      if (!qk(0)) { ok = false; break; }
-      for (int32_t j = 0; j < n; ++j) {
-        if (j + 1 < n && !qk(j + 1)) { ok = false; break; }
+      auto pv = [&](int32_t j) -> bool {
         const uint32_t u = kv + 2 * j + 1;
-        if (!landed(u)) { ok = false; break; }
-        if (it.len - j * kKeys < kKeys)
-          clear_rows<kChunks, kKeys>(sKV + (u % kSlots) * kKvTile, it.len - j * kKeys);
-        if (j == 0 && k > 0 && !warp_wait_far(bar_o_free, (k - 1) & 1)) { ok = false; break; }
-        if (!warp_wait_far(&bar_p_full[npv & 1], (npv >> 1) & 1)) { ok = false; break; }
+        if (!warp_wait_far(&bar_p_full[npv & 1], (npv >> 1) & 1)) return false;
         tc_fence_after();
         mma_pv(tmem + kOCol, tmem + kPCol + (npv & 1) * (kKeys / 2),
                dv0 + static_cast<uint64_t>((u % kSlots) * (kKvTile >> 4)), idesc_pv, j > 0 ? 1u : 0u);
         mma_commit(&bar_pv_done[npv & 1]);
         mma_commit(&bar_empty[u % kSlots]);
         ++npv;
+        return true;
+      };
+      // (the first output and the last tile are taken out of the loop: its path is what the softmax waits for)
+      if (!qk(0)) { ok = false; break; }
+      for (int32_t j = 0; j < n - 1; ++j) {
+        if (!qk(j + 1)) { ok = false; break; }
+        if (j == 0 && k > 0 && !warp_wait_far(bar_o_free, (k - 1) & 1)) { ok = false; break; }
+        if (!landed(kv + 2 * j + 1) || !pv(j)) { ok = false; break; }
       }
+      if (!ok) break;
+      mma_commit(bar_q_empty);
+      const uint32_t u = kv + 2 * n - 1;
+      if (!landed(u)) { ok = false; break; }
+      if (it.len - (n - 1) * kKeys < kKeys)
+        clear_rows<kChunks, kKeys>(sKV + (u % kSlots) * kKvTile, it.len - (n - 1) * kKeys);
+      if (n == 1 && k > 0 && !warp_wait_far(bar_o_free, (k - 1) & 1)) { ok = false; break; }
+      if (!pv(n - 1)) { ok = false; break; }
       kv += 2 * n;
     }
     // before tensor memory is freed, every MMA issued must have completed
@@ -271,20 +280,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_wide_kernel(const PromptAr
         if (!warp_wait_far(&bar_s_full[b], (nt >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[kKeys];
-        tmem_ld32_issue(tS, s);
-        tmem_ld32_issue(tS + 32, s + 32);
-        tmem_wait_ld32(s);
-        tmem_wait_ld32(s + 32);
-        if ((j + 1) * kKeys > it.blk[0] * kM) {  // the tile reaches past the block's first row
+        float top;
+        if ((j + 1) * kKeys <= it.blk[0] * kM) {
+          uint32_t mx[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) tmem_ld32_max_issue(tS + 32 * c, s + 32 * c, mx[c]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_wait_ld32(s + 32 * c);
+            tmem_wait_max(mx[c]);
+          }
+          top = fmaxf(__uint_as_float(mx[0]), __uint_as_float(mx[1]));
+        } else {  // the tile reaches past the block's first row
+          tmem_ld32_issue(tS, s);
+          tmem_ld32_issue(tS + 32, s + 32);
+          tmem_wait_ld32(s);
+          tmem_wait_ld32(s + 32);
           const int32_t last = tok - j * kKeys;  // this row sees keys <= last of the tile
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < kKeys; ++e) s[e] = e <= last ? s[e] : 0xFF800000u;
+          for (int e = 0; e < kKeys; ++e) {
+            s[e] = e <= last ? s[e] : 0xFF800000u;
+            mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+          }
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < kKeys; e += 2)
-          mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.score_scale;
+        top *= a.score_scale;
         if (j == 0) {
           m = top;
         } else {
