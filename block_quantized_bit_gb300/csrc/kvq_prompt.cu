@@ -1,5 +1,5 @@
-// kvq_prompt.cu -- (head_dim 64 and 128; 256: kvq_prompt_wide.cu) causal attention over whole prompts, packed one behind the other, grouped heads, bf16, on the
-// tcgen05 tensor cores:
+// kvq_prompt.cu -- causal attention over whole prompts, packed one behind the other, grouped heads, bf16, on the tcgen05
+// tensor cores (head_dim 64 and 128; 256: kvq_prompt_wide.cu):
 //   out[i][h] = sum_{t <= i} softmax_t(sm_scale q[i][h].k[t][g]) v[t][g],  g = h / G, within each sequence.
 // 4 D FLOPs per (row, visible key) against 2 D bytes per row: bound by the tensor pipe once prompts pass some
 // hundred tokens, and by the softmax's exponentials, one per (row, key), close behind.
@@ -15,22 +15,29 @@
 // both tiles see the same keys.
 //
 // Warps 0-3 and 4-7: softmax of A and of B, one thread per row; the row's 128 scores stay in registers from the
-// one tensor-memory load to P.  Lazy rescaling as in the extend kernel (the running max moves only when a score
-// passes it by more than 2^8).
+// one tensor-memory load, which also returns their maxima, to P.  Lazy rescaling as in the extend kernel (the running max
+// moves only when a score passes it by more than 2^8).  O is read into registers at once, so that the next item's first PV
+// may overwrite it, and leaves through shared memory.
 // Warp 8 issues all MMAs.  Warp 9 takes items off a global counter, the longest first, and loads Q, K and V
 // tiles with TMA (128-byte swizzle), K and V of a key tile as one stage.
 // Only a tile's last key tile is masked: token blocks and key tiles both start at the sequence's start, so its
-// rule is key <= row.  Keys behind the sequence's end are never visible, but their V rows belong to whatever follows
-// and may be anything, so the MMA warp clears those rows in shared memory (0 * NaN would be NaN).
+// rule is key <= row, and a warp's 32 rows meet the diagonal in one 32-key chunk.  Keys behind the sequence's end are never
+// visible, but their V rows belong to whatever follows and may be anything, so the MMA warp clears those rows in
+// shared memory (0 * NaN would be NaN).
 // Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
 //
-// Measured, one prompt of 16384 tokens, 32 heads of 128: 1424 us = 1544 TFLOP/s, 82% of the measured GEMM burst rate;
-// back to back, under the board's power cap, 1504 us.  A trace of one CTA (per pair of key tiles, 3100 clocks of which
-// the MMAs are 2000): QK to S visible 900, softmax 1300, P to PV issued 200, PV to QK issued 600.  What the steps were
-// worth: short MMA-warp code (one stage and one wait for K and V, eight MMAs per elect) 1720 -> 1430 us, since
-// each wait on its path costs some 200 clocks.  Measured slower, and not kept: P handed over in halves, P formed against the
-// old maximum with the row's maximum beside it (1517), two threads per row (1491), polling waits (1475-1650), the
-// scores read twice from tensor memory in rolled loops (1571), three-input maxima and four partial sums (1456).
+// Measured, 32 heads of 128 over 8, one prompt of 16384 tokens: 1280 us = 1718 TFLOP/s, 90% of the measured GEMM burst
+// rate (long runs back to back, under the board's power cap: 1380 us); 8192 tokens 334 us; 16 heads over 8, eight prompts
+// of 150 to 2048 tokens: 44 us, of which the longest item's chain of key tiles is 25.  What bounds it: the MMA warp's
+// path (four MMA groups and five waits per pair of key tiles), then the board's power.  A trace of one CTA's key tile:
+// QK to S visible 500 clocks, softmax 1400, P to PV issued 350.
+// What the steps were worth, 16384 tokens: one stage and one wait for K and V, eight MMAs per elect 1720 -> 1430; maxima with
+// the tensor-memory load, waits' unlikely parts out of line 1400; output through shared memory, the diagonal's masks
+// on 32 keys 1366; the MMA loop without the branches of its first and last step 1280.
+// Measured slower, and not kept: P handed over in halves, P formed against the old maximum with the row's maximum
+// beside it, two threads per row, polling waits, the scores read twice from tensor memory in rolled loops; (against
+// 1370) the next item's first QK before this item's last PV 1410, a warp of its own for Q 1395; (against 1280) a softmax loop
+// of its own for the diagonal 1293, commits of the key stage behind the second QK 1557.
 #include <cuda.h>
 #include <math.h>
 
