@@ -26,6 +26,8 @@
  *     library allocates nothing and keeps no state between calls.  The one exception is
  *     kvq_decode_noalloc (with kvq_noalloc_status), whose scratch is a fixed array in the library's own
  *     device memory that keeps its contents from one call to the next.
+ *   - A workspace serves one call at a time: calls that may run on the GPU at the same time (on other streams, or in
+ *     graphs that are replayed side by side) need workspaces of their own.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls are asynchronous on it.
  *   - Arguments are validated on the host before anything is launched.  A failed validation returns
  *     a negative kvq_status and leaves every buffer untouched.  A launch failure returns KVQ_ECUDA.
