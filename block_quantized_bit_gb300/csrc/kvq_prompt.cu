@@ -27,17 +27,17 @@
 // Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
 //
 // Measured, 32 heads of 128 over 8, one prompt of 16384 tokens: 1280 us = 1718 TFLOP/s, 90% of the measured GEMM burst
-// rate (long runs back to back, under the board's power cap: 1380 us); 8192 tokens 334 us; 16 heads over 8, eight prompts
-// of 150 to 2048 tokens: 44 us, of which the longest item's chain of key tiles is 25.  What bounds it: the MMA warp's
-// path (four MMA groups and five waits per pair of key tiles), then the board's power.  A trace of one CTA's key tile:
-// QK to S visible 500 clocks, softmax 1400, P to PV issued 350.
-// What the steps were worth, 16384 tokens: one stage and one wait for K and V, eight MMAs per elect 1720 -> 1430; maxima with
-// the tensor-memory load, waits' unlikely parts out of line 1400; output through shared memory, the diagonal's masks
-// on 32 keys 1366; the MMA loop without the branches of its first and last step 1280.
-// Measured slower, and not kept: P handed over in halves, P formed against the old maximum with the row's maximum
-// beside it, two threads per row, polling waits, the scores read twice from tensor memory in rolled loops; (against
-// 1370) the next item's first QK before this item's last PV 1410, a warp of its own for Q 1395; (against 1280) a softmax loop
-// of its own for the diagonal 1293, commits of the key stage behind the second QK 1557.
+// rate (long runs back to back, under the board's power cap: 1380 us); 8192 tokens 334 us; 16 heads over 8, eight
+// prompts of 150 to 2048 tokens: 44 us, of which the longest item's chain of key tiles is 25.  What bounds it: the MMA
+// warp's path (four MMA groups and five waits per pair of key tiles), then the board's power.  A trace of one CTA's
+// key tile: QK to S visible 500 clocks, softmax 1400, P to PV issued 350. What the steps were worth, 16384 tokens: one
+// stage and one wait for K and V, eight MMAs per elect 1720 -> 1430; maxima with the tensor-memory load, waits'
+// unlikely parts out of line 1400; output through shared memory, the diagonal's masks on 32 keys 1366; the MMA loop
+// without the branches of its first and last step 1280. Measured slower, and not kept: P handed over in halves, P
+// formed against the old maximum with the row's maximum beside it, two threads per row, polling waits, the scores read
+// twice from tensor memory in rolled loops; (against 1370) the next item's first QK before this item's last PV 1410, a
+// warp of its own for Q 1395; (against 1280) a softmax loop of its own for the diagonal 1293, commits of the key stage
+// behind the second QK 1557.
 #include <cuda.h>
 #include <math.h>
 

@@ -24,18 +24,19 @@
 // Roles of a CTA's 28 warps: 0-7 softmax (two per lane quarter, each on half of a tile's keys; quarters without a row
 // only keep the barriers' counts), 8-15 dequantize K and 16-23 V, 26 looks up pages, 27 issues the MMAs.
 //
-// Measured: 32 sequences of 3..16 drafted tokens over 0.7k..8k, 4 heads per kv head (q8_0): 117 us, 2.8 TB/s; 4 x 32 over
-// 64k at head_dim 256, 8 heads per kv head (two blocks): 166 us, 829 TFLOP/s.  What bounds it: instruction issue.  A
-// tile costs a sub-partition about 2300 instructions (16 warps converting 64 codes each, the softmax, waits of some
+// Measured: 32 sequences of 3..16 drafted tokens over 0.7k..8k, 4 heads per kv head (q8_0): 117 us, 2.8 TB/s; 4 x 32
+// over 64k at head_dim 256, 8 heads per kv head (two blocks): 166 us, 829 TFLOP/s.  What bounds it: instruction issue.
+// A tile costs a sub-partition about 2300 instructions (16 warps converting 64 codes each, the softmax, waits of some
 // 100 clocks), against 1480 clocks that its bytes take at the memory's rate.  Of a tile's 2950 clocks (first case) the
-// softmax warps wait 300, the dequant warps 1050 and the MMA warp 2000; of 2700 (second) 700, 1050 and 1200.  What the steps were worth, first case / second:
-// one copy of the dequant code for K and V, one masked pass, eight MMAs per elect 183 -> 159 / 218; K and V by warps of
-// their own 157 / 204; the merge by a warp per row and without a clearing launch 146 / 201; loads straight into registers
-// instead of a staging ring, conflict-free stores without selects, waits' unlikely parts out of line 131 / 178; Q and P in
-// tensor memory 124 / 168.  Measured slower, and not kept: sixteen warps each taking K and then V (166), rows repeated in idle
-// lane quarters with the keys divided among them (137 / 183), one register set per warp rotated by moves (147); (against 117)
-// scores kept in registers from the maximum to P (125), a dequant warp less beside the softmax of short blocks (123), the MMA
-// loop without the branches of its first steps (120), no mask words on tiles without masks (117 / 169).
+// softmax warps wait 300, the dequant warps 1050 and the MMA warp 2000; of 2700 (second) 700, 1050 and 1200.  What the
+// steps were worth, first case / second: one copy of the dequant code for K and V, one masked pass, eight MMAs per
+// elect 183 -> 159 / 218; K and V by warps of their own 157 / 204; the merge by a warp per row and without a clearing
+// launch 146 / 201; loads straight into registers instead of a staging ring, conflict-free stores without selects,
+// waits' unlikely parts out of line 131 / 178; Q and P in tensor memory 124 / 168.  Measured slower, and not kept:
+// sixteen warps each taking K and then V (166), rows repeated in idle lane quarters with the keys divided among them
+// (137 / 183), one register set per warp rotated by moves (147); (against 117) scores kept in registers from the
+// maximum to P (125), a dequant warp less beside the softmax of short blocks (123), the MMA loop without the branches
+// of its first steps (120), no mask words on tiles without masks (117 / 169).
 #include <math.h>
 
 #include <algorithm>
