@@ -11,7 +11,8 @@
 // pace; that and the N = 64 QK (whose operands' shared-memory reads take 1.5 times its MMAs) bound it.
 // Measured, 8192 tokens, 16 heads of 256 over 2: 381 us = 1443 TFLOP/s, 75% of the measured GEMM burst rate (440 before
 // the waits' unlikely parts moved out of line and the rows left through shared memory, 404 before the MMA loop lost its
-// branches).
+// branches); 4 prompts of 900 to 2048 tokens 65.5 us.  Not kept: Q in tensor memory and P over S, which spares the QKs' reads
+// of Q (371 us) but puts a copy of Q between items (69 us).
 #include <cuda.h>
 #include <math.h>
 
