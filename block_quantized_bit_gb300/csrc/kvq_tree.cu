@@ -234,7 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
   __syncthreads();
 
   // ---- plan: units before every sequence
+  bool falls = false;  // q_start falls somewhere
   for (int32_t b = tid; b < a.batch; b += kThreads) {
+    falls |= __ldg(a.q_start + b + 1) < __ldg(a.q_start + b);
     const int32_t n = drafted(a, b, blockIdx.x == 0 ? my_status : nullptr);
     sTab[b + 1] = n == 0 ? 0 : row_blocks(n, G) * a.num_kv_heads * ((__ldg(a.seq_lens + b) + T - 1) / T);
   }
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     for (int i = 0; i < 12; ++i) mbar_init(&bar_pair[i], 2);
     fence_mbar_init();
   }
-  __syncthreads();
+  falls = __syncthreads_or(falls);
   if (warp == 0) {  // inclusive prefix, 32 sequences at a time
     int32_t run = 0;
     for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {
@@ -340,16 +342,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
     // While the first tile is on its way, the V warps write down the sequence of each query row for the merge, the
     // CTAs taking rows in turn: the last sequence whose rows begin at or before it, -1 where that one does not reach it.
+    // Where q_start falls, and so does not order the sequences, they are tried one by one: wrong entries take nothing
+    // from the valid sequences beside them.
     auto write_row_seq = [&]() {
+      auto covers = [&](int32_t b, int32_t i) -> bool {
+        return i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr);
+      };
       for (int32_t i = blockIdx.x * kDwThreads + wi * 32 + lane; i < a.total_q; i += gridDim.x * kDwThreads) {
-        int lo = 0, hi = a.batch;  // first b with q_start[b] > i
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(a.q_start + mid) <= i) lo = mid + 1;
-          else hi = mid;
+        int32_t b;
+        if (falls) {
+          b = a.batch - 1;
+          while (b >= 0 && !covers(b, i)) --b;
+        } else {
+          int lo = 0, hi = a.batch;  // first b with q_start[b] > i
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(a.q_start + mid) <= i) lo = mid + 1;
+            else hi = mid;
+          }
+          b = lo - 1;
+          if (b >= 0 && !covers(b, i)) b = -1;
         }
-        const int32_t b = lo - 1;
-        a.row_seq[i] = b >= 0 && i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr) ? b : -1;
+        a.row_seq[i] = b;
       }
     };
     struct Pieces {

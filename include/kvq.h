@@ -393,7 +393,8 @@ kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t
  * device: a sequence with n_b < 0, n_b > seq_lens[b], n_b > 64 * mask_words, q_start[b + 1] > total_q or
  * seq_lens[b] > max_pages_per_seq * 16 is skipped and makes kvq_workspace_status report KVQ_EINVAL, as does a
  * block-table entry >= layout->num_pages (that page is skipped).  Output rows of skipped sequences and behind the
- * last one are left as they are.
+ * last one are left as they are.  A wrong entry of q_start spoils the sequences on its two sides only; what a row
+ * receives that two consistent sequences claim is unspecified.
  */
 size_t kvq_tree_workspace_bytes(const kvq_layout* layout, int32_t batch, int32_t total_q, int32_t num_q_heads,
                                 int32_t max_pages_per_seq, int32_t path);
