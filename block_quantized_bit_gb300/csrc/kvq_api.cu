@@ -452,6 +452,11 @@ kvq_status pages_common(int32_t* block_table, int32_t max_pages, int32_t* seq_le
   return KVQ_OK;
 }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return b != nullptr && x < y + b_bytes && y < x + a_bytes;
+}
+
 // The status word of a page call with an empty list.
 kvq_status clear_status(void* workspace, cudaStream_t s) {
   return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
@@ -988,6 +993,13 @@ kvq_status kvq_pages_compact(void* pool, void* scales, const int32_t* block_tabl
                         static_cast<const void*>(q_start), static_cast<const void*>(new_lens),
                         static_cast<const void*>(page_refs)})
     if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  // new_lens is written while other CTAs still read the rest
+  const size_t b = batch, ints = b * sizeof(int32_t);
+  if (overlap(new_lens, ints, seq_lens, ints) || overlap(new_lens, ints, q_start, ints + sizeof(int32_t)) ||
+      overlap(new_lens, ints, block_table, ints * max_pages_per_seq) ||
+      overlap(new_lens, ints, keep, b * mask_words * sizeof(int64_t)) ||
+      overlap(new_lens, ints, page_refs, static_cast<size_t>(layout->num_pages) * sizeof(int32_t)))
+    return KVQ_EINVAL;
   st = kvq_device_check();
   if (st != KVQ_OK) return st;
   if (batch == 0) return clear_status(workspace, static_cast<cudaStream_t>(stream));

@@ -466,7 +466,9 @@ kvq_status kvq_pages_resize(int32_t* block_table, int32_t max_pages_per_seq, int
  * new_lens releases the surplus pages, once all layers are compacted.  A sequence is left as it is, with
  * new_lens[b] = seq_lens[b] and KVQ_EINVAL reported by kvq_workspace_status, when its numbers are inconsistent,
  * a page of its last n_b tokens is masked or past the pool, or, with page_refs not NULL, a page that rows would
- * move to is held by another row too.  workspace: at least 256 bytes, 16-byte aligned.
+ * move to is held by another row too.  new_lens may not overlap seq_lens or another input (KVQ_EINVAL): the old
+ * lengths are needed until every layer is compacted, and by the kvq_pages_resize behind them.  workspace: at least
+ * 256 bytes, 16-byte aligned.
  */
 kvq_status kvq_pages_compact(void* pool, void* scales, const int32_t* block_table, int32_t max_pages_per_seq,
                              const int32_t* seq_lens, const int32_t* q_start, const int64_t* keep, int32_t mask_words,
