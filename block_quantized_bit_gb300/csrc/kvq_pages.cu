@@ -225,11 +225,12 @@ __device__ __forceinline__ void release_page(const PagesArgs& a, int32_t p) {
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) {
   extern __shared__ int32_t s_pre[];  // [chunks] free pages before each chunk
-  __shared__ int32_t s_red[3][kPlanThreads / 32];
+  __shared__ int64_t s_need[2][kPlanThreads / 32];
+  __shared__ int32_t s_free[kPlanThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // pages needed by the entries before this one and by all; is every entry good?
-  int32_t before = 0, total = 0;
+  // pages needed by the entries before this one and by all (the demand may pass 32 bits); is every entry good?
+  int64_t before = 0, total = 0;
   bool bad = false;
   for (int32_t j = tid; j < a.n; j += kPlanThreads) {
     const PagesEntry& e = a.entries[j];
@@ -249,13 +250,13 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
       const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) s_red[2][warp] = incl;
+    if (lane == 31) s_free[warp] = incl;
     __syncthreads();
     int32_t off = 0, tot = 0;
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 32; ++w) {
-      off += w < warp ? s_red[2][w] : 0;
-      tot += s_red[2][w];
+      off += w < warp ? s_free[w] : 0;
+      tot += s_free[w];
     }
     if (c < a.chunks) s_pre[c] = free_total + off + incl - x;
     free_total += tot;
@@ -267,21 +268,22 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   if (lane == 0) {
-    s_red[0][warp] = before;
-    s_red[1][warp] = total;
+    s_need[0][warp] = before;
+    s_need[1][warp] = total;
   }
   bad = __syncthreads_or(bad);
   before = total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    before += s_red[0][w];
-    total += s_red[1][w];
+    before += s_need[0][w];
+    total += s_need[1][w];
   }
   if (bad || total > free_total) {
     if (i == 0 && blockIdx.y == 0 && tid == 0) set_status(a.status, bad ? kStatusBadPages : kStatusNoPages);
     if (FORK && blockIdx.y == 0 && tid == 0) a.copy_src[i] = a.copy_dst[i] = -1;
     return;
   }
+  const int32_t rank = static_cast<int32_t>(before);  // (at most the free pages)
   const PagesEntry e = a.entries[i];
   int32_t* row = a.block_table + static_cast<int64_t>(e.row) * a.max_pages;
   const int32_t c0 = blockIdx.y * kSliceCols, c1 = min(c0 + kSliceCols, a.max_pages);
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
       const int32_t old = row[c];
       int32_t now = c < e.used_new ? from[c] : -1;
       if (c == tail_col) {
-        now = free_page(a, s_pre, before);
+        now = free_page(a, s_pre, rank);
         a.copy_src[i] = e.tail;
         a.copy_dst[i] = now;
       }
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
     const int32_t lo = max(min(e.used_old, e.used_new), c0), hi = min(max(e.used_old, e.used_new), c1);
     for (int32_t c = lo + tid; c < hi; c += kPlanThreads) {
       if (e.used_new > e.used_old) {
-        const int32_t p = free_page(a, s_pre, before + c - e.used_old);
+        const int32_t p = free_page(a, s_pre, rank + c - e.used_old);
         a.page_refs[p] = 1;
         row[c] = p;
       } else {
