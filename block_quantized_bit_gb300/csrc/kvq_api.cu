@@ -396,7 +396,7 @@ struct PagesPlan {
 };
 
 bool plan_pages(const kvq_layout& L, int32_t n, int32_t max_pages, PagesPlan* pp) {
-  if (n < 0 || max_pages <= 0) return false;
+  if (n < 0 || n > kMaxPagesList || max_pages <= 0 || max_pages > kMaxPagesCols) return false;
   const int64_t chunks = (L.num_pages + kPagesChunk - 1) / kPagesChunk;
   if (chunks > kMaxPagesChunks) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -200,6 +200,9 @@ kvq_status launch_prompt_wide(const PromptArgs& a, cudaStream_t stream);
 // Pages of the cache (kvq_pages_*).
 constexpr int32_t kPagesChunk = 8192;       // pages whose counts one CTA of the plan reads
 constexpr int32_t kMaxPagesChunks = 8192;   // chunks whose prefixes fit the apply kernel's shared memory
+constexpr int32_t kPagesSlice = 2048;       // block-table columns one CTA of a fork or a resize works on
+constexpr int32_t kMaxPagesCols = 65535 * kPagesSlice;  // slices are a grid's y dimension
+constexpr int32_t kMaxPagesList = 0x7fffffff - kMaxPagesChunks;  // entries and chunks are its x dimension
 constexpr int32_t kMaxMaskWords = 4;        // 64-bit words of a drafted token's mask: 256 drafted tokens
 
 // What the plan finds for one list entry of a fork or a resize.

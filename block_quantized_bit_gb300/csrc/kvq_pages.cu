@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(uint4* codes, 
 constexpr int kPlanThreads = 256;
 constexpr int kChunkPages = kPagesChunk;           // pages one CTA of the plan looks at
 constexpr int kChunkWords = kChunkPages / 32;
-constexpr int kSliceCols = 8 * kPlanThreads;       // block-table columns one CTA works on
+constexpr int kSliceCols = kPagesSlice;            // block-table columns one CTA works on
+static_assert(kSliceCols % kPlanThreads == 0, "whole rounds of a CTA's threads");
 
 __device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t page_size) {
   return static_cast<int32_t>((static_cast<int64_t>(tokens) + page_size - 1) / page_size);
