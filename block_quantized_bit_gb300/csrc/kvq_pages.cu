@@ -214,10 +214,11 @@ __device__ __forceinline__ int32_t free_page(const PagesArgs& a, const int32_t* 
 }
 
 // One row less holds page p.  A count that is 0 already (a table that lists a page nobody counted) stays 0 and
-// is reported.
+// is reported: that the page was free before the call is in the bitmap, since another row may have taken it by now.
 __device__ __forceinline__ void release_page(const PagesArgs& a, int32_t p) {
   if (p < 0 || p >= a.num_pages) return;
-  if (atomicSub(a.page_refs + p, 1) <= 0) {
+  const bool was_free = (a.bits[p >> 5] >> (p & 31)) & 1u;
+  if (atomicSub(a.page_refs + p, 1) <= 0 || was_free) {
     atomicAdd(a.page_refs + p, 1);
     set_status(a.status, kStatusBadPages);
   }
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
     for (int32_t c = lo + tid; c < hi; c += kPlanThreads) {
       if (e.used_new > e.used_old) {
         const int32_t p = free_page(a, s_pre, rank + c - e.used_old);
-        a.page_refs[p] = 1;
+        atomicAdd(a.page_refs + p, 1);  // (0 -> 1; a wrong table may release the page at the same time)
         row[c] = p;
       } else {
         release_page(a, row[c]);

@@ -420,7 +420,8 @@ kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const i
  * [0, batch), the same row twice among those that change, a length outside [0, max_pages_per_seq * page_size])
  * changes nothing and makes kvq_workspace_status report KVQ_EINVAL; one that finds too few free pages changes
  * nothing and makes it report KVQ_ENOPAGES.  A count that would fall below 0 stays 0 and is reported as
- * KVQ_EINVAL.  Entries >= num_pages are kept in the rows but never counted.
+ * KVQ_EINVAL (where a fork both adds to and takes from a count that is too low, as timing has it: with the adds
+ * first it need not fall below 0).  Entries >= num_pages are kept in the rows but never counted.
  * workspace: at least kvq_pages_workspace_bytes for n list entries (0 if invalid), 16-byte aligned; its content on
  * entry is irrelevant.  All arrays int32, 4-byte aligned.  KVQ_EUNSUPPORTED (and 0 bytes): pools of more than 2^26
  * pages, rows of more than 65535 * 2048 pages, lists of more than 2^31 - 8193 entries.
