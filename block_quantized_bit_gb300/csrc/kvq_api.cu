@@ -20,7 +20,6 @@ namespace kvq {
 namespace {
 
 constexpr size_t kAlign = 16;
-constexpr uint32_t kStatusTimeoutWord = 0x7100u;  // written by a kernel that gave up a bounded wait
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) % kAlign) == 0; }
 

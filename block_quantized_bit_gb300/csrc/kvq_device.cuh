@@ -25,7 +25,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded waits give up after
 
 // Values a kernel writes to the workspace status word: it gave up a bounded wait; or a block-table
 // entry pointed past the pool (that page was skipped).
-constexpr uint32_t kStatusTimeout = 0x7100u;
+constexpr uint32_t kStatusTimeout = kStatusTimeoutWord;
 constexpr uint32_t kStatusBadPage = 0x7200u;
 constexpr uint32_t kStatusBadExtend = 0x7300u;  // q_start inconsistent with seq_lens or total_q
 constexpr uint32_t kStatusBadPages = 0x7400u;   // a page call's list, table or counts are inconsistent
@@ -106,8 +106,12 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       : "memory");
 }
 
+// The gravest report stays, whichever comes last; calls clear the word first.
+static_assert(kStatusTimeout > kStatusNoPages && kStatusTimeout > kStatusBadPages && kStatusTimeout > kStatusBadExtend &&
+                  kStatusTimeout > kStatusBadPage,
+              "no report may hide a timeout");
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t code) {
-  if (status) atomicExch(status, code);
+  if (status) atomicMax(status, code);
 }
 
 // ------------------------------------------------------------------------------ store conversions

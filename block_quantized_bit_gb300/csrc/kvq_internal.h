@@ -52,7 +52,10 @@ struct DecodeArgs {
 // Tokens per page the decode kernels support, and the workspace's leading status block.
 constexpr int kPageTokens = 16;
 constexpr size_t kWorkspaceHeader = 256;
-constexpr uint32_t kStatusNoPagesWord = 0x7500u;  // status word of a page call that found too few free pages
+// Status words.  Of two reports the larger one stays, so a wait that was given up, after which no output is valid, has
+// the largest.
+constexpr uint32_t kStatusNoPagesWord = 0x7500u;  // a page call found too few free pages
+constexpr uint32_t kStatusTimeoutWord = 0x7F00u;  // a kernel gave up a bounded wait
 
 // Work-item planning constants shared by the host (workspace bound) and the kernels.
 constexpr int kTargetItems = 1216;  // items when the host sets no target; also the SM count assumed without a device
