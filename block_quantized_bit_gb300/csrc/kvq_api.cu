@@ -350,7 +350,7 @@ struct TreePlan {
 
 bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t max_pages, int32_t path,
                TreePlan* tp) {
-  if (path < 0 || path > 2 || batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages <= 0) return false;
+  if (path < 0 || path > 2 || batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages <= 0 || max_pages > kMaxTreePages) return false;
   if (num_q_heads % L.num_kv_heads != 0) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int64_t G = num_q_heads / L.num_kv_heads;
@@ -768,6 +768,7 @@ kvq_status kvq_tree(const void* q, const void* pool, const void* scales, const i
   if (!(sm_scale > 0.0f) || sm_scale > std::numeric_limits<float>::max()) return KVQ_EINVAL;  // finite, > 0
   if (layout->page_size != kPageTokens || mask_words > kMaxMaskWords) return KVQ_EUNSUPPORTED;
   if (static_cast<int64_t>(max_pages_per_seq) * kPageTokens > std::numeric_limits<int32_t>::max()) return KVQ_EINVAL;
+  if (max_pages_per_seq > kMaxTreePages) return KVQ_EUNSUPPORTED;
   TreePlan tp;
   if (!plan_tree(*layout, batch, total_q, num_q_heads, max_pages_per_seq, path, &tp)) return KVQ_EUNSUPPORTED;
   if (!workspace) return KVQ_EINVAL;

@@ -167,6 +167,7 @@ struct TreeArgs {
   kvq_out_dtype out_dtype;
   kvq_kind kind;
 };
+constexpr int32_t kMaxTreePages = (0x7fffffff - 127) / kPageTokens;  // lengths are rounded up to tiles in 32 bits
 constexpr int32_t kMaxTreeBatch = 2048;  // sequences whose unit prefixes fit the kernel's shared table
 bool tree_tc_supported(int32_t head_dim, int32_t v_dim, int32_t mla, int32_t batch);
 kvq_status launch_tree_tc(const TreeArgs& a, cudaStream_t stream);

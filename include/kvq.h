@@ -389,7 +389,9 @@ kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t
  * launches.  Other shapes, the MLA row, and path 1: each drafted token is decoded as a sequence of its own with
  * the decode kernels and the mask, reading its context once per drafted token (mostly from L2).
  * Supported: page_size 16 and every kvq_decode shape (path 2: GQA with head_dim 128 or 256, or the MLA row with the
- * tensor-core decode's query heads); the flash kernel takes batch <= 2048.  q_start and seq_lens are read on the
+ * tensor-core decode's query heads); rows of at most 2^31 - 128 tokens.  The flash kernel takes batch <= 2048, and
+ * with G query heads per kv head batch * (2 G + 1) * num_kv_heads * (max_pages_per_seq / 4 + 1) < 2e9 and total_q *
+ * num_q_heads < 2e9; past that path 2 is KVQ_EUNSUPPORTED and path 0 takes path 1.  q_start and seq_lens are read on the
  * device: a sequence with n_b < 0, n_b > seq_lens[b], n_b > 64 * mask_words, q_start[b + 1] > total_q or
  * seq_lens[b] > max_pages_per_seq * 16 is skipped and makes kvq_workspace_status report KVQ_EINVAL, as does a
  * block-table entry >= layout->num_pages (that page is skipped).  Output rows of skipped sequences and behind the
