@@ -418,8 +418,8 @@ def run_e2e(args, case, L, codes, scales, sk, sv, ss, ix, decode, flush, world):
 
 # The sources the decode call is built from (host planning, kernels, shared device code): the traffic record
 # stays valid while these are unchanged, whatever else changes in the library.
-DECODE_SOURCES = ("kvq_api.cu", "kvq_decode.cu", "kvq_decode_mla.cu", "kvq_decode_tc.cu", "kvq_device.cuh",
-                  "kvq_internal.h", "kvq_plan.cuh", "kvq_tc.cuh")
+DECODE_SOURCES = ("kvq_api.cu", "kvq_decode.cu", "kvq_decode_cc.cuh", "kvq_decode_mla.cu", "kvq_decode_tc.cu",
+                  "kvq_device.cuh", "kvq_internal.h", "kvq_plan.cuh", "kvq_tc.cuh")
 
 
 def sources_sha256(files):

@@ -254,7 +254,9 @@ __device__ __forceinline__ int32_t mla_phys(const KParams& p, const MlaIter& t, 
   return (e >= 0 && e < p.num_pages) ? e : -1;
 }
 
-template <int KIND>
+// TREE: the sequences are drafted tokens (kvq_tree), each with a mask over the tail of its tokens.  An instance of its
+// own: the bit test of every token and the direct output cost plain decodes 1.7% (32 x 4096 356 -> 362 us).
+template <int KIND, bool TREE>
 __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KParams p,
                                                                      const __grid_constant__ CUtensorMap tmap) {
   using namespace mla;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
     mla_first(t, sTab, p, C, n_items);
     uint32_t n = 0;
     while (ok && t.live) {
-      int32_t phys = -1, vis = 0;  // vis: the page's tokens that are attended to
+      int32_t phys = -1, vis = 0;  // vis: the page's tokens that are attended to (TREE: a bit each, else their number)
       if (lane < kPagesPerTile) {
         const int32_t pg = t.pg0 + t.i * kPagesPerTile + lane;
         if (pg < t.pg1) {
@@ -361,7 +363,8 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
             set_status(p.status, kStatusBadPage);
             phys = -1;
           }
-          if (phys >= 0) vis = static_cast<int32_t>(page_vis(p, t.b, pg, t.L));
+          if (phys >= 0)  // (else >= 1: pg < the sequence's page count)
+            vis = TREE ? static_cast<int32_t>(page_vis(p, t.b, pg, t.L)) : min(kPage, t.L - pg * kPage);
         }
       }
       const uint32_t npg = __reduce_add_sync(0xffffffffu, phys >= 0 ? 1u : 0u);
@@ -430,7 +433,8 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
         const int rs = u % kRing, ks = u & 1;
         if (!mbar_wait_bounded(&bar_full[rs], (u / kRing) & 1)) { ok = false; break; }
         if (j == 0) {
-          v_ok = (sMeta[rs * kPagesPerTile + pi] >> off) & 1;
+          const int32_t vis = sMeta[rs * kPagesPerTile + pi];
+          v_ok = TREE ? (vis >> off) & 1 : off < vis;
           // the validity slot of this tile parity was last read by the softmax of tile n - 2
           if (n >= 2 && !mbar_wait_bounded(&bar_p_full[n & 1], ((n >> 1) - 1) & 1)) { ok = false; break; }
           if (part == 0) sValid[(n & 1) * kTile + tt] = v_ok ? 1 : 0;  // published with sc_free (last slab)
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(mla::kThreads, 1) decode_mla_kernel(const KPar
       // ---- item end: O^T -> partials (thread = dim within each 128-dim block); (m, l) per head
       if (!mbar_wait_bounded(&bar_pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
       mla_fence_after();
-      if (p.tree_mask != nullptr && t.pg0 == 0 && t.pg1 == seq_pages(p, t.b)) {
+      if (TREE && t.pg0 == 0 && t.pg1 == seq_pages(p, t.b)) {
         // A drafted token's only split (kvq_tree): its output, no partial.  (1024 drafted tokens of 64: the partials
         // alone were half a gigabyte each way.)
 #pragma unroll
@@ -892,12 +896,18 @@ bool decode_mla_tc_supported(int32_t head_dim, int32_t v_dim, int32_t is_mla, in
 }
 
 kvq_status launch_decode_mla_tc(const DecodeArgs& a, cudaStream_t stream) {
-  decltype(&decode_mla_kernel<KVQ_FP8_E4M3>) kern = nullptr;
+  const bool tree = a.tree_mask != nullptr;
+  decltype(&decode_mla_kernel<KVQ_FP8_E4M3, false>) kern = nullptr;
+  auto pick = [&](auto plain, auto masked) { kern = tree ? masked : plain; };
   switch (a.kind) {
-    case KVQ_FP8_E4M3: kern = decode_mla_kernel<KVQ_FP8_E4M3>; break;
-    case KVQ_Q8_0: kern = decode_mla_kernel<KVQ_Q8_0>; break;
-    case KVQ_FP8_E4M3_UNSCALED: kern = decode_mla_kernel<KVQ_FP8_E4M3_UNSCALED>; break;
-    case KVQ_FP8_E5M2_UNSCALED: kern = decode_mla_kernel<KVQ_FP8_E5M2_UNSCALED>; break;
+    case KVQ_FP8_E4M3: pick(decode_mla_kernel<KVQ_FP8_E4M3, false>, decode_mla_kernel<KVQ_FP8_E4M3, true>); break;
+    case KVQ_Q8_0: pick(decode_mla_kernel<KVQ_Q8_0, false>, decode_mla_kernel<KVQ_Q8_0, true>); break;
+    case KVQ_FP8_E4M3_UNSCALED:
+      pick(decode_mla_kernel<KVQ_FP8_E4M3_UNSCALED, false>, decode_mla_kernel<KVQ_FP8_E4M3_UNSCALED, true>);
+      break;
+    case KVQ_FP8_E5M2_UNSCALED:
+      pick(decode_mla_kernel<KVQ_FP8_E5M2_UNSCALED, false>, decode_mla_kernel<KVQ_FP8_E5M2_UNSCALED, true>);
+      break;
   }
   if (kern == nullptr) return KVQ_EKIND;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, mla::SMEM_BYTES) != cudaSuccess)

@@ -83,6 +83,7 @@ int32_t decode_mla_tc_heads_per_item(int32_t group);
 kvq_status launch_decode_mla_tc(const DecodeArgs& a, cudaStream_t stream);
 kvq_status launch_decode_tc(const DecodeArgs& a, cudaStream_t stream);
 kvq_status launch_decode_cc(const DecodeArgs& a, cudaStream_t stream);
+kvq_status launch_decode_cc_masked(const DecodeArgs& a, cudaStream_t stream);  // with a.tree_mask
 kvq_status launch_merge(const DecodeArgs& a, int32_t query_groups, cudaStream_t stream);
 
 // Sparse decode: the gather of the selected columns into a compact pool (pages b * cpages ..).
