@@ -128,14 +128,6 @@ __device__ __forceinline__ uint32_t mla_idesc(bool a_mn_major, bool b_mn_major) 
 // and the lane chosen by elect.sync issues (the descriptors stay in uniform registers, which a probe measured
 // at 15 to 40 clocks per MMA against 56 from a lane-0 branch).  The full mask elects the same lane every
 // time, so a commit tracks every MMA issued before it.
-__device__ __forceinline__ void mla_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 __device__ __forceinline__ void mla_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                            uint32_t acc) {
   asm volatile(

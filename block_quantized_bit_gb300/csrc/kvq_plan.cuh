@@ -75,23 +75,19 @@ __device__ __forceinline__ uint64_t tree_window(const int64_t* mask, int32_t wor
   return s == 0 ? word(w) : (word(w) >> s) | (word(w + 1) << (64 - s));
 }
 
-// Tokens of page pg that sequence b attends to (bit t = token t of the page): those before its end, and of
-// the drafted tokens those in its mask.
+// Drafted tokens (kvq_tree): those of page pg that sequence b, one of them, attends to (bit t = token t of the page):
+// the ones before its end, and of the drafted ones those in its mask.
 __device__ __forceinline__ uint32_t page_vis(const KParams& p, int32_t b, int32_t pg, int32_t L) {
   const int32_t left = L - pg * kPage;
   uint32_t v = left >= kPage ? 0xFFFFu : left > 0 ? (1u << left) - 1u : 0u;
-  if (p.tree_mask != nullptr) {
-    const int32_t j0 = pg * kPage - __ldg(p.tree_base + b);
-    if (j0 > -kPage)
-      v &= static_cast<uint32_t>(tree_window(p.tree_mask + static_cast<int64_t>(b) * p.tree_words, p.tree_words, j0));
-  }
+  const int32_t j0 = pg * kPage - __ldg(p.tree_base + b);
+  if (j0 > -kPage)
+    v &= static_cast<uint32_t>(tree_window(p.tree_mask + static_cast<int64_t>(b) * p.tree_words, p.tree_words, j0));
   return v;
 }
 
 // A query row that no sequence covers (kvq_tree): its output is left as it was.
-__device__ __forceinline__ bool uncovered(const KParams& p, int32_t b) {
-  return p.tree_mask != nullptr && __ldg(p.bt_row + b) < 0;
-}
+__device__ __forceinline__ bool uncovered(const KParams& p, int32_t b) { return __ldg(p.bt_row + b) < 0; }
 
 __device__ __forceinline__ int32_t seq_pages(const KParams& p, int32_t b) {
   const int32_t L = max(__ldg(p.seq_lens + b), 0);

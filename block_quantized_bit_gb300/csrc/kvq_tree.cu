@@ -169,7 +169,6 @@ struct TreeIter {
       t = s.t0;
     }
   }
-  __device__ __forceinline__ bool last_tile() const { return t == s.t1 - 1; }
   __device__ __forceinline__ void next_segment(const int32_t* tab, const TreeArgs& a, int32_t G) {
     u += s.t1 - s.t0;
     live = u < r.u1;
