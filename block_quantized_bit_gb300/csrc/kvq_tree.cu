@@ -109,6 +109,19 @@ __device__ __forceinline__ int32_t drafted(const TreeArgs& a, int32_t b, uint32_
   return n;
 }
 
+// The last valid sequence that covers query row i, or -1, when q_start falls and so does not order the sequences: wrong
+// entries take nothing from the valid sequences beside them.  (Out of line, and its condition in shared memory: in the
+// dequant warps' code and registers it cost 1%, 112.3 -> 113.7 us at 32 sequences of 3..16 drafts.)
+__device__ __noinline__ int32_t search_sequence(const int32_t* q_start, const int32_t* seq_lens, int32_t batch,
+                                                int32_t total_q, int32_t max_drafts, int64_t max_tokens, int32_t i) {
+  int32_t b = batch - 1;
+  for (; b >= 0; --b) {
+    const int32_t q0 = __ldg(q_start + b), q1 = __ldg(q_start + b + 1), L = __ldg(seq_lens + b);
+    if (q0 >= 0 && q0 <= i && i < q1 && q1 <= total_q && q1 - q0 <= L && q1 - q0 <= max_drafts && L <= max_tokens) break;
+  }
+  return b;
+}
+
 __device__ __forceinline__ int32_t row_blocks(int32_t n, int32_t G) { return (n * G + kM - 1) / kM; }
 
 // A segment: the tiles [t0, t1) of row block blk of (sequence b, kv head g); slot: where its partial goes, or -1
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
   uint64_t* bar_o_free = bar_k_full + 11;         // a segment's O read out (softmax warps), once per segment
   uint64_t* bar_pair = bar_k_full + 14;           // [4 quarters][2 parities] both half-tile maxima written
   uint64_t* bar_sum = bar_k_full + 22;            // [4 quarters] both half row sums written, once per segment
-  uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);  // address; does q_start fall?
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t G = a.num_q_heads / a.num_kv_heads;
@@ -258,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     fence_mbar_init();
   }
   falls = __syncthreads_or(falls);
+  if (tid == 0) sTmem[1] = falls;
   if (warp == 0) {  // inclusive prefix, 32 sequences at a time
     int32_t run = 0;
     for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {
@@ -341,17 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
     const uint32_t total = range.u1 - range.u0;  // tiles of this CTA
     // While the first tile is on its way, the V warps write down the sequence of each query row for the merge, the
     // CTAs taking rows in turn: the last sequence whose rows begin at or before it, -1 where that one does not reach it.
-    // Where q_start falls, and so does not order the sequences, they are tried one by one: wrong entries take nothing
-    // from the valid sequences beside them.
     auto write_row_seq = [&]() {
-      auto covers = [&](int32_t b, int32_t i) -> bool {
-        return i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr);
-      };
       for (int32_t i = blockIdx.x * kDwThreads + wi * 32 + lane; i < a.total_q; i += gridDim.x * kDwThreads) {
         int32_t b;
-        if (falls) {
-          b = a.batch - 1;
-          while (b >= 0 && !covers(b, i)) --b;
+        if (sTmem[1]) {  // q_start falls somewhere
+          b = search_sequence(a.q_start, a.seq_lens, a.batch, a.total_q, 64 * a.mask_words,
+                              static_cast<int64_t>(a.max_pages) * kPage, i);
         } else {
           int lo = 0, hi = a.batch;  // first b with q_start[b] > i
           while (lo < hi) {
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a) 
             else hi = mid;
           }
           b = lo - 1;
-          if (b >= 0 && !covers(b, i)) b = -1;
+          if (b >= 0 && !(i >= __ldg(a.q_start + b) && i < __ldg(a.q_start + b) + drafted(a, b, nullptr))) b = -1;
         }
         a.row_seq[i] = b;
       }
