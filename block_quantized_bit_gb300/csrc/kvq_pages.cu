@@ -227,18 +227,21 @@ __device__ __forceinline__ void release_page(const PagesArgs& a, int32_t p) {
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) {
   extern __shared__ int32_t s_pre[];  // [chunks] free pages before each chunk
-  __shared__ int64_t s_need[2][kPlanThreads / 32];
+  __shared__ uint32_t s_need[2][kPlanThreads / 32];
   __shared__ int32_t s_free[kPlanThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // pages needed by the entries before this one and by all (the demand may pass 32 bits); is every entry good?
-  int64_t before = 0, total = 0;
+  // pages needed by the entries before this one and by all; is every entry good?  (The demand may pass 32 bits: sums
+  // stop at a number that no pool has.)
+  constexpr uint32_t kTooMany = 1u << 27;
+  static_assert(kTooMany > static_cast<int64_t>(kMaxPagesChunks) * kPagesChunk, "more than the pages of any pool");
+  uint32_t before = 0, total = 0;
   bool bad = false;
   for (int32_t j = tid; j < a.n; j += kPlanThreads) {
     const PagesEntry& e = a.entries[j];
-    const int32_t need = e.need;
-    total += need;
-    before += j < i ? need : 0;
+    const uint32_t need = e.need;
+    total = min(total + need, kTooMany);
+    before = min(before + (j < i ? need : 0u), kTooMany);
     bad |= e.row < 0;
   }
   // exclusive prefix over the chunks, kPlanThreads at a time
@@ -266,8 +269,8 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before = min(before + __shfl_xor_sync(0xffffffffu, before, o), kTooMany);
+    total = min(total + __shfl_xor_sync(0xffffffffu, total, o), kTooMany);
   }
   if (lane == 0) {
     s_need[0][warp] = before;
@@ -277,10 +280,10 @@ __global__ void __launch_bounds__(kPlanThreads) apply_pages_kernel(PagesArgs a) 
   before = total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    before += s_need[0][w];
-    total += s_need[1][w];
+    before = min(before + s_need[0][w], kTooMany);
+    total = min(total + s_need[1][w], kTooMany);
   }
-  if (bad || total > free_total) {
+  if (bad || total > static_cast<uint32_t>(free_total)) {
     if (i == 0 && blockIdx.y == 0 && tid == 0) set_status(a.status, bad ? kStatusBadPages : kStatusNoPages);
     if (FORK && blockIdx.y == 0 && tid == 0) a.copy_src[i] = a.copy_dst[i] = -1;
     return;
