@@ -17,11 +17,11 @@
 // The bitmap is a snapshot, so apply never reads a count that another CTA of it may have changed.
 //
 // Both move few bytes (4 B per page of the rows, 4 B per page of the pool); they are bound by the latency of
-// two dependent launches: in a graph a fork of 64 rows takes 7.6 us, of 32 rows over 2048 columns 11 us, a resize 3.4 to
-// 4.7 us.  A caller that launches them one by one waits for the host instead (9 us per call from Python).
+// two dependent launches: in a graph a fork of 64 rows takes 8 us, of 32 rows over 2048 columns 12 us, a resize of 1 to
+// 64 rows 5 to 6 us.  A caller that launches them one by one waits for the host instead (9 us per call from Python).
 //
 // copy is bound by HBM: 16384 pages (570 MB read and written) 87.9 us, 6.5 TB/s, 96% of the measured copy rate; a call of
-// some pages takes 2.4 us in a graph.  compact moves the few kept rows of each sequence, a CTA per (sequence, K or V,
+// some pages takes 2.7 us in a graph.  compact moves the few kept rows of each sequence, a CTA per (sequence, K or V,
 // head), and is bound by its chain of dependent loads: 4 to 6 us in a graph.
 #include <cuda_runtime.h>
 

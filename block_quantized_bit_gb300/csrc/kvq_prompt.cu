@@ -26,9 +26,11 @@
 // shared memory (0 * NaN would be NaN).
 // Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
 //
-// Measured, 32 heads of 128 over 8, one prompt of 16384 tokens: 1280 us = 1718 TFLOP/s, 90% of the measured GEMM burst
-// rate (long runs back to back, under the board's power cap: 1380 us); 8192 tokens 334 us; 16 heads over 8, eight
-// prompts of 150 to 2048 tokens: 44 us, of which the longest item's chain of key tiles is 25.  What bounds it: the MMA
+// Measured, 32 heads of 128 over 8, one prompt of 16384 tokens: 1280 us = 1718 TFLOP/s, 91% of the measured GEMM burst
+// rate (long runs back to back, under the board's power cap: 1390 us); 8192 tokens 336 us; 16 heads over 8, eight
+// prompts of 150 to 2048 tokens: 40.5 us in a graph, of which the longest item's chain of key tiles is 25.  32 heads of 64
+// over 8, 8192 tokens: 263 us = 1045 TFLOP/s, eight prompts of 150 to 2048 tokens 54.5 us: half the products for the
+// same softmax, so a tile's own chain (2340 clocks a key tile, see the trace) paces it.  What bounds head_dim 128: the MMA
 // warp's path (four MMA groups and five waits per pair of key tiles), then the board's power.  A trace of one CTA's
 // key tile: QK to S visible 500 clocks, softmax 1400, P to PV issued 350. What the steps were worth, 16384 tokens: one
 // stage and one wait for K and V, eight MMAs per elect 1720 -> 1430; maxima with the tensor-memory load, waits'

@@ -9,9 +9,9 @@
 // Warps 0-3: softmax, one thread per row.  Warp 4 issues the MMAs, warp 5 takes items and loads tiles.
 // A K/V tile pair (64 KB) serves 128 x 64 scores only, so L2 feeds each SM about 50 B per clock at the tensor pipe's
 // pace; that and the N = 64 QK (whose operands' shared-memory reads take 1.5 times its MMAs) bound it.
-// Measured, 8192 tokens, 16 heads of 256 over 2: 381 us = 1443 TFLOP/s, 75% of the measured GEMM burst rate (440 before
+// Measured, 8192 tokens, 16 heads of 256 over 2: 383 us = 1437 TFLOP/s, 76% of the measured GEMM burst rate (440 before
 // the waits' unlikely parts moved out of line and the rows left through shared memory, 404 before the MMA loop lost its
-// branches); 4 prompts of 900 to 2048 tokens 65.5 us.  Not kept: Q in tensor memory and P over S, which spares the QKs' reads
+// branches); 4 prompts of 900 to 2048 tokens 65.5 us, 8 of 150 to 2048 77.  Not kept: Q in tensor memory and P over S, which spares the QKs' reads
 // of Q (371 us) but puts a copy of Q between items (69 us).
 #include <cuda.h>
 #include <math.h>

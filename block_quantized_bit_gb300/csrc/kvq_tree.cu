@@ -24,12 +24,13 @@
 // Roles of a CTA's 28 warps: 0-7 softmax (two per lane quarter, each on half of a tile's keys; quarters without a row
 // only keep the barriers' counts), 8-15 dequantize K and 16-23 V, 26 looks up pages, 27 issues the MMAs.
 //
-// Measured: 32 sequences of 3..16 drafted tokens over 0.7k..8k, 4 heads per kv head (q8_0): 117 us, 2.8 TB/s; 4 x 32
-// over 64k at head_dim 256, 8 heads per kv head (two blocks): 166 us, 829 TFLOP/s.  What bounds it: instruction issue.
-// A tile costs a sub-partition about 2300 instructions (16 warps converting 64 codes each, the softmax, waits of some
-// 100 clocks), against 1480 clocks that its bytes take at the memory's rate.  Of a tile's 2950 clocks (first case) the
-// softmax warps wait 300, the dequant warps 1050 and the MMA warp 2000; of 2700 (second) 700, 1050 and 1200.  What the
-// steps were worth, first case / second: one copy of the dequant code for K and V, one masked pass, eight MMAs per
+// Measured: 32 sequences of 3..16 drafted tokens over 0.7k..8k, 4 heads per kv head (q8_0): 113 us in a graph, 2.9
+// TB/s; 4 x 32 over 64k at head_dim 256, 8 heads per kv head (two blocks): 162 us, 847 TFLOP/s.  What bounds it: the
+// latency of the softmax's chain.  Of a tile's 2950 clocks (first case) the softmax warps wait 300, the dequant warps
+// 1050 and the MMA warp 2000: blocks of 12 to 64 rows leave the softmax to one or two of four lane quarters, whose two
+// passes and the meeting between them follow one another.  No unit is full (issue slots 57%, tensor pipe 36%, DRAM 39%;
+// the first stall is long_scoreboard).  Of 2700 clocks (second case) the three wait 700, 1050 and 1200 on one another, and
+// each of the two blocks converts every tile for itself.  What the steps were worth, first case / second: one copy of the dequant code for K and V, one masked pass, eight MMAs per
 // elect 183 -> 159 / 218; K and V by warps of their own 157 / 204; the merge by a warp per row and without a clearing
 // launch 146 / 201; loads straight into registers instead of a staging ring, conflict-free stores without selects,
 // waits' unlikely parts out of line 131 / 178; Q and P in tensor memory 124 / 168.  Measured slower, and not kept:
@@ -851,8 +852,9 @@ kvq_status launch_tree_d(const TreeArgs& a, cudaStream_t stream) {
     return KVQ_ECUDA;
   kern<<<static_cast<unsigned>(a.grid), kThreads, Cfg::SMEM_BYTES, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
-  // Few rows: a CTA for each (their blocks are cut into many segments); else a warp for each (64 rows 5.7 us, 9600
-  // rows 23 us with a CTA each).
+  // Few rows: a CTA for each; else a warp for each.  The whole call with a CTA / a warp: 128 rows in many segments (one
+  // sequence of 64k) 42.2 / 77.4 us, 1024 86.9 / 97.3, 2048 163.7 / 166.5 (four of 64k) and 52.6 / 53.1 (eight of 8k),
+  // 3072 75.7 / 75.4, 4096 302.0 / 298.2; in few segments 2048 53.7 / 53.0, 9216 103.0 / 91.3, 32768 113.3 / 73.5.
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.num_q_heads;
   const bool few = rows <= 2048;
   cudaLaunchConfig_t cfg = {};

@@ -359,7 +359,8 @@ kvq_status kvq_workspace_status(const void* workspace, void* stream);
  * within a sequence v must be finite (a non-finite row also spoils up to 127 rows before it).
  * Supported: head_dim 64, 128 and 256, any number of query heads per kv head, batch <= 2048.  q_start is read on
  * the device: a sequence with q_start[b] < 0, q_start[b + 1] < q_start[b] or q_start[b + 1] > total is skipped
- * and makes kvq_workspace_status report KVQ_EINVAL.  Output rows that no sequence covers are left as they are.
+ * and makes kvq_workspace_status report KVQ_EINVAL.  Output rows that no sequence covers are left as they are; what a
+ * row receives that two consistent sequences claim is unspecified.
  */
 typedef struct kvq_prompt_strides {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
