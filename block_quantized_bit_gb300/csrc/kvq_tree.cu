@@ -854,7 +854,7 @@ kvq_status launch_tree_d(const TreeArgs& a, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
   // Few rows: a CTA for each; else a warp for each.  The whole call with a CTA / a warp: 128 rows in many segments (one
   // sequence of 64k) 42.2 / 77.4 us, 1024 86.9 / 97.3, 2048 163.7 / 166.5 (four of 64k) and 52.6 / 53.1 (eight of 8k),
-  // 3072 75.7 / 75.4, 4096 302.0 / 298.2; in few segments 2048 53.7 / 53.0, 9216 103.0 / 91.3, 32768 113.3 / 73.5.
+  // 2560 54.0 / 53.5, 4096 302.0 / 298.2; in few segments 2048 53.7 / 53.0, 9216 103.0 / 91.3, 32768 113.3 / 73.5.
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.num_q_heads;
   const bool few = rows <= 2048;
   cudaLaunchConfig_t cfg = {};
