@@ -427,11 +427,12 @@ def _own(s):
         return _shown(s)
     if case["op"] == "decode":
         if "ws" not in s:
-            s["ws"] = kvq.alloc_workspace(L, s["lens"].numel(), hq, s["table"].shape[1], DEV)
+            s["ws"] = kvq.alloc_workspace(L, s["lens"].numel(), hq, s["table"].shape[1], DEV, kind=kind)
         kvq.kvq_decode(s["q"], s["codes"], s["scales"], s["table"], s["lens"], s["out"], s["ws"], L, kind, s["scale"])
     else:
         if "ws" not in s:
-            s["ws"] = kvq.alloc_extend_workspace(DEV, L, s["q"].shape[0], hq, s["table"].shape[1])
+            s["ws"] = kvq.alloc_extend_workspace(DEV, L, s["q"].shape[0], hq, s["table"].shape[1], kind=kind,
+                                                 batch=s["lens"].numel())
         kvq.kvq_extend(s["q"], s["codes"], s["scales"], s["table"], s["lens"], s["start"], s["out"], s["ws"], L, kind,
                        s["scale"])
     return s["out"]
