@@ -5,8 +5,8 @@ The compute lives in ``libkvq.so`` (CUDA, sm_103a, built from ``csrc/``); ``kvq`
 binding and ``workloads`` the seeded synthetic inputs.
 """
 from . import kvq  # noqa: F401
-from .kvq import (Layout, KvqError, alloc_pages_workspace, alloc_pool, alloc_prompt_workspace,  # noqa: F401
-                  alloc_tree_workspace, alloc_workspace, kvq_bytes_per_token, kvq_decode,
+from .kvq import (Layout, KvqError, alloc_append_workspace, alloc_pages_workspace, alloc_pool,  # noqa: F401
+                  alloc_prompt_workspace, alloc_tree_workspace, alloc_workspace, kvq_append, kvq_bytes_per_token, kvq_decode,
                   kvq_decode_workspace_bytes, kvq_dequant_probe, kvq_device_check, kvq_encode_probe, kvq_num_pages,
                   kvq_pages_compact, kvq_pages_copy, kvq_pages_fork, kvq_pages_resize, kvq_pool_bytes, kvq_prompt,
                   kvq_scale_bytes, kvq_store, kvq_tree, kvq_version, kvq_workspace_status)

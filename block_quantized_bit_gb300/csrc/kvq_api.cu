@@ -45,8 +45,11 @@ bool kind_ok(int kind) { return kind == KVQ_FP8_E4M3 || kind == KVQ_Q8_0; }
 // Kinds the attention entry points read: the block-scaled ones and the unscaled fp8 casts.
 bool kind_read_ok(int kind) { return kind_ok(kind) || kind == KVQ_FP8_E4M3_UNSCALED || kind == KVQ_FP8_E5M2_UNSCALED; }
 
+// Kinds that kvq_append writes: these and the one whose scale belongs to a page and head.
+bool kind_append_ok(int kind) { return kind_read_ok(kind) || kind == KVQ_FP8_E4M3_PAGE; }
+
 // The unscaled kinds have no scale array: their scales pointer is ignored (it may be NULL).
-bool has_scales(int kind) { return kind_ok(kind); }
+bool has_scales(int kind) { return kind_ok(kind) || kind == KVQ_FP8_E4M3_PAGE; }
 
 // SMs of the current device (the MLA tensor-core plan targets one work item per SM).
 int32_t sm_count() {
@@ -387,6 +390,104 @@ bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   return true;
 }
 
+// Attention over a KVQ_FP8_E4M3_PAGE cache: the rows kernel and what joins its runs.  max_bytes caps the workspace, and
+// with it the CTAs (0: no cap).
+struct PagePlan {
+  int32_t grid;
+  size_t ml_offset, acc_offset, total;
+};
+
+bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t max_pages,
+               size_t max_bytes, PagePlan* pp) {
+  if (batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages <= 0 || num_q_heads % L.num_kv_heads != 0) return false;
+  if (L.mla || L.page_size != kPageTokens || !page_supported(L.head_dim)) return false;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t tab = up((static_cast<size_t>(batch) + 1) * sizeof(int64_t));
+  const size_t slot = kPageRowsTile * (static_cast<size_t>(L.head_dim) + 2) * sizeof(float);
+  // units of work at most: pages of tiles of 16 rows
+  const double tiles = batch + static_cast<double>(total_q) * (num_q_heads / L.num_kv_heads) / kPageRowsTile;
+  const double units = tiles * L.num_kv_heads * max_pages;
+  int64_t grid = page_rows_grid(L.head_dim, sm_count());
+  if (units < static_cast<double>(grid) * kPageMinUnits) grid = static_cast<int64_t>(units / kPageMinUnits) + 1;
+  if (max_bytes > 0) {
+    if (max_bytes < kWorkspaceHeader + tab + 1024) return false;
+    grid = std::min<int64_t>(grid, (max_bytes - kWorkspaceHeader - tab - 512) / (2 * slot));
+  }
+  if (grid < 1) return false;
+  const size_t slots = 2 * static_cast<size_t>(grid);
+  pp->grid = static_cast<int32_t>(grid);
+  pp->ml_offset = kWorkspaceHeader + tab;
+  pp->acc_offset = pp->ml_offset + up(slots * kPageRowsTile * 2 * sizeof(float));
+  pp->total = pp->acc_offset + up(slots * kPageRowsTile * L.head_dim * sizeof(float));
+  return true;
+}
+
+// q_start null: one row per sequence (kvq_decode).  The host's checks that the kinds share are done.
+kvq_status page_common(const void* q, const void* pool, const void* scales, const int32_t* block_table, int32_t max_pages,
+                       const int32_t* seq_lens, const int32_t* q_start, int32_t total_q, int32_t batch,
+                       int32_t num_q_heads, float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace,
+                       size_t workspace_bytes, const kvq_layout* layout, bool cap, cudaStream_t s) {
+  if (layout->mla || layout->page_size != kPageTokens || !page_supported(layout->head_dim)) return KVQ_EUNSUPPORTED;
+  if (static_cast<int64_t>(max_pages) * kPageTokens > std::numeric_limits<int32_t>::max()) return KVQ_EINVAL;
+  if (static_cast<int64_t>(total_q) * num_q_heads > std::numeric_limits<int32_t>::max()) return KVQ_EUNSUPPORTED;
+  PagePlan pp;
+  if (!plan_page(*layout, batch, total_q, num_q_heads, max_pages, cap ? workspace_bytes : 0, &pp))
+    return cap ? KVQ_EWORKSPACE : KVQ_EINVAL;
+  const bool empty = batch == 0 || total_q == 0;
+  if (!workspace) return empty && q_start == nullptr ? KVQ_OK : KVQ_EINVAL;
+  if (workspace_bytes < pp.total) return KVQ_EWORKSPACE;
+  if (!empty && (!q || !pool || !scales || !block_table || !seq_lens || !out)) return KVQ_EINVAL;
+  if (!aligned(workspace) || !aligned(q) || !aligned(pool) || !aligned(scales) || !aligned(out)) return KVQ_EALIGN;
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(q_start)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  const kvq_status st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  if (empty) return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PageArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.codes = static_cast<const uint8_t*>(pool);
+  a.scales = static_cast<const float*>(scales);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.out = out;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.tab = reinterpret_cast<int64_t*>(ws + kWorkspaceHeader);
+  a.part_ml = reinterpret_cast<float*>(ws + pp.ml_offset);
+  a.part_acc = reinterpret_cast<float*>(ws + pp.acc_offset);
+  a.num_pages = layout->num_pages;
+  a.max_pages = max_pages;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = layout->num_kv_heads;
+  a.head_dim = layout->head_dim;
+  a.grid = pp.grid;
+  a.score_scale = sm_scale * 1.4426950408889634f;  // log2(e)
+  a.out_dtype = out_dtype;
+  return launch_page_rows(a, s);
+}
+
+kvq_status page_decode(const void* q, const void* pool, const void* scales, const int32_t* block_table, int32_t max_pages,
+                       const int32_t* seq_lens, int32_t batch, int32_t num_q_heads, float sm_scale, void* out,
+                       kvq_out_dtype out_dtype, void* workspace, size_t workspace_bytes, const kvq_layout* layout,
+                       const kvq_decode_options* options, bool cap, void* stream) {
+  const kvq_status st = check_layout(layout);
+  if (st != KVQ_OK) return st;
+  if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_F32) return KVQ_EINVAL;
+  if (batch < 0 || num_q_heads <= 0 || max_pages <= 0) return KVQ_EINVAL;
+  if (num_q_heads % layout->num_kv_heads != 0) return KVQ_EINVAL;
+  if (!(sm_scale == sm_scale) || sm_scale > std::numeric_limits<float>::max() ||
+      sm_scale < -std::numeric_limits<float>::max())
+    return KVQ_EINVAL;
+  if (options && (options->pages_per_split < 0 || options->path < 0 || options->path > 2)) return KVQ_EINVAL;
+  if (options && (options->pages_per_split > 0 || options->path > 0)) return KVQ_EUNSUPPORTED;
+  return page_common(q, pool, scales, block_table, max_pages, seq_lens, nullptr, batch, batch, num_q_heads, sm_scale, out,
+                     out_dtype, workspace, workspace_bytes, layout, cap, static_cast<cudaStream_t>(stream));
+}
+
 // Workspace of a fork or a resize of n list entries: the status word, the entries, the free pages' bitmap with
 // its prefixes, and the parents' rows.
 struct PagesPlan {
@@ -463,6 +564,15 @@ kvq_status clear_status(void* workspace, cudaStream_t s) {
 
 }  // namespace
 
+namespace kvq {
+kvq_status decode_pages_capped(const void* q, const void* pool, const void* scales, const int32_t* block_table,
+                               int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                               float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                               const kvq_layout* layout, void* stream) {
+  return page_decode(q, pool, scales, block_table, max_pages, seq_lens, batch, num_q_heads, sm_scale, out, out_dtype,
+                     workspace, workspace_bytes, layout, nullptr, true, stream);
+}
+}  // namespace kvq
 
 extern "C" {
 
@@ -474,7 +584,8 @@ const char* kvq_strerror(kvq_status s) {
     case KVQ_EINVAL: return "invalid argument";
     case KVQ_EKIND:
       return "quantization kind not accepted by this call (the block-scaled stores take KVQ_FP8_E4M3 or KVQ_Q8_0; "
-             "kvq_store_unscaled the unscaled kinds; the attention calls all four)";
+             "kvq_store_unscaled the unscaled kinds; the attention calls all four; KVQ_FP8_E4M3_PAGE belongs to kvq_append, "
+             "kvq_decode, kvq_extend and kvq_pages_copy)";
     case KVQ_EHEADDIM: return "head_dim and v_dim must be positive multiples of 32 (the quantization block)";
     case KVQ_EALIGN: return "device pointers must be 16-byte aligned";
     case KVQ_EWORKSPACE: return "workspace smaller than kvq_decode_workspace_bytes()";
@@ -512,16 +623,18 @@ int64_t kvq_num_pages(const kvq_layout* layout, size_t budget_bytes) {
 }
 
 double kvq_bytes_per_token_ex(const kvq_layout* layout, kvq_kind kind) {
-  if (check_layout(layout) != KVQ_OK || !kind_read_ok(kind)) return -1.0;
-  if (has_scales(kind)) return kvq_bytes_per_token(layout);
-  return static_cast<double>(n_kv_of(*layout)) * layout->num_kv_heads * layout->head_dim;
+  if (check_layout(layout) != KVQ_OK || !kind_append_ok(kind)) return -1.0;
+  if (kind_ok(kind)) return kvq_bytes_per_token(layout);
+  const double rows = static_cast<double>(n_kv_of(*layout)) * layout->num_kv_heads;
+  return rows * layout->head_dim + (kind == KVQ_FP8_E4M3_PAGE ? rows * sizeof(float) / layout->page_size : 0.0);
 }
 
 int64_t kvq_num_pages_ex(const kvq_layout* layout, kvq_kind kind, size_t budget_bytes) {
-  if (check_layout(layout) != KVQ_OK || !kind_read_ok(kind)) return -1;
-  if (has_scales(kind)) return kvq_num_pages(layout, budget_bytes);
+  if (check_layout(layout) != KVQ_OK || !kind_append_ok(kind)) return -1;
+  if (kind_ok(kind)) return kvq_num_pages(layout, budget_bytes);
+  const uint64_t rows = static_cast<uint64_t>(n_kv_of(*layout)) * layout->num_kv_heads;
   const uint64_t bytes_per_page =
-      static_cast<uint64_t>(n_kv_of(*layout)) * layout->num_kv_heads * layout->page_size * layout->head_dim;
+      rows * layout->page_size * layout->head_dim + (kind == KVQ_FP8_E4M3_PAGE ? rows * sizeof(float) : 0);
   return static_cast<int64_t>(budget_bytes / bytes_per_page);
 }
 
@@ -581,6 +694,9 @@ kvq_status kvq_decode_ex(const void* q, const void* pool, const void* scales, co
                          float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace,
                          size_t workspace_bytes, const kvq_layout* layout, kvq_kind kind,
                          const kvq_decode_options* options, void* stream) {
+  if (kind == KVQ_FP8_E4M3_PAGE)
+    return page_decode(q, pool, scales, block_table, max_pages_per_seq, seq_lens, batch, num_q_heads, sm_scale, out,
+                       out_dtype, workspace, workspace_bytes, layout, options, false, stream);
   return decode_common(q, pool, scales, block_table, max_pages_per_seq, seq_lens, batch, num_q_heads, sm_scale, out,
                        out_dtype, workspace, workspace_bytes, layout, kind, options, stream, true);
 }
@@ -591,6 +707,17 @@ kvq_status kvq_decode(const void* q, const void* pool, const void* scales, const
                       const kvq_layout* layout, kvq_kind kind, void* stream) {
   return kvq_decode_ex(q, pool, scales, block_table, max_pages_per_seq, seq_lens, batch, num_q_heads, sm_scale, out,
                        out_dtype, workspace, workspace_bytes, layout, kind, nullptr, stream);
+}
+
+size_t kvq_decode_workspace_bytes_kind(const kvq_layout* layout, kvq_kind kind, int32_t batch, int32_t num_q_heads,
+                                       int32_t max_pages_per_seq, const kvq_decode_options* options) {
+  if (check_layout(layout) != KVQ_OK) return 0;
+  if (kind_read_ok(kind)) return kvq_decode_workspace_bytes_ex(layout, batch, num_q_heads, max_pages_per_seq, options);
+  PagePlan pp;
+  if (kind != KVQ_FP8_E4M3_PAGE || (options && (options->pages_per_split != 0 || options->path != 0)) ||
+      !plan_page(*layout, batch, batch, num_q_heads, max_pages_per_seq, 0, &pp))
+    return 0;
+  return pp.total;
 }
 
 size_t kvq_decode_sparse_workspace_bytes(const kvq_layout* layout, int32_t batch, int32_t num_q_heads, int32_t topk) {
@@ -661,6 +788,18 @@ size_t kvq_extend_workspace_bytes_ex(const kvq_layout* layout, int32_t total_q, 
   return ep.total;
 }
 
+size_t kvq_extend_workspace_bytes_kind(const kvq_layout* layout, kvq_kind kind, int32_t batch, int32_t total_q,
+                                       int32_t num_q_heads, int32_t max_pages_per_seq, const kvq_extend_options* options) {
+  if (check_layout(layout) != KVQ_OK) return 0;
+  if (kind_read_ok(kind))
+    return kvq_extend_workspace_bytes_ex(layout, total_q, num_q_heads, max_pages_per_seq, options);
+  PagePlan pp;
+  if (kind != KVQ_FP8_E4M3_PAGE || (options && (options->path != 0 || options->precise_p != 0)) ||
+      !plan_page(*layout, batch, total_q, num_q_heads, max_pages_per_seq, 0, &pp))
+    return 0;
+  return pp.total;
+}
+
 int32_t kvq_extend_path(const kvq_layout* layout, int32_t total_q, int32_t num_q_heads, int32_t max_pages_per_seq,
                         const kvq_extend_options* options) {
   if (check_layout(layout) != KVQ_OK) return KVQ_EINVAL;
@@ -692,7 +831,7 @@ kvq_status kvq_extend_ex(const void* q, const void* pool, const void* scales, co
                          kvq_kind kind, const kvq_extend_options* options, void* stream) {
   kvq_status st = check_layout(layout);
   if (st != KVQ_OK) return st;
-  if (!kind_read_ok(kind)) return KVQ_EKIND;
+  if (!kind_read_ok(kind) && kind != KVQ_FP8_E4M3_PAGE) return KVQ_EKIND;
   if (!has_scales(kind)) scales = nullptr;
   if (out_dtype != KVQ_OUT_BF16 && out_dtype != KVQ_OUT_F32) return KVQ_EINVAL;
   if (batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages_per_seq <= 0) return KVQ_EINVAL;
@@ -703,6 +842,13 @@ kvq_status kvq_extend_ex(const void* q, const void* pool, const void* scales, co
   if (!(sm_scale > 0.0f) || sm_scale > std::numeric_limits<float>::max()) return KVQ_EINVAL;  // finite, > 0
   if (layout->page_size != kPageTokens) return KVQ_EUNSUPPORTED;
   if (batch > kMaxExtendBatch) return KVQ_EUNSUPPORTED;
+  if (kind == KVQ_FP8_E4M3_PAGE) {
+    if (options && (options->path != 0 || options->precise_p != 0)) return KVQ_EUNSUPPORTED;
+    if (!q_start && batch > 0 && total_q > 0) return KVQ_EINVAL;
+    return page_common(q, pool, scales, block_table, max_pages_per_seq, seq_lens, q_start, total_q, batch, num_q_heads,
+                       sm_scale, out, out_dtype, workspace, workspace_bytes, layout, false,
+                       static_cast<cudaStream_t>(stream));
+  }
   ExtendPlan ep;
   if (!plan_extend(*layout, total_q, num_q_heads, max_pages_per_seq, options, &ep)) return KVQ_EUNSUPPORTED;
   if (!workspace) return KVQ_EINVAL;
@@ -906,6 +1052,97 @@ kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t
   return launch_prompt(a, s);
 }
 
+size_t kvq_append_workspace_bytes(void) { return kWorkspaceHeader; }
+
+kvq_status kvq_append(void* pool, void* scales, const void* q, const void* k, const void* v, const int32_t* block_table,
+                      int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* q_start,
+                      const int32_t* positions, int32_t total, int32_t batch, int32_t num_q_heads, void* q_out,
+                      const kvq_rope* rope, const kvq_prompt_strides* strides, void* workspace, size_t workspace_bytes,
+                      const kvq_layout* layout, kvq_kind kind, void* stream) {
+  kvq_status st = check_layout(layout);
+  if (st != KVQ_OK) return st;
+  if (!kind_append_ok(kind)) return KVQ_EKIND;
+  if (!has_scales(kind)) scales = nullptr;
+  if (total < 0 || batch < 0 || num_q_heads < 0 || max_pages_per_seq <= 0) return KVQ_EINVAL;
+  if (static_cast<int64_t>(max_pages_per_seq) * layout->page_size > std::numeric_limits<int32_t>::max()) return KVQ_EINVAL;
+  if ((num_q_heads == 0) != (q == nullptr) || (q == nullptr) != (q_out == nullptr)) return KVQ_EINVAL;
+  if (layout->mla && v != nullptr) return KVQ_EINVAL;
+  const int64_t d = layout->head_dim;
+  AppendArgs a;
+  a.cos_sin = nullptr;
+  a.max_position = a.rot_dim = a.rot_offset = a.interleaved = 0;
+  if (rope != nullptr) {
+    if (rope->cos_sin == nullptr || rope->max_position <= 0 || (rope->interleaved != 0 && rope->interleaved != 1))
+      return KVQ_EINVAL;
+    // pieces of 8 elements lie in one half of a rotation, or outside
+    if (rope->rot_dim <= 0 || rope->rot_dim % 16 != 0 || rope->rot_offset < 0 || rope->rot_offset % 8 != 0 ||
+        rope->rot_dim > d || rope->rot_offset > d - rope->rot_dim)
+      return KVQ_EINVAL;
+    if (!aligned(rope->cos_sin)) return KVQ_EALIGN;
+    a.cos_sin = rope->cos_sin;
+    a.max_position = rope->max_position;
+    a.rot_dim = rope->rot_dim;
+    a.rot_offset = rope->rot_offset;
+    a.interleaved = rope->interleaved;
+  }
+  if (kind == KVQ_FP8_E4M3_PAGE && (layout->mla || layout->page_size != kPageTokens)) return KVQ_EUNSUPPORTED;
+  if (!append_supported(layout->head_dim, kind)) return KVQ_EUNSUPPORTED;
+  a.q_head = a.k_head = a.v_head = a.out_head = d;
+  a.q_token = a.out_token = num_q_heads * d;
+  a.k_token = a.v_token = layout->num_kv_heads * d;
+  if (strides != nullptr) {
+    auto take = [&](int64_t token, int64_t head, int32_t heads, int64_t* t, int64_t* h) {
+      if (heads > 1) *h = head;
+      if (total > 1) *t = token;
+      return *t > 0 && *h > 0 && *t % 8 == 0 && *h % 8 == 0 && *t < (1LL << 39) && *h < (1LL << 39);
+    };
+    if ((num_q_heads > 0 && (!take(strides->q_token, strides->q_head, num_q_heads, &a.q_token, &a.q_head) ||
+                             !take(strides->out_token, strides->out_head, num_q_heads, &a.out_token, &a.out_head))) ||
+        !take(strides->k_token, strides->k_head, layout->num_kv_heads, &a.k_token, &a.k_head) ||
+        (!layout->mla && !take(strides->v_token, strides->v_head, layout->num_kv_heads, &a.v_token, &a.v_head)))
+      return KVQ_EINVAL;
+  }
+  if (q != nullptr && q == q_out && total > 0 && (a.q_token != a.out_token || a.q_head != a.out_head)) return KVQ_EINVAL;
+  a.num_kv_heads = layout->num_kv_heads;
+  a.num_q_heads = num_q_heads;
+  a.n_kv = n_kv_of(*layout);
+  a.head_dim = layout->head_dim;
+  a.page_size = layout->page_size;
+  a.max_pages = max_pages_per_seq;
+  a.batch = batch;
+  a.total = total;
+  a.kind = kind;
+  a.num_pages = layout->num_pages;
+  if (!workspace) return KVQ_EINVAL;
+  if (workspace_bytes < kWorkspaceHeader) return KVQ_EWORKSPACE;
+  const bool empty = batch == 0 || total == 0;
+  if (!empty && (!pool || (has_scales(kind) && !scales) || !k || (!layout->mla && !v) || !block_table || !seq_lens || !q_start))
+    return KVQ_EINVAL;
+  if (!aligned(workspace) || !aligned(pool) || !aligned(scales) || !aligned(q) || !aligned(k) || !aligned(v) || !aligned(q_out))
+    return KVQ_EALIGN;
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(q_start), static_cast<const void*>(positions)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KVQ_EALIGN;
+  const int64_t grid = append_grid(&a, sm_count());
+  if (grid > std::numeric_limits<int32_t>::max()) return KVQ_EUNSUPPORTED;  // a grid dimension
+  st = kvq_device_check();
+  if (st != KVQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (empty) return clear_status(workspace, s);
+  a.codes = static_cast<uint8_t*>(pool);
+  a.scales = scales;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.positions = positions;
+  a.status = static_cast<uint32_t*>(workspace);
+  return launch_append(a, grid, s);
+}
+
 size_t kvq_pages_workspace_bytes(const kvq_layout* layout, int32_t n, int32_t max_pages_per_seq) {
   PagesPlan pp;
   if (check_layout(layout) != KVQ_OK || !plan_pages(*layout, n, max_pages_per_seq, &pp)) return 0;
@@ -916,13 +1153,17 @@ kvq_status kvq_pages_copy(void* pool, void* scales, const int32_t* src, const in
                           const kvq_layout* layout, kvq_kind kind, void* stream) {
   kvq_status st = check_layout(layout);
   if (st != KVQ_OK) return st;
-  if (!kind_read_ok(kind)) return KVQ_EKIND;
+  if (!kind_append_ok(kind)) return KVQ_EKIND;
   if (!has_scales(kind)) scales = nullptr;
   if (n < 0) return KVQ_EINVAL;
   const int64_t page_bytes =
       static_cast<int64_t>(n_kv_of(*layout)) * layout->num_kv_heads * layout->page_size * layout->head_dim;
-  const int64_t scale_bytes = has_scales(kind) ? page_bytes / 16 : 0;
-  if (scale_bytes % 16 != 0 || page_bytes > (1LL << 34)) return KVQ_EUNSUPPORTED;  // whole 16-byte pieces, 32-bit counts
+  const bool by_page = kind == KVQ_FP8_E4M3_PAGE;
+  if (by_page && layout->mla) return KVQ_EUNSUPPORTED;
+  const int64_t scale_bytes = by_page         ? static_cast<int64_t>(2 * sizeof(float)) * layout->num_kv_heads
+                              : kind_ok(kind) ? page_bytes / 16
+                                              : 0;
+  if ((!by_page && scale_bytes % 16 != 0) || page_bytes > (1LL << 34)) return KVQ_EUNSUPPORTED;  // whole 16-byte pieces, 32-bit counts
   if (n == 0) return KVQ_OK;
   if (!pool || (has_scales(kind) && !scales) || !src || !dst) return KVQ_EINVAL;
   if (!aligned(pool) || !aligned(scales) || (reinterpret_cast<uintptr_t>(src) % 4) != 0 ||
@@ -931,7 +1172,7 @@ kvq_status kvq_pages_copy(void* pool, void* scales, const int32_t* src, const in
   st = kvq_device_check();
   if (st != KVQ_OK) return st;
   return launch_copy_pages(pool, scales, src, dst, n, layout->num_pages, static_cast<uint32_t>(page_bytes / 16),
-                           static_cast<uint32_t>(scale_bytes / 16), static_cast<cudaStream_t>(stream));
+                           static_cast<uint32_t>(scale_bytes), static_cast<cudaStream_t>(stream));
 }
 
 kvq_status kvq_pages_fork(int32_t* block_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t batch,

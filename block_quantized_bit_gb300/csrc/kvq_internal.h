@@ -202,6 +202,64 @@ bool prompt_supported(int32_t head_dim, int32_t batch);
 kvq_status launch_prompt(const PromptArgs& a, cudaStream_t stream);
 kvq_status launch_prompt_wide(const PromptArgs& a, cudaStream_t stream);
 
+// Appends with the position rotation (kvq_append).  Strides in elements.
+struct AppendArgs {
+  uint8_t* codes;
+  void* scales;
+  const uint16_t* q;          // [total][num_q_heads][head_dim] bf16, or null with num_q_heads = 0
+  const uint16_t* k;          // [total][num_kv_heads][head_dim] bf16
+  const uint16_t* v;          // null: the latent row
+  uint16_t* q_out;
+  const int32_t* block_table; // [batch][max_pages]
+  const int32_t* seq_lens;    // [batch]
+  const int32_t* q_start;     // [batch + 1]
+  const int32_t* positions;   // [total], or null: the places in the sequences
+  const float* cos_sin;       // [max_position][rot_dim]
+  uint32_t* status;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+  int64_t num_pages;
+  int64_t page_ctas;          // CTAs of the pages kernel that write pages (append_grid)
+  int32_t max_pages, batch, total, num_q_heads, num_kv_heads, n_kv, head_dim, page_size;
+  int32_t max_position, rot_dim, rot_offset, interleaved;  // rot_dim 0: no rotation
+  int32_t row_chunks, part_chunks;                         // CTAs of one token, of one page (append_grid)
+  kvq_kind kind;
+};
+// Exponents that the power of two of a KVQ_FP8_E4M3_PAGE page may have: codes from 2^-41 to 448 * 2^32.
+constexpr int32_t kPageScaleMin = -32, kPageScaleMax = 32;
+bool append_supported(int32_t head_dim, kvq_kind kind);
+int64_t append_grid(AppendArgs* a, int32_t sms);  // sets the chunks; CTAs of the call
+kvq_status launch_append(const AppendArgs& a, int64_t grid, cudaStream_t stream);
+
+// Attention over a KVQ_FP8_E4M3_PAGE cache.
+struct PageArgs {
+  const uint16_t* q;          // [total_q][num_q_heads][head_dim] bf16
+  const uint8_t* codes;
+  const float* scales;        // [num_pages][2][num_kv_heads]
+  const int32_t* block_table; // [batch][max_pages]
+  const int32_t* seq_lens;    // [batch]
+  const int32_t* q_start;     // [batch + 1], or null: one row per sequence
+  void* out;                  // [total_q][num_q_heads][head_dim]
+  uint32_t* status;
+  int64_t* tab;               // [batch + 1] units before each sequence, and in all
+  float* part_acc;            // [2 * grid][kPageRowsTile][head_dim]
+  float* part_ml;             // [2 * grid][kPageRowsTile][2]
+  int64_t num_pages;
+  int32_t max_pages, batch, total_q, num_q_heads, num_kv_heads, head_dim;
+  int32_t grid;               // CTAs launched
+  float score_scale;          // sm_scale * log2(e)
+  kvq_out_dtype out_dtype;
+};
+constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel
+constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
+bool page_supported(int32_t head_dim);
+int32_t page_rows_grid(int32_t head_dim, int32_t sms);  // CTAs that are resident at once
+kvq_status launch_page_rows(const PageArgs& a, cudaStream_t stream);
+// kvq_decode of that kind with no more CTAs than the workspace has room for.
+kvq_status decode_pages_capped(const void* q, const void* pool, const void* scales, const int32_t* block_table,
+                               int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                               float sm_scale, void* out, kvq_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                               const kvq_layout* layout, void* stream);
+
 // Pages of the cache (kvq_pages_*).
 constexpr int32_t kPagesChunk = 8192;       // pages whose counts one CTA of the plan reads
 constexpr int32_t kMaxPagesChunks = 8192;   // chunks whose prefixes fit the apply kernel's shared memory
@@ -255,7 +313,7 @@ struct CompactArgs {
 };
 
 kvq_status launch_copy_pages(void* codes, void* scales, const int32_t* src, const int32_t* dst, int32_t n,
-                             int64_t num_pages, uint32_t code_vecs, uint32_t scale_vecs, cudaStream_t stream);
+                             int64_t num_pages, uint32_t code_vecs, uint32_t scale_bytes, cudaStream_t stream);
 kvq_status launch_fork_pages(const PagesArgs& a, cudaStream_t stream);
 kvq_status launch_resize_pages(const PagesArgs& a, cudaStream_t stream);
 kvq_status launch_compact(const CompactArgs& a, cudaStream_t stream);

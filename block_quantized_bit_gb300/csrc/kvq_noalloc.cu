@@ -57,7 +57,8 @@ extern "C" kvq_status kvq_decode_noalloc(const void* q, const void* pool, const 
                                          const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
                                          float sm_scale, void* out, kvq_out_dtype out_dtype,
                                          const kvq_layout* layout, kvq_kind kind, void* stream) {
-  const size_t need = kvq_decode_workspace_bytes(layout, batch, num_q_heads, max_pages_per_seq);
+  const bool by_page = kind == KVQ_FP8_E4M3_PAGE;  // takes as many CTAs as have room
+  const size_t need = by_page ? 1 : kvq_decode_workspace_bytes(layout, batch, num_q_heads, max_pages_per_seq);
   if (need == 0) return KVQ_EINVAL;
   if (need > static_cast<size_t>(KVQ_NOALLOC_SCRATCH_BYTES)) return KVQ_EWORKSPACE;
   kvq_status st = kvq_device_check();
@@ -65,6 +66,9 @@ extern "C" kvq_status kvq_decode_noalloc(const void* q, const void* pool, const 
   void* scratch = nullptr;
   st = kvq::scratch_address(&scratch);
   if (st != KVQ_OK) return st;
+  if (by_page)
+    return kvq::decode_pages_capped(q, pool, scales, block_table, max_pages_per_seq, seq_lens, batch, num_q_heads, sm_scale,
+                                    out, out_dtype, scratch, static_cast<size_t>(KVQ_NOALLOC_SCRATCH_BYTES), layout, stream);
   return kvq_decode(q, pool, scales, block_table, max_pages_per_seq, seq_lens, batch, num_q_heads, sm_scale, out,
                     out_dtype, scratch, static_cast<size_t>(KVQ_NOALLOC_SCRATCH_BYTES), layout, kind, stream);
 }

@@ -1,0 +1,639 @@
+// kvq_page_rows.cu -- attention of few query rows over a KVQ_FP8_E4M3_PAGE cache (kvq_decode, and kvq_extend's short
+// turns): K = 2^ek[page] code, V = 2^ev[page] code, one exponent per page of 16 tokens and head, so that
+//   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t:
+// the scales never meet a code.  Codes become f16 exactly, two per conversion; the products run on the warp-level tensor-core
+// instructions with f16 inputs and fp32 sums.  q enters as f16 as well, each row scaled by a power of two (exact: bf16
+// has 8 significant bits; only elements 2^31 times smaller than the row's largest lose some).  P is rounded to f16
+// (2^-11 of each), with the reference m at most 2^15 below the largest, so that what is 2^-40 of the largest
+// still counts.  2 D bytes per token and kv head are read once for up to 16 query rows: bound by HBM.
+//
+// A tile is 16 query rows of one kv head (heads of its group, and for kvq_extend tokens times heads), the MMA's M.  Of
+// every warp-level product m16n8k16 the tile's rows are A, 8 tokens (scores) or 8 dims (output) are B, and
+// the scores come out in the very lanes that feed them to the output's products.  Nothing is transposed: a lane reads
+// 16 bytes of its token's K row, and of V 16 bytes of four tokens, whose codes pair up by byte permutes.
+// Work: a unit is a (tile, page).  All units of the call lie in one order, sequence by sequence, and every CTA takes an
+// equal run of them, whatever the lengths.  The four warps of a CTA walk every fourth page, each with its own ring of TMA
+// boxes (swizzled: no bank conflicts), and join at the end of each tile's run.  A run that is all of a tile's pages
+// gives the output, other runs leave partial sums, which a second kernel, its programmatic dependent, joins.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "kvq_device.cuh"
+#include "kvq_flash.cuh"
+#include "kvq_internal.h"
+#include "kvq_page.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = kPageRowsTile;   // query rows of a tile
+constexpr float kNoMax = -1e30f;       // reference of a row that has seen nothing
+constexpr float kHead = 7.0f;          // log2 of the largest p when the reference moves ...
+constexpr float kLimit = 15.0f;        // ... and at most (f16 ends at 2^16)
+
+template <int D>
+struct RCfg {
+  static constexpr int PAGE_BYTES = kPage * D;         // codes of K or V of a page
+  static constexpr int STAGE = 2 * PAGE_BYTES;
+  static constexpr int STAGES = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int SLICES = D == 256 ? 2 : 1;      // 128-byte (D = 64: 64-byte) slices of a row
+  static constexpr int KSTEPS = D / 16;
+  static constexpr bool Q_SHARED = D == 256;           // q fragments in shared memory (registers hold O)
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int JOIN = kWarps * kRows * (D + 2) * 4;  // the warps' sums, over the ring
+  static constexpr int DATA = RING > JOIN ? RING : JOIN;
+  static constexpr int Q_OFF = (DATA + 127) / 128 * 128;
+  static constexpr int BAR_OFF = Q_OFF + (Q_SHARED ? KSTEPS * 512 : 0);
+  static constexpr int SMEM = BAR_OFF + kWarps * STAGES * 8 + 1024;  // + slack to align the base
+  static constexpr int CTAS = D == 256 ? 2 : 4;        // resident per SM
+};
+
+// One sequence's rows and pages.  n < 0: nothing to do.
+struct Seq {
+  int32_t q0, n, len, pages, tiles;
+  int64_t units;
+};
+
+__device__ __forceinline__ Seq page_sequence(const PageArgs& a, int32_t b, bool& bad) {
+  Seq s;
+  const int32_t room = a.max_pages * kPage;
+  s.len = __ldg(a.seq_lens + b);
+  if (a.q_start == nullptr) {  // one row per sequence
+    s.q0 = b;
+    s.n = 1;
+    s.len = min(max(s.len, 0), room);
+  } else {
+    s.q0 = __ldg(a.q_start + b);
+    const int64_t q1 = __ldg(a.q_start + b + 1), n = q1 - s.q0;
+    const bool ok = s.q0 >= 0 && n >= 0 && q1 <= a.total_q && n <= s.len && s.len <= room;
+    bad |= !ok;
+    s.n = ok ? static_cast<int32_t>(n) : 0;
+    if (s.n == 0) s.len = 0;
+  }
+  s.pages = (s.len + kPage - 1) / kPage;
+  s.tiles = (s.n * (a.num_q_heads / a.num_kv_heads) + kRows - 1) / kRows;
+  s.units = static_cast<int64_t>(s.pages) * s.tiles * a.num_kv_heads;
+  return s;
+}
+
+// CTAs that share U units, and the first unit of CTA c.
+__device__ __forceinline__ int32_t sharers(int64_t U, int32_t grid) {
+  return static_cast<int32_t>(min(static_cast<int64_t>(grid), max(U / kPageMinUnits, static_cast<int64_t>(1))));
+}
+__device__ __forceinline__ int64_t first_unit(int64_t U, int32_t C, int32_t c) { return U * c / C; }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The units before every sequence (CTA 0 leaves them for the joining kernel), their sum, and where unit `want`
+// lies.  Every thread of the CTA calls it.
+struct Place {
+  int64_t total, before;  // units of the call; of the sequences before b
+  int32_t b;
+};
+
+__device__ __forceinline__ Place page_place(const PageArgs& a, int32_t cta) {
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ Place s_place;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t per = (a.batch + kThreads - 1) / kThreads;
+  const int32_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+  bool bad = false;
+  int64_t mine = 0;
+  for (int32_t b = b0; b < b1; ++b) mine += page_sequence(a, b, bad).units;
+  if (bad && cta == 0) set_status(a.status, kStatusBadExtend);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  if (tid == 0) s_place.b = -1;
+  __syncthreads();
+  int64_t run = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) run += s_sum[w];
+    total += s_sum[w];
+  }
+  const int32_t C = sharers(total, a.grid);
+  const int64_t want = cta < C && total > 0 ? first_unit(total, C, cta) : total;
+  if (cta == 0 && tid == 0) a.tab[a.batch] = total;
+  for (int32_t b = b0; b < b1; ++b) {
+    const int64_t u = page_sequence(a, b, bad).units;
+    if (cta == 0) a.tab[b] = run;
+    if (want >= run && want < run + u) {
+      s_place.b = b;
+      s_place.before = run;
+    }
+    run += u;
+  }
+  __syncthreads();
+  Place p = s_place;
+  p.total = total;
+  return p;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
+    page_rows_kernel(const PageArgs a, const __grid_constant__ CUtensorMap map) {
+  using Cfg = RCfg<D>;
+  constexpr int STAGES = Cfg::STAGES, SLICES = Cfg::SLICES, KSTEPS = Cfg::KSTEPS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint4* sQ = reinterpret_cast<uint4*>(smem + Cfg::Q_OFF);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g8 = lane >> 2, t4 = lane & 3;  // of a product: row or column g8, columns 2 t4 and 2 t4 + 1
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF) + warp * STAGES;
+  uint8_t* ring = smem + warp * STAGES * Cfg::STAGE;
+
+  if (lane < STAGES) mbar_init(&bars[lane], 1);
+  fence_mbar_init();
+  __syncwarp();
+  const Place place = page_place(a, blockIdx.x);
+  if (place.b < 0) return;
+  const int32_t C = sharers(place.total, a.grid);
+  int64_t u = first_unit(place.total, C, blockIdx.x);
+  const int64_t u_first = u, u_end = first_unit(place.total, C, blockIdx.x + 1);
+  const int32_t G = a.num_q_heads / a.num_kv_heads;
+  int32_t b = place.b;
+  int64_t before = place.before;
+  uint32_t done = 0;  // pages that went through this warp's ring
+  bool ok = true, bad = false;
+
+  while (u < u_end) {
+    Seq s = page_sequence(a, b, bad);
+    if (u >= before + s.units) {
+      before += s.units;
+      ++b;
+      continue;
+    }
+    // the run: pages [pg0, pg1) of a tile
+    const int64_t local = u - before;
+    const int32_t tile_at = static_cast<int32_t>(local / s.pages);
+    const int32_t pg0 = static_cast<int32_t>(local - static_cast<int64_t>(tile_at) * s.pages);
+    const int32_t pg1 = static_cast<int32_t>(min(static_cast<int64_t>(s.pages), pg0 + (u_end - u)));
+    const int32_t g = tile_at / s.tiles, tile = tile_at - g * s.tiles;
+    const int32_t rows = min(kRows, s.n * G - tile * kRows);
+    const int64_t tile_first = u - pg0;  // the tile's first unit
+
+    // ---- this lane's two rows: where their q lies, how many tokens they see
+    const uint16_t* qrow[2];
+    int32_t sees[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t r = min(g8 + 8 * h, rows - 1) + tile * kRows, tok = r / G;
+      qrow[h] = a.q + (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + g * G + (r - tok * G)) * D;
+      sees[h] = s.len - s.n + tok + 1;
+    }
+    const int32_t sees_least = s.len - s.n + tile * kRows / G + 1;
+
+    // ---- pages: 32 at a time, one per lane, the next 32 fetched meanwhile
+    const int32_t np = pg1 - pg0, nw = np > warp ? (np - warp + kWarps - 1) / kWarps : 0;
+    const int32_t* table = a.block_table + static_cast<int64_t>(b) * a.max_pages + pg0 + warp;
+    auto fetch = [&](int32_t batch) -> int32_t {
+      const int32_t i = batch * 32 + lane;
+      if (i >= nw) return -1;
+      const int32_t p = __ldg(table + i * kWarps);
+      if (p < a.num_pages) return p;
+      set_status(a.status, kStatusBadPage);
+      return -1;
+    };
+    auto scales = [&](int32_t p, float& ks, float& vs) {
+      ks = vs = 1.0f;
+      if (p < 0) return;
+      const float* x = a.scales + static_cast<int64_t>(p) * 2 * a.num_kv_heads + g;
+      ks = __ldg(x);
+      vs = __ldg(x + a.num_kv_heads);
+    };
+    int32_t phys = fetch(0), phys_next = fetch(1);
+    float ks, vs, ks_next = 1.0f, vs_next = 1.0f;
+    scales(phys, ks, vs);
+    auto issue = [&](int32_t i, int32_t p) {  // page i of this warp's, in slot (done + i) % STAGES
+      if (lane != 0) return;
+      const uint32_t slot = (done + i) % STAGES;
+      if (p < 0) {
+        bar_arrive(&bars[slot]);
+        return;
+      }
+      mbar_arrive_expect_tx(&bars[slot], Cfg::STAGE);
+      uint8_t* dst = ring + slot * Cfg::STAGE;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int x = 0; x < SLICES; ++x)
+          tma_load_codes(smem_u32(dst + kv * Cfg::PAGE_BYTES + x * 2048), &map, x, g * kPage, kv, p, &bars[slot]);
+    };
+    fence_proxy_async_smem();  // (the ring held the warps' sums)
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      const int32_t p = __shfl_sync(0xffffffffu, phys, i);
+      if (i < nw) issue(i, p);
+    }
+
+    // ---- q as f16 fragments, the row's largest element brought to [2^14, 2^15)
+    float rowscale[2];
+    uint32_t qf[Cfg::Q_SHARED ? 1 : KSTEPS][4];
+    {
+      float top[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow[h] + (x * 4 + t4) * 8));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack_bf16x2(w[k]);
+            top[h] = fmaxf(top[h], fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+      }
+      float up[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = min(max((__float_as_int(top[h]) >> 23) - 127, -100), 100);
+        up[h] = __int_as_float((14 - e + 127) << 23);
+        rowscale[h] = a.score_scale * __int_as_float((e - 14 + 127) << 23);
+      }
+      // k-step (x, c, i): lane t4 holds dims 128 x + 32 t4 + 16 c + 4 i ... + 3 of its rows (D = 64: 16 t4 + 4 i)
+#pragma unroll
+      for (int k = 0; k < KSTEPS; ++k) {
+        const int x = k / 8, c = (k / 4) % 2, i = k % 4;
+        const int d = D == 64 ? 16 * t4 + 4 * i : 128 * x + 32 * t4 + 16 * c + 4 * i;
+        uint32_t f[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(qrow[h] + d));
+          const float2 lo = unpack_bf16x2(v.x), hi = unpack_bf16x2(v.y);
+          f[h] = pack_f16x2(lo.x * up[h], lo.y * up[h]);
+          f[2 + h] = pack_f16x2(hi.x * up[h], hi.y * up[h]);
+        }
+        if constexpr (Cfg::Q_SHARED) {
+          if (warp == k % kWarps) sQ[k * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[k][e] = f[e];
+        }
+      }
+      if constexpr (Cfg::Q_SHARED) __syncthreads();
+    }
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+    float m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
+    int32_t landed = 0;
+
+    for (int32_t i = 0; i < nw; ++i) {
+      if (i > 0 && i % 32 == 0) {
+        phys = phys_next;
+        ks = ks_next;
+        vs = vs_next;
+        phys_next = fetch(i / 32 + 1);
+      }
+      if (i % 32 == 8) scales(phys_next, ks_next, vs_next);
+      const uint32_t slot = (done + i) % STAGES;
+      if (!warp_wait(&bars[slot], ((done + i) / STAGES) & 1)) { ok = false; break; }
+      landed = i + 1;
+      const int32_t p = __shfl_sync(0xffffffffu, phys, i & 31);
+      const float kscale = __shfl_sync(0xffffffffu, ks, i & 31), vscale = __shfl_sync(0xffffffffu, vs, i & 31);
+      if (p >= 0) {
+        const uint8_t* kc = ring + slot * Cfg::STAGE;
+        const uint8_t* vc = kc + Cfg::PAGE_BYTES;
+        const int32_t t0 = (pg0 + warp + i * kWarps) * kPage;  // the page's first token
+        // ---- scores of tokens 8 j + (2 t4, 2 t4 + 1)
+        float sc[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+          const int row = 8 * j + g8;
+#pragma unroll
+          for (int q = 0; q < KSTEPS / 4; ++q) {
+            uint4 w;
+            if constexpr (D == 64) {
+              w = *reinterpret_cast<const uint4*>(kc + row * 64 + ((t4 ^ ((row >> 1) & 3)) << 4));
+            } else {
+              w = *reinterpret_cast<const uint4*>(kc + (q / 2) * 2048 + row * 128 + (((2 * t4 + q % 2) ^ (row & 7)) << 4));
+            }
+            const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t b0, b1;
+              codes_to_f16x2<KVQ_FP8_E4M3>(c[e], b0, b1);
+              if constexpr (Cfg::Q_SHARED) {
+                const uint4 x = sQ[(q * 4 + e) * 32 + lane];
+                const uint32_t f[4] = {x.x, x.y, x.z, x.w};
+                mma_f16(sc[j], f, b0, b1);
+              } else {
+                mma_f16(sc[j], qf[q * 4 + e], b0, b1);
+              }
+            }
+          }
+        }
+        // ---- y = score + ev in the exponent; what a row does not see is -inf
+        const float ev = static_cast<float>((__float_as_int(vscale) >> 23) - 127);
+        const float unv = __int_as_float(0x7F000000 - __float_as_int(vscale));  // 1 / vscale
+        float top[2];
+        const bool whole = t0 + kPage <= sees_least;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mult = rowscale[h] * kscale;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& x = sc[j][2 * h + e];
+              x = fmaf(x, mult, ev);
+              if (!whole && t0 + 8 * j + 2 * t4 + e >= sees[h]) x = -INFINITY;
+            }
+          top[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] + kLimit || top[1] > m[1] + kLimit)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = top[h];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            const float now = fmaxf(m[h], x - kHead);
+            const float alpha = ex2(m[h] - now);
+            m[h] = now;
+            l[h] *= alpha;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+              o[j][2 * h] *= alpha;
+              o[j][2 * h + 1] *= alpha;
+            }
+          }
+        }
+        uint32_t pf[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float p0 = ex2(sc[j][2 * h] - m[h]), p1 = ex2(sc[j][2 * h + 1] - m[h]);
+            l[h] = fmaf(p0 + p1, unv, l[h]);
+            pf[2 * j + h] = pack_f16x2(p0, p1);
+          }
+        // ---- output: dims 128 x + 16 g8 + byte (D = 64: 8 g8 + byte) of tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
+        constexpr int WORDS = D == 64 ? 2 : 4;
+#pragma unroll
+        for (int x = 0; x < SLICES; ++x) {
+          uint32_t v[4][WORDS];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 2 * t4 + (r & 1) + 8 * (r >> 1);
+            if constexpr (D == 64) {
+              const uint2 w = *reinterpret_cast<const uint2*>(vc + row * 64 + (((g8 >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g8 & 1));
+              v[r][0] = w.x; v[r][1] = w.y;
+            } else {
+              const uint4 w = *reinterpret_cast<const uint4*>(vc + x * 2048 + row * 128 + ((g8 ^ (row & 7)) << 4));
+              v[r][0] = w.x; v[r][1] = w.y; v[r][2] = w.z; v[r][3] = w.w;
+            }
+            if (!whole && t0 + row >= s.len) {  // rows behind the last token may hold anything, NaN codes too
+#pragma unroll
+              for (int k = 0; k < WORDS; ++k) v[r][k] = 0u;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < WORDS; ++k)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t pick = half == 0 ? 0x5140u : 0x7362u;
+              uint32_t b0[2], b1[2];
+              codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[0][k], v[1][k], pick), b0[0], b0[1]);
+              codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[2][k], v[3][k], pick), b1[0], b1[1]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) mma_f16(o[(x * WORDS + k) * 4 + half * 2 + e], pf, b0[e], b1[e]);
+            }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      const int32_t j = i + STAGES;
+      const int32_t pj = __shfl_sync(0xffffffffu, (j ^ i) & 32 ? phys_next : phys, j & 31);
+      if (j < nw) issue(j, pj);
+    }
+    if (!ok) {
+      set_status(a.status, kStatusTimeout);
+      for (int32_t i = landed; i < min(nw, landed + STAGES); ++i)  // no copy may still be in flight at the end
+        (void)mbar_wait_bounded(&bars[(done + i) % STAGES], ((done + i) / STAGES) & 1);
+    }
+    done += nw;
+
+    // ---- the warps' sums, joined in shared memory over the ring
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    __syncthreads();
+    float2* sml = reinterpret_cast<float2*>(smem);                        // [warps][rows]
+    float* sacc = reinterpret_cast<float*>(smem + kWarps * kRows * 8);    // [warps][rows][D]
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g8 + 8 * h;
+      if (r < rows) {
+        if (t4 == 0) sml[warp * kRows + r] = make_float2(m[h], l[h]);
+        // the lane's dims: 128 x + 32 t4 ... + 31 (D = 64: 16 t4 ... + 15), first those of column 2 t4
+        constexpr int RUN = D == 64 ? 8 : 16;
+        float* dst = sacc + (warp * kRows + r) * D;
+#pragma unroll
+        for (int x = 0; x < SLICES; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < RUN; k += 4) {
+              const int j = x * RUN + k;
+              *reinterpret_cast<float4*>(dst + x * 128 + (2 * t4 + e) * RUN + k) =
+                  make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e], o[j + 3][2 * h + e]);
+            }
+      }
+    }
+    ok = __syncthreads_and(ok);
+    const bool whole_tile = pg0 == 0 && pg1 == s.pages;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (tile_first > u_first ? 1 : 0);
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float M = kNoMax;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w * kRows + r].x);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = sml[w * kRows + r];
+        const float f = ex2(ml.x - M);
+        const float4 y = *reinterpret_cast<const float4*>(sacc + (w * kRows + r) * D + d);
+        x.x = fmaf(y.x, f, x.x);
+        x.y = fmaf(y.y, f, x.y);
+        x.z = fmaf(y.z, f, x.z);
+        x.w = fmaf(y.w, f, x.w);
+        sum = fmaf(ml.y, f, sum);
+      }
+      if (whole_tile) {
+        const int32_t R = tile * kRows + r, tok = R / G;
+        page_store_out(a, (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + g * G + (R - tok * G)) * D + d, x,
+                       sum > 0.0f ? 1.0f / sum : 0.0f);
+      } else {
+        *reinterpret_cast<float4*>(a.part_acc + (slot * kRows + r) * D + d) = x;
+        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * kRows + r) * 2) = make_float2(M, sum);
+      }
+    }
+    __syncthreads();
+    if (!ok) break;
+    u += np;
+  }
+}
+
+// Joins the runs of each output row whose tile several CTAs worked on, and clears the rows of sequences without tokens.
+// A CTA per (query row, head), a warp per run in turn.
+constexpr int kJoinWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageArgs a) {
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ __align__(16) float s_a[kJoinWarps][D];
+  __shared__ int32_t s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t t = blockIdx.x / a.num_q_heads, head = blockIdx.x - t * a.num_q_heads;
+  const int32_t G = a.num_q_heads / a.num_kv_heads, g = head / G;
+  bool bad = false;
+  int32_t b = t;
+  if (a.q_start != nullptr) {  // the sequence of row t
+    if (tid == 0) s_b = a.batch;
+    __syncthreads();
+    for (int32_t i = tid; i < a.batch; i += kJoinWarps * 32) {
+      const Seq s = page_sequence(a, i, bad);
+      if (t >= s.q0 && t - s.q0 < s.n) atomicMin(&s_b, i);
+    }
+    __syncthreads();
+    b = s_b;
+    if (b >= a.batch) return;
+  }
+  const Seq s = page_sequence(a, b, bad);
+  const int32_t R = (t - s.q0) * G + head - g * G, tile = R / kRows, r = R - tile * kRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t U = a.tab[a.batch];
+  const int64_t first = a.tab[b] + (static_cast<int64_t>(g) * s.tiles + tile) * s.pages, last = first + s.pages - 1;
+  const int64_t out = (static_cast<int64_t>(t) * a.num_q_heads + head) * D;
+  if (s.pages == 0) {
+    if (tid < D / 4) page_store_out(a, out + tid * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
+    return;
+  }
+  const int32_t C = sharers(U, a.grid);
+  auto owner = [&](int64_t u) {  // the CTA among whose units u is
+    int32_t c = static_cast<int32_t>(u * C / U);
+    while (c > 0 && first_unit(U, C, c) > u) --c;
+    while (c + 1 < C && first_unit(U, C, c + 1) <= u) ++c;
+    return c;
+  };
+  const int32_t c0 = owner(first), c1 = owner(last);
+  if (c0 == c1) return;  // its CTA has written the output
+  auto part = [&](int32_t c) {
+    return (2 * static_cast<int64_t>(c) + (first > first_unit(U, C, c) ? 1 : 0)) * kRows + r;
+  };
+  constexpr int V4 = D / 128 > 0 ? D / 128 : 1;  // float4 of a lane (D = 64: of half the lanes)
+  float m = kNoMax, l = 0.0f;
+  float4 x[V4];
+#pragma unroll
+  for (int k = 0; k < V4; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+  for (int32_t c = c0 + warp; c <= c1; c += kJoinWarps) {
+    const int64_t at = part(c);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    const float now = fmaxf(m, ml.x), f = ex2(ml.x - now), keep = ex2(m - now);
+    m = now;
+    l = fmaf(ml.y, f, l * keep);
+#pragma unroll
+    for (int k = 0; k < V4; ++k) {
+      if (D == 64 && lane >= 16) continue;
+      const float4 y = *reinterpret_cast<const float4*>(a.part_acc + at * D + k * 128 + lane * 4);
+      x[k].x = fmaf(y.x, f, x[k].x * keep);
+      x[k].y = fmaf(y.y, f, x[k].y * keep);
+      x[k].z = fmaf(y.z, f, x[k].z * keep);
+      x[k].w = fmaf(y.w, f, x[k].w * keep);
+    }
+  }
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int k = 0; k < V4; ++k)
+    if (D != 64 || lane < 16) *reinterpret_cast<float4*>(&s_a[warp][k * 128 + lane * 4]) = x[k];
+  __syncthreads();
+  for (int d = tid * 4; d < D; d += kJoinWarps * 32 * 4) {
+    float M = kNoMax, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = ex2(s_m[w] - M);
+      sum = fmaf(s_l[w], f, sum);
+      y.x = fmaf(s_a[w][d], f, y.x);
+      y.y = fmaf(s_a[w][d + 1], f, y.y);
+      y.z = fmaf(s_a[w][d + 2], f, y.z);
+      y.w = fmaf(s_a[w][d + 3], f, y.w);
+    }
+    page_store_out(a, out + d, y, sum > 0.0f ? 1.0f / sum : 0.0f);
+  }
+}
+
+template <int D>
+kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
+  using Cfg = RCfg<D>;
+  CUtensorMap map;
+  if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
+  auto kern = page_rows_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess) return KVQ_ECUDA;
+  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream) != cudaSuccess) return KVQ_ECUDA;
+  kern<<<a.grid, kThreads, Cfg::SMEM, stream>>>(a, map);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.total_q) * a.num_q_heads);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, page_join_kernel<D>, a) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+}
+
+}  // namespace
+
+bool page_supported(int32_t head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
+
+int32_t page_rows_grid(int32_t head_dim, int32_t sms) {
+  return sms * (head_dim == 64 ? RCfg<64>::CTAS : head_dim == 128 ? RCfg<128>::CTAS : RCfg<256>::CTAS);
+}
+
+kvq_status launch_page_rows(const PageArgs& a, cudaStream_t stream) {
+  if (a.head_dim == 64) return launch_d<64>(a, stream);
+  if (a.head_dim == 128) return launch_d<128>(a, stream);
+  return launch_d<256>(a, stream);
+}
+
+}  // namespace kvq

@@ -38,8 +38,9 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;  // 16-byte pieces in flight per thread
 
 // Piece u of the call: piece u % per_page of pair u / per_page; a page's code pieces come first, then its
-// scale pieces.  Every CTA moves kCopyThreads * kCopyVecs consecutive pieces, all loads before the stores.
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(uint4* codes, uint4* scales, const int32_t* __restrict__ src,
+// scale pieces, of 16 bytes or (ScaleVec uint2: an odd number of heads with a scale per page) of 8.  Every CTA moves kCopyThreads * kCopyVecs consecutive pieces, all loads before the stores.
+template <typename ScaleVec>
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(uint4* codes, ScaleVec* scales, const int32_t* __restrict__ src,
                                                                   const int32_t* __restrict__ dst, int32_t n,
                                                                   int64_t num_pages, uint32_t code_vecs,
                                                                   uint32_t scale_vecs) {
@@ -59,9 +60,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(uint4* codes, 
     const int64_t s = __ldg(src + pair), d = __ldg(dst + pair);
     if (s < 0 || d < 0 || s >= num_pages || d >= num_pages) continue;
     const bool code = u < code_vecs;
-    const uint4* from = code ? codes + s * code_vecs + u : scales + s * scale_vecs + (u - code_vecs);
-    to[j] = code ? codes + d * code_vecs + u : scales + d * scale_vecs + (u - code_vecs);
-    v[j] = *from;
+    if constexpr (sizeof(ScaleVec) < sizeof(uint4)) {
+      if (!code) {
+        scales[d * scale_vecs + (u - code_vecs)] = scales[s * scale_vecs + (u - code_vecs)];
+        continue;
+      }
+      to[j] = codes + d * code_vecs + u;
+      v[j] = codes[s * code_vecs + u];
+    } else {
+      const uint4* from = code ? codes + s * code_vecs + u : scales + s * scale_vecs + (u - code_vecs);
+      to[j] = code ? codes + d * code_vecs + u : scales + d * scale_vecs + (u - code_vecs);
+      v[j] = *from;
+    }
   }
 #pragma unroll
   for (int j = 0; j < kCopyVecs; ++j)
@@ -479,12 +489,18 @@ kvq_status launch_pages(const PagesArgs& a, cudaStream_t stream) {
 }  // namespace
 
 kvq_status launch_copy_pages(void* codes, void* scales, const int32_t* src, const int32_t* dst, int32_t n,
-                             int64_t num_pages, uint32_t code_vecs, uint32_t scale_vecs, cudaStream_t stream) {
+                             int64_t num_pages, uint32_t code_vecs, uint32_t scale_bytes, cudaStream_t stream) {
+  const bool small = scale_bytes % 16 != 0;
+  const uint32_t scale_vecs = scale_bytes / (small ? 8 : 16);
   const int64_t per_cta = kCopyThreads * kCopyVecs;
   const int64_t grid = (static_cast<int64_t>(n) * (code_vecs + scale_vecs) + per_cta - 1) / per_cta;
   if (grid > 0x7fffffffLL) return KVQ_EUNSUPPORTED;
-  copy_pages_kernel<<<static_cast<unsigned>(grid), kCopyThreads, 0, stream>>>(
-      static_cast<uint4*>(codes), static_cast<uint4*>(scales), src, dst, n, num_pages, code_vecs, scale_vecs);
+  if (small)
+    copy_pages_kernel<<<static_cast<unsigned>(grid), kCopyThreads, 0, stream>>>(
+        static_cast<uint4*>(codes), static_cast<uint2*>(scales), src, dst, n, num_pages, code_vecs, scale_vecs);
+  else
+    copy_pages_kernel<<<static_cast<unsigned>(grid), kCopyThreads, 0, stream>>>(
+        static_cast<uint4*>(codes), static_cast<uint4*>(scales), src, dst, n, num_pages, code_vecs, scale_vecs);
   return launched();
 }
 

@@ -206,20 +206,21 @@ inline EncodeTiledFn tensor_map_encoder() {
 }
 
 // 5-D view of the code pool [page][kv][head][token][D] as (128-byte slice offset, slice, head*16 + token,
-// kv, page); a box is one slice of the 16 rows of one head, of K or of V: 2 KB, 128-byte swizzled.
+// kv, page); a box is one slice of the 16 rows of one head, of K or of V: 2 KB, 128-byte swizzled.  Rows of 64 are one
+// slice of 64 bytes with the 64-byte swizzle.
 inline bool encode_code_map(CUtensorMap* map, const uint8_t* codes, int64_t num_pages, int32_t num_kv_heads, int D) {
   const EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t H = static_cast<cuuint64_t>(num_kv_heads);
   const cuuint64_t pages = static_cast<cuuint64_t>(std::max<int64_t>(num_pages, 1));  // no copy reads past it
-  const cuuint64_t dims[5] = {128, static_cast<cuuint64_t>(D / 128), H * kPage, 2, pages};
-  const cuuint64_t Dc = static_cast<cuuint64_t>(D);
-  const cuuint64_t strides[4] = {128, Dc, H * kPage * Dc, 2 * H * kPage * Dc};
-  const cuuint32_t box[5] = {128, 1, kPage, 1, 1};
+  const cuuint64_t Dc = static_cast<cuuint64_t>(D), width = std::min<cuuint64_t>(Dc, 128);
+  const cuuint64_t dims[5] = {width, Dc / width, H * kPage, 2, pages};
+  const cuuint64_t strides[4] = {width, Dc, H * kPage * Dc, 2 * H * kPage * Dc};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(width), 1, kPage, 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(codes), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace kvq

@@ -22,8 +22,9 @@ KVQ_FP8_E4M3 = 1
 KVQ_Q8_0 = 2
 KVQ_FP8_E4M3_UNSCALED = 3
 KVQ_FP8_E5M2_UNSCALED = 4
+KVQ_FP8_E4M3_PAGE = 6
 KIND = {"fp8_e4m3": KVQ_FP8_E4M3, "q8_0": KVQ_Q8_0, "fp8_e4m3_unscaled": KVQ_FP8_E4M3_UNSCALED,
-        "fp8_e5m2_unscaled": KVQ_FP8_E5M2_UNSCALED}
+        "fp8_e5m2_unscaled": KVQ_FP8_E5M2_UNSCALED, "fp8_e4m3_page": KVQ_FP8_E4M3_PAGE}
 KVQ_OUT_BF16 = 0
 KVQ_OUT_F32 = 1
 
@@ -40,7 +41,8 @@ EXPORTS = ["kvq_pool_bytes", "kvq_scale_bytes", "kvq_bytes_per_token", "kvq_num_
            "kvq_bytes_per_token_ex", "kvq_num_pages_ex", "kvq_exp2_probe", "kvq_extend_workspace_bytes_ex",
            "kvq_extend_ex", "kvq_extend_path", "kvq_pages_workspace_bytes", "kvq_pages_copy", "kvq_pages_fork",
            "kvq_pages_resize", "kvq_pages_compact", "kvq_tree_workspace_bytes", "kvq_tree",
-           "kvq_prompt_workspace_bytes", "kvq_prompt"]
+           "kvq_prompt_workspace_bytes", "kvq_prompt", "kvq_append_workspace_bytes", "kvq_append",
+           "kvq_decode_workspace_bytes_kind", "kvq_extend_workspace_bytes_kind"]
 
 
 class kvq_layout(ctypes.Structure):
@@ -58,6 +60,11 @@ class kvq_extend_options(ctypes.Structure):
 
 class kvq_prompt_strides(ctypes.Structure):
     _fields_ = [(x + "_" + y, ctypes.c_int64) for x in ("q", "k", "v", "out") for y in ("token", "head")]
+
+
+class kvq_rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("rot_offset", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class KvqError(RuntimeError):
@@ -118,6 +125,11 @@ def lib():
             "kvq_prompt_workspace_bytes": (sz, []),
             "kvq_prompt": (i32, [P, P, P, P, i32, i32, i32, i32, i32, ctypes.c_float, P, i32,
                                  ctypes.POINTER(kvq_prompt_strides), P, sz, P]),
+            "kvq_append_workspace_bytes": (sz, []),
+            "kvq_append": (i32, [P, P, P, P, P, P, i32, P, P, P, i32, i32, i32, P, ctypes.POINTER(kvq_rope),
+                                 ctypes.POINTER(kvq_prompt_strides), P, sz, LP, i32, P]),
+            "kvq_decode_workspace_bytes_kind": (sz, [LP, i32, i32, i32, i32, OP]),
+            "kvq_extend_workspace_bytes_kind": (sz, [LP, i32, i32, i32, i32, i32, EP]),
             "kvq_tree_workspace_bytes": (sz, [LP, i32, i32, i32, i32, i32]),
             "kvq_tree": (i32, [P, P, P, P, i32, P, P, P, i32, i32, i32, i32, ctypes.c_float, P, i32, P, sz, LP, i32, i32,
                                P]),
@@ -184,6 +196,10 @@ class Layout:
     def scales_shape(self):
         return (self.num_pages, self.n_kv, self.num_kv_heads, self.page_size, self.head_dim // 32)
 
+    def page_scales_shape(self):
+        """Of the kind fp8_e4m3_page."""
+        return (self.num_pages, self.n_kv, self.num_kv_heads)
+
 
 # ---------------------------------------------------------------------------- cost model
 def kvq_pool_bytes(layout: Layout) -> int:
@@ -210,9 +226,12 @@ def kvq_num_pages_ex(layout: Layout, kind, budget_bytes: int) -> int:
     return lib().kvq_num_pages_ex(ctypes.byref(layout.c()), _kind(kind), int(budget_bytes))
 
 
-def alloc_pool(layout: Layout, device="cuda"):
-    """(codes uint8, scales as int16 bit patterns) tensors of the pool's shapes on ``device``."""
+def alloc_pool(layout: Layout, device="cuda", kind=None):
+    """(codes uint8, scales as int16 bit patterns) tensors of the pool's shapes on ``device``; scales are float32, one
+    per page, K or V, and head, for the kind fp8_e4m3_page."""
     codes = torch.empty(layout.codes_shape(), dtype=torch.uint8, device=device)
+    if kind is not None and _kind(kind) == KVQ_FP8_E4M3_PAGE:
+        return codes, torch.empty(layout.page_scales_shape(), dtype=torch.float32, device=device)
     scales = torch.empty(layout.scales_shape(), dtype=torch.int16, device=device)
     return codes, scales
 
@@ -245,8 +264,14 @@ def kvq_decode_path(layout: Layout, batch: int, num_q_heads: int, max_pages_per_
                                  ctypes.byref(o))
 
 
-def alloc_workspace(layout: Layout, batch, num_q_heads, max_pages_per_seq, device="cuda", **opts):
-    n = kvq_decode_workspace_bytes(layout, batch, num_q_heads, max_pages_per_seq, **opts)
+def alloc_workspace(layout: Layout, batch, num_q_heads, max_pages_per_seq, device="cuda", kind=None, **opts):
+    """The decode's workspace; the kind fp8_e4m3_page has one of its own size, the others share theirs."""
+    if kind is None:
+        n = kvq_decode_workspace_bytes(layout, batch, num_q_heads, max_pages_per_seq, **opts)
+    else:
+        o = _opts(**opts)
+        n = lib().kvq_decode_workspace_bytes_kind(ctypes.byref(layout.c()), _kind(kind), int(batch), int(num_q_heads),
+                                                  int(max_pages_per_seq), ctypes.byref(o))
     if n == 0:
         raise KvqError(-1, "kvq_decode_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -262,6 +287,7 @@ def kvq_decode(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
         od = KVQ_OUT_F32
     else:
         raise TypeError("out must be bfloat16 or float32")
+    _check_by_page(pool, scales, layout, kind)
     o = _opts(pages_per_split, path)
     _check(lib().kvq_decode_ex(_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]),
                                _ptr(seq_lens), int(seq_lens.shape[0]), int(q.shape[1]), float(sm_scale), _ptr(out),
@@ -279,6 +305,7 @@ def kvq_decode_noalloc(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor
     overlap on the GPU share it and race.
     """
     od = KVQ_OUT_BF16 if out.dtype == torch.bfloat16 else KVQ_OUT_F32
+    _check_by_page(pool, scales, layout, kind)
     _check(lib().kvq_decode_noalloc(_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]),
                                     _ptr(seq_lens), int(seq_lens.shape[0]), int(q.shape[1]), float(sm_scale),
                                     _ptr(out), od, ctypes.byref(layout.c()), _kind(kind), _stream(stream)),
@@ -334,12 +361,18 @@ def _extend_opts(path, precise_p=False):
 
 
 def alloc_extend_workspace(device="cuda", layout: Optional[Layout] = None, total_q=0, num_q_heads=1,
-                           max_pages_per_seq=1, path=None, precise_p=False):
+                           max_pages_per_seq=1, path=None, precise_p=False, kind=None, batch=1):
     """The extend's workspace for these sizes and kernel choice (path None or 0: automatic; 1: each new
     token's prefix on the CUDA-core decode; 2: the flash kernel / the MLA tensor-core decode; precise_p: P
-    carried to 16 bits or more).  Without a layout: the flash kernel's status word."""
+    carried to 16 bits or more).  Without a layout: the flash kernel's status word.  The kind fp8_e4m3_page has a
+    workspace of its own size, which depends on the batch too."""
     if layout is None:
         n = lib().kvq_extend_workspace_bytes()
+    elif kind is not None:
+        n = lib().kvq_extend_workspace_bytes_kind(ctypes.byref(layout.c()), _kind(kind), int(batch), int(total_q),
+                                                  int(num_q_heads), int(max_pages_per_seq), _extend_opts(path, precise_p))
+        if n == 0:
+            raise KvqError(-1, "kvq_extend_workspace_bytes_kind")
     else:
         n = lib().kvq_extend_workspace_bytes_ex(ctypes.byref(layout.c()), int(total_q), int(num_q_heads),
                                                 int(max_pages_per_seq), _extend_opts(path, precise_p))
@@ -367,6 +400,7 @@ def kvq_extend(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
         od = KVQ_OUT_F32
     else:
         raise TypeError("out must be bfloat16 or float32")
+    _check_by_page(pool, scales, layout, kind)
     total_q, Hq = q.shape[0], q.shape[1]
     B = seq_lens.numel()
     args = (_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
@@ -387,13 +421,14 @@ _layouts: dict = {}
 
 
 def _layout_info(L: Layout):
-    """(pointer to the C struct, code bytes, scales) of a layout."""
+    """(pointer to the C struct, code bytes, scales, scales of fp8_e4m3_page) of a layout."""
     key = (L.num_pages, L.page_size, L.num_kv_heads, L.head_dim, L.v_dim, L.mla)
     info = _layouts.get(key)
     if info is None:
         if len(_layouts) >= 1024:
             _layouts.clear()
-        info = _layouts[key] = (ctypes.byref(L.c()), math.prod(L.codes_shape()), math.prod(L.scales_shape()))
+        info = _layouts[key] = (ctypes.byref(L.c()), math.prod(L.codes_shape()), math.prod(L.scales_shape()),
+                               math.prod(L.page_scales_shape()))
     return info
 
 
@@ -434,11 +469,24 @@ def _check_pool(pool, scales, info, kind, device):
             raise ValueError("scales must be contiguous and hold the layout's %d scales of 16 bits" % info[2])
         if scales.get_device() != device:
             raise ValueError("scales is on %s, not on the current CUDA device" % scales.device)
+    elif k == KVQ_FP8_E4M3_PAGE:
+        if scales is None or scales.dtype is not torch.float32:
+            raise TypeError("scales must be torch.float32 for the kind fp8_e4m3_page")
+        if scales.numel() < info[3] or not scales.is_contiguous():
+            raise ValueError("scales must be contiguous and hold the layout's %d scales" % info[3])
+        if scales.get_device() != device:
+            raise ValueError("scales is on %s, not on the current CUDA device" % scales.device)
     else:
         scales = None
     if pool.get_device() != device:
         raise ValueError("pool is on %s, not on the current CUDA device" % pool.device)
     return k, None if scales is None else scales.data_ptr()
+
+
+def _check_by_page(pool, scales, layout, kind):
+    """What the decode and the extend check of a pool whose scales belong to pages: they are fp32 and fewer."""
+    if _kind(kind) == KVQ_FP8_E4M3_PAGE:
+        _check_pool(pool, scales, _layout_info(layout), KVQ_FP8_E4M3_PAGE, torch.cuda.current_device())
 
 
 def _out_dtype(out):
@@ -447,6 +495,81 @@ def _out_dtype(out):
     if out.dtype is torch.float32:
         return KVQ_OUT_F32
     raise TypeError("out must be bfloat16 or float32")
+
+
+# ---------------------------------------------------------------------------- append
+_APPEND_NAMES = ("block_table", "seq_lens", "q_start", "workspace")
+_APPEND_TYPES = (_I32, _I32, _I32, _U8)
+
+
+def alloc_append_workspace(device="cuda"):
+    return torch.empty(lib().kvq_append_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _check_rows(name, t, total, heads, dim, device):
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
+    if t.dim() != 3 or t.shape[0] != total or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s must be [%d, %s, %d]" % (name, total, "heads" if heads is None else heads, dim))
+    if t.stride(2) != 1 and dim > 1:
+        raise ValueError("the last dimension of %s must be dense" % name)
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
+
+
+def kvq_append(pool: torch.Tensor, scales: Optional[torch.Tensor], k: torch.Tensor, v: Optional[torch.Tensor],
+               block_table: torch.Tensor, seq_lens: torch.Tensor, q_start: torch.Tensor, workspace: torch.Tensor,
+               layout: Layout, kind, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+               cos_sin: Optional[torch.Tensor] = None, rot_offset: int = 0, interleaved: bool = False,
+               positions: Optional[torch.Tensor] = None, stream=None):
+    """Appends keys and values to the cache, rotated to their positions on the way, and rotates the queries.
+
+    Rows q_start[b] .. q_start[b+1]-1 of k and v ([total, Hkv, D] bf16; v None for a latent row) become the last tokens
+    of sequence b, whose seq_lens count them and whose block_table has their pages.  q ([total, Hq, D] bf16) is rotated
+    into q_out (q itself: in place).  cos_sin ([max_position, rot_dim] float32: the cosines of rot_dim / 2 angles, then
+    the sines) rotates elements rot_offset .. rot_offset + rot_dim - 1 of q and k, each half with the other or, when
+    interleaved, neighbours; None: no rotation.  positions ([total] int32): other positions than the tokens' places.
+    q, k, v and q_out may be strided between tokens and heads."""
+    total, D = k.shape[0], layout.head_dim
+    _check_tables(block_table, seq_lens, None, layout)
+    if q_start.numel() != seq_lens.numel() + 1:
+        raise ValueError("q_start must be [batch + 1]")
+    info = _layout_info(layout)
+    device = _check_args(_APPEND_NAMES, _APPEND_TYPES, block_table, seq_lens, q_start, workspace)
+    code, sc = _check_pool(pool, scales, info, kind, device)
+    _check_rows("k", k, total, layout.num_kv_heads, D, device)
+    if v is not None:
+        _check_rows("v", v, total, layout.num_kv_heads, D, device)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        _check_rows("q", q, total, None, D, device)
+        _check_rows("q_out", q_out, total, q.shape[1], D, device)
+    rope = None
+    if cos_sin is not None:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [max_position, rot_dim]")
+        if cos_sin.get_device() != device:
+            raise ValueError("cos_sin is on %s, not on the current CUDA device" % cos_sin.device)
+        rope = ctypes.byref(kvq_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], rot_offset,
+                                     1 if interleaved else 0))
+    if positions is not None:
+        if positions.numel() != total:
+            raise ValueError("positions must be [total]")
+        _check_args(("positions",), (_I32,), positions)
+    strides = None
+    if not (k.is_contiguous() and (v is None or v.is_contiguous()) and
+            (q is None or (q.is_contiguous() and q_out.is_contiguous()))):
+        strides = ctypes.byref(kvq_prompt_strides(*[x for t in (k if q is None else q, k, k if v is None else v,
+                                                                k if q is None else q_out) for x in t.stride()[:2]]))
+    st = lib().kvq_append(pool.data_ptr(), sc, None if q is None else q.data_ptr(), k.data_ptr(),
+                          None if v is None else v.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                          seq_lens.data_ptr(), q_start.data_ptr(), None if positions is None else positions.data_ptr(),
+                          total, seq_lens.numel(), 0 if q is None else q.shape[1],
+                          None if q is None else q_out.data_ptr(), rope, strides, workspace.data_ptr(),
+                          workspace.numel(), info[0], code, _raw_stream(stream, device))
+    if st:
+        raise KvqError(st, "kvq_append")
 
 
 # ---------------------------------------------------------------------------- whole prompts

@@ -44,13 +44,17 @@ extern "C" {
 #endif
 
 /* Code format.  The first two use one fp16 scale per 32 elements; the unscaled ones have no scale array
- * (written by kvq_store_unscaled; every attention entry point reads all four, ignoring `scales` for the
- * unscaled kinds, which may then be NULL). */
+ * (written by kvq_store_unscaled; every attention entry point reads these four, ignoring `scales` for the
+ * unscaled kinds, which may then be NULL).  The last one has its scales per block of tokens: its codes' scale factors
+ * out of every dot product.  It is written by kvq_append, copied by kvq_pages_copy, and read by kvq_decode (also
+ * _ex and _noalloc) and kvq_extend (also _ex), for separate K and V rows with head_dim 64, 128 or 256 and page_size
+ * 16; the other calls that take a kind return KVQ_EKIND for it. */
 typedef enum {
     KVQ_FP8_E4M3 = 1,          /* OCP E4M3 "fn" codes, s = amax / 448 */
     KVQ_Q8_0 = 2,              /* int8 codes,          s = amax / 127 */
     KVQ_FP8_E4M3_UNSCALED = 3, /* the plain E4M3 cast, no scales, 1 byte per element (kvq_store_unscaled) */
-    KVQ_FP8_E5M2_UNSCALED = 4  /* the plain E5M2 cast, no scales, 1 byte per element (kvq_store_unscaled) */
+    KVQ_FP8_E5M2_UNSCALED = 4, /* the plain E5M2 cast, no scales, 1 byte per element (kvq_store_unscaled) */
+    KVQ_FP8_E4M3_PAGE = 6      /* E4M3 codes, one power of two for each page, K or V, and head (kvq_append) */
 } kvq_kind;
 
 /* Element type of kvq_decode's output. */
@@ -77,6 +81,7 @@ typedef enum {
  * Pool layout (one layer).  With n_kv = 2 for GQA (K and V) and n_kv = 1 for MLA:
  *   codes : uint8  [num_pages][n_kv][num_kv_heads][page_size][head_dim]
  *   scales: fp16   [num_pages][n_kv][num_kv_heads][page_size][head_dim / 32]
+ *           (KVQ_FP8_E4M3_PAGE: fp32 [num_pages][n_kv][num_kv_heads], powers of two from 2^-32 to 2^32)
  * Token slot s lives in page s / page_size at offset s % page_size.  Each (page, kv, head) chunk is
  * contiguous, so one page of one head is one bulk copy.
  */
@@ -99,8 +104,8 @@ double kvq_bytes_per_token(const kvq_layout* layout);
 /* Whole pages (codes + scales) that fit in `budget_bytes`; num_pages of `layout` is ignored.  -1 if invalid. */
 int64_t kvq_num_pages(const kvq_layout* layout, size_t budget_bytes);
 /* The same two for any kind: 17/16 bytes per element for the block-scaled kinds, 1 for the unscaled fp8 casts
- * ("Add fp8 KV-cache quantization (--kv-dtype)", section "Benchmark": twice the bf16 token budget).  -1 if the
- * layout or the kind is invalid. */
+ * ("Add fp8 KV-cache quantization (--kv-dtype)", section "Benchmark": twice the bf16 token budget), and 1 byte and 4
+ * more per page and row of heads for KVQ_FP8_E4M3_PAGE.  -1 if the layout or the kind is invalid. */
 double kvq_bytes_per_token_ex(const kvq_layout* layout, kvq_kind kind);
 int64_t kvq_num_pages_ex(const kvq_layout* layout, kvq_kind kind, size_t budget_bytes);
 
@@ -121,6 +126,57 @@ int64_t kvq_num_pages_ex(const kvq_layout* layout, kvq_kind kind, size_t budget_
 kvq_status kvq_store(void* pool, void* scales, const void* k, const void* v, const int64_t* slot_mapping,
                      int64_t num_tokens, const kvq_layout* layout, kvq_kind kind, void* stream);
 
+/* ---------------------------------------------------------------- append */
+/*
+ * Appends a step's keys and values to the cache, rotated to their positions on the way, and rotates its queries; one
+ * call in place of a rotation, a slot mapping and a store.  The upstream pages store rows that the model has rotated.
+ * Arguments as kvq_extend, which may follow with the same block_table, seq_lens and q_start: give each sequence its
+ * pages first (kvq_pages_resize); the new tokens are its last n_b = q_start[b + 1] - q_start[b].
+ *   q            device bf16 [total][num_q_heads][head_dim], or NULL with num_q_heads = 0: keys and values only
+ *   k, v         device bf16 [total][num_kv_heads][head_dim]; v must be NULL when layout->mla (the latent row is k)
+ *   positions    device int32 [total]: positions to rotate to (of a tree's drafts, say), or NULL: token i of sequence b
+ *                is rotated to its place seq_lens[b] - n_b + i
+ *   q_out        device bf16, as q; may be q itself (with the same strides), and may not overlap k, v or q otherwise
+ *   rope         the rotation, or NULL: none (q is then copied)
+ *   strides      NULL: dense; else as kvq_prompt, out_* for q_out.  q, k and v may be slices of one projection
+ *   workspace    at least kvq_append_workspace_bytes(), 16-byte aligned, device
+ * Rotation, in fp32 with every product and sum rounded by itself: x'[i] = x[i] cos - x[j] sin, x'[j] = x[j] cos +
+ * x[i] sin over the rot_dim elements from rot_offset on, with pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * interleaved; other elements stay.  Queries are rounded to bf16.  Keys and values are quantized from fp32 as kvq_store
+ * (the block-scaled kinds, IEEE division) and kvq_store_unscaled do from bf16.
+ * KVQ_FP8_E4M3_PAGE: the page's scale is 2^e with the least e for which |x| <= 448 * 2^e for all its rows (within 2^-32
+ * .. 2^32: larger values saturate).  Where a page's new rows need a larger scale than it has, its older codes are
+ * multiplied by the quotient and rounded to nearest-even, which is exact but for codes that leave E4M3's normal
+ * range.  A page whose first row is among the new ones starts afresh; its scale does not shrink otherwise, also when
+ * rows are given up.  A page belongs to one row of the block table while it is appended to (kvq_pages_fork sees to
+ * that).  Rows of a page behind the new ones are left as they are.
+ * A new token whose page is masked (-1) is rotated but not stored.  q_start, seq_lens and positions are read on the
+ * device: a sequence with n_b < 0, n_b > seq_lens[b], q_start[b] < 0, q_start[b + 1] > total or seq_lens[b] >
+ * max_pages_per_seq * page_size is skipped and makes kvq_workspace_status report KVQ_EINVAL, as do a block-table entry >=
+ * layout->num_pages (the token is not stored) and a position outside [0, max_position) (the nearest one is taken).
+ * Rows of q_out that no sequence covers are left as they are.  Supported: every layout and page size for the kinds with a
+ * scale per row (head_dim up to 2048); KVQ_FP8_E4M3_PAGE as said at kvq_kind; otherwise KVQ_EUNSUPPORTED, as for more
+ * than 2^31 - 1 CTAs.  Two calls that store to the same page must not run at the same time.
+ */
+typedef struct kvq_rope {
+    const float* cos_sin;  /* device fp32 [max_position][rot_dim], 16-byte aligned: the cosines of a position's
+                              rot_dim / 2 angles, then their sines */
+    int32_t max_position;
+    int32_t rot_dim;       /* a multiple of 16 */
+    int32_t rot_offset;    /* first rotated element of a row, a multiple of 8 */
+    int32_t interleaved;   /* 0: element i turns with element i + rot_dim / 2; 1: neighbours turn with one another */
+} kvq_rope;
+/* kvq_prompt's strides (below), here too. */
+typedef struct kvq_prompt_strides {
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+} kvq_prompt_strides;
+size_t kvq_append_workspace_bytes(void);
+kvq_status kvq_append(void* pool, void* scales, const void* q, const void* k, const void* v, const int32_t* block_table,
+                      int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* q_start,
+                      const int32_t* positions, int32_t total, int32_t batch, int32_t num_q_heads, void* q_out,
+                      const kvq_rope* rope, const kvq_prompt_strides* strides, void* workspace, size_t workspace_bytes,
+                      const kvq_layout* layout, kvq_kind kind, void* stream);
+
 /* ---------------------------------------------------------------- decode */
 /* Options for kvq_decode_ex.  Zero-initialise for the defaults. */
 typedef struct {
@@ -133,6 +189,10 @@ size_t kvq_decode_workspace_bytes(const kvq_layout* layout, int32_t batch, int32
                                   int32_t max_pages_per_seq);
 size_t kvq_decode_workspace_bytes_ex(const kvq_layout* layout, int32_t batch, int32_t num_q_heads,
                                      int32_t max_pages_per_seq, const kvq_decode_options* options);
+
+/* The same for a kind; the two above say nothing of KVQ_FP8_E4M3_PAGE.  0 if invalid or unsupported. */
+size_t kvq_decode_workspace_bytes_kind(const kvq_layout* layout, kvq_kind kind, int32_t batch, int32_t num_q_heads,
+                                       int32_t max_pages_per_seq, const kvq_decode_options* options);
 
 /*
  * Decode attention for one new query token per sequence.
@@ -160,6 +220,10 @@ size_t kvq_decode_workspace_bytes_ex(const kvq_layout* layout, int32_t batch, in
  * grows with the magnitude of V (about 2^-9 of max |V|).  Automatic (0) picks 2 for 8..16 query heads
  * per kv head, and for the MLA row when batch * max_pages_per_seq * 16 >= 1024 (the MLA tensor-core
  * kernel has a fixed cost of ~50 us); 1 otherwise; kvq_decode_path tells which.
+ * KVQ_FP8_E4M3_PAGE has one kernel of its own, for every number of query heads per kv head: options must be 0 or NULL (else
+ * KVQ_EUNSUPPORTED), kvq_decode_path does not speak of it, and the workspace is kvq_decode_workspace_bytes_kind's.  Its
+ * products are those of the exact values code * scale, with P rounded to fp16 (error about 2^-12 of sum p|v|) and
+ * fp32 sums.
  */
 kvq_status kvq_decode(const void* q, const void* pool, const void* scales, const int32_t* block_table,
                       int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
@@ -278,6 +342,9 @@ size_t kvq_extend_workspace_bytes(void);
  * invalid or unsupported. */
 size_t kvq_extend_workspace_bytes_ex(const kvq_layout* layout, int32_t total_q, int32_t num_q_heads,
                                      int32_t max_pages_per_seq, const kvq_extend_options* options);
+/* The same for a kind; the two above say nothing of KVQ_FP8_E4M3_PAGE. */
+size_t kvq_extend_workspace_bytes_kind(const kvq_layout* layout, kvq_kind kind, int32_t batch, int32_t total_q,
+                                       int32_t num_q_heads, int32_t max_pages_per_seq, const kvq_extend_options* options);
 /* The extend kernel kvq_extend_ex would run: 3 (flash), 4 (flash with P as two bf16 terms), or the decode
  * kernel of the prefixes, 1 (CUDA cores) or 2 (tensor cores).  Otherwise a negative kvq_status (KVQ_EINVAL for invalid sizes or options,
  * KVQ_EUNSUPPORTED when no kernel supports the shape).  Host only; options may be NULL. */
@@ -349,8 +416,8 @@ kvq_status kvq_workspace_status(const void* workspace, void* stream);
  *   k, v         [total, num_kv_heads, head_dim] bf16, device
  *   q_start      [batch + 1] int32, device: rows q_start[b] .. q_start[b + 1] - 1 are sequence b
  *   out          [total, num_q_heads, head_dim], bf16 or f32 (out_dtype), device
- *   strides      NULL: dense.  Else elements between tokens and between heads of each tensor, multiples of 8 (the
- *                last dimension is dense), so that q, k and v may be slices of one projection; ignored along a
+ *   strides      NULL: dense.  Else elements between tokens and between heads of each tensor (kvq_prompt_strides),
+ *                multiples of 8 (the last dimension is dense), so that q, k and v may be slices of one projection; ignored along a
  *                dimension of one.  Tensors are 16-byte aligned.
  *   workspace    at least kvq_prompt_workspace_bytes(), 16-byte aligned, device
  * Row i of a sequence, query head h gets softmax(sm_scale * q.k^T) v over rows 0 .. i of that sequence and kv head
@@ -362,9 +429,6 @@ kvq_status kvq_workspace_status(const void* workspace, void* stream);
  * and makes kvq_workspace_status report KVQ_EINVAL.  Output rows that no sequence covers are left as they are; what a
  * row receives that two consistent sequences claim is unspecified.
  */
-typedef struct kvq_prompt_strides {
-    int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
-} kvq_prompt_strides;
 size_t kvq_prompt_workspace_bytes(void);
 kvq_status kvq_prompt(const void* q, const void* k, const void* v, const int32_t* q_start, int32_t total, int32_t batch,
                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float sm_scale, void* out,
