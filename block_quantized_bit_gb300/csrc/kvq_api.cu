@@ -390,9 +390,10 @@ bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   return true;
 }
 
-// Attention over a KVQ_FP8_E4M3_PAGE cache: the rows kernel and what joins its runs.  max_bytes caps the workspace, and
+// Attention over a KVQ_FP8_E4M3_PAGE cache: the kernel and what joins its runs.  max_bytes caps the workspace, and
 // with it the CTAs (0: no cap).
 struct PagePlan {
+  bool flash;  // the kernel for many query rows
   int32_t grid;
   size_t ml_offset, acc_offset, total;
 };
@@ -403,12 +404,18 @@ bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   if (L.mla || L.page_size != kPageTokens || !page_supported(L.head_dim)) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t tab = up((static_cast<size_t>(batch) + 1) * sizeof(int64_t));
-  const size_t slot = kPageRowsTile * (static_cast<size_t>(L.head_dim) + 2) * sizeof(float);
-  // units of work at most: pages of tiles of 16 rows
-  const double tiles = batch + static_cast<double>(total_q) * (num_q_heads / L.num_kv_heads) / kPageRowsTile;
-  const double units = tiles * L.num_kv_heads * max_pages;
-  int64_t grid = page_rows_grid(L.head_dim, sm_count());
-  if (units < static_cast<double>(grid) * kPageMinUnits) grid = static_cast<int64_t>(units / kPageMinUnits) + 1;
+  // a tile of the rows kernel holds a sequence's rows of a kv head, or the flash kernel takes them
+  const double rows = static_cast<double>(total_q) * (num_q_heads / L.num_kv_heads);
+  pp->flash = total_q > batch && rows > static_cast<double>(kPageRowsTile) * batch;
+  const int32_t tile = pp->flash ? page_flash_rows(L.head_dim) : kPageRowsTile;
+  const int32_t least = pp->flash ? kPageFlashUnits : kPageMinUnits;
+  const size_t slot = tile * (static_cast<size_t>(L.head_dim) + 2) * sizeof(float);
+  // units of work at most: pages of tiles of 16 rows, or tiles of 64 keys or more of items (of half their rows at least)
+  const double tiles = batch + rows / (pp->flash ? tile / 4 : tile) + (pp->flash ? total_q : 0);
+  const double units = tiles * L.num_kv_heads * (pp->flash ? max_pages / 4 + 1.0 : max_pages);
+  if (units > 1e14) return false;  // (units times CTAs are counted in 64 bits)
+  int64_t grid = pp->flash ? sm_count() : page_rows_grid(L.head_dim, sm_count());
+  if (units < static_cast<double>(grid) * least) grid = static_cast<int64_t>(units / least) + 1;
   if (max_bytes > 0) {
     if (max_bytes < kWorkspaceHeader + tab + 1024) return false;
     grid = std::min<int64_t>(grid, (max_bytes - kWorkspaceHeader - tab - 512) / (2 * slot));
@@ -417,8 +424,8 @@ bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   const size_t slots = 2 * static_cast<size_t>(grid);
   pp->grid = static_cast<int32_t>(grid);
   pp->ml_offset = kWorkspaceHeader + tab;
-  pp->acc_offset = pp->ml_offset + up(slots * kPageRowsTile * 2 * sizeof(float));
-  pp->total = pp->acc_offset + up(slots * kPageRowsTile * L.head_dim * sizeof(float));
+  pp->acc_offset = pp->ml_offset + up(slots * tile * 2 * sizeof(float));
+  pp->total = pp->acc_offset + up(slots * tile * L.head_dim * sizeof(float));
   return true;
 }
 
@@ -467,7 +474,7 @@ kvq_status page_common(const void* q, const void* pool, const void* scales, cons
   a.grid = pp.grid;
   a.score_scale = sm_scale * 1.4426950408889634f;  // log2(e)
   a.out_dtype = out_dtype;
-  return launch_page_rows(a, s);
+  return pp.flash ? launch_page_flash(a, s) : launch_page_rows(a, s);
 }
 
 kvq_status page_decode(const void* q, const void* pool, const void* scales, const int32_t* block_table, int32_t max_pages,

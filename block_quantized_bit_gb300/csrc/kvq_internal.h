@@ -241,8 +241,8 @@ struct PageArgs {
   void* out;                  // [total_q][num_q_heads][head_dim]
   uint32_t* status;
   int64_t* tab;               // [batch + 1] units before each sequence, and in all
-  float* part_acc;            // [2 * grid][kPageRowsTile][head_dim]
-  float* part_ml;             // [2 * grid][kPageRowsTile][2]
+  float* part_acc;            // [2 * grid][rows][head_dim], rows: kPageRowsTile or page_flash_rows()
+  float* part_ml;             // [2 * grid][rows][2]
   int64_t num_pages;
   int32_t max_pages, batch, total_q, num_q_heads, num_kv_heads, head_dim;
   int32_t grid;               // CTAs launched
@@ -251,9 +251,12 @@ struct PageArgs {
 };
 constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
+constexpr int kPageFlashUnits = 4; // key tiles that are worth a CTA of the flash kernel
 bool page_supported(int32_t head_dim);
 int32_t page_rows_grid(int32_t head_dim, int32_t sms);  // CTAs that are resident at once
 kvq_status launch_page_rows(const PageArgs& a, cudaStream_t stream);
+int32_t page_flash_rows(int32_t head_dim);  // query rows of an item of the flash kernel
+kvq_status launch_page_flash(const PageArgs& a, cudaStream_t stream);
 // kvq_decode of that kind with no more CTAs than the workspace has room for.
 kvq_status decode_pages_capped(const void* q, const void* pool, const void* scales, const int32_t* block_table,
                                int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,

@@ -1,4 +1,5 @@
-// kvq_page.cuh -- pieces shared by the kernels over a KVQ_FP8_E4M3_PAGE cache: output stores.
+// kvq_page.cuh -- pieces shared by the kernels over a KVQ_FP8_E4M3_PAGE cache: how a call's work is cut into equal runs,
+// output stores.
 #pragma once
 
 #include "kvq_device.cuh"
@@ -6,6 +7,103 @@
 
 namespace kvq {
 namespace {
+
+constexpr float kNoMax = -1e30f;  // reference of a row that has seen nothing
+constexpr float kHead = 7.0f;     // log2 of the largest p when a row's reference moves ...
+constexpr float kLimit = 15.0f;   // ... and at most (P is f16, which ends at 2^16)
+
+// One sequence's query rows and stored tokens; n = 0: nothing to do.
+struct PageSeq {
+  int32_t q0, n, len;
+};
+
+__device__ __forceinline__ PageSeq page_sequence(const PageArgs& a, int32_t b, bool& bad) {
+  PageSeq s;
+  const int32_t room = a.max_pages * kPage;
+  s.len = __ldg(a.seq_lens + b);
+  if (a.q_start == nullptr) {  // one row per sequence
+    s.q0 = b;
+    s.n = 1;
+    s.len = min(max(s.len, 0), room);
+    return s;
+  }
+  s.q0 = __ldg(a.q_start + b);
+  const int64_t q1 = __ldg(a.q_start + b + 1), n = q1 - s.q0;
+  const bool ok = s.q0 >= 0 && n >= 0 && q1 <= a.total_q && n <= s.len && s.len <= room;
+  bad |= !ok;
+  s.n = ok ? static_cast<int32_t>(n) : 0;
+  return s;
+}
+
+// All units of a call lie in one order, sequence by sequence.  U of them are shared by C CTAs, each taking an equal
+// run, whatever the lengths.
+__device__ __forceinline__ int32_t sharers(int64_t U, int32_t grid, int32_t least) {
+  return static_cast<int32_t>(min(static_cast<int64_t>(grid), max(U / least, static_cast<int64_t>(1))));
+}
+__device__ __forceinline__ int64_t first_unit(int64_t U, int32_t C, int32_t c) { return U * c / C; }
+
+// The CTA among whose units u is.
+__device__ __forceinline__ int32_t owner_of(int64_t U, int32_t C, int64_t u) {
+  int32_t c = static_cast<int32_t>(u * C / U);
+  while (c > 0 && first_unit(U, C, c) > u) --c;
+  while (c + 1 < C && first_unit(U, C, c + 1) <= u) ++c;
+  return c;
+}
+
+// The slot of partial sums that CTA c has for a tile whose first unit is `first`: a run's tile that began before it, or
+// fills it, has the first of the two.
+__device__ __forceinline__ int64_t part_slot(int64_t U, int32_t C, int32_t c, int64_t first) {
+  return 2 * static_cast<int64_t>(c) + (first > first_unit(U, C, c) ? 1 : 0);
+}
+
+// The sequence in which unit want(total) lies, and the units before it.
+struct Place {
+  int64_t total, before;
+  int32_t b;  // -1: none
+};
+
+// units(b): a sequence's units; every thread of the CTA (of WARPS warps) calls it.  `tab`, where not null, receives the
+// units before each sequence and, behind them, their sum.
+template <int WARPS, typename Units, typename Want>
+__device__ __forceinline__ Place page_place(int32_t batch, int64_t* tab, Units units, Want want_of) {
+  __shared__ int64_t s_sum[WARPS];
+  __shared__ Place s_place;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t per = (batch + WARPS * 32 - 1) / (WARPS * 32);
+  const int32_t b0 = min(tid * per, batch), b1 = min(b0 + per, batch);
+  int64_t mine = 0;
+  for (int32_t b = b0; b < b1; ++b) mine += units(b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  if (tid == 0) s_place.b = -1;
+  __syncthreads();
+  int64_t run = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) run += s_sum[w];
+    total += s_sum[w];
+  }
+  const int64_t want = want_of(total);
+  if (tab != nullptr && tid == 0) tab[batch] = total;
+  for (int32_t b = b0; b < b1; ++b) {
+    const int64_t u = units(b);
+    if (tab != nullptr) tab[b] = run;
+    if (want >= run && want < run + u) {
+      s_place.b = b;
+      s_place.before = run;
+    }
+    run += u;
+  }
+  __syncthreads();
+  Place p = s_place;
+  p.total = total;
+  return p;
+}
 
 // Four neighbouring outputs x * scale from element `at` on (a multiple of 4), bf16 or fp32.
 __device__ __forceinline__ void page_store_out(const PageArgs& a, int64_t at, float4 x, float scale) {
@@ -18,6 +116,16 @@ __device__ __forceinline__ void page_store_out(const PageArgs& a, int64_t at, fl
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The exponent of a page's scale, and the scale's reciprocal.
+__device__ __forceinline__ float scale_exponent(float s) { return static_cast<float>((__float_as_int(s) >> 23) - 127); }
+__device__ __forceinline__ float scale_inverse(float s) { return __int_as_float(0x7F000000 - __float_as_int(s)); }
 
 }  // namespace
 }  // namespace kvq

@@ -1,0 +1,904 @@
+// kvq_page_flash.cu -- causal attention of many query rows over a KVQ_FP8_E4M3_PAGE cache (kvq_extend), on the tcgen05 tensor
+// cores, head_dim 64, 128 and 256, any number of query heads per kv head.  With K = 2^ek[page] code, V = 2^ev[page] code:
+//   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t.
+// 4 D FLOPs per (row, key) against 2 D bytes per key for up to 256 rows: bound by the tensor pipe.
+//
+// The scales never meet a code, so K's codes go to the tensor cores as they lie in the pool: S = Q . K^T in 8 bits, with
+// each row of q, scaled by a power of two, as the sum of two E4M3 terms (bf16 has 8 significant bits, a term
+// 4; what is 2^-10 of the row's largest or less loses some, at most 2^-18 of the largest).  Two 8-bit products take the
+// time of one 16-bit one and need no conversion.  For the output P has to keep more bits than 8-bit terms give cheaply
+// (two terms would cost five instructions a probability), so V's codes become f16 instead, exactly and once for up
+// to 256 rows, and P is rounded to f16 (2^-11).
+//
+// A tile is 128 query rows of one kv head: tokens times heads of its group (at most 128 heads; larger groups are cut).
+// Tensor memory at head_dim 64 and 128: S_A, S_B, O_A, O_B, two tiles A and B of a CTA whose softmax and MMAs alternate; at
+// 256 one tile, with two S buffers of 64 keys.  P (f16) replaces the S it was made from.
+// Warps: softmax (one per lane quarter and tile, one thread per row), one that issues all MMAs, one that finds the work,
+// reads block table and scales and loads K and V codes with TMA (a page's 16 rows as one box), six that turn V's codes into
+// f16 (and clear rows behind the sequence's end and of masked pages, which may hold anything: 0 * NaN would be NaN).
+// Work: a unit is a key tile of an item (one or two tiles of a kv head).  All units lie in one order, and every CTA takes an
+// equal run of them, so that a few long contexts fill the GPU as well as many short ones.  A run that is all of an item
+// gives its output, other runs leave partial sums for a second kernel, its programmatic dependent.
+// Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "kvq_device.cuh"
+#include "kvq_flash.cuh"
+#include "kvq_internal.h"
+#include "kvq_page.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kM = 128;           // rows of a tile
+constexpr int kConvWarps = 6;     // that turn V's codes into f16
+constexpr int kInfo = 8;          // key tiles whose pages are described in shared memory
+constexpr int kTmemCols = 512;
+
+template <int D>
+struct FCfg {
+  static constexpr int TILES = D == 256 ? 1 : 2;
+  static constexpr int KT = D == 256 ? 64 : 128;        // keys of a key tile
+  static constexpr int PAGES = KT / kPage;
+  static constexpr int SLICES = D == 256 ? 2 : 1;       // 128-byte (D = 64: 64-byte) slices of a row of codes
+  static constexpr int SLICE = D == 64 ? 64 : 128;
+  static constexpr int Q_TERM = kM * D;                 // bytes of one term of a tile's q
+  static constexpr int K_TILE = KT * D, V_TILE = 2 * KT * D;
+  static constexpr int KST = D == 64 ? 4 : 3, VST = 2;  // stages of K codes; of V codes and of V in f16
+  static constexpr int SM_WARPS = 4 * TILES;
+  static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1, CONV_WARP = SM_WARPS + 2;
+  static constexpr int THREADS = (SM_WARPS + 2 + kConvWarps) * 32;  // whole groups of four warps: 512 or 384
+  static constexpr int Q_OFF = 0;                       // 1024-byte aligned: swizzle atoms
+  static constexpr int K_OFF = Q_OFF + TILES * 2 * Q_TERM;
+  static constexpr int C_OFF = K_OFF + KST * K_TILE;    // V codes
+  static constexpr int V_OFF = C_OFF + VST * K_TILE;
+  static constexpr int INFO_OFF = V_OFF + VST * V_TILE;
+  static constexpr int ITEM_OFF = INFO_OFF + kInfo * PAGES * 16;
+  static constexpr int BAR_OFF = ITEM_OFF + 2 * 64;
+  static constexpr int NBARS = 2 * KST + 4 * VST + 2 * kInfo + 14;
+  static constexpr int SMEM = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
+  static constexpr int O_COL = D == 256 ? 128 : 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(O_COL + TILES * D <= kTmemCols, "tensor memory");
+};
+
+// What the softmax and the converting warps know of a page of a key tile.
+struct PageInfo {
+  float ks;       // K's scale (1 for a masked page)
+  float ev, unv;  // V's exponent, and 2^-ev
+  int32_t rows;   // rows that hold tokens; 0: masked
+};
+static_assert(sizeof(PageInfo) == 16, "info slots");
+
+// A run of an item's key tiles.
+struct Item {
+  int64_t first;                  // the item's first unit
+  int32_t live, q0, n, len;
+  int32_t head0, heads;           // first query head of the group, heads of it
+  int32_t tok0;                   // first token of the item
+  int32_t kt0, kt1, whole;        // key tiles of the run; whether they are all of the item's
+};
+static_assert(sizeof(Item) <= 64, "item slots");
+
+// Sum over i < n of floor((a i + b) / m), a, b >= 0 (the lattice points under a line, by the Euclidean algorithm).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t top = a * n + b;
+    n = top / m;
+    b = top % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+    if (m == 0) break;
+  }
+  return s;
+}
+
+// How a call's rows fall into items: groups of at most 128 heads, tokens of a tile and of an item.
+template <int D>
+struct Shape {
+  using Cfg = FCfg<D>;
+  int32_t G, groups, heads, tile_tok, item_tok;  // groups: per kv head; heads: of a group (the last may have fewer)
+  __device__ __forceinline__ explicit Shape(const PageArgs& a) {
+    G = a.num_q_heads / a.num_kv_heads;
+    groups = (G + kM - 1) / kM;
+    heads = (G + groups - 1) / groups;
+    groups = (G + heads - 1) / heads;
+    tile_tok = kM / heads;
+    item_tok = tile_tok * Cfg::TILES;
+  }
+  __device__ __forceinline__ int32_t items(const PageSeq& s) const { return (s.n + item_tok - 1) / item_tok; }
+  // key tiles that item p of a sequence sees
+  __device__ __forceinline__ int32_t key_tiles(const PageSeq& s, int32_t p) const {
+    const int64_t last = s.len - s.n + min(static_cast<int64_t>(s.n), static_cast<int64_t>(p + 1) * item_tok);
+    return static_cast<int32_t>((last + Cfg::KT - 1) / Cfg::KT);
+  }
+  // key tiles of the items before p (p < items: all of these have item_tok tokens)
+  __device__ __forceinline__ int64_t before(const PageSeq& s, int32_t p) const {
+    return floor_sum(p, Cfg::KT, item_tok, static_cast<int64_t>(s.len - s.n) + item_tok + Cfg::KT - 1);
+  }
+  __device__ __forceinline__ int64_t per_group(const PageSeq& s) const {
+    if (s.n == 0) return 0;
+    const int32_t p = items(s) - 1;
+    return before(s, p) + key_tiles(s, p);
+  }
+  __device__ __forceinline__ int64_t units(const PageArgs& a, const PageSeq& s) const {
+    return per_group(s) * groups * a.num_kv_heads;
+  }
+  // the item in which unit `local` of a sequence lies; returns the units from the item's start to it
+  __device__ __forceinline__ int64_t locate(const PageSeq& s, int64_t local, int32_t& group, int32_t& p) const {
+    const int64_t per = per_group(s);
+    group = static_cast<int32_t>(local / per);
+    const int64_t rest = local - group * per;
+    int32_t lo = 0, hi = items(s) - 1;  // the last item that begins at or before `rest`
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) / 2;
+      if (before(s, mid) <= rest) lo = mid;
+      else hi = mid - 1;
+    }
+    p = lo;
+    return rest - before(s, p);
+  }
+};
+
+// S = Q . K^T in E4M3, the terms of q one after the other into the same sums; a k-step is 32 bytes.  STEPS of a slice.
+template <int STEPS>
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (STEPS == 4) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  } else {
+    static_assert(STEPS == 2, "2 or 4 steps");
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, b1;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+
+// Instruction descriptor: M = 128, N columns, fp32 sums; E4M3 x E4M3 and f16 x f16 both have code 0.
+__device__ __forceinline__ uint32_t page_idesc(int n, bool b_mn_major) {
+  return 1u << 4 | static_cast<uint32_t>(b_mn_major) << 16 | static_cast<uint32_t>(n >> 3) << 17 |
+         static_cast<uint32_t>(kM >> 4) << 24;
+}
+
+// 16 columns of this lane's row and their maximum.
+__device__ __forceinline__ void tmem_ld16_max_issue(uint32_t taddr, uint32_t* r, uint32_t& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(top)
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait16_max(uint32_t* r, uint32_t& top) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(top)
+               :
+               : "memory");
+}
+
+// Two E4M3 codes (low byte = a) and the values they stand for.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b, float& va, float& vb) {
+  const uint32_t c = encode_fp8x2(a, b);
+  uint32_t h, unused;
+  codes_to_f16x2<KVQ_FP8_E4M3>(c, h, unused);
+  va = half_bits_to_float(lo16(h));
+  vb = half_bits_to_float(hi16(h));
+  return c;
+}
+
+template <int D>
+__global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
+    page_flash_kernel(const PageArgs a, const __grid_constant__ CUtensorMap map) {
+  using Cfg = FCfg<D>;
+  constexpr int TILES = Cfg::TILES, KT = Cfg::KT, PAGES = Cfg::PAGES, SLICES = Cfg::SLICES;
+  constexpr int KST = Cfg::KST, VST = Cfg::VST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem + Cfg::Q_OFF;  // [tile][term]
+  uint8_t* sK = smem + Cfg::K_OFF;  // [KST]
+  uint8_t* sC = smem + Cfg::C_OFF;  // [VST] codes of V
+  uint8_t* sV = smem + Cfg::V_OFF;  // [VST] V in f16
+  PageInfo* sInfo = reinterpret_cast<PageInfo*>(smem + Cfg::INFO_OFF);  // [kInfo][PAGES]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
+  uint64_t* bar_k_full = bars;                    // [KST] K codes landed
+  uint64_t* bar_k_empty = bar_k_full + KST;       // [KST] their last QK completed (commit)
+  uint64_t* bar_c_full = bar_k_empty + KST;       // [VST] V codes landed
+  uint64_t* bar_c_empty = bar_c_full + VST;       // [VST] turned into f16
+  uint64_t* bar_v_full = bar_c_empty + VST;       // [VST] V in f16 written
+  uint64_t* bar_v_empty = bar_v_full + VST;       // [VST] its last PV completed (commit)
+  uint64_t* bar_info = bar_v_empty + VST;         // [kInfo] the key tile's pages are described
+  uint64_t* bar_s_full = bar_info + kInfo;        // [2] QK into S buffer w completed (commit)
+  uint64_t* bar_p_full = bar_s_full + 2;          // [2] P of buffer w written
+  uint64_t* bar_pv_done = bar_p_full + 2;         // [2] PV of buffer w completed (commit)
+  uint64_t* bar_q_full = bar_pv_done + 2;         // [TILES] q of the item written
+  uint64_t* bar_o_free = bar_q_full + 2;          // [TILES] O read out
+  uint64_t* bar_item = bar_o_free + 2;            // [2] item slot published
+  uint64_t* bar_item_free = bar_item + 2;         // [2] item slot read by every consuming warp
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
+  auto sItem = [&](uint32_t k) { return reinterpret_cast<Item*>(smem + Cfg::ITEM_OFF + (k & 1) * 64); };
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t cta = blockIdx.x;
+  const Shape<D> shape(a);
+  bool ok = true, bad = false;
+
+  if (tid == 0) {
+    for (int i = 0; i < KST; ++i) {
+      mbar_init(&bar_k_full[i], 1);
+      mbar_init(&bar_k_empty[i], 1);
+    }
+    for (int i = 0; i < VST; ++i) {
+      mbar_init(&bar_c_full[i], 1);
+      mbar_init(&bar_c_empty[i], kConvWarps);
+      mbar_init(&bar_v_full[i], kConvWarps);
+      mbar_init(&bar_v_empty[i], 1);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(&bar_info[i], 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bar_s_full[w], 1);
+      mbar_init(&bar_p_full[w], 4);
+      mbar_init(&bar_pv_done[w], 1);
+      mbar_init(&bar_q_full[w], 4);
+      mbar_init(&bar_o_free[w], 4);
+      mbar_init(&bar_item[w], 1);
+      mbar_init(&bar_item_free[w], Cfg::SM_WARPS + 1 + kConvWarps);
+    }
+    fence_mbar_init();
+  }
+  if (warp == Cfg::MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  const Place place = page_place<Cfg::THREADS / 32>(
+      a.batch, cta == 0 ? a.tab : nullptr, [&](int32_t i) { return shape.units(a, page_sequence(a, i, bad)); },
+      [&](int64_t U) {  // this CTA's first unit
+        const int32_t C = sharers(U, a.grid, kPageFlashUnits);
+        return cta < C && U > 0 ? first_unit(U, C, cta) : U;
+      });
+  if (cta == 0 && bad) set_status(a.status, kStatusBadExtend);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sTmem;
+
+  // the k-th item of this CTA, for a consuming warp
+  auto take_item = [&](uint32_t k, Item& it) -> bool {
+    if (!warp_wait_far(&bar_item[k & 1], (k >> 1) & 1)) return false;
+    it = *sItem(k);
+    __syncwarp();
+    if (lane == 0) bar_arrive(&bar_item_free[k & 1]);
+    return true;
+  };
+
+  if (warp == Cfg::LOAD_WARP) {
+    // ===================================================================== items, pages, loads
+    const int32_t C = sharers(place.total, a.grid, kPageFlashUnits);
+    int64_t u = place.b < 0 ? 0 : first_unit(place.total, C, cta);
+    const int64_t u_end = place.b < 0 ? 0 : first_unit(place.total, C, cta + 1);
+    int64_t before = place.before;
+    int32_t b = place.b;
+    uint32_t kv = 0, kc = 0, vc = 0;  // key tiles; K and V stages that hold copies
+    for (uint32_t k = 0; ok; ++k) {
+      Item it;
+      it.live = 0;
+      int32_t g = 0;
+      while (u < u_end) {
+        const PageSeq s = page_sequence(a, b, bad);
+        const int64_t units = shape.units(a, s);
+        if (u >= before + units) {
+          before += units;
+          ++b;
+          continue;
+        }
+        int32_t group, p;
+        const int64_t at = shape.locate(s, u - before, group, p);
+        it.live = 1;
+        it.first = u - at;
+        it.q0 = s.q0;
+        it.n = s.n;
+        it.len = s.len;
+        g = group / shape.groups;
+        const int32_t part = group - g * shape.groups;
+        it.head0 = g * shape.G + part * shape.heads;
+        it.heads = min(shape.heads, shape.G - part * shape.heads);
+        it.tok0 = p * shape.item_tok;
+        it.kt0 = static_cast<int32_t>(at);
+        const int32_t all = shape.key_tiles(s, p);
+        it.kt1 = static_cast<int32_t>(min(static_cast<int64_t>(all), it.kt0 + (u_end - u)));
+        it.whole = it.kt0 == 0 && it.kt1 == all;
+        break;
+      }
+      if (k >= 2 && !warp_wait_far(&bar_item_free[k & 1], ((k >> 1) - 1) & 1)) { ok = false; break; }
+      if (lane == 0) {
+        *sItem(k) = it;
+        bar_arrive(&bar_item[k & 1]);
+      }
+      __syncwarp();
+      if (!it.live) break;
+      // pages of the run, 32 at a time, one per lane, the next 32 fetched meanwhile
+      const int32_t pg0 = it.kt0 * PAGES, np = min(it.kt1 * PAGES, (it.len + kPage - 1) / kPage) - pg0;
+      const int32_t* table = a.block_table + static_cast<int64_t>(b) * a.max_pages + pg0;
+      auto fetch = [&](int32_t batch) -> int32_t {
+        const int32_t i = batch * 32 + lane;
+        if (i >= np) return -1;
+        const int32_t x = __ldg(table + i);
+        if (x < a.num_pages) return x;
+        set_status(a.status, kStatusBadPage);
+        return -1;
+      };
+      auto scales = [&](int32_t x, float& ks, float& vs) {
+        ks = vs = 1.0f;
+        if (x < 0) return;
+        const float* at = a.scales + static_cast<int64_t>(x) * 2 * a.num_kv_heads + g;
+        ks = __ldg(at);
+        vs = __ldg(at + a.num_kv_heads);
+      };
+      constexpr int BATCH = 32 / PAGES;  // key tiles whose pages the lanes hold
+      int32_t phys = fetch(0), phys_next = fetch(1);
+      float ks, vs, ks_next = 1.0f, vs_next = 1.0f;
+      scales(phys, ks, vs);
+      for (int32_t j = 0; j < it.kt1 - it.kt0; ++j, ++kv) {
+        if (j > 0 && j % BATCH == 0) {
+          phys = phys_next;
+          ks = ks_next;
+          vs = vs_next;
+          phys_next = fetch(j / BATCH + 1);
+        }
+        if (j % BATCH == 1) scales(phys_next, ks_next, vs_next);
+        const int32_t first = j % BATCH * PAGES;            // the lane of the tile's first page
+        const bool mine = lane >= first && lane < first + PAGES;
+        const int32_t x = lane - first;                     // page of the tile
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine && phys >= 0));
+        const int sk = kv % KST, sv = kv % VST;
+        if (kv >= KST && !warp_wait_far(&bar_k_empty[sk], (kv / KST - 1) & 1)) { ok = false; break; }
+        if (mine) {
+          PageInfo f;
+          f.ks = phys >= 0 ? ks : 1.0f;
+          f.ev = phys >= 0 ? scale_exponent(vs) : 0.0f;
+          f.unv = phys >= 0 ? scale_inverse(vs) : 1.0f;
+          f.rows = phys >= 0 ? min(kPage, it.len - (pg0 + j * PAGES + x) * kPage) : 0;
+          sInfo[kv % kInfo * PAGES + x] = f;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&bar_info[kv % kInfo]);
+          mbar_arrive_expect_tx(&bar_k_full[sk], count * kPage * D);
+        }
+        __syncwarp();
+        if (mine && phys >= 0) {
+#pragma unroll
+          for (int s = 0; s < SLICES; ++s)
+            tma_load_codes(smem_u32(sK + sk * Cfg::K_TILE + s * KT * Cfg::SLICE + x * kPage * Cfg::SLICE), &map, s, g * kPage,
+                           0, phys, &bar_k_full[sk]);
+        }
+        kc = kv + 1;
+        __syncwarp();
+        if (kv >= VST && !warp_wait_far(&bar_c_empty[sv], (kv / VST - 1) & 1)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(&bar_c_full[sv], count * kPage * D);
+        __syncwarp();
+        if (mine && phys >= 0) {
+#pragma unroll
+          for (int s = 0; s < SLICES; ++s)
+            tma_load_codes(smem_u32(sC + sv * Cfg::K_TILE + s * KT * Cfg::SLICE + x * kPage * Cfg::SLICE), &map, s, g * kPage,
+                           1, phys, &bar_c_full[sv]);
+        }
+        vc = kv + 1;
+        __syncwarp();
+      }
+      if (!ok) break;
+      u += it.kt1 - it.kt0;
+    }
+    // no copy may still be in flight when the CTA exits
+    for (uint32_t j = 1; j <= kc && j <= static_cast<uint32_t>(KST); ++j)
+      (void)mbar_wait_bounded(&bar_k_full[(kc - j) % KST], ((kc - j) / KST) & 1);
+    for (uint32_t j = 1; j <= vc && j <= static_cast<uint32_t>(VST); ++j)
+      (void)mbar_wait_bounded(&bar_c_full[(vc - j) % VST], ((vc - j) / VST) & 1);
+  } else if (warp >= Cfg::CONV_WARP) {
+    // ===================================================================== V's codes to f16
+    // A warp takes 8 rows x 64 codes at a time: lanes 4 h .. 4 h + 3 the four 16-byte pieces of a row, rows r and r ^ 5
+    // side by side, so that neither the reads of 16 bytes nor the writes of 2 x 16 meet in a bank.
+    const int32_t cw = warp - Cfg::CONV_WARP;
+    const int r8 = (lane >> 3) ^ (lane & 4 ? 5 : 0), c4 = lane & 3;
+    uint32_t kv = 0;
+    Item it;
+    for (uint32_t k = 0; ok; ++k) {
+      if (!take_item(k, it)) { ok = false; break; }
+      if (!it.live) break;
+      for (int32_t j = it.kt0; j < it.kt1; ++j, ++kv) {
+        const int s = kv % VST;
+        if (!warp_wait_far(&bar_info[kv % kInfo], (kv / kInfo) & 1) || !warp_wait_far(&bar_c_full[s], (kv / VST) & 1) ||
+            (kv >= VST && !warp_wait_far(&bar_v_empty[s], (kv / VST - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = sC + s * Cfg::K_TILE;
+        uint8_t* dst = sV + s * Cfg::V_TILE;
+        const PageInfo* info = sInfo + kv % kInfo * PAGES;
+        constexpr int PER_ROW = D / 64;  // steps of 64 codes in a row
+#pragma unroll 2
+        for (int i = cw; i < KT / 8 * PER_ROW; i += kConvWarps) {
+          const int row = i / PER_ROW * 8 + r8, step = i % PER_ROW;
+          const int c = step * 4 + c4;   // 16-byte piece of the row of codes
+          uint4 w;
+          if constexpr (D == 64)
+            w = *reinterpret_cast<const uint4*>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+          else
+            w = *reinterpret_cast<const uint4*>(src + c / 8 * KT * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+          const bool live = row % kPage < info[row / kPage].rows;
+          const uint32_t in[4] = {live ? w.x : 0u, live ? w.y : 0u, live ? w.z : 0u, live ? w.w : 0u};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) codes_to_f16x2<KVQ_FP8_E4M3>(in[e], h[2 * e], h[2 * e + 1]);
+          uint8_t* to = dst + step * KT * 128 + row * 128;  // 64 f16: 128-byte rows
+          *reinterpret_cast<uint4*>(to + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(to + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&bar_v_full[s]);
+          bar_arrive(&bar_c_empty[s]);
+        }
+      }
+    }
+  } else if (warp == Cfg::MMA_WARP) {
+    // ===================================================================== MMA issue (elected lane)
+    const uint32_t idesc_qk = page_idesc(KT, false), idesc_pv = page_idesc(D, true);
+    auto k_major = [&](const uint8_t* p) {
+      return D == 64 ? smem_desc(smem_u32(p), 16, 512) | static_cast<uint64_t>(4) << 61 : sw128_desc(smem_u32(p), 16, 1024);
+    };
+    const uint64_t dq0 = k_major(sQ), dk0 = k_major(sK), dv0 = sw128_desc(smem_u32(sV), KT * 128, 1024);
+    uint32_t kv = 0;               // key tiles of finished items
+    uint32_t nt[2] = {0, 0};       // PVs issued from S buffer w
+    uint32_t ni[2] = {0, 0};       // items of tile w
+    Item it;
+    auto qk = [&](int w, int buf, uint32_t stage) -> bool {
+      // P of the buffer's last PV lies in the columns that this QK writes
+      if (nt[buf] > 0 && !warp_wait_far(&bar_pv_done[buf], (nt[buf] - 1) & 1)) return false;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * KT;
+      const uint64_t q = dq0 + ((w * 2 * Cfg::Q_TERM) >> 4), kk = dk0 + ((stage * Cfg::K_TILE) >> 4);
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int s = 0; s < SLICES; ++s)
+          mma_fp8<Cfg::SLICE / 32>(d, q + ((term * Cfg::Q_TERM + s * kM * 128) >> 4), kk + ((s * KT * 128) >> 4), idesc_qk,
+                                   term + s > 0 ? 1u : 0u);
+      mma_commit(&bar_s_full[buf]);
+      return true;
+    };
+    auto pv = [&](int w, int buf, uint32_t stage, bool first) -> bool {
+      if (first && ni[w] > 1 && !warp_wait_far(&bar_o_free[w], (ni[w] - 2) & 1)) return false;
+      if (!warp_wait_far(&bar_p_full[buf], nt[buf] & 1)) return false;
+      tc_fence_after();
+      const uint64_t v = dv0 + ((stage * Cfg::V_TILE) >> 4);
+      // a k-step is 16 keys: 8 columns of P, 16 rows of V
+      if constexpr (KT == 128)
+        mma8_bf16_tmem_a(tmem + Cfg::O_COL + w * D, tmem + buf * KT, 8u, v, static_cast<uint64_t>((16 * 128) >> 4), idesc_pv,
+                         first ? 0u : 1u);
+      else
+        mma4_bf16_tmem_a(tmem + Cfg::O_COL + w * D, tmem + buf * KT, 8u, v, static_cast<uint64_t>((16 * 128) >> 4), idesc_pv,
+                         first ? 0u : 1u);
+      mma_commit(&bar_pv_done[buf]);
+      ++nt[buf];
+      return true;
+    };
+    for (uint32_t k = 0; ok; ++k) {
+      if (!take_item(k, it)) { ok = false; break; }
+      if (!it.live) break;
+      const int32_t n = it.kt1 - it.kt0;
+      const bool two = TILES == 2 && it.tok0 + shape.tile_tok < it.n;
+      if (!warp_wait_far(&bar_q_full[0], ni[0]++ & 1)) { ok = false; break; }
+      if (two && !warp_wait_far(&bar_q_full[1], ni[1]++ & 1)) { ok = false; break; }
+      if constexpr (TILES == 2) {
+        for (int32_t j = 0; j <= n; ++j) {
+          if (j < n) {
+            if (!warp_wait_far(&bar_k_full[(kv + j) % KST], ((kv + j) / KST) & 1) || !qk(0, 0, (kv + j) % KST)) {
+              ok = false;
+              break;
+            }
+            if (!two) mma_commit(&bar_k_empty[(kv + j) % KST]);
+          }
+          if (j > 0) {
+            const uint32_t before = (kv + j - 1) % VST;
+            if (two && !pv(1, 1, before, j == 1)) { ok = false; break; }
+            mma_commit(&bar_v_empty[before]);
+          }
+          if (j < n) {
+            if (two) {
+              if (!qk(1, 1, (kv + j) % KST)) { ok = false; break; }
+              mma_commit(&bar_k_empty[(kv + j) % KST]);
+            }
+            if (!warp_wait_far(&bar_v_full[(kv + j) % VST], ((kv + j) / VST) & 1) || !pv(0, 0, (kv + j) % VST, j == 0)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+      } else {
+        for (int32_t j = 0; j <= n; ++j) {
+          if (j < n) {
+            if (!warp_wait_far(&bar_k_full[(kv + j) % KST], ((kv + j) / KST) & 1) || !qk(0, (kv + j) & 1, (kv + j) % KST)) {
+              ok = false;
+              break;
+            }
+            mma_commit(&bar_k_empty[(kv + j) % KST]);
+          }
+          if (j > 0) {
+            const uint32_t x = kv + j - 1;
+            if (!warp_wait_far(&bar_v_full[x % VST], (x / VST) & 1) || !pv(0, x & 1, x % VST, j == 1)) { ok = false; break; }
+            mma_commit(&bar_v_empty[x % VST]);
+          }
+        }
+      }
+      kv += n;
+    }
+    // before tensor memory is freed, every MMA issued must have completed
+    for (int w = 0; w < 2; ++w)
+      if (nt[w] > 0) (void)mbar_wait_bounded(&bar_pv_done[w], (nt[w] - 1) & 1);
+  } else {
+    // ===================================================================== softmax warps
+    const int w = warp >> 2;                   // tile
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + Cfg::O_COL + w * D + lane_base;
+    const int32_t r = (warp & 3) * 32 + lane;  // this thread's row of the tile
+    uint8_t* const q_hi = sQ + w * 2 * Cfg::Q_TERM;
+    uint8_t* const stage = q_hi + (warp & 3) * 32 * Cfg::SLICE;  // output goes through the q of the warp's own rows
+    uint32_t kv = 0;  // key tiles of finished items
+    uint32_t nt = 0;  // key tiles processed
+    Item it;
+    for (uint32_t k = 0; ok; ++k) {
+      if (!take_item(k, it)) { ok = false; break; }
+      if (!it.live) break;
+      const int32_t n = it.kt1 - it.kt0, tok_w = it.tok0 + w * shape.tile_tok;
+      if (w == 1 && tok_w >= it.n) {  // no such tile
+        kv += n;
+        continue;
+      }
+      // ---- the row, its q as two E4M3 terms
+      const int32_t rt = r / it.heads, tok = tok_w + rt;
+      const bool live = rt < shape.tile_tok && tok < it.n;
+      const int32_t lim = live ? it.len - it.n + tok + 1 : 0x7fffffff;  // tokens that the row sees
+      const int32_t lim_least = __reduce_min_sync(0xffffffffu, lim);
+      float mult;
+      {
+        const uint16_t* q =
+            a.q + (static_cast<int64_t>(it.q0 + (live ? tok : 0)) * a.num_q_heads + it.head0 + (r - rt * it.heads)) * D;
+        float top = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16x2(x[e]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        const int e2 = min(max((__float_as_int(top) >> 23) - 127, -100), 100);
+        const float up = __int_as_float((7 - e2 + 127) << 23);  // the largest comes to [2^7, 2^8)
+        mult = a.score_scale * __int_as_float((e2 - 7 + 127) << 23);
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q) + 2 * c + half) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 f = unpack_bf16x2(x[2 * e]), g = unpack_bf16x2(x[2 * e + 1]);
+              float a0, a1, b0, b1;
+              const uint32_t h0 = e4m3x2(f.x * up, f.y * up, a0, a1), h1 = e4m3x2(g.x * up, g.y * up, b0, b1);
+              hi[2 * half + e] = h0 | h1 << 16;
+              lo[2 * half + e] = encode_fp8x2(f.x * up - a0, f.y * up - a1) |
+                                 static_cast<uint32_t>(encode_fp8x2(g.x * up - b0, g.y * up - b1)) << 16;
+            }
+          }
+          uint8_t* to = D == 64 ? q_hi + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                                : q_hi + c / 8 * kM * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + Cfg::Q_TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar_q_full[w]);
+      }
+      float m = kNoMax, l = 0.0f;
+      for (int32_t j = 0; j < n; ++j, ++nt) {
+        const int buf = TILES == 2 ? w : (kv + j) & 1;
+        const uint32_t uses = TILES == 2 ? nt : (kv + j) >> 1;
+        const uint32_t tS = tmem + buf * KT + lane_base;
+        const uint32_t slot = (kv + j) % kInfo;
+        if (!warp_wait_far(&bar_info[slot], ((kv + j) / kInfo) & 1) || !warp_wait_far(&bar_s_full[buf], uses & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const PageInfo* info = sInfo + slot * PAGES;
+        const int32_t t0 = (it.kt0 + j) * KT;
+        bool plain = t0 + KT <= lim_least;
+        if (plain) {
+          int32_t least = kPage;
+#pragma unroll
+          for (int p = 0; p < PAGES; ++p) least = min(least, info[p].rows);
+          plain = least == kPage;
+        }
+        // 64 scores of the row (half h of a key tile of 128), and the maxima of their pages.  The second half is read twice:
+        // 128 scores in registers, beside what else a thread holds, pass the 128 registers of 512 threads.
+        uint32_t s[64], mx[PAGES];
+        auto scores = [&](int h) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) tmem_ld16_max_issue(tS + 64 * h + 16 * p, s + 16 * p, mx[4 * h + p]);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) tmem_wait16_max(s + 16 * p, mx[4 * h + p]);
+          if (!plain) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const int32_t see = info[4 * h + p].rows > 0 ? lim - t0 - (4 * h + p) * kPage : 0;
+              float x = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                s[16 * p + e] = e < see ? s[16 * p + e] : 0xFF800000u;
+                x = fmaxf(x, __uint_as_float(s[16 * p + e]));
+              }
+              mx[4 * h + p] = __float_as_uint(x);
+            }
+          }
+        };
+        if constexpr (KT == 128) scores(1);
+        scores(0);
+        float top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < PAGES; ++p) top = fmaxf(top, fmaf(__uint_as_float(mx[p]), mult * info[p].ks, info[p].ev));
+        // the reference moves when some row's largest passes it by more than 2^15; O and l are then rescaled
+        const bool moved = top > m + kLimit;
+        if (__any_sync(0xffffffffu, moved)) {
+          const float now = moved ? top - kHead : m;
+          const float alpha = moved ? ex2(m - now) : 1.0f;
+          m = now;
+          l *= alpha;
+          if (j > 0) {
+            // (one tile: the PV before may still run; two: this QK was issued after it had completed)
+            if (TILES == 1 && !warp_wait_far(&bar_pv_done[(kv + j - 1) & 1], ((kv + j - 1) >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {  // (8 columns at a time: the row's scores stay in registers)
+              float o[8];
+              tmem_ld8(tO + c * 8, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= alpha;
+              tmem_st8(tO + c * 8, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < KT / 64; ++h) {
+          if (h > 0) scores(h);
+          uint32_t pw[32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const PageInfo f = info[4 * h + q];
+            const float2 sc2 = make_float2(mult * f.ks, mult * f.ks), m2 = make_float2(f.ev - m, f.ev - m);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int i = q * 16 + 2 * e;
+              const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, m2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              sum = fadd2(sum, p);
+              pw[q * 8 + e] = pack_f16x2(p.x, p.y);
+            }
+            l = fmaf(sum.x + sum.y, f.unv, l);
+          }
+          tmem_st32(tS + h * 32, pw);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar_p_full[buf]);
+      }
+      if (!ok) break;
+      // ---- O, once the item's last PV has completed
+      {
+        const int buf = TILES == 2 ? w : (kv + n - 1) & 1;
+        const uint32_t uses = TILES == 2 ? nt - 1 : (kv + n - 1) >> 1;
+        if (!warp_wait_far(&bar_pv_done[buf], uses & 1)) { ok = false; break; }
+      }
+      tc_fence_after();
+      kv += n;
+      const float inv = it.whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+      const int64_t slot = part_slot(place.total, sharers(place.total, a.grid, kPageFlashUnits), cta, it.first);
+      // rows pass through the warp's 2 KB, 32 columns at a time, so that four lanes write 64 or 128 bytes of one row
+      const int r0 = lane >> 2, c4 = lane & 3;
+      int64_t at[4];  // where rows r0 + 8 i begin, -1: no such row
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t row = (warp & 3) * 32 + r0 + 8 * i, t = row / it.heads;
+        const bool there = t < shape.tile_tok && tok_w + t < it.n;
+        if (!it.whole) at[i] = there ? ((slot * TILES + w) * kM + row) * D : -1;
+        else at[i] = there ? (static_cast<int64_t>(it.q0 + tok_w + t) * a.num_q_heads + it.head0 + (row - t * it.heads)) * D : -1;
+      }
+      if (!it.whole && live)
+        *reinterpret_cast<float2*>(a.part_ml + ((slot * TILES + w) * kM + r) * 2) = make_float2(m, l);
+      auto put = [&](int h, uint4 x) {
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((h ^ ((lane >> 1) & 3)) << 4)) = x;
+      };
+      auto get = [&](int i) {
+        const int row = r0 + 8 * i;
+        return *reinterpret_cast<const uint4*>(stage + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
+      };
+      const bool f32 = !it.whole || a.out_dtype == KVQ_OUT_F32;
+      float* const out32 = it.whole ? static_cast<float*>(a.out) : a.part_acc;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(tO + c * 32, ov);
+        if (c == D / 32 - 1) {  // the reads are ordered before the arrival that lets the next PV overwrite O
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bar_o_free[w]);
+        }
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * inv;
+        if (f32) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const float* x = o + 16 * f + 4 * h;
+              put(h, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (at[i] >= 0) *reinterpret_cast<uint4*>(out32 + at[i] + c * 32 + 16 * f + 4 * c4) = get(i);
+          }
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            put(h, make_uint4(pack_bf16x2(o[8 * h], o[8 * h + 1]), pack_bf16x2(o[8 * h + 2], o[8 * h + 3]),
+                              pack_bf16x2(o[8 * h + 4], o[8 * h + 5]), pack_bf16x2(o[8 * h + 6], o[8 * h + 7])));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (at[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at[i] + c * 32 + 8 * c4) = get(i);
+        }
+      }
+      __syncwarp();  // (the next item's q is written over the staged rows)
+    }
+  }
+  if (!ok) set_status(a.status, kStatusTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == Cfg::MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// Joins the runs of the items that several CTAs worked on.  CTA (c - 1, y): the item in which CTA c's first unit lies, if
+// that is its first joint; rows 32 y ... + 31, a warp for every eighth.
+constexpr int kJoinWarps = 8, kJoinRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) page_flash_join_kernel(const PageArgs a) {
+  using Cfg = FCfg<D>;
+  const Shape<D> shape(a);
+  const int32_t c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  bool bad = false;
+  const Place place = page_place<kJoinWarps>(
+      a.batch, nullptr, [&](int32_t i) { return shape.units(a, page_sequence(a, i, bad)); },
+      [&](int64_t U) {
+        const int32_t C = sharers(U, a.grid, kPageFlashUnits);
+        return c < C && U > 0 ? first_unit(U, C, c) : U;
+      });
+  if (place.b < 0) return;
+  const int64_t U = place.total;
+  const int32_t C = sharers(U, a.grid, kPageFlashUnits);
+  const PageSeq s = page_sequence(a, place.b, bad);
+  int32_t group, p;
+  const int64_t u = first_unit(U, C, c), inside = shape.locate(s, u - place.before, group, p), first = u - inside;
+  // its first joint only: the run before begins at or before the item
+  if (inside == 0 || first_unit(U, C, c - 1) > first) return;
+  const int32_t c1 = owner_of(U, C, first + shape.key_tiles(s, p) - 1);
+  const int32_t g = group / shape.groups, part = group - g * shape.groups;
+  const int32_t heads = min(shape.heads, shape.G - part * shape.heads);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V2 = D / 64;  // float2 of a lane
+  for (int32_t row = blockIdx.y * kJoinRows + (threadIdx.x >> 5); row < (blockIdx.y + 1) * kJoinRows; row += kJoinWarps) {
+    const int32_t w = row / kM, r = row - w * kM, rt = r / heads;
+    const int32_t tok = p * shape.item_tok + w * shape.tile_tok + rt;
+    if (rt >= shape.tile_tok || tok >= s.n) continue;
+    float m = kNoMax, l = 0.0f;
+    float2 x[V2];
+#pragma unroll
+    for (int k = 0; k < V2; ++k) x[k] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t i = c - 1; i <= c1; ++i) {
+      const int64_t at = (part_slot(U, C, i, first) * Cfg::TILES + w) * kM + r;
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+      const float now = fmaxf(m, ml.x), f = ex2(ml.x - now), keep = ex2(m - now);
+      m = now;
+      l = fmaf(ml.y, f, l * keep);
+#pragma unroll
+      for (int k = 0; k < V2; ++k) {
+        const float2 y = *reinterpret_cast<const float2*>(a.part_acc + at * D + k * 64 + lane * 2);
+        x[k].x = fmaf(y.x, f, x[k].x * keep);
+        x[k].y = fmaf(y.y, f, x[k].y * keep);
+      }
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int64_t out = (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + g * shape.G + part * shape.heads + (r - rt * heads)) * D;
+#pragma unroll
+    for (int k = 0; k < V2; ++k) {
+      const int64_t at = out + k * 64 + lane * 2;
+      if (a.out_dtype == KVQ_OUT_F32)
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(x[k].x * inv, x[k].y * inv);
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack_bf16x2(x[k].x * inv, x[k].y * inv);
+    }
+  }
+}
+
+template <int D>
+kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
+  using Cfg = FCfg<D>;
+  CUtensorMap map;
+  if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
+  auto kern = page_flash_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess) return KVQ_ECUDA;
+  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream) != cudaSuccess) return KVQ_ECUDA;
+  kern<<<a.grid, Cfg::THREADS, Cfg::SMEM, stream>>>(a, map);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
+  if (a.grid == 1) return KVQ_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.grid - 1, Cfg::TILES * kM / kJoinRows);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, page_flash_join_kernel<D>, a) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+}
+
+}  // namespace
+
+int32_t page_flash_rows(int32_t head_dim) { return head_dim == 256 ? kM : 2 * kM; }
+
+kvq_status launch_page_flash(const PageArgs& a, cudaStream_t stream) {
+  if (a.head_dim == 64) return launch_d<64>(a, stream);
+  if (a.head_dim == 128) return launch_d<128>(a, stream);
+  return launch_d<256>(a, stream);
+}
+
+}  // namespace kvq

@@ -31,9 +31,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = kPageRowsTile;   // query rows of a tile
-constexpr float kNoMax = -1e30f;       // reference of a row that has seen nothing
-constexpr float kHead = 7.0f;          // log2 of the largest p when the reference moves ...
-constexpr float kLimit = 15.0f;        // ... and at most (f16 ends at 2^16)
 
 template <int D>
 struct RCfg {
@@ -52,101 +49,26 @@ struct RCfg {
   static constexpr int CTAS = D == 256 ? 2 : 4;        // resident per SM
 };
 
-// One sequence's rows and pages.  n < 0: nothing to do.
-struct Seq {
-  int32_t q0, n, len, pages, tiles;
+// One sequence's rows, pages and tiles.
+struct Seq : PageSeq {
+  int32_t pages, tiles;
   int64_t units;
 };
 
-__device__ __forceinline__ Seq page_sequence(const PageArgs& a, int32_t b, bool& bad) {
+__device__ __forceinline__ Seq rows_sequence(const PageArgs& a, int32_t b, bool& bad) {
   Seq s;
-  const int32_t room = a.max_pages * kPage;
-  s.len = __ldg(a.seq_lens + b);
-  if (a.q_start == nullptr) {  // one row per sequence
-    s.q0 = b;
-    s.n = 1;
-    s.len = min(max(s.len, 0), room);
-  } else {
-    s.q0 = __ldg(a.q_start + b);
-    const int64_t q1 = __ldg(a.q_start + b + 1), n = q1 - s.q0;
-    const bool ok = s.q0 >= 0 && n >= 0 && q1 <= a.total_q && n <= s.len && s.len <= room;
-    bad |= !ok;
-    s.n = ok ? static_cast<int32_t>(n) : 0;
-    if (s.n == 0) s.len = 0;
-  }
-  s.pages = (s.len + kPage - 1) / kPage;
+  static_cast<PageSeq&>(s) = page_sequence(a, b, bad);
+  s.pages = s.n > 0 ? (s.len + kPage - 1) / kPage : 0;
   s.tiles = (s.n * (a.num_q_heads / a.num_kv_heads) + kRows - 1) / kRows;
   s.units = static_cast<int64_t>(s.pages) * s.tiles * a.num_kv_heads;
   return s;
 }
-
-// CTAs that share U units, and the first unit of CTA c.
-__device__ __forceinline__ int32_t sharers(int64_t U, int32_t grid) {
-  return static_cast<int32_t>(min(static_cast<int64_t>(grid), max(U / kPageMinUnits, static_cast<int64_t>(1))));
-}
-__device__ __forceinline__ int64_t first_unit(int64_t U, int32_t C, int32_t c) { return U * c / C; }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The units before every sequence (CTA 0 leaves them for the joining kernel), their sum, and where unit `want`
-// lies.  Every thread of the CTA calls it.
-struct Place {
-  int64_t total, before;  // units of the call; of the sequences before b
-  int32_t b;
-};
-
-__device__ __forceinline__ Place page_place(const PageArgs& a, int32_t cta) {
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ Place s_place;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t per = (a.batch + kThreads - 1) / kThreads;
-  const int32_t b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-  bool bad = false;
-  int64_t mine = 0;
-  for (int32_t b = b0; b < b1; ++b) mine += page_sequence(a, b, bad).units;
-  if (bad && cta == 0) set_status(a.status, kStatusBadExtend);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  if (tid == 0) s_place.b = -1;
-  __syncthreads();
-  int64_t run = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) run += s_sum[w];
-    total += s_sum[w];
-  }
-  const int32_t C = sharers(total, a.grid);
-  const int64_t want = cta < C && total > 0 ? first_unit(total, C, cta) : total;
-  if (cta == 0 && tid == 0) a.tab[a.batch] = total;
-  for (int32_t b = b0; b < b1; ++b) {
-    const int64_t u = page_sequence(a, b, bad).units;
-    if (cta == 0) a.tab[b] = run;
-    if (want >= run && want < run + u) {
-      s_place.b = b;
-      s_place.before = run;
-    }
-    run += u;
-  }
-  __syncthreads();
-  Place p = s_place;
-  p.total = total;
-  return p;
 }
 
 template <int D>
@@ -165,19 +87,27 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
   if (lane < STAGES) mbar_init(&bars[lane], 1);
   fence_mbar_init();
   __syncwarp();
-  const Place place = page_place(a, blockIdx.x);
+  const int32_t cta = blockIdx.x;
+  bool bad = false;
+  const Place place = page_place<kWarps>(
+      a.batch, cta == 0 ? a.tab : nullptr, [&](int32_t i) { return rows_sequence(a, i, bad).units; },
+      [&](int64_t U) {  // this CTA's first unit
+        const int32_t C = sharers(U, a.grid, kPageMinUnits);
+        return cta < C && U > 0 ? first_unit(U, C, cta) : U;
+      });
+  if (cta == 0 && bad) set_status(a.status, kStatusBadExtend);
   if (place.b < 0) return;
-  const int32_t C = sharers(place.total, a.grid);
-  int64_t u = first_unit(place.total, C, blockIdx.x);
-  const int64_t u_first = u, u_end = first_unit(place.total, C, blockIdx.x + 1);
+  const int32_t C = sharers(place.total, a.grid, kPageMinUnits);
+  int64_t u = first_unit(place.total, C, cta);
+  const int64_t u_end = first_unit(place.total, C, cta + 1);
   const int32_t G = a.num_q_heads / a.num_kv_heads;
   int32_t b = place.b;
   int64_t before = place.before;
   uint32_t done = 0;  // pages that went through this warp's ring
-  bool ok = true, bad = false;
+  bool ok = true;
 
   while (u < u_end) {
-    Seq s = page_sequence(a, b, bad);
+    Seq s = rows_sequence(a, b, bad);
     if (u >= before + s.units) {
       before += s.units;
       ++b;
@@ -352,8 +282,7 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
           }
         }
         // ---- y = score + ev in the exponent; what a row does not see is -inf
-        const float ev = static_cast<float>((__float_as_int(vscale) >> 23) - 127);
-        const float unv = __int_as_float(0x7F000000 - __float_as_int(vscale));  // 1 / vscale
+        const float ev = scale_exponent(vscale), unv = scale_inverse(vscale);
         float top[2];
         const bool whole = t0 + kPage <= sees_least;
 #pragma unroll
@@ -472,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
     }
     ok = __syncthreads_and(ok);
     const bool whole_tile = pg0 == 0 && pg1 == s.pages;
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (tile_first > u_first ? 1 : 0);
+    const int64_t slot = part_slot(place.total, C, cta, tile_first);
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float M = kNoMax;
@@ -523,14 +452,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
     if (tid == 0) s_b = a.batch;
     __syncthreads();
     for (int32_t i = tid; i < a.batch; i += kJoinWarps * 32) {
-      const Seq s = page_sequence(a, i, bad);
+      const PageSeq s = page_sequence(a, i, bad);
       if (t >= s.q0 && t - s.q0 < s.n) atomicMin(&s_b, i);
     }
     __syncthreads();
     b = s_b;
     if (b >= a.batch) return;
   }
-  const Seq s = page_sequence(a, b, bad);
+  const Seq s = rows_sequence(a, b, bad);
   const int32_t R = (t - s.q0) * G + head - g * G, tile = R / kRows, r = R - tile * kRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t U = a.tab[a.batch];
@@ -540,18 +469,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
     if (tid < D / 4) page_store_out(a, out + tid * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
     return;
   }
-  const int32_t C = sharers(U, a.grid);
-  auto owner = [&](int64_t u) {  // the CTA among whose units u is
-    int32_t c = static_cast<int32_t>(u * C / U);
-    while (c > 0 && first_unit(U, C, c) > u) --c;
-    while (c + 1 < C && first_unit(U, C, c + 1) <= u) ++c;
-    return c;
-  };
-  const int32_t c0 = owner(first), c1 = owner(last);
+  const int32_t C = sharers(U, a.grid, kPageMinUnits);
+  const int32_t c0 = owner_of(U, C, first), c1 = owner_of(U, C, last);
   if (c0 == c1) return;  // its CTA has written the output
-  auto part = [&](int32_t c) {
-    return (2 * static_cast<int64_t>(c) + (first > first_unit(U, C, c) ? 1 : 0)) * kRows + r;
-  };
+  auto part = [&](int32_t c) { return part_slot(U, C, c, first) * kRows + r; };
   constexpr int V4 = D / 128 > 0 ? D / 128 : 1;  // float4 of a lane (D = 64: of half the lanes)
   float m = kNoMax, l = 0.0f;
   float4 x[V4];
