@@ -34,9 +34,18 @@ namespace kvq {
 namespace {
 
 constexpr int kM = 128;           // rows of a tile
-constexpr int kConvWarps = 6;     // that turn V's codes into f16
+constexpr int kConvWarps = 2;     // that turn V's codes into f16
 constexpr int kInfo = 8;          // key tiles whose pages are described in shared memory
 constexpr int kTmemCols = 512;
+
+// What the softmax and the converting warps know of the pages of a key tile.
+template <int PAGES>
+struct alignas(16) PageInfo {
+  float ks[PAGES];                // K's scale (1 for a masked page)
+  float ev[PAGES], unv[PAGES];    // V's exponent, and 2^-ev
+  int32_t rows[PAGES];            // rows that hold tokens; 0: masked
+  int32_t full, pad[3];           // every page of the tile has all its rows
+};
 
 template <int D>
 struct FCfg {
@@ -50,13 +59,13 @@ struct FCfg {
   static constexpr int KST = D == 64 ? 4 : 3, VST = 2;  // stages of K codes; of V codes and of V in f16
   static constexpr int SM_WARPS = 4 * TILES;
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1, CONV_WARP = SM_WARPS + 2;
-  static constexpr int THREADS = (SM_WARPS + 2 + kConvWarps) * 32;  // whole groups of four warps: 512 or 384
+  static constexpr int THREADS = (SM_WARPS + 2 + kConvWarps) * 32;
   static constexpr int Q_OFF = 0;                       // 1024-byte aligned: swizzle atoms
   static constexpr int K_OFF = Q_OFF + TILES * 2 * Q_TERM;
   static constexpr int C_OFF = K_OFF + KST * K_TILE;    // V codes
   static constexpr int V_OFF = C_OFF + VST * K_TILE;
   static constexpr int INFO_OFF = V_OFF + VST * V_TILE;
-  static constexpr int ITEM_OFF = INFO_OFF + kInfo * PAGES * 16;
+  static constexpr int ITEM_OFF = INFO_OFF + kInfo * static_cast<int>(sizeof(PageInfo<PAGES>));
   static constexpr int BAR_OFF = ITEM_OFF + 2 * 64;
   static constexpr int NBARS = 2 * KST + 4 * VST + 2 * kInfo + 14;
   static constexpr int SMEM = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
@@ -64,14 +73,6 @@ struct FCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(O_COL + TILES * D <= kTmemCols, "tensor memory");
 };
-
-// What the softmax and the converting warps know of a page of a key tile.
-struct PageInfo {
-  float ks;       // K's scale (1 for a masked page)
-  float ev, unv;  // V's exponent, and 2^-ev
-  int32_t rows;   // rows that hold tokens; 0: masked
-};
-static_assert(sizeof(PageInfo) == 16, "info slots");
 
 // A run of an item's key tiles.
 struct Item {
@@ -223,7 +224,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   uint8_t* sK = smem + Cfg::K_OFF;  // [KST]
   uint8_t* sC = smem + Cfg::C_OFF;  // [VST] codes of V
   uint8_t* sV = smem + Cfg::V_OFF;  // [VST] V in f16
-  PageInfo* sInfo = reinterpret_cast<PageInfo*>(smem + Cfg::INFO_OFF);  // [kInfo][PAGES]
+  using Info = PageInfo<PAGES>;
+  Info* sInfo = reinterpret_cast<Info*>(smem + Cfg::INFO_OFF);  // [kInfo]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
   uint64_t* bar_k_full = bars;                    // [KST] K codes landed
   uint64_t* bar_k_empty = bar_k_full + KST;       // [KST] their last QK completed (commit)
@@ -377,13 +379,15 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine && phys >= 0));
         const int sk = kv % KST, sv = kv % VST;
         if (kv >= KST && !warp_wait_far(&bar_k_empty[sk], (kv / KST - 1) & 1)) { ok = false; break; }
+        Info& info = sInfo[kv % kInfo];
+        const int32_t rows = mine && phys >= 0 ? min(kPage, it.len - (pg0 + j * PAGES + x) * kPage) : 0;
+        const uint32_t fulls = __popc(__ballot_sync(0xffffffffu, rows == kPage));
         if (mine) {
-          PageInfo f;
-          f.ks = phys >= 0 ? ks : 1.0f;
-          f.ev = phys >= 0 ? scale_exponent(vs) : 0.0f;
-          f.unv = phys >= 0 ? scale_inverse(vs) : 1.0f;
-          f.rows = phys >= 0 ? min(kPage, it.len - (pg0 + j * PAGES + x) * kPage) : 0;
-          sInfo[kv % kInfo * PAGES + x] = f;
+          info.ks[x] = phys >= 0 ? ks : 1.0f;
+          info.ev[x] = phys >= 0 ? scale_exponent(vs) : 0.0f;
+          info.unv[x] = phys >= 0 ? scale_inverse(vs) : 1.0f;
+          info.rows[x] = rows;
+          if (x == 0) info.full = fulls == PAGES;
         }
         __syncwarp();
         if (lane == 0) {
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         }
         const uint8_t* src = sC + s * Cfg::K_TILE;
         uint8_t* dst = sV + s * Cfg::V_TILE;
-        const PageInfo* info = sInfo + kv % kInfo * PAGES;
+        const Info& info = sInfo[kv % kInfo];
         constexpr int PER_ROW = D / 64;  // steps of 64 codes in a row
 #pragma unroll 2
         for (int i = cw; i < KT / 8 * PER_ROW; i += kConvWarps) {
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
             w = *reinterpret_cast<const uint4*>(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
           else
             w = *reinterpret_cast<const uint4*>(src + c / 8 * KT * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-          const bool live = row % kPage < info[row / kPage].rows;
+          const bool live = row % kPage < info.rows[row / kPage];
           const uint32_t in[4] = {live ? w.x : 0u, live ? w.y : 0u, live ? w.z : 0u, live ? w.w : 0u};
           uint32_t h[8];
 #pragma unroll
@@ -636,47 +640,39 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const uint32_t uses = TILES == 2 ? nt : (kv + j) >> 1;
         const uint32_t tS = tmem + buf * KT + lane_base;
         const uint32_t slot = (kv + j) % kInfo;
-        if (!warp_wait_far(&bar_info[slot], ((kv + j) / kInfo) & 1) || !warp_wait_far(&bar_s_full[buf], uses & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const PageInfo* info = sInfo + slot * PAGES;
+        if (!warp_wait_far(&bar_info[slot], ((kv + j) / kInfo) & 1)) { ok = false; break; }
+        const Info& info = sInfo[slot];
         const int32_t t0 = (it.kt0 + j) * KT;
-        bool plain = t0 + KT <= lim_least;
-        if (plain) {
-          int32_t least = kPage;
+        const bool plain = t0 + KT <= lim_least && info.full;
+        float ks[PAGES], ev[PAGES];
 #pragma unroll
-          for (int p = 0; p < PAGES; ++p) least = min(least, info[p].rows);
-          plain = least == kPage;
+        for (int p = 0; p < PAGES; ++p) {
+          ks[p] = mult * info.ks[p];
+          ev[p] = info.ev[p];
         }
-        // 64 scores of the row (half h of a key tile of 128), and the maxima of their pages.  The second half is read twice:
-        // 128 scores in registers, beside what else a thread holds, pass the 128 registers of 512 threads.
-        uint32_t s[64], mx[PAGES];
-        auto scores = [&](int h) {
+        if (!warp_wait_far(&bar_s_full[buf], uses & 1)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[KT], mx[PAGES];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) tmem_ld16_max_issue(tS + 64 * h + 16 * p, s + 16 * p, mx[4 * h + p]);
+        for (int p = 0; p < PAGES; ++p) tmem_ld16_max_issue(tS + 16 * p, s + 16 * p, mx[p]);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) tmem_wait16_max(s + 16 * p, mx[4 * h + p]);
-          if (!plain) {
+        for (int p = 0; p < PAGES; ++p) tmem_wait16_max(s + 16 * p, mx[p]);
+        if (!plain) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              const int32_t see = info[4 * h + p].rows > 0 ? lim - t0 - (4 * h + p) * kPage : 0;
-              float x = -INFINITY;
+          for (int p = 0; p < PAGES; ++p) {
+            const int32_t see = info.rows[p] > 0 ? lim - t0 - p * kPage : 0;
+            float x = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                s[16 * p + e] = e < see ? s[16 * p + e] : 0xFF800000u;
-                x = fmaxf(x, __uint_as_float(s[16 * p + e]));
-              }
-              mx[4 * h + p] = __float_as_uint(x);
+            for (int e = 0; e < 16; ++e) {
+              s[16 * p + e] = e < see ? s[16 * p + e] : 0xFF800000u;
+              x = fmaxf(x, __uint_as_float(s[16 * p + e]));
             }
+            mx[p] = __float_as_uint(x);
           }
-        };
-        if constexpr (KT == 128) scores(1);
-        scores(0);
-        float top = -INFINITY;
+        }
+        float top = fmaf(__uint_as_float(mx[0]), ks[0], ev[0]);
 #pragma unroll
-        for (int p = 0; p < PAGES; ++p) top = fmaxf(top, fmaf(__uint_as_float(mx[p]), mult * info[p].ks, info[p].ev));
+        for (int p = 1; p < PAGES; ++p) top = fmaxf(top, fmaf(__uint_as_float(mx[p]), ks[p], ev[p]));
         // the reference moves when some row's largest passes it by more than 2^15; O and l are then rescaled
         const bool moved = top > m + kLimit;
         if (__any_sync(0xffffffffu, moved)) {
@@ -700,22 +696,21 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         }
 #pragma unroll
         for (int h = 0; h < KT / 64; ++h) {
-          if (h > 0) scores(h);
           uint32_t pw[32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const PageInfo f = info[4 * h + q];
-            const float2 sc2 = make_float2(mult * f.ks, mult * f.ks), m2 = make_float2(f.ev - m, f.ev - m);
+            const int pg = 4 * h + q;
+            const float2 sc2 = make_float2(ks[pg], ks[pg]), m2 = make_float2(ev[pg] - m, ev[pg] - m);
             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int i = q * 16 + 2 * e;
+              const int i = pg * 16 + 2 * e;
               const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, m2);
               const float2 p = make_float2(ex2(x.x), ex2(x.y));
               sum = fadd2(sum, p);
               pw[q * 8 + e] = pack_f16x2(p.x, p.y);
             }
-            l = fmaf(sum.x + sum.y, f.unv, l);
+            l = fmaf(sum.x + sum.y, info.unv[pg], l);
           }
           tmem_st32(tS + h * 32, pw);
         }
