@@ -403,7 +403,6 @@ bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   if (batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages <= 0 || num_q_heads % L.num_kv_heads != 0) return false;
   if (L.mla || L.page_size != kPageTokens || !page_supported(L.head_dim)) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t tab = up((static_cast<size_t>(batch) + 1) * sizeof(int64_t));
   // a tile of the rows kernel holds a sequence's rows of a kv head, or the flash kernel takes them
   const double rows = static_cast<double>(total_q) * (num_q_heads / L.num_kv_heads);
   pp->flash = total_q > batch && rows > static_cast<double>(kPageRowsTile) * batch;
@@ -417,13 +416,13 @@ bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   int64_t grid = pp->flash ? sm_count() : page_rows_grid(L.head_dim, sm_count());
   if (units < static_cast<double>(grid) * least) grid = static_cast<int64_t>(units / least) + 1;
   if (max_bytes > 0) {
-    if (max_bytes < kWorkspaceHeader + tab + 1024) return false;
-    grid = std::min<int64_t>(grid, (max_bytes - kWorkspaceHeader - tab - 512) / (2 * slot));
+    if (max_bytes < kWorkspaceHeader + 1024) return false;
+    grid = std::min<int64_t>(grid, (max_bytes - kWorkspaceHeader - 1024) / (2 * slot + kPageRunBytes));
   }
   if (grid < 1) return false;
   const size_t slots = 2 * static_cast<size_t>(grid);
   pp->grid = static_cast<int32_t>(grid);
-  pp->ml_offset = kWorkspaceHeader + tab;
+  pp->ml_offset = kWorkspaceHeader + up(static_cast<size_t>(grid) * kPageRunBytes);
   pp->acc_offset = pp->ml_offset + up(slots * tile * 2 * sizeof(float));
   pp->total = pp->acc_offset + up(slots * tile * L.head_dim * sizeof(float));
   return true;
@@ -461,7 +460,8 @@ kvq_status page_common(const void* q, const void* pool, const void* scales, cons
   a.q_start = q_start;
   a.out = out;
   a.status = reinterpret_cast<uint32_t*>(ws);
-  a.tab = reinterpret_cast<int64_t*>(ws + kWorkspaceHeader);
+  a.total = reinterpret_cast<int64_t*>(ws + 64);
+  a.runs = ws + kWorkspaceHeader;
   a.part_ml = reinterpret_cast<float*>(ws + pp.ml_offset);
   a.part_acc = reinterpret_cast<float*>(ws + pp.acc_offset);
   a.num_pages = layout->num_pages;

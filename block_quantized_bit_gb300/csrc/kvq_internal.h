@@ -240,7 +240,8 @@ struct PageArgs {
   const int32_t* q_start;     // [batch + 1], or null: one row per sequence
   void* out;                  // [total_q][num_q_heads][head_dim]
   uint32_t* status;
-  int64_t* tab;               // [batch + 1] units before each sequence, and in all
+  int64_t* total;             // the call's units
+  void* runs;                 // [grid] of kPageRunBytes: each CTA's first run
   float* part_acc;            // [2 * grid][rows][head_dim], rows: kPageRowsTile or page_flash_rows()
   float* part_ml;             // [2 * grid][rows][2]
   int64_t num_pages;
@@ -251,6 +252,7 @@ struct PageArgs {
 };
 constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
+constexpr int kPageRunBytes = 64;
 constexpr int kPageFlashUnits = 4; // key tiles that are worth a CTA of the flash kernel
 bool page_supported(int32_t head_dim);
 int32_t page_rows_grid(int32_t head_dim, int32_t sms);  // CTAs that are resident at once

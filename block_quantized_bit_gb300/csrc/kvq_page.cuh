@@ -62,10 +62,10 @@ struct Place {
   int32_t b;  // -1: none
 };
 
-// units(b): a sequence's units; every thread of the CTA (of WARPS warps) calls it.  `tab`, where not null, receives the
-// units before each sequence and, behind them, their sum.
+// units(b): a sequence's units; every thread of the CTA (of WARPS warps) calls it.  total_out, where not null, receives
+// the units of the call.
 template <int WARPS, typename Units, typename Want>
-__device__ __forceinline__ Place page_place(int32_t batch, int64_t* tab, Units units, Want want_of) {
+__device__ __forceinline__ Place page_place(int32_t batch, int64_t* total_out, Units units, Want want_of) {
   __shared__ int64_t s_sum[WARPS];
   __shared__ Place s_place;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -89,10 +89,9 @@ __device__ __forceinline__ Place page_place(int32_t batch, int64_t* tab, Units u
     total += s_sum[w];
   }
   const int64_t want = want_of(total);
-  if (tab != nullptr && tid == 0) tab[batch] = total;
+  if (total_out != nullptr && tid == 0) *total_out = total;
   for (int32_t b = b0; b < b1; ++b) {
-    const int64_t u = units(b);
-    if (tab != nullptr) tab[b] = run;
+    const int64_t u = per == 1 ? mine : units(b);
     if (want >= run && want < run + u) {
       s_place.b = b;
       s_place.before = run;

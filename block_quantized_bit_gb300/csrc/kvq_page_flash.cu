@@ -14,8 +14,8 @@
 // Tensor memory at head_dim 64 and 128: S_A, S_B, O_A, O_B, two tiles A and B of a CTA whose softmax and MMAs alternate; at
 // 256 one tile, with two S buffers of 64 keys.  P (f16) replaces the S it was made from.
 // Warps: softmax (one per lane quarter and tile, one thread per row), one that issues all MMAs, one that finds the work,
-// reads block table and scales and loads K and V codes with TMA (a page's 16 rows as one box), six that turn V's codes into
-// f16 (and clear rows behind the sequence's end and of masked pages, which may hold anything: 0 * NaN would be NaN).
+// reads block table and scales and loads K and V codes with TMA (a page's 16 rows as one box), two that turn V's codes
+// into f16 (and clear rows behind the sequence's end and of masked pages, which may hold anything: 0 * NaN would be NaN).
 // Work: a unit is a key tile of an item (one or two tiles of a kv head).  All units lie in one order, and every CTA takes an
 // equal run of them, so that a few long contexts fill the GPU as well as many short ones.  A run that is all of an item
 // gives its output, other runs leave partial sums for a second kernel, its programmatic dependent.
@@ -35,7 +35,6 @@ namespace {
 
 constexpr int kM = 128;           // rows of a tile
 constexpr int kConvWarps = 2;     // that turn V's codes into f16
-constexpr int kInfo = 8;          // key tiles whose pages are described in shared memory
 constexpr int kTmemCols = 512;
 
 // What the softmax and the converting warps know of the pages of a key tile.
@@ -43,8 +42,8 @@ template <int PAGES>
 struct alignas(16) PageInfo {
   float ks[PAGES];                // K's scale (1 for a masked page)
   float ev[PAGES], unv[PAGES];    // V's exponent, and 2^-ev
-  int32_t rows[PAGES];            // rows that hold tokens; 0: masked
-  int32_t full, pad[3];           // every page of the tile has all its rows
+  uint8_t rows[PAGES];            // rows that hold tokens; 0: masked
+  int32_t full;                   // every page of the tile has all its rows
 };
 
 template <int D>
@@ -56,7 +55,12 @@ struct FCfg {
   static constexpr int SLICE = D == 64 ? 64 : 128;
   static constexpr int Q_TERM = kM * D;                 // bytes of one term of a tile's q
   static constexpr int K_TILE = KT * D, V_TILE = 2 * KT * D;
-  static constexpr int KST = D == 64 ? 4 : 3, VST = 2;  // stages of K codes; of V codes and of V in f16
+  static constexpr int KST = 3, VST = 2;                // stages of K codes; of V codes and of V in f16
+  // Key tiles whose pages are described in shared memory.  A slot is written once QK of the tile KST before has completed; by
+  // then all have read that of the tile before that one (one tile per CTA: two before).
+  static constexpr int INFO = TILES == 2 ? 4 : 8;
+  static_assert(INFO >= KST + (TILES == 2 ? 1 : 2), "info slots");
+  static constexpr int ITEMS = 4;                       // item slots
   static constexpr int SM_WARPS = 4 * TILES;
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1, CONV_WARP = SM_WARPS + 2;
   static constexpr int THREADS = (SM_WARPS + 2 + kConvWarps) * 32;
@@ -64,25 +68,31 @@ struct FCfg {
   static constexpr int K_OFF = Q_OFF + TILES * 2 * Q_TERM;
   static constexpr int C_OFF = K_OFF + KST * K_TILE;    // V codes
   static constexpr int V_OFF = C_OFF + VST * K_TILE;
-  static constexpr int INFO_OFF = V_OFF + VST * V_TILE;
-  static constexpr int ITEM_OFF = INFO_OFF + kInfo * static_cast<int>(sizeof(PageInfo<PAGES>));
-  static constexpr int BAR_OFF = ITEM_OFF + 2 * 64;
-  static constexpr int NBARS = 2 * KST + 4 * VST + 2 * kInfo + 14;
+  static constexpr int STG_OFF = V_OFF + VST * V_TILE;  // [softmax warps] 2 KB of output
+  static constexpr int INFO_OFF = STG_OFF + SM_WARPS * 2048;
+  static constexpr int ITEM_OFF = INFO_OFF + INFO * static_cast<int>(sizeof(PageInfo<PAGES>));
+  static constexpr int BAR_OFF = ITEM_OFF + ITEMS * 64;
+  static constexpr int NBARS = 2 * KST + 4 * VST + INFO + 10 + 2 * ITEMS;
   static constexpr int SMEM = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
   static constexpr int O_COL = D == 256 ? 128 : 256;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(O_COL + TILES * D <= kTmemCols, "tensor memory");
 };
 
-// A run of an item's key tiles.
+// A run of an item's key tiles.  A CTA leaves its first one in the workspace where that begins inside an item, for the
+// joining kernel.
 struct Item {
+  __device__ __forceinline__ int32_t token_of(int32_t r) const { return static_cast<int32_t>(r * per_head >> 16); }
   int64_t first;                  // the item's first unit
   int32_t live, q0, n, len;
   int32_t head0, heads;           // first query head of the group, heads of it
   int32_t tok0;                   // first token of the item
-  int32_t kt0, kt1, whole;        // key tiles of the run; whether they are all of the item's
+  uint32_t per_head;              // 2^16 / heads, rounded up: r * per_head >> 16 = r / heads for r < 128
+  int32_t kt0, kt1, all;          // key tiles of the run; of the item
+  int32_t pad;
+  __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == all; }
 };
-static_assert(sizeof(Item) <= 64, "item slots");
+static_assert(sizeof(Item) <= kPageRunBytes && kPageRunBytes == 64, "item slots");
 
 // Sum over i < n of floor((a i + b) / m), a, b >= 0 (the lattice points under a line, by the Euclidean algorithm).
 __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
@@ -202,14 +212,18 @@ __device__ __forceinline__ void tmem_wait16_max(uint32_t* r, uint32_t& top) {
                : "memory");
 }
 
-// Two E4M3 codes (low byte = a) and the values they stand for.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b, float& va, float& vb) {
-  const uint32_t c = encode_fp8x2(a, b);
-  uint32_t h, unused;
-  codes_to_f16x2<KVQ_FP8_E4M3>(c, h, unused);
-  va = half_bits_to_float(lo16(h));
-  vb = half_bits_to_float(hi16(h));
-  return c;
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void cp_async16(uint8_t* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+
+// Two values as the sum of two E4M3 terms each: codes of the nearest and of what is left.
+__device__ __forceinline__ void e4m3_terms(uint32_t f16x2, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\tsub.f16x2 d, %2, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\tcvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+      : "=r"(hi), "=r"(lo)
+      : "r"(f16x2));
 }
 
 template <int D>
@@ -217,7 +231,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     page_flash_kernel(const PageArgs a, const __grid_constant__ CUtensorMap map) {
   using Cfg = FCfg<D>;
   constexpr int TILES = Cfg::TILES, KT = Cfg::KT, PAGES = Cfg::PAGES, SLICES = Cfg::SLICES;
-  constexpr int KST = Cfg::KST, VST = Cfg::VST;
+  constexpr int KST = Cfg::KST, VST = Cfg::VST, INFO = Cfg::INFO, ITEMS = Cfg::ITEMS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem + Cfg::Q_OFF;  // [tile][term]
@@ -225,7 +239,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   uint8_t* sC = smem + Cfg::C_OFF;  // [VST] codes of V
   uint8_t* sV = smem + Cfg::V_OFF;  // [VST] V in f16
   using Info = PageInfo<PAGES>;
-  Info* sInfo = reinterpret_cast<Info*>(smem + Cfg::INFO_OFF);  // [kInfo]
+  Info* sInfo = reinterpret_cast<Info*>(smem + Cfg::INFO_OFF);  // [INFO]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
   uint64_t* bar_k_full = bars;                    // [KST] K codes landed
   uint64_t* bar_k_empty = bar_k_full + KST;       // [KST] their last QK completed (commit)
@@ -233,21 +247,22 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   uint64_t* bar_c_empty = bar_c_full + VST;       // [VST] turned into f16
   uint64_t* bar_v_full = bar_c_empty + VST;       // [VST] V in f16 written
   uint64_t* bar_v_empty = bar_v_full + VST;       // [VST] its last PV completed (commit)
-  uint64_t* bar_info = bar_v_empty + VST;         // [kInfo] the key tile's pages are described
-  uint64_t* bar_s_full = bar_info + kInfo;        // [2] QK into S buffer w completed (commit)
+  uint64_t* bar_info = bar_v_empty + VST;         // [INFO] the key tile's pages are described
+  uint64_t* bar_s_full = bar_info + INFO;        // [2] QK into S buffer w completed (commit)
   uint64_t* bar_p_full = bar_s_full + 2;          // [2] P of buffer w written
   uint64_t* bar_pv_done = bar_p_full + 2;         // [2] PV of buffer w completed (commit)
   uint64_t* bar_q_full = bar_pv_done + 2;         // [TILES] q of the item written
   uint64_t* bar_o_free = bar_q_full + 2;          // [TILES] O read out
-  uint64_t* bar_item = bar_o_free + 2;            // [2] item slot published
-  uint64_t* bar_item_free = bar_item + 2;         // [2] item slot read by every consuming warp
+  uint64_t* bar_item = bar_o_free + 2;            // [ITEMS] item slot published
+  uint64_t* bar_item_free = bar_item + ITEMS;     // [ITEMS] every consuming warp is done with the item
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
-  auto sItem = [&](uint32_t k) { return reinterpret_cast<Item*>(smem + Cfg::ITEM_OFF + (k & 1) * 64); };
+  auto sItem = [&](uint32_t k) { return reinterpret_cast<Item*>(smem + Cfg::ITEM_OFF + k % ITEMS * 64); };
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t cta = blockIdx.x;
   const Shape<D> shape(a);
   bool ok = true, bad = false;
+  asm volatile("griddepcontrol.launch_dependents;");  // (the joining kernel waits for this one's end)
 
   if (tid == 0) {
     for (int i = 0; i < KST; ++i) {
@@ -260,15 +275,17 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       mbar_init(&bar_v_full[i], kConvWarps);
       mbar_init(&bar_v_empty[i], 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(&bar_info[i], 1);
+    for (int i = 0; i < INFO; ++i) mbar_init(&bar_info[i], 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bar_s_full[w], 1);
       mbar_init(&bar_p_full[w], 4);
       mbar_init(&bar_pv_done[w], 1);
       mbar_init(&bar_q_full[w], 4);
       mbar_init(&bar_o_free[w], 4);
-      mbar_init(&bar_item[w], 1);
-      mbar_init(&bar_item_free[w], Cfg::SM_WARPS + 1 + kConvWarps);
+    }
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(&bar_item[i], 1);
+      mbar_init(&bar_item_free[i], Cfg::SM_WARPS + 1 + kConvWarps);
     }
     fence_mbar_init();
   }
@@ -278,7 +295,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   const Place place = page_place<Cfg::THREADS / 32>(
-      a.batch, cta == 0 ? a.tab : nullptr, [&](int32_t i) { return shape.units(a, page_sequence(a, i, bad)); },
+      a.batch, cta == 0 ? a.total : nullptr, [&](int32_t i) { return shape.units(a, page_sequence(a, i, bad)); },
       [&](int64_t U) {  // this CTA's first unit
         const int32_t C = sharers(U, a.grid, kPageFlashUnits);
         return cta < C && U > 0 ? first_unit(U, C, cta) : U;
@@ -289,38 +306,32 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *sTmem;
 
-  // the k-th item of this CTA, for a consuming warp
-  auto take_item = [&](uint32_t k, Item& it) -> bool {
-    if (!warp_wait_far(&bar_item[k & 1], (k >> 1) & 1)) return false;
-    it = *sItem(k);
+  // The k-th item of this CTA, for a consuming warp, stays in its slot until the warp is done with it: as registers its
+  // fields would be spilled, and be read back from L2 when they are needed.
+  auto take_item = [&](uint32_t k) { return warp_wait_far(&bar_item[k % ITEMS], (k / ITEMS) & 1); };
+  auto end_item = [&](uint32_t k) {
     __syncwarp();
-    if (lane == 0) bar_arrive(&bar_item_free[k & 1]);
-    return true;
+    if (lane == 0) bar_arrive(&bar_item_free[k % ITEMS]);
   };
 
   if (warp == Cfg::LOAD_WARP) {
     // ===================================================================== items, pages, loads
+    // The first item is searched for; from there on they are taken in order.
     const int32_t C = sharers(place.total, a.grid, kPageFlashUnits);
     int64_t u = place.b < 0 ? 0 : first_unit(place.total, C, cta);
     const int64_t u_end = place.b < 0 ? 0 : first_unit(place.total, C, cta + 1);
-    int64_t before = place.before;
-    int32_t b = place.b;
+    int32_t b = place.b, group = 0, p = 0, at = 0;  // the next item, and its key tiles before the run
+    PageSeq s = {0, 0, 0};
+    if (u < u_end) {
+      s = page_sequence(a, b, bad);
+      at = static_cast<int32_t>(shape.locate(s, u - place.before, group, p));
+    }
     uint32_t kv = 0, kc = 0, vc = 0;  // key tiles; K and V stages that hold copies
     for (uint32_t k = 0; ok; ++k) {
       Item it;
-      it.live = 0;
+      it.live = u < u_end;
       int32_t g = 0;
-      while (u < u_end) {
-        const PageSeq s = page_sequence(a, b, bad);
-        const int64_t units = shape.units(a, s);
-        if (u >= before + units) {
-          before += units;
-          ++b;
-          continue;
-        }
-        int32_t group, p;
-        const int64_t at = shape.locate(s, u - before, group, p);
-        it.live = 1;
+      if (it.live) {
         it.first = u - at;
         it.q0 = s.q0;
         it.n = s.n;
@@ -330,16 +341,20 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         it.head0 = g * shape.G + part * shape.heads;
         it.heads = min(shape.heads, shape.G - part * shape.heads);
         it.tok0 = p * shape.item_tok;
-        it.kt0 = static_cast<int32_t>(at);
-        const int32_t all = shape.key_tiles(s, p);
-        it.kt1 = static_cast<int32_t>(min(static_cast<int64_t>(all), it.kt0 + (u_end - u)));
-        it.whole = it.kt0 == 0 && it.kt1 == all;
-        break;
+        it.per_head = (65536u + it.heads - 1) / it.heads;
+        it.kt0 = at;
+        it.all = shape.key_tiles(s, p);
+        it.kt1 = static_cast<int32_t>(min(static_cast<int64_t>(it.all), at + (u_end - u)));
       }
-      if (k >= 2 && !warp_wait_far(&bar_item_free[k & 1], ((k >> 1) - 1) & 1)) { ok = false; break; }
+      if (k == 0 && lane == 0) {
+        Item x = it;
+        x.live &= at > 0;
+        static_cast<Item*>(a.runs)[cta] = x;
+      }
+      if (k >= ITEMS && !warp_wait_far(&bar_item_free[k % ITEMS], (k / ITEMS - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
         *sItem(k) = it;
-        bar_arrive(&bar_item[k & 1]);
+        bar_arrive(&bar_item[k % ITEMS]);
       }
       __syncwarp();
       if (!it.live) break;
@@ -379,19 +394,19 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine && phys >= 0));
         const int sk = kv % KST, sv = kv % VST;
         if (kv >= KST && !warp_wait_far(&bar_k_empty[sk], (kv / KST - 1) & 1)) { ok = false; break; }
-        Info& info = sInfo[kv % kInfo];
+        Info& info = sInfo[kv % INFO];
         const int32_t rows = mine && phys >= 0 ? min(kPage, it.len - (pg0 + j * PAGES + x) * kPage) : 0;
         const uint32_t fulls = __popc(__ballot_sync(0xffffffffu, rows == kPage));
         if (mine) {
           info.ks[x] = phys >= 0 ? ks : 1.0f;
           info.ev[x] = phys >= 0 ? scale_exponent(vs) : 0.0f;
           info.unv[x] = phys >= 0 ? scale_inverse(vs) : 1.0f;
-          info.rows[x] = rows;
+          info.rows[x] = static_cast<uint8_t>(rows);
           if (x == 0) info.full = fulls == PAGES;
         }
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(&bar_info[kv % kInfo]);
+          bar_arrive(&bar_info[kv % INFO]);
           mbar_arrive_expect_tx(&bar_k_full[sk], count * kPage * D);
         }
         __syncwarp();
@@ -417,6 +432,15 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       }
       if (!ok) break;
       u += it.kt1 - it.kt0;
+      at = 0;
+      if (u < u_end && ++p == shape.items(s)) {  // (a run that ends inside an item is the CTA's last)
+        p = 0;
+        if (++group == shape.groups * a.num_kv_heads) {
+          group = 0;
+          do s = page_sequence(a, ++b, bad);
+          while (s.n == 0);
+        }
+      }
     }
     // no copy may still be in flight when the CTA exits
     for (uint32_t j = 1; j <= kc && j <= static_cast<uint32_t>(KST); ++j)
@@ -430,20 +454,22 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     const int32_t cw = warp - Cfg::CONV_WARP;
     const int r8 = (lane >> 3) ^ (lane & 4 ? 5 : 0), c4 = lane & 3;
     uint32_t kv = 0;
-    Item it;
     for (uint32_t k = 0; ok; ++k) {
-      if (!take_item(k, it)) { ok = false; break; }
+      if (!take_item(k)) { ok = false; break; }
+      const Item& it = *sItem(k);
       if (!it.live) break;
-      for (int32_t j = it.kt0; j < it.kt1; ++j, ++kv) {
+      const int32_t n = it.kt1 - it.kt0;
+      end_item(k);
+      for (int32_t j = 0; j < n; ++j, ++kv) {
         const int s = kv % VST;
-        if (!warp_wait_far(&bar_info[kv % kInfo], (kv / kInfo) & 1) || !warp_wait_far(&bar_c_full[s], (kv / VST) & 1) ||
+        if (!warp_wait_far(&bar_info[kv % INFO], (kv / INFO) & 1) || !warp_wait_far(&bar_c_full[s], (kv / VST) & 1) ||
             (kv >= VST && !warp_wait_far(&bar_v_empty[s], (kv / VST - 1) & 1))) {
           ok = false;
           break;
         }
         const uint8_t* src = sC + s * Cfg::K_TILE;
         uint8_t* dst = sV + s * Cfg::V_TILE;
-        const Info& info = sInfo[kv % kInfo];
+        const Info& info = sInfo[kv % INFO];
         constexpr int PER_ROW = D / 64;  // steps of 64 codes in a row
 #pragma unroll 2
         for (int i = cw; i < KT / 8 * PER_ROW; i += kConvWarps) {
@@ -481,7 +507,6 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     uint32_t kv = 0;               // key tiles of finished items
     uint32_t nt[2] = {0, 0};       // PVs issued from S buffer w
     uint32_t ni[2] = {0, 0};       // items of tile w
-    Item it;
     auto qk = [&](int w, int buf, uint32_t stage) -> bool {
       // P of the buffer's last PV lies in the columns that this QK writes
       if (nt[buf] > 0 && !warp_wait_far(&bar_pv_done[buf], (nt[buf] - 1) & 1)) return false;
@@ -514,10 +539,12 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       return true;
     };
     for (uint32_t k = 0; ok; ++k) {
-      if (!take_item(k, it)) { ok = false; break; }
+      if (!take_item(k)) { ok = false; break; }
+      const Item& it = *sItem(k);
       if (!it.live) break;
       const int32_t n = it.kt1 - it.kt0;
       const bool two = TILES == 2 && it.tok0 + shape.tile_tok < it.n;
+      end_item(k);
       if (!warp_wait_far(&bar_q_full[0], ni[0]++ & 1)) { ok = false; break; }
       if (two && !warp_wait_far(&bar_q_full[1], ni[1]++ & 1)) { ok = false; break; }
       if constexpr (TILES == 2) {
@@ -572,77 +599,169 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + Cfg::O_COL + w * D + lane_base;
     const int32_t r = (warp & 3) * 32 + lane;  // this thread's row of the tile
-    uint8_t* const q_hi = sQ + w * 2 * Cfg::Q_TERM;
-    uint8_t* const stage = q_hi + (warp & 3) * 32 * Cfg::SLICE;  // output goes through the q of the warp's own rows
+    uint8_t* const stage = smem + Cfg::STG_OFF + warp * 2048;
     uint32_t kv = 0;  // key tiles of finished items
     uint32_t nt = 0;  // key tiles processed
-    Item it;
-    for (uint32_t k = 0; ok; ++k) {
-      if (!take_item(k, it)) { ok = false; break; }
-      if (!it.live) break;
-      const int32_t n = it.kt1 - it.kt0, tok_w = it.tok0 + w * shape.tile_tok;
-      if (w == 1 && tok_w >= it.n) {  // no such tile
-        kv += n;
-        continue;
-      }
-      // ---- the row, its q as two E4M3 terms
-      const int32_t rt = r / it.heads, tok = tok_w + rt;
-      const bool live = rt < shape.tile_tok && tok < it.n;
-      const int32_t lim = live ? it.len - it.n + tok + 1 : 0x7fffffff;  // tokens that the row sees
-      const int32_t lim_least = __reduce_min_sync(0xffffffffu, lim);
-      float mult;
-      {
-        const uint16_t* q =
-            a.q + (static_cast<int64_t>(it.q0 + (live ? tok : 0)) * a.num_q_heads + it.head0 + (r - rt * it.heads)) * D;
-        float top = 0.0f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16x2(x[e]);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-        const int e2 = min(max((__float_as_int(top) >> 23) - 127, -100), 100);
-        const float up = __int_as_float((7 - e2 + 127) << 23);  // the largest comes to [2^7, 2^8)
-        mult = a.score_scale * __int_as_float((e2 - 7 + 127) << 23);
+    float m = kNoMax, l = 0.0f, mult = 0.0f;
+    int32_t lim = 0, lim_least = 0;  // tokens that the row sees; the least of the warp's
+    constexpr int PER_LINE = D / 8, ROWS = 32 / PER_LINE;  // lanes of a row of q, rows of a step
+    const int c16 = lane % PER_LINE, sub = lane / PER_LINE;
+    uint8_t* const q_own = sQ + w * 2 * Cfg::Q_TERM;
+    auto q_raw = [&](int rr) {  // this lane's 16 bytes of row rr of the tile
+      const int at = c16 * 16 % D;
+      return q_own + c16 * 16 / D * Cfg::Q_TERM + at / 128 * kM * 128 + rr * Cfg::SLICE + at % 128;
+    };
+    bool open = false;  // an item's output is still to be written: k - 1
+    for (uint32_t k = 0;; ++k) {
+      if (!take_item(k)) { ok = false; break; }
+      const Item& it = *sItem(k);
+      const bool mine = it.live && it.tok0 + w * shape.tile_tok < it.n;  // it has this tile
+      const bool was_live = lim != 0x7fffffff;
+      // ---- its q, before the output of the item before, so that its first QK runs meanwhile.  The QKs of the item before
+      // have completed.  The warp's 32 rows are fetched into their own place, 16 bytes a lane, the first half of a row where
+      // its first terms will be, the second where its second ones will be.
+      if (mine) {
+        const uint16_t* q = a.q + (static_cast<int64_t>(it.q0) * a.num_q_heads + it.head0) * D + c16 * 8;
 #pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t hi[4], lo[4];
+        for (int i = 0; i < 32 / ROWS; ++i) {
+          const int rr = (warp & 3) * 32 + i * ROWS + sub, t = it.token_of(rr), tok = it.tok0 + w * shape.tile_tok + t;
+          const bool there = t < shape.tile_tok && tok < it.n;
+          cp_async16(q_raw(rr), q + (static_cast<int64_t>(there ? tok : 0) * a.num_q_heads + (there ? rr - t * it.heads : 0)) * D,
+                     there);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        const int32_t rt = it.token_of(r), tok = it.tok0 + w * shape.tile_tok + rt;
+        lim = rt < shape.tile_tok && tok < it.n ? it.len - it.n + tok + 1 : 0x7fffffff;
+        lim_least = __reduce_min_sync(0xffffffffu, lim);
+        // as two E4M3 terms, in place: the lanes of a row find its largest element together, all read before any writes
+        constexpr int STEPS = 32 / ROWS, AT_ONCE = 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < STEPS; i0 += AT_ONCE) {
+          uint4 v[AT_ONCE];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q) + 2 * c + half) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < AT_ONCE; ++i) v[i] = *reinterpret_cast<const uint4*>(q_raw((warp & 3) * 32 + (i0 + i) * ROWS + sub));
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 f = unpack_bf16x2(x[2 * e]), g = unpack_bf16x2(x[2 * e + 1]);
-              float a0, a1, b0, b1;
-              const uint32_t h0 = e4m3x2(f.x * up, f.y * up, a0, a1), h1 = e4m3x2(g.x * up, g.y * up, b0, b1);
-              hi[2 * half + e] = h0 | h1 << 16;
-              lo[2 * half + e] = encode_fp8x2(f.x * up - a0, f.y * up - a1) |
-                                 static_cast<uint32_t>(encode_fp8x2(g.x * up - b0, g.y * up - b1)) << 16;
+          for (int i = 0; i < AT_ONCE; ++i) {
+            const int rr = (warp & 3) * 32 + (i0 + i) * ROWS + sub;
+            uint32_t big = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                    __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));  // bf16 magnitudes sort as integers
+#pragma unroll
+            for (int o = PER_LINE / 2; o > 0; o >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const int e2 = min(max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -100), 100);
+            const float up = __int_as_float((7 - e2 + 127) << 23);  // the largest comes to [2^7, 2^8)
+            const int of_mine = __shfl_sync(0xffffffffu, e2, lane % ROWS * PER_LINE);  // (row lane % ROWS of this step)
+            if (lane / ROWS == i0 + i) mult = a.score_scale * __int_as_float((of_mine - 7 + 127) << 23);
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack_bf16x2(x[e]);
+              e4m3_terms(pack_f16x2(f.x * up, f.y * up), hi[e], lo[e]);  // (f16 holds a scaled bf16 exactly, down to 2^-24)
             }
+            uint8_t* to = q_own + c16 % 2 * 8 +
+                          (D == 64 ? rr * 64 + (((c16 / 2) ^ ((rr >> 1) & 3)) << 4)
+                                   : c16 / 16 * kM * 128 + rr * 128 + (((c16 / 2 & 7) ^ (rr & 7)) << 4));
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(to + Cfg::Q_TERM) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           }
-          uint8_t* to = D == 64 ? q_hi + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
-                                : q_hi + c / 8 * kM * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(to + Cfg::Q_TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&bar_q_full[w]);
       }
-      float m = kNoMax, l = 0.0f;
+      // ---- the output of the item before, once its last PV has completed
+      if (open) {
+        open = false;
+        const int last_buf = TILES == 2 ? w : (kv - 1) & 1;
+        const uint32_t last_use = TILES == 2 ? nt - 1 : (kv - 1) >> 1;
+        if (!warp_wait_far(&bar_pv_done[last_buf], last_use & 1)) { ok = false; break; }
+        tc_fence_after();
+        const Item& was = *sItem(k - 1);
+        const float inv = was.whole() ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+        const int64_t slot = part_slot(place.total, sharers(place.total, a.grid, kPageFlashUnits), cta, was.first);
+        const int32_t tok_w = was.tok0 + w * shape.tile_tok;
+        // rows pass through the warp's 2 KB, 32 columns at a time, so that four lanes write 64 or 128 bytes of one row
+        const int r0 = lane >> 2, c4 = lane & 3;
+        int64_t at[4];  // where rows r0 + 8 i begin, -1: no such row
+        const int64_t base = was.whole() ? (static_cast<int64_t>(was.q0 + tok_w) * a.num_q_heads + was.head0) * D
+                                      : (slot * TILES + w) * kM * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t x = (warp & 3) * 32 + r0 + 8 * i, t = was.token_of(x);
+          at[i] = t >= shape.tile_tok || tok_w + t >= was.n ? -1
+                  : was.whole()                               ? base + (static_cast<int64_t>(t) * a.num_q_heads + (x - t * was.heads)) * D
+                                                           : base + x * D;
+        }
+        if (!was.whole() && was_live)
+          *reinterpret_cast<float2*>(a.part_ml + ((slot * TILES + w) * kM + r) * 2) = make_float2(m, l);
+        auto put = [&](int h, uint4 x) {
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((h ^ ((lane >> 1) & 3)) << 4)) = x;
+        };
+        auto get = [&](int i) {
+          const int row = r0 + 8 * i;
+          return *reinterpret_cast<const uint4*>(stage + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
+        };
+        const bool f32 = !was.whole() || a.out_dtype == KVQ_OUT_F32;
+        float* const out32 = was.whole() ? static_cast<float*>(a.out) : a.part_acc;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          if (c == D / 32 - 1) {  // the reads are ordered before the arrival that lets the next PV overwrite O
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bar_o_free[w]);
+          }
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * inv;
+          if (f32) {
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const float* y = o + 16 * f + 4 * h;
+                put(h, make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (at[i] >= 0) *reinterpret_cast<uint4*>(out32 + at[i] + c * 32 + 16 * f + 4 * c4) = get(i);
+            }
+          } else {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              put(h, make_uint4(pack_bf16x2(o[8 * h], o[8 * h + 1]), pack_bf16x2(o[8 * h + 2], o[8 * h + 3]),
+                                pack_bf16x2(o[8 * h + 4], o[8 * h + 5]), pack_bf16x2(o[8 * h + 6], o[8 * h + 7])));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (at[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at[i] + c * 32 + 8 * c4) = get(i);
+          }
+        }
+        end_item(k - 1);
+      }
+      if (!it.live) break;
+      const int32_t n = it.kt1 - it.kt0, first_key = it.kt0 * KT;
+      if (!mine) {
+        kv += n;
+        end_item(k);
+        continue;
+      }
+      m = kNoMax;
+      l = 0.0f;
       for (int32_t j = 0; j < n; ++j, ++nt) {
         const int buf = TILES == 2 ? w : (kv + j) & 1;
         const uint32_t uses = TILES == 2 ? nt : (kv + j) >> 1;
         const uint32_t tS = tmem + buf * KT + lane_base;
-        const uint32_t slot = (kv + j) % kInfo;
-        if (!warp_wait_far(&bar_info[slot], ((kv + j) / kInfo) & 1)) { ok = false; break; }
+        const uint32_t slot = (kv + j) % INFO;
+        if (!warp_wait_far(&bar_info[slot], ((kv + j) / INFO) & 1)) { ok = false; break; }
         const Info& info = sInfo[slot];
-        const int32_t t0 = (it.kt0 + j) * KT;
+        const int32_t t0 = first_key + j * KT;
         const bool plain = t0 + KT <= lim_least && info.full;
         float ks[PAGES], ev[PAGES];
 #pragma unroll
@@ -660,6 +779,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         if (!plain) {
 #pragma unroll
           for (int p = 0; p < PAGES; ++p) {
+            if (info.rows[p] == kPage && t0 + (p + 1) * kPage <= lim_least) continue;  // all of the page is seen
             const int32_t see = info.rows[p] > 0 ? lim - t0 - p * kPage : 0;
             float x = -INFINITY;
 #pragma unroll
@@ -720,76 +840,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         if (lane == 0) bar_arrive(&bar_p_full[buf]);
       }
       if (!ok) break;
-      // ---- O, once the item's last PV has completed
-      {
-        const int buf = TILES == 2 ? w : (kv + n - 1) & 1;
-        const uint32_t uses = TILES == 2 ? nt - 1 : (kv + n - 1) >> 1;
-        if (!warp_wait_far(&bar_pv_done[buf], uses & 1)) { ok = false; break; }
-      }
-      tc_fence_after();
       kv += n;
-      const float inv = it.whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-      const int64_t slot = part_slot(place.total, sharers(place.total, a.grid, kPageFlashUnits), cta, it.first);
-      // rows pass through the warp's 2 KB, 32 columns at a time, so that four lanes write 64 or 128 bytes of one row
-      const int r0 = lane >> 2, c4 = lane & 3;
-      int64_t at[4];  // where rows r0 + 8 i begin, -1: no such row
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t row = (warp & 3) * 32 + r0 + 8 * i, t = row / it.heads;
-        const bool there = t < shape.tile_tok && tok_w + t < it.n;
-        if (!it.whole) at[i] = there ? ((slot * TILES + w) * kM + row) * D : -1;
-        else at[i] = there ? (static_cast<int64_t>(it.q0 + tok_w + t) * a.num_q_heads + it.head0 + (row - t * it.heads)) * D : -1;
-      }
-      if (!it.whole && live)
-        *reinterpret_cast<float2*>(a.part_ml + ((slot * TILES + w) * kM + r) * 2) = make_float2(m, l);
-      auto put = [&](int h, uint4 x) {
-        *reinterpret_cast<uint4*>(stage + lane * 64 + ((h ^ ((lane >> 1) & 3)) << 4)) = x;
-      };
-      auto get = [&](int i) {
-        const int row = r0 + 8 * i;
-        return *reinterpret_cast<const uint4*>(stage + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
-      };
-      const bool f32 = !it.whole || a.out_dtype == KVQ_OUT_F32;
-      float* const out32 = it.whole ? static_cast<float*>(a.out) : a.part_acc;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t ov[32];
-        tmem_ld32(tO + c * 32, ov);
-        if (c == D / 32 - 1) {  // the reads are ordered before the arrival that lets the next PV overwrite O
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&bar_o_free[w]);
-        }
-        float o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * inv;
-        if (f32) {
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const float* x = o + 16 * f + 4 * h;
-              put(h, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (at[i] >= 0) *reinterpret_cast<uint4*>(out32 + at[i] + c * 32 + 16 * f + 4 * c4) = get(i);
-          }
-        } else {
-          __syncwarp();
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            put(h, make_uint4(pack_bf16x2(o[8 * h], o[8 * h + 1]), pack_bf16x2(o[8 * h + 2], o[8 * h + 3]),
-                              pack_bf16x2(o[8 * h + 4], o[8 * h + 5]), pack_bf16x2(o[8 * h + 6], o[8 * h + 7])));
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (at[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at[i] + c * 32 + 8 * c4) = get(i);
-        }
-      }
-      __syncwarp();  // (the next item's q is written over the staged rows)
+      open = true;
     }
   }
   if (!ok) set_status(a.status, kStatusTimeout);
@@ -800,66 +852,52 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-// Joins the runs of the items that several CTAs worked on.  CTA (c - 1, y): the item in which CTA c's first unit lies, if
-// that is its first joint; rows 32 y ... + 31, a warp for every eighth.
-constexpr int kJoinWarps = 8, kJoinRows = 32;
+// Joins the runs of the items that several CTAs worked on.  CTA (c - 1, y): the item that CTA c went on with first, if that
+// is the item's first joint; rows 8 y ... + 7, a warp for each.
+constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) page_flash_join_kernel(const PageArgs a) {
   using Cfg = FCfg<D>;
   const Shape<D> shape(a);
   const int32_t c = blockIdx.x + 1, lane = threadIdx.x & 31;
-  bool bad = false;
-  const Place place = page_place<kJoinWarps>(
-      a.batch, nullptr, [&](int32_t i) { return shape.units(a, page_sequence(a, i, bad)); },
-      [&](int64_t U) {
-        const int32_t C = sharers(U, a.grid, kPageFlashUnits);
-        return c < C && U > 0 ? first_unit(U, C, c) : U;
-      });
-  if (place.b < 0) return;
-  const int64_t U = place.total;
-  const int32_t C = sharers(U, a.grid, kPageFlashUnits);
-  const PageSeq s = page_sequence(a, place.b, bad);
-  int32_t group, p;
-  const int64_t u = first_unit(U, C, c), inside = shape.locate(s, u - place.before, group, p), first = u - inside;
-  // its first joint only: the run before begins at or before the item
-  if (inside == 0 || first_unit(U, C, c - 1) > first) return;
-  const int32_t c1 = owner_of(U, C, first + shape.key_tiles(s, p) - 1);
-  const int32_t g = group / shape.groups, part = group - g * shape.groups;
-  const int32_t heads = min(shape.heads, shape.G - part * shape.heads);
+  const int32_t row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), w = row / kM, r = row - w * kM;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t U = *a.total;
+  const int32_t C = sharers(U, a.grid, kPageFlashUnits);
+  if (c >= C || U == 0) return;
+  const Item& it = static_cast<const Item*>(a.runs)[c];
+  if (!it.live || first_unit(U, C, c - 1) > it.first) return;
+  const int32_t rt = it.token_of(r), tok = it.tok0 + w * shape.tile_tok + rt;
+  if (rt >= shape.tile_tok || tok >= it.n) return;
+  const int32_t c1 = owner_of(U, C, it.first + it.all - 1);
   constexpr int V2 = D / 64;  // float2 of a lane
-  for (int32_t row = blockIdx.y * kJoinRows + (threadIdx.x >> 5); row < (blockIdx.y + 1) * kJoinRows; row += kJoinWarps) {
-    const int32_t w = row / kM, r = row - w * kM, rt = r / heads;
-    const int32_t tok = p * shape.item_tok + w * shape.tile_tok + rt;
-    if (rt >= shape.tile_tok || tok >= s.n) continue;
-    float m = kNoMax, l = 0.0f;
-    float2 x[V2];
+  float m = kNoMax, l = 0.0f;
+  float2 x[V2];
 #pragma unroll
-    for (int k = 0; k < V2; ++k) x[k] = make_float2(0.0f, 0.0f);
+  for (int k = 0; k < V2; ++k) x[k] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-    for (int32_t i = c - 1; i <= c1; ++i) {
-      const int64_t at = (part_slot(U, C, i, first) * Cfg::TILES + w) * kM + r;
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-      const float now = fmaxf(m, ml.x), f = ex2(ml.x - now), keep = ex2(m - now);
-      m = now;
-      l = fmaf(ml.y, f, l * keep);
-#pragma unroll
-      for (int k = 0; k < V2; ++k) {
-        const float2 y = *reinterpret_cast<const float2*>(a.part_acc + at * D + k * 64 + lane * 2);
-        x[k].x = fmaf(y.x, f, x[k].x * keep);
-        x[k].y = fmaf(y.y, f, x[k].y * keep);
-      }
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int64_t out = (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + g * shape.G + part * shape.heads + (r - rt * heads)) * D;
+  for (int32_t i = c - 1; i <= c1; ++i) {
+    const int64_t at = (part_slot(U, C, i, it.first) * Cfg::TILES + w) * kM + r;
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    const float now = fmaxf(m, ml.x), f = ex2(ml.x - now), keep = ex2(m - now);
+    m = now;
+    l = fmaf(ml.y, f, l * keep);
 #pragma unroll
     for (int k = 0; k < V2; ++k) {
-      const int64_t at = out + k * 64 + lane * 2;
-      if (a.out_dtype == KVQ_OUT_F32)
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(x[k].x * inv, x[k].y * inv);
-      else
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack_bf16x2(x[k].x * inv, x[k].y * inv);
+      const float2 y = *reinterpret_cast<const float2*>(a.part_acc + at * D + k * 64 + lane * 2);
+      x[k].x = fmaf(y.x, f, x[k].x * keep);
+      x[k].y = fmaf(y.y, f, x[k].y * keep);
     }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const int64_t out = (static_cast<int64_t>(it.q0 + tok) * a.num_q_heads + it.head0 + (r - rt * it.heads)) * D;
+#pragma unroll
+  for (int k = 0; k < V2; ++k) {
+    const int64_t at = out + k * 64 + lane * 2;
+    if (a.out_dtype == KVQ_OUT_F32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(x[k].x * inv, x[k].y * inv);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack_bf16x2(x[k].x * inv, x[k].y * inv);
   }
 }
 
@@ -875,7 +913,7 @@ kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
   if (a.grid == 1) return KVQ_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid - 1, Cfg::TILES * kM / kJoinRows);
+  cfg.gridDim = dim3(a.grid - 1, Cfg::TILES * kM / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -49,6 +49,13 @@ struct RCfg {
   static constexpr int CTAS = D == 256 ? 2 : 4;        // resident per SM
 };
 
+// A tile that a CTA went on with first, for the joining kernel.
+struct Run {
+  int64_t first;                         // the tile's first unit
+  int32_t live, pages, q0, g, row0, rows; // its pages; sequence's first row; kv head; first row of the group's, and how many
+};
+static_assert(sizeof(Run) <= kPageRunBytes, "run slots");
+
 // One sequence's rows, pages and tiles.
 struct Seq : PageSeq {
   int32_t pages, tiles;
@@ -89,8 +96,15 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
   __syncwarp();
   const int32_t cta = blockIdx.x;
   bool bad = false;
+  asm volatile("griddepcontrol.launch_dependents;");  // (the joining kernel waits for this one's end)
+  if (a.q_start == nullptr) {  // the rows of sequences without tokens
+    for (int32_t b = cta; b < a.batch; b += a.grid)
+      if (__ldg(a.seq_lens + b) <= 0)
+        for (int32_t i = tid; i < a.num_q_heads * (D / 4); i += kThreads)
+          page_store_out(a, static_cast<int64_t>(b) * a.num_q_heads * D + i * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
+  }
   const Place place = page_place<kWarps>(
-      a.batch, cta == 0 ? a.tab : nullptr, [&](int32_t i) { return rows_sequence(a, i, bad).units; },
+      a.batch, cta == 0 ? a.total : nullptr, [&](int32_t i) { return rows_sequence(a, i, bad).units; },
       [&](int64_t U) {  // this CTA's first unit
         const int32_t C = sharers(U, a.grid, kPageMinUnits);
         return cta < C && U > 0 ? first_unit(U, C, cta) : U;
@@ -99,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
   if (place.b < 0) return;
   const int32_t C = sharers(place.total, a.grid, kPageMinUnits);
   int64_t u = first_unit(place.total, C, cta);
-  const int64_t u_end = first_unit(place.total, C, cta + 1);
+  const int64_t u_first = u, u_end = first_unit(place.total, C, cta + 1);
   const int32_t G = a.num_q_heads / a.num_kv_heads;
   int32_t b = place.b;
   int64_t before = place.before;
@@ -121,6 +135,8 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
     const int32_t g = tile_at / s.tiles, tile = tile_at - g * s.tiles;
     const int32_t rows = min(kRows, s.n * G - tile * kRows);
     const int64_t tile_first = u - pg0;  // the tile's first unit
+    if (tid == 0 && u == u_first)
+      static_cast<Run*>(a.runs)[cta] = {tile_first, pg0 > 0, s.pages, s.q0, g, tile * kRows, rows};
 
     // ---- this lane's two rows: where their q lies, how many tokens they see
     const uint16_t* qrow[2];
@@ -435,52 +451,30 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
   }
 }
 
-// Joins the runs of each output row whose tile several CTAs worked on, and clears the rows of sequences without tokens.
-// A CTA per (query row, head), a warp per run in turn.
-constexpr int kJoinWarps = 4;
+// Joins the runs of the tiles that several CTAs worked on.  CTA (c - 1, r): row r of the tile that CTA c went on with
+// first, if that is the tile's first joint; its warps share the runs.
+constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageArgs a) {
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   __shared__ __align__(16) float s_a[kJoinWarps][D];
-  __shared__ int32_t s_b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t t = blockIdx.x / a.num_q_heads, head = blockIdx.x - t * a.num_q_heads;
-  const int32_t G = a.num_q_heads / a.num_kv_heads, g = head / G;
-  bool bad = false;
-  int32_t b = t;
-  if (a.q_start != nullptr) {  // the sequence of row t
-    if (tid == 0) s_b = a.batch;
-    __syncthreads();
-    for (int32_t i = tid; i < a.batch; i += kJoinWarps * 32) {
-      const PageSeq s = page_sequence(a, i, bad);
-      if (t >= s.q0 && t - s.q0 < s.n) atomicMin(&s_b, i);
-    }
-    __syncthreads();
-    b = s_b;
-    if (b >= a.batch) return;
-  }
-  const Seq s = rows_sequence(a, b, bad);
-  const int32_t R = (t - s.q0) * G + head - g * G, tile = R / kRows, r = R - tile * kRows;
+  const int32_t c = blockIdx.x + 1, r = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t U = a.tab[a.batch];
-  const int64_t first = a.tab[b] + (static_cast<int64_t>(g) * s.tiles + tile) * s.pages, last = first + s.pages - 1;
-  const int64_t out = (static_cast<int64_t>(t) * a.num_q_heads + head) * D;
-  if (s.pages == 0) {
-    if (tid < D / 4) page_store_out(a, out + tid * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
-    return;
-  }
+  const int64_t U = *a.total;
   const int32_t C = sharers(U, a.grid, kPageMinUnits);
-  const int32_t c0 = owner_of(U, C, first), c1 = owner_of(U, C, last);
-  if (c0 == c1) return;  // its CTA has written the output
-  auto part = [&](int32_t c) { return part_slot(U, C, c, first) * kRows + r; };
+  if (c >= C || U == 0) return;
+  const Run run = static_cast<const Run*>(a.runs)[c];
+  if (!run.live || r >= run.rows || first_unit(U, C, c - 1) > run.first) return;
+  const int32_t c1 = owner_of(U, C, run.first + run.pages - 1);
   constexpr int V4 = D / 128 > 0 ? D / 128 : 1;  // float4 of a lane (D = 64: of half the lanes)
   float m = kNoMax, l = 0.0f;
   float4 x[V4];
 #pragma unroll
   for (int k = 0; k < V4; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-  for (int32_t c = c0 + warp; c <= c1; c += kJoinWarps) {
-    const int64_t at = part(c);
+#pragma unroll 4
+  for (int32_t i = c - 1 + warp; i <= c1; i += kJoinWarps) {
+    const int64_t at = part_slot(U, C, i, run.first) * kRows + r;
     const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
     const float now = fmaxf(m, ml.x), f = ex2(ml.x - now), keep = ex2(m - now);
     m = now;
@@ -503,7 +497,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
   for (int k = 0; k < V4; ++k)
     if (D != 64 || lane < 16) *reinterpret_cast<float4*>(&s_a[warp][k * 128 + lane * 4]) = x[k];
   __syncthreads();
-  for (int d = tid * 4; d < D; d += kJoinWarps * 32 * 4) {
+  const int32_t G = a.num_q_heads / a.num_kv_heads, R = run.row0 + r, tok = R / G;
+  const int64_t out = (static_cast<int64_t>(run.q0 + tok) * a.num_q_heads + run.g * G + (R - tok * G)) * D;
+  if (tid < D / 4) {
+    const int d = tid * 4;
     float M = kNoMax, sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
@@ -511,11 +508,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
       const float f = ex2(s_m[w] - M);
+      const float4 v = *reinterpret_cast<const float4*>(&s_a[w][d]);
       sum = fmaf(s_l[w], f, sum);
-      y.x = fmaf(s_a[w][d], f, y.x);
-      y.y = fmaf(s_a[w][d + 1], f, y.y);
-      y.z = fmaf(s_a[w][d + 2], f, y.z);
-      y.w = fmaf(s_a[w][d + 3], f, y.w);
+      y.x = fmaf(v.x, f, y.x);
+      y.y = fmaf(v.y, f, y.y);
+      y.z = fmaf(v.z, f, y.z);
+      y.w = fmaf(v.w, f, y.w);
     }
     page_store_out(a, out + d, y, sum > 0.0f ? 1.0f / sum : 0.0f);
   }
@@ -532,7 +530,8 @@ kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
   kern<<<a.grid, kThreads, Cfg::SMEM, stream>>>(a, map);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.total_q) * a.num_q_heads);
+  if (a.grid == 1) return KVQ_OK;
+  cfg.gridDim = dim3(a.grid - 1, std::min<int64_t>(kRows, static_cast<int64_t>(a.total_q) * (a.num_q_heads / a.num_kv_heads)));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
