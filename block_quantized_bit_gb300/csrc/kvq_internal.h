@@ -253,7 +253,7 @@ struct PageArgs {
 constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
 constexpr int kPageRunBytes = 64;
-constexpr int kPageFlashUnits = 8; // key tiles that are worth a CTA of the flash kernel
+constexpr int kPageFlashUnits = 4; // key tiles that are worth a CTA of the flash kernel
 bool page_supported(int32_t head_dim);
 int32_t page_rows_grid(int32_t head_dim, int32_t sms);  // CTAs that are resident at once
 kvq_status launch_page_rows(const PageArgs& a, cudaStream_t stream);

@@ -34,7 +34,7 @@ namespace kvq {
 namespace {
 
 constexpr int kM = 128;           // rows of a tile
-constexpr int kConvWarps = 5;     // that turn V's codes into f16
+constexpr int kConvWarps = 2;     // that turn V's codes into f16
 constexpr int kTmemCols = 512;
 
 // What the softmax and the converting warps know of the pages of a key tile.
@@ -49,22 +49,21 @@ struct alignas(16) PageInfo {
 template <int D>
 struct FCfg {
   static constexpr int TILES = D == 256 ? 1 : 2;
-  static constexpr int KT = 64;                         // keys of a key tile
+  static constexpr int KT = D == 256 ? 64 : 128;        // keys of a key tile
   static constexpr int PAGES = KT / kPage;
   static constexpr int SLICES = D == 256 ? 2 : 1;       // 128-byte (D = 64: 64-byte) slices of a row of codes
   static constexpr int SLICE = D == 64 ? 64 : 128;
   static constexpr int Q_TERM = kM * D;                 // bytes of one term of a tile's q
   static constexpr int K_TILE = KT * D, V_TILE = 2 * KT * D;
-  static constexpr int KST = D == 256 ? 3 : 6;          // stages of K codes
-  static constexpr int VST = D == 256 ? 2 : 4;          // stages of V codes, and of V in f16
+  static constexpr int KST = 3, VST = 2;                // stages of K codes; of V codes and of V in f16
   // Key tiles whose pages are described in shared memory.  A slot is written once QK of the tile KST before has completed; by
-  // then PV of the tile two before that one has, and all have read that tile's.
-  static constexpr int INFO = 8;
-  static_assert(INFO >= KST + 2, "info slots");
+  // then all have read that of the tile before that one (one tile per CTA: two before).
+  static constexpr int INFO = TILES == 2 ? 4 : 8;
+  static_assert(INFO >= KST + (TILES == 2 ? 1 : 2), "info slots");
   static constexpr int ITEMS = 4;                       // item slots
   static constexpr int SM_WARPS = 4 * TILES;
-  static constexpr int QK_WARP = SM_WARPS, PV_WARP = SM_WARPS + 1, LOAD_WARP = SM_WARPS + 2, CONV_WARP = SM_WARPS + 3;
-  static constexpr int THREADS = (SM_WARPS + 3 + kConvWarps) * 32;
+  static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1, CONV_WARP = SM_WARPS + 2;
+  static constexpr int THREADS = (SM_WARPS + 2 + kConvWarps) * 32;
   static constexpr int Q_OFF = 0;                       // 1024-byte aligned: swizzle atoms
   static constexpr int K_OFF = Q_OFF + TILES * 2 * Q_TERM;
   static constexpr int C_OFF = K_OFF + KST * K_TILE;    // V codes
@@ -73,9 +72,9 @@ struct FCfg {
   static constexpr int INFO_OFF = STG_OFF + SM_WARPS * 2048;
   static constexpr int ITEM_OFF = INFO_OFF + INFO * static_cast<int>(sizeof(PageInfo<PAGES>));
   static constexpr int BAR_OFF = ITEM_OFF + ITEMS * 64;
-  static constexpr int NBARS = 2 * KST + 4 * VST + INFO + 16 + 2 * ITEMS;
+  static constexpr int NBARS = 2 * KST + 4 * VST + INFO + 10 + 2 * ITEMS;
   static constexpr int SMEM = BAR_OFF + NBARS * 8 + 16 + 1024;  // + slack to align the base
-  static constexpr int O_COL = TILES * 2 * KT;          // behind two S buffers a tile
+  static constexpr int O_COL = D == 256 ? 128 : 256;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(O_COL + TILES * D <= kTmemCols, "tensor memory");
 };
@@ -257,11 +256,11 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   uint64_t* bar_v_full = bar_c_empty + VST;       // [VST] V in f16 written
   uint64_t* bar_v_empty = bar_v_full + VST;       // [VST] its last PV completed (commit)
   uint64_t* bar_info = bar_v_empty + VST;         // [INFO] the key tile's pages are described
-  uint64_t* bar_s_full = bar_info + INFO;         // [4] QK into an S buffer completed (commit)
-  uint64_t* bar_p_full = bar_s_full + 4;          // [4] P written there
-  uint64_t* bar_pv_done = bar_p_full + 4;         // [4] PV from there completed (commit)
-  uint64_t* bar_q_full = bar_pv_done + 4;         // [2] q of the item's tile written
-  uint64_t* bar_o_free = bar_q_full + 2;          // [2] O of the tile read out
+  uint64_t* bar_s_full = bar_info + INFO;        // [2] QK into S buffer w completed (commit)
+  uint64_t* bar_p_full = bar_s_full + 2;          // [2] P of buffer w written
+  uint64_t* bar_pv_done = bar_p_full + 2;         // [2] PV of buffer w completed (commit)
+  uint64_t* bar_q_full = bar_pv_done + 2;         // [TILES] q of the item written
+  uint64_t* bar_o_free = bar_q_full + 2;          // [TILES] O read out
   uint64_t* bar_item = bar_o_free + 2;            // [ITEMS] item slot published
   uint64_t* bar_item_free = bar_item + ITEMS;     // [ITEMS] every consuming warp is done with the item
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Cfg::BAR_OFF + Cfg::NBARS * 8);
@@ -285,22 +284,20 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       mbar_init(&bar_v_empty[i], 1);
     }
     for (int i = 0; i < INFO; ++i) mbar_init(&bar_info[i], 1);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&bar_s_full[i], 1);
-      mbar_init(&bar_p_full[i], 4);
-      mbar_init(&bar_pv_done[i], 1);
-    }
     for (int w = 0; w < 2; ++w) {
+      mbar_init(&bar_s_full[w], 1);
+      mbar_init(&bar_p_full[w], 4);
+      mbar_init(&bar_pv_done[w], 1);
       mbar_init(&bar_q_full[w], 4);
       mbar_init(&bar_o_free[w], 4);
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&bar_item[i], 1);
-      mbar_init(&bar_item_free[i], Cfg::SM_WARPS + 2 + kConvWarps);
+      mbar_init(&bar_item_free[i], Cfg::SM_WARPS + 1 + kConvWarps);
     }
     fence_mbar_init();
   }
-  if (warp == Cfg::QK_WARP) {
+  if (warp == Cfg::MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)),
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -508,28 +505,55 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         }
       }
     }
-  } else if (warp == Cfg::QK_WARP) {
-    // ===================================================================== QK issue (elected lane)
-    const uint32_t idesc = page_idesc(KT, false);
+  } else if (warp == Cfg::MMA_WARP) {
+    // ===================================================================== MMA issue (elected lane)
+    const uint32_t idesc_qk = page_idesc(KT, false), idesc_pv = page_idesc(D, true);
     auto k_major = [&](const uint8_t* p) {
       return D == 64 ? smem_desc(smem_u32(p), 16, 512) | static_cast<uint64_t>(4) << 61 : sw128_desc(smem_u32(p), 16, 1024);
     };
-    const uint64_t dq0 = k_major(sQ), dk0 = k_major(sK);
-    uint32_t stage = 0, parity = 0;           // of the K ring
-    uint32_t nq[2] = {0, 0}, ni[2] = {0, 0};  // QKs and items of tile w: the x-th QK goes into its S buffer x % 2
-    auto qk = [&](int w) -> bool {
-      const uint32_t buf = 2 * w + (nq[w] & 1), uses = nq[w] >> 1;
+    const uint64_t dq0 = k_major(sQ), dk0 = k_major(sK), dv0 = sw128_desc(smem_u32(sV), KT * 128, 1024);
+    uint32_t ks = 0, kp = 0, vs = 0, vp = 0;   // stage and parity of the K and the V ring
+    uint32_t nt[2] = {0, 0}, ni[2] = {0, 0};   // PVs issued from S buffer w; items of tile w
+    auto qk = [&](int w, uint32_t buf) -> bool {
       // P of the buffer's last PV lies in the columns that this QK writes
-      if (uses > 0 && !warp_wait_far(&bar_pv_done[buf], (uses - 1) & 1)) return false;
+      if (nt[buf] > 0 && !warp_wait_far(&bar_pv_done[buf], (nt[buf] - 1) & 1)) return false;
       tc_fence_after();
-      const uint64_t q = dq0 + ((w * 2 * Cfg::Q_TERM) >> 4), kk = dk0 + stage * (Cfg::K_TILE >> 4);
+      const uint64_t q = dq0 + ((w * 2 * Cfg::Q_TERM) >> 4), kk = dk0 + ks * (Cfg::K_TILE >> 4);
 #pragma unroll
       for (int s = 0; s < SLICES; ++s)
-        mma_fp8<Cfg::SLICE / 32>(tmem + buf * KT, q + ((s * kM * 128) >> 4), kk + ((s * KT * 128) >> 4), Cfg::Q_TERM >> 4, idesc,
-                                 s > 0 ? 1u : 0u);
+        mma_fp8<Cfg::SLICE / 32>(tmem + buf * KT, q + ((s * kM * 128) >> 4), kk + ((s * KT * 128) >> 4), Cfg::Q_TERM >> 4,
+                                 idesc_qk, s > 0 ? 1u : 0u);
       mma_commit(&bar_s_full[buf]);
-      ++nq[w];
       return true;
+    };
+    auto pv = [&](int w, uint32_t buf, bool first) -> bool {
+      if (first && ni[w] > 1 && !warp_wait_far(&bar_o_free[w], (ni[w] - 2) & 1)) return false;
+      if (!warp_wait_far(&bar_p_full[buf], nt[buf] & 1)) return false;
+      tc_fence_after();
+      // a k-step is 16 keys: 8 columns of P, 16 rows of V
+      const uint32_t o = tmem + Cfg::O_COL + w * D, acc = first ? 0u : 1u;
+      const uint64_t v = dv0 + vs * (Cfg::V_TILE >> 4), step = (16 * 128) >> 4;
+      if constexpr (KT == 128) mma8_bf16_tmem_a(o, tmem + buf * KT, 8u, v, step, idesc_pv, acc);
+      else mma4_bf16_tmem_a(o, tmem + buf * KT, 8u, v, step, idesc_pv, acc);
+      mma_commit(&bar_pv_done[buf]);
+      ++nt[buf];
+      return true;
+    };
+    auto k_there = [&] { return warp_wait_far(&bar_k_full[ks], kp); };
+    auto v_there = [&] { return warp_wait_far(&bar_v_full[vs], vp); };
+    auto k_done = [&] {
+      mma_commit(&bar_k_empty[ks]);
+      if (++ks == KST) {
+        ks = 0;
+        kp ^= 1;
+      }
+    };
+    auto v_done = [&] {
+      mma_commit(&bar_v_empty[vs]);
+      if (++vs == VST) {
+        vs = 0;
+        vp ^= 1;
+      }
     };
     for (uint32_t k = 0; ok; ++k) {
       if (!take_item(k)) { ok = false; break; }
@@ -540,56 +564,51 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       end_item(k);
       if (!warp_wait_far(&bar_q_full[0], ni[0]++ & 1)) { ok = false; break; }
       if (two && !warp_wait_far(&bar_q_full[1], ni[1]++ & 1)) { ok = false; break; }
-      for (int32_t j = 0; j < n; ++j) {
-        if (!warp_wait_far(&bar_k_full[stage], parity) || !qk(0) || (two && !qk(1))) { ok = false; break; }
-        mma_commit(&bar_k_empty[stage]);
-        if (++stage == KST) {
-          stage = 0;
-          parity ^= 1;
+      if (two) {
+        // QK_A(j), PV_B(j - 1), QK_B(j), PV_A(j): a softmax has the time of two MMA groups
+        ok = k_there() && qk(0, 0) && qk(1, 1);
+        if (ok) {
+          k_done();
+          ok = v_there() && pv(0, 0, true);
         }
+        for (int32_t j = 1; ok && j < n; ++j) {
+          ok = k_there() && qk(0, 0) && pv(1, 1, j == 1);
+          if (!ok) break;
+          v_done();
+          ok = qk(1, 1);
+          if (!ok) break;
+          k_done();
+          ok = v_there() && pv(0, 0, false);
+        }
+        ok = ok && pv(1, 1, n == 1);
+        if (ok) v_done();
+      } else {
+        // one tile: QK(j), PV(j - 1), through two S buffers where there is but one tile anyway
+        const uint32_t alt = TILES == 1 ? 1u : 0u;
+        uint32_t buf = TILES == 1 ? (nt[0] + nt[1]) & 1 : 0u;
+        for (int32_t j = 0; ok && j < n; ++j) {
+          if (alt || j == 0) ok = k_there() && qk(0, buf);
+          if (ok && (alt || j == 0)) k_done();
+          if (alt) {
+            if (ok && j > 0) ok = v_there() && pv(0, buf ^ 1, j == 1);
+            if (ok && j > 0) v_done();
+            buf ^= 1;
+          } else {
+            if (ok) ok = v_there() && pv(0, 0, j == 0);
+            if (ok) v_done();
+            if (ok && j + 1 < n) {
+              ok = k_there() && qk(0, 0);
+              if (ok) k_done();
+            }
+          }
+        }
+        if (alt && ok) ok = v_there() && pv(0, buf ^ 1, n == 1);
+        if (alt && ok) v_done();
       }
     }
     // before tensor memory is freed, every MMA issued must have completed
-    for (int w = 0; w < TILES; ++w)
-      for (uint32_t x = 1; x <= 2 && x <= nq[w]; ++x)
-        (void)mbar_wait_bounded(&bar_s_full[2 * w + ((nq[w] - x) & 1)], ((nq[w] - x) >> 1) & 1);
-  } else if (warp == Cfg::PV_WARP) {
-    // ===================================================================== PV issue (elected lane)
-    const uint32_t idesc = page_idesc(D, true);
-    const uint64_t dv0 = sw128_desc(smem_u32(sV), KT * 128, 1024);
-    uint32_t stage = 0, parity = 0;           // of the V ring
-    uint32_t nt[2] = {0, 0}, ni[2] = {0, 0};  // PVs and items of tile w
-    auto pv = [&](int w, bool first) -> bool {
-      const uint32_t buf = 2 * w + (nt[w] & 1);
-      if (first && ni[w]++ > 0 && !warp_wait_far(&bar_o_free[w], (ni[w] - 2) & 1)) return false;
-      if (!warp_wait_far(&bar_p_full[buf], (nt[w] >> 1) & 1)) return false;
-      tc_fence_after();
-      // a k-step is 16 keys: 8 columns of P, 16 rows of V
-      mma4_bf16_tmem_a(tmem + Cfg::O_COL + w * D, tmem + buf * KT, 8u, dv0 + stage * (Cfg::V_TILE >> 4),
-                       static_cast<uint64_t>((16 * 128) >> 4), idesc, first ? 0u : 1u);
-      mma_commit(&bar_pv_done[buf]);
-      ++nt[w];
-      return true;
-    };
-    for (uint32_t k = 0; ok; ++k) {
-      if (!take_item(k)) { ok = false; break; }
-      const Item& it = *sItem(k);
-      if (!it.live) break;
-      const int32_t n = it.kt1 - it.kt0;
-      const bool two = TILES == 2 && it.tok0 + shape.tile_tok < it.n;
-      end_item(k);
-      for (int32_t j = 0; j < n; ++j) {
-        if (!warp_wait_far(&bar_v_full[stage], parity) || !pv(0, j == 0) || (two && !pv(1, j == 0))) { ok = false; break; }
-        mma_commit(&bar_v_empty[stage]);
-        if (++stage == VST) {
-          stage = 0;
-          parity ^= 1;
-        }
-      }
-    }
-    for (int w = 0; w < TILES; ++w)
-      for (uint32_t x = 1; x <= 2 && x <= nt[w]; ++x)
-        (void)mbar_wait_bounded(&bar_pv_done[2 * w + ((nt[w] - x) & 1)], ((nt[w] - x) >> 1) & 1);
+    for (int w = 0; w < 2; ++w)
+      if (nt[w] > 0) (void)mbar_wait_bounded(&bar_pv_done[w], (nt[w] - 1) & 1);
   } else {
     // ===================================================================== softmax warps
     const int w = warp >> 2;                   // tile
@@ -671,7 +690,9 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       // ---- the output of the item before, once its last PV has completed
       if (open) {
         open = false;
-        if (!warp_wait_far(&bar_pv_done[2 * w + ((nt - 1) & 1)], ((nt - 1) >> 1) & 1)) { ok = false; break; }
+        const int last_buf = TILES == 2 ? w : (kv - 1) & 1;
+        const uint32_t last_use = TILES == 2 ? nt - 1 : (kv - 1) >> 1;
+        if (!warp_wait_far(&bar_pv_done[last_buf], last_use & 1)) { ok = false; break; }
         tc_fence_after();
         const Item& was = *sItem(k - 1);
         const float inv = was.whole() ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
@@ -750,7 +771,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       m = kNoMax;
       l = 0.0f;
       for (int32_t j = 0; j < n; ++j, ++nt) {
-        const uint32_t buf = 2 * w + (nt & 1), uses = nt >> 1;
+        const int buf = TILES == 2 ? w : (kv + j) & 1;
+        const uint32_t uses = TILES == 2 ? nt : (kv + j) >> 1;
         const uint32_t tS = tmem + buf * KT + lane_base;
         const uint32_t slot = (kv + j) % INFO;
         if (!warp_wait_far(&bar_info[slot], ((kv + j) / INFO) & 1)) { ok = false; break; }
@@ -795,7 +817,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
           m = now;
           l *= alpha;
           if (j > 0) {
-            if (!warp_wait_far(&bar_pv_done[2 * w + ((nt - 1) & 1)], ((nt - 1) >> 1) & 1)) { ok = false; break; }
+            // (one tile: the PV before may still run; two: this QK was issued after it had completed)
+            if (TILES == 1 && !warp_wait_far(&bar_pv_done[(kv + j - 1) & 1], ((kv + j - 1) >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 8; ++c) {  // (8 columns at a time: the row's scores stay in registers)
@@ -807,22 +830,26 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
             }
           }
         }
-        uint32_t pw[32];
 #pragma unroll
-        for (int p = 0; p < PAGES; ++p) {
-          const float2 sc2 = make_float2(ks[p], ks[p]), m2 = make_float2(ev[p] - m, ev[p] - m);
-          float2 sum = make_float2(0.0f, 0.0f);
+        for (int h = 0; h < KT / 64; ++h) {
+          uint32_t pw[32];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = p * 16 + 2 * e;
-            const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, m2);
-            const float2 y = make_float2(ex2(x.x), ex2(x.y));
-            sum = fadd2(sum, y);
-            pw[p * 8 + e] = pack_f16x2(y.x, y.y);
+          for (int q = 0; q < 4; ++q) {
+            const int pg = 4 * h + q;
+            const float2 sc2 = make_float2(ks[pg], ks[pg]), m2 = make_float2(ev[pg] - m, ev[pg] - m);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int i = pg * 16 + 2 * e;
+              const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, m2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              sum = fadd2(sum, p);
+              pw[q * 8 + e] = pack_f16x2(p.x, p.y);
+            }
+            l = fmaf(sum.x + sum.y, info.unv[pg], l);
           }
-          l = fmaf(sum.x + sum.y, info.unv[p], l);
+          tmem_st32(tS + h * 32, pw);
         }
-        tmem_st32(tS, pw);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -837,7 +864,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == Cfg::QK_WARP)
+  if (warp == Cfg::MMA_WARP)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
