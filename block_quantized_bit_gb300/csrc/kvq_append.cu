@@ -8,12 +8,19 @@
 // query element or 1 B per key or value element (and its scales) out.
 //
 // append_rows_kernel: queries, and the keys and values of the kinds whose scale belongs to one row.  A thread owns 8
-// elements of a row (16 bytes), four lanes a block of 32; a CTA takes a token, so that its place, page and angles are
-// found once, and walks its rows.
+// elements of a row (16 bytes), four lanes a block of 32, and its partners' elements come from their lane where a row lies in
+// one warp (head_dim 64, 128, 256; otherwise from a second load).  A CTA takes up to 8 tokens, and finds their places, pages
+// and angles once, into shared memory, while its first rows are on their way; 3 or 4 rows a thread are in flight.  With
+// one row in flight and one token a CTA, four prompts of 400 to 2048 tokens with 128 heads of 576 (64 of them rotated) and
+// their latent rows took 666 us, eight turns of 500 to 4096 tokens with 32 + 2 x 8 heads of 128 197 us; now 385 us (4.9 of
+// the 6.8 TB/s that a copy reaches) and 121 us (3.8 TB/s, with the pages below).  What bounds it
+// now is the arithmetic between loads: without a rotation, 18400 x 32 heads of 128 go at 5.5 TB/s, with one at 4.2.
 // append_pages_kernel: KVQ_FP8_E4M3_PAGE.  A warp owns one (page, K or V, head): its scale is a power of two that only
 // grows, s = 2^e with the least e that lets every row stored since the page was opened fit (|x| <= 448 s), so a page that outgrows
 // its scale has its older codes multiplied by 2^(e_old - e_new): exact but for values that fall below E4M3's normal
-// range.  The rows are read twice, for the maximum and for the codes, the second time from L1.
+// range.  The page's new rows are read once, all loads in flight together, and stay in registers as they came; they are
+// turned twice, for the maximum and for the codes (kept turned they would take twice the registers).  18400 tokens x 2 x 8
+// heads of 128: 47 us, read twice from memory 58 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 8;  // tokens of a CTA at most
 
 __device__ __forceinline__ void append_report(const AppendArgs& a, uint32_t code) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the clearing kernel before this one has completed
@@ -71,15 +79,15 @@ __device__ __forceinline__ int32_t append_page(const AppendArgs& a, int32_t b, i
   return -1;
 }
 
-// The angles of row t, at place p of its sequence: cos of rot_dim / 2, then sin.
-__device__ __forceinline__ const float* append_angles(const AppendArgs& a, int32_t t, int32_t p) {
-  if (a.rot_dim == 0) return nullptr;
+// The position to which row t, at place p of its sequence, is rotated.
+__device__ __forceinline__ int32_t append_position(const AppendArgs& a, int32_t t, int32_t p) {
+  if (a.rot_dim == 0) return 0;
   int32_t at = a.positions ? __ldg(a.positions + t) : p;
   if (at < 0 || at >= a.max_position) {
     append_report(a, kStatusBadExtend);
     at = at < 0 ? 0 : a.max_position - 1;
   }
-  return a.cos_sin + static_cast<int64_t>(at) * a.rot_dim;
+  return at;
 }
 
 __device__ __forceinline__ void bf16x8(uint4 v, float (&x)[8]) {
@@ -91,10 +99,10 @@ __device__ __forceinline__ void bf16x8(uint4 v, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ void floats8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// Angles of a token in shared memory, rot_dim floats in quads.  Halves that pair: a thread takes two neighbouring quads of
+// the cosines and of the sines, so the even ones come first, which lets eight neighbouring threads read 128 bytes in a row.
+__device__ __forceinline__ int32_t quad_place(const AppendArgs& a, int32_t quad) {
+  return a.interleaved ? quad : (quad & 1) * (a.rot_dim / 8) + (quad >> 1);
 }
 
 // Where a thread's 8 elements from `e` on lie in the rotation, and their cos and sin (of 4 pairs when neighbours pair).
@@ -110,17 +118,21 @@ struct Turn {
   }
   __device__ __forceinline__ void angles(const AppendArgs& a, const float* row, int32_t e) {
     if (!on) return;
-    const int32_t half = a.rot_dim / 2;
+    const float4* p = reinterpret_cast<const float4*>(row);
+    const int32_t half = a.rot_dim / 2, j = e - a.rot_offset;
     if (a.interleaved) {
-      const float* p = row + (e - a.rot_offset) / 2;
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p + half));
-      c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
-      s[0] = y.x; s[1] = y.y; s[2] = y.z; s[3] = y.w;
+      four(p[j / 8], c);
+      four(p[j / 8 + half / 4], s);
     } else {
-      const float* p = row + (e - a.rot_offset) - (low ? 0 : half);
-      floats8(p, c);
-      floats8(p + half, s);
+      const int32_t q = (low ? j : j - half) / 8, odd = a.rot_dim / 8;  // quads 2 q and 2 q + 1, then half / 4 further
+      four(p[q], c);
+      four(p[q + odd], c + 4);
+      four(p[q + half / 8], s);
+      four(p[q + half / 8 + odd], s + 4);
     }
+  }
+  __device__ __forceinline__ static void four(float4 v, float* x) {
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   }
   // x: the thread's elements, y: their partners
   __device__ __forceinline__ void apply(float (&x)[8], const float (&y)[8]) const {
@@ -185,77 +197,163 @@ __device__ __forceinline__ uint2 block_codes(float (&x)[8], __half& scale) {
   }
 }
 
-// The rows of token t, from row r0 on `step` at a time: first the queries' heads, then (KIND != KVQ_FP8_E4M3_PAGE) the
-// keys' and the values'.  All threads of the CTA call it; thread i of a row's D / 8 takes its elements 8 i ...
-template <int KIND>
-__device__ __forceinline__ void append_rows(const AppendArgs& a, int32_t t, int32_t r0, int32_t step) {
+// What a CTA finds out about its tokens before it turns their rows.
+struct Tokens {
+  int32_t seq[kTokens], page[kTokens], off[kTokens], angle[kTokens];
+};
+
+// The rows of tokens t0 ... (nt of them): the CTA takes as many rows at once as its threads hold, passes of queries' heads
+// first, then (KIND != KVQ_FP8_E4M3_PAGE) of the keys' and the values', every row_chunks-th pass of a token from `chunk`
+// on.  All threads of the CTA call it; thread i of a row's D / 8 takes its elements 8 i ...  SHFL: a row's threads lie in one
+// warp, and a thread gets its partners' elements from there.  `turns`: shared memory for the tokens' angles.
+template <int KIND, bool SHFL>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, int32_t t0, int32_t nt, int32_t chunk, Tokens& tok,
+                                            float* turns) {
   constexpr bool kQuant = KIND != KVQ_FP8_E4M3_PAGE;
-  const int32_t b = append_find(
-      a, [&](int32_t, int32_t q0, int32_t n, int32_t) { return t >= q0 && t - q0 < n; });
-  if (b >= a.batch) return;
-  int32_t q0, n, len;
-  append_sequence(a, b, q0, n, len);
-  const int32_t place = len - n + (t - q0);
+  constexpr int U = SHFL ? 4 : 3;  // passes whose loads are in flight together
   const int32_t per_row = a.head_dim / 8, lanes = kThreads / per_row;
   const int32_t i = threadIdx.x % per_row, slot = threadIdx.x / per_row, e = i * 8;
-  const int32_t rows = a.num_q_heads + (kQuant ? a.n_kv * a.num_kv_heads : 0);
+  const int32_t kv_rows = kQuant ? a.n_kv * a.num_kv_heads : 0;
+  const int32_t q_passes = (a.num_q_heads + lanes - 1) / lanes, passes = q_passes + (kv_rows + lanes - 1) / lanes;
   Turn turn;
   turn.place(a, e);
-  const float* angles = append_angles(a, t, place);
-  if (angles) turn.angles(a, angles, e);
-  else turn.on = false;
-  int32_t page = -1, off = 0;
-  if (kQuant) {
-    page = append_page(a, b, place / a.page_size);
-    off = place % a.page_size;
-  }
-  for (int32_t base = r0; base < rows; base += step) {
-    const int32_t r = base + slot;
-    const bool live = slot < lanes && r < rows;
-    const bool is_q = r < a.num_q_heads;
-    const int32_t kv = is_q || r - a.num_q_heads < a.num_kv_heads ? 0 : 1;
-    const int32_t h = is_q ? r : r - a.num_q_heads - kv * a.num_kv_heads;
-    float x[8];
-    if (live) {
-      const uint16_t* row = is_q   ? a.q + t * a.q_token + h * a.q_head
-                            : kv == 0 ? a.k + t * a.k_token + h * a.k_head
-                                      : a.v + t * a.v_token + h * a.v_head;
-      bf16x8(__ldg(reinterpret_cast<const uint4*>(row + e)), x);
-      if (kv == 0 && turn.on) {
-        float y[8];
-        if (turn.partner != 0) bf16x8(__ldg(reinterpret_cast<const uint4*>(row + e + turn.partner)), y);
-        turn.apply(x, y);
+  uint4 raw[U], other[SHFL ? 1 : U];
+  struct Cursor {
+    int32_t k, p;  // token, pass
+    __device__ __forceinline__ void next(int32_t chunk, int32_t by, int32_t passes) {
+      p += by;
+      if (p >= passes) {
+        p = chunk;
+        ++k;
       }
-    } else {
+    }
+  };
+  auto load = [&](Cursor c) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    for (int u = 0; u < U; ++u) {
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (!SHFL) other[u] = raw[u];
+      if (c.k < nt) {
+        const int64_t t = t0 + c.k;
+        const uint16_t* row = nullptr;
+        bool turns_too = true;
+        if (c.p < q_passes) {
+          const int32_t h = c.p * lanes + slot;
+          if (h < a.num_q_heads) row = a.q + t * a.q_token + h * a.q_head;
+        } else if (kQuant) {
+          const int32_t r = (c.p - q_passes) * lanes + slot;
+          turns_too = r < a.num_kv_heads;
+          if (r < kv_rows)
+            row = turns_too ? a.k + t * a.k_token + r * a.k_head : a.v + t * a.v_token + (r - a.num_kv_heads) * a.v_head;
+        }
+        if (row != nullptr && slot < lanes) {
+          // (plain loads: the queries may be turned where they lie, and these stay before the barrier below)
+          raw[u] = *reinterpret_cast<const uint4*>(row + e);
+          if constexpr (!SHFL)
+            if (turns_too && turn.partner != 0) other[u] = *reinterpret_cast<const uint4*>(row + e + turn.partner);
+        }
+      }
+      c.next(chunk, a.row_chunks, passes);
     }
-    if (a.q_out == a.q) __syncthreads();  // (a thread's partners have been read before they are overwritten)
-    if (live && is_q) {
-      uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                           pack_bf16x2(x[6], x[7]));
-      *reinterpret_cast<uint4*>(a.q_out + t * a.out_token + h * a.out_head + e) = o;
-    }
-    if constexpr (kQuant) {
-      __half scale;
-      const uint2 c = block_codes<KIND>(x, scale);
-      if (live && !is_q && page >= 0) {
-        const int64_t row = ((static_cast<int64_t>(page) * a.n_kv + kv) * a.num_kv_heads + h) * a.page_size + off;
-        *reinterpret_cast<uint2*>(a.codes + row * a.head_dim + e) = c;
-        if (KindTraits<KIND>::kScaled && i % 4 == 0)
-          static_cast<__half*>(a.scales)[row * (a.head_dim / kBlock) + i / 4] = scale;
+  };
+  Cursor at = {0, chunk};
+  load(at);
+  // ---- meanwhile: the tokens' sequences, pages and angles
+  if (threadIdx.x < kTokens) tok.seq[threadIdx.x] = a.batch;
+  __syncthreads();
+  for (int32_t b = threadIdx.x; b < a.batch; b += kThreads) {
+    int32_t q0, n, len;
+    if (!append_sequence(a, b, q0, n, len)) continue;
+    for (int32_t k = max(q0 - t0, 0); k < min(q0 + n - t0, nt); ++k) atomicMin(&tok.seq[k], b);
+  }
+  __syncthreads();
+  if (threadIdx.x < nt) {
+    const int32_t k = threadIdx.x, b = tok.seq[k];
+    if (b < a.batch) {
+      int32_t q0, n, len;
+      append_sequence(a, b, q0, n, len);
+      const int32_t place = len - n + (t0 + k - q0);
+      tok.angle[k] = append_position(a, t0 + k, place);
+      if (kQuant) {
+        tok.page[k] = append_page(a, b, place / a.page_size);
+        tok.off[k] = place % a.page_size;
       }
     }
+  }
+  __syncthreads();
+  const int32_t quads = a.rot_dim / 4;
+  for (int32_t x = threadIdx.x; x < nt * quads; x += kThreads) {
+    const int32_t k = x / quads;
+    if (tok.seq[k] < a.batch)
+      reinterpret_cast<float4*>(turns)[k * quads + quad_place(a, x - k * quads)] =
+          __ldg(reinterpret_cast<const float4*>(a.cos_sin + static_cast<int64_t>(tok.angle[k]) * a.rot_dim) + (x - k * quads));
+  }
+  __syncthreads();
+  // ---- the rows
+  auto turned = [&](int u, int32_t k, float (&x)[8]) {
+    if (turn.on) {
+      float y[8];
+      if constexpr (SHFL) bf16x8(raw[u], y);  // (exchanged below)
+      else bf16x8(other[u], y);
+      turn.angles(a, turns + k * a.rot_dim, e);
+      turn.apply(x, y);
+    }
+  };
+  while (at.k < nt) {
+    if (!SHFL && a.q_out == a.q) __syncthreads();  // (a thread's partners have been read before they are overwritten)
+    Cursor c = at;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c.k >= nt) break;  // (the same for the whole CTA)
+      const bool known = tok.seq[c.k] < a.batch;
+      float x[8];
+      bf16x8(raw[u], x);
+      const uint4 own = raw[u];
+      if constexpr (SHFL) {
+        if (a.rot_dim > 0) {
+          const int from = (threadIdx.x & 31) + turn.partner / 8;
+          raw[u] = make_uint4(__shfl_sync(0xffffffffu, own.x, from), __shfl_sync(0xffffffffu, own.y, from),
+                              __shfl_sync(0xffffffffu, own.z, from), __shfl_sync(0xffffffffu, own.w, from));
+        }
+      }
+      if (c.p < q_passes) {
+        const int32_t h = c.p * lanes + slot;
+        turned(u, c.k, x);
+        if (known && slot < lanes && h < a.num_q_heads) {
+          const uint4 o = turn.on ? make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                               pack_bf16x2(x[6], x[7]))
+                                  : own;
+          *reinterpret_cast<uint4*>(a.q_out + static_cast<int64_t>(t0 + c.k) * a.out_token + h * a.out_head + e) = o;
+        }
+      } else if constexpr (kQuant) {
+        const int32_t r = (c.p - q_passes) * lanes + slot;
+        if (r < a.num_kv_heads) turned(u, c.k, x);
+        __half scale;
+        const uint2 code = block_codes<KIND>(x, scale);
+        if (known && slot < lanes && r < kv_rows && tok.page[c.k] >= 0) {
+          const int32_t kv = r < a.num_kv_heads ? 0 : 1;
+          const int64_t row = ((static_cast<int64_t>(tok.page[c.k]) * a.n_kv + kv) * a.num_kv_heads + r - kv * a.num_kv_heads) *
+                                  a.page_size + tok.off[c.k];
+          *reinterpret_cast<uint2*>(a.codes + row * a.head_dim + e) = code;
+          if (KindTraits<KIND>::kScaled && i % 4 == 0)
+            static_cast<__half*>(a.scales)[row * (a.head_dim / kBlock) + i / 4] = scale;
+        }
+      }
+      c.next(chunk, a.row_chunks, passes);
+    }
+    at = c;
+    if (at.k < nt) load(at);
   }
 }
 
-// grid: (token, row chunk), row chunks fastest
-template <int KIND>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs a) {
+// grid: (tokens, row chunk), row chunks fastest
+template <int KIND, bool SHFL>
+__global__ void __launch_bounds__(kThreads, 4) append_rows_kernel(const AppendArgs a) {
+  extern __shared__ __align__(16) float turns[];
+  __shared__ Tokens tok;
   if (blockIdx.x == 0) append_check(a);
-  const int32_t lanes = kThreads / (a.head_dim / 8);
-  const int32_t t = blockIdx.x / a.row_chunks, chunk = blockIdx.x % a.row_chunks;
-  append_rows<KIND>(a, t, chunk * lanes, a.row_chunks * lanes);
+  const int32_t t = blockIdx.x / a.row_chunks * a.tokens;
+  append_rows<KIND, SHFL>(a, t, min(a.tokens, a.total - t), blockIdx.x % a.row_chunks, tok, turns);
 }
 
 // The least e with m <= 448 * 2^e (448 = 1.75 * 2^8), within the exponents that a page's scale may have.
@@ -273,15 +371,18 @@ __device__ __forceinline__ int64_t pages_before(int32_t b, int32_t q0) {
   return (static_cast<int64_t>(q0) + 14LL * b) / kPage + b;
 }
 
-// grid: (page, chunk of its 2 * heads parts) first, then (token, row chunk) of the queries
+// grid: (page, chunk of its 2 * heads parts) first, then (tokens, row chunk) of the queries
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_pages_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) append_pages_kernel(const AppendArgs a) {
   constexpr int PER_ROW = D / 8;               // threads of a row
   constexpr int ROWS = 32 / PER_ROW;           // rows of a pass
+  constexpr int PASSES = kPage / ROWS;
+  extern __shared__ __align__(16) float turns[];
+  __shared__ Tokens tok;
   if (blockIdx.x == 0) append_check(a);
   if (blockIdx.x >= a.page_ctas) {
-    const int32_t lanes = kThreads / PER_ROW, q = blockIdx.x - a.page_ctas;
-    append_rows<KVQ_FP8_E4M3_PAGE>(a, q / a.row_chunks, q % a.row_chunks * lanes, a.row_chunks * lanes);
+    const int32_t q = blockIdx.x - a.page_ctas, t = q / a.row_chunks * a.tokens;
+    append_rows<KVQ_FP8_E4M3_PAGE, true>(a, t, min(a.tokens, a.total - t), q % a.row_chunks, tok, turns);
     return;
   }
   const int32_t item = blockIdx.x / a.part_chunks, chunk = blockIdx.x % a.part_chunks;
@@ -295,39 +396,69 @@ __global__ void __launch_bounds__(kThreads) append_pages_kernel(const AppendArgs
   int32_t q0, n, len;
   append_sequence(a, b, q0, n, len);
   const int32_t j = static_cast<int32_t>(item - pages_before(b, q0)) + (len - n) / kPage;
-  const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t part = chunk * kWarps + warp;
-  if (part >= 2 * a.num_kv_heads) return;
   const int32_t page = append_page(a, b, j);
   if (page < 0) return;
-  const int32_t kv = part / a.num_kv_heads, h = part - kv * a.num_kv_heads;
   const int32_t lo = max(len - n - j * kPage, 0), hi = min(len - j * kPage, kPage);  // new rows of the page
+  const int32_t t0 = q0 + j * kPage - (len - n);                                     // row r of it is the call's row t0 + r
+  const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t part = chunk * kWarps + warp, parts = 2 * a.num_kv_heads;
+  const int32_t kv = part / a.num_kv_heads, h = part - kv * a.num_kv_heads;
   const int32_t e = lane % PER_ROW * 8, sub = lane / PER_ROW;
+  // ---- the new rows, all loads at once
+  uint4 raw[PASSES];
+#pragma unroll
+  for (int x = 0; x < PASSES; ++x) {
+    const int32_t r = x * ROWS + sub;
+    const int64_t t = t0 + r;
+    raw[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (part < parts && r >= lo && r < hi)
+      raw[x] = __ldg(reinterpret_cast<const uint4*>(
+          (kv == 0 ? a.k + t * a.k_token + h * a.k_head : a.v + t * a.v_token + h * a.v_head) + e));
+  }
+  // ---- meanwhile their angles
+  if (a.rot_dim > 0 && chunk * kWarps < a.num_kv_heads) {
+    const int32_t quads = a.rot_dim / 4;
+    for (int32_t x = threadIdx.x; x < kPage * quads; x += kThreads) {
+      const int32_t r = x / quads;
+      if (r >= lo && r < hi)
+        reinterpret_cast<float4*>(turns)[r * quads + quad_place(a, x - r * quads)] = __ldg(
+            reinterpret_cast<const float4*>(a.cos_sin + static_cast<int64_t>(append_position(a, t0 + r, j * kPage + r)) * a.rot_dim) +
+            (x - r * quads));
+    }
+    __syncthreads();
+  }
+  if (part >= parts) return;
   const int64_t row0 = (static_cast<int64_t>(page) * 2 + kv) * a.num_kv_heads + h;
   uint8_t* codes = a.codes + row0 * kPage * D + e;
   float* scale = static_cast<float*>(a.scales) + row0;
 
   Turn turn;
   turn.place(a, e);
-  turn.on &= kv == 0 && a.rot_dim > 0;
-  auto load = [&](int32_t r, float (&x)[8]) {  // row r of the page
-    const int32_t p = j * kPage + r, t = q0 + p - (len - n);
-    const uint16_t* row = kv == 0 ? a.k + t * a.k_token + h * a.k_head : a.v + t * a.v_token + h * a.v_head;
-    bf16x8(__ldg(reinterpret_cast<const uint4*>(row + e)), x);
-    if (turn.on) {
-      turn.angles(a, append_angles(a, t, p), e);
-      float y[8];
-      if (turn.partner != 0) bf16x8(__ldg(reinterpret_cast<const uint4*>(row + e + turn.partner)), y);
-      turn.apply(x, y);
+  const bool turns_too = kv == 0 && a.rot_dim > 0;  // (the same for the whole warp)
+  auto value = [&](int pass, float (&x)[8]) {  // the thread's elements of row pass * ROWS + sub
+    const uint4 own = raw[pass];
+    bf16x8(own, x);
+    if (turns_too) {
+      const int from = lane + turn.partner / 8;
+      const uint4 other = make_uint4(__shfl_sync(0xffffffffu, own.x, from), __shfl_sync(0xffffffffu, own.y, from),
+                                     __shfl_sync(0xffffffffu, own.z, from), __shfl_sync(0xffffffffu, own.w, from));
+      const int32_t r = pass * ROWS + sub;
+      if (turn.on && r >= lo && r < hi) {
+        float y[8];
+        bf16x8(other, y);
+        turn.angles(a, turns + r * a.rot_dim, e);
+        turn.apply(x, y);
+      }
     }
   };
   const float had = lo > 0 ? *scale : 0.0f;
   float m = 0.0f;
-#pragma unroll 4
-  for (int32_t r = lo + sub; r < hi; r += ROWS) {
-    float x[8];
-    load(r, x);
-    m = fmaxf(m, amax8(x));
+#pragma unroll
+  for (int x = 0; x < PASSES; ++x) {
+    if (x * ROWS + ROWS <= lo || x * ROWS >= hi) continue;  // (the same for the whole warp)
+    float y[8];
+    value(x, y);
+    m = fmaxf(m, amax8(y));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -336,7 +467,6 @@ __global__ void __launch_bounds__(kThreads) append_pages_kernel(const AppendArgs
     const int32_t old = min(max(((__float_as_int(had) >> 23) & 255) - 127, kPageScaleMin), kPageScaleMax);
     if (exp > old) {
       const float f = power_of_two(old - exp);
-#pragma unroll 4
       for (int32_t r = sub; r < lo; r += ROWS) {
         const uint2 c = *reinterpret_cast<const uint2*>(codes + r * D);
         uint32_t w[4];
@@ -354,13 +484,16 @@ __global__ void __launch_bounds__(kThreads) append_pages_kernel(const AppendArgs
     exp = max(exp, old);
   }
   const float inv = power_of_two(-exp);
-#pragma unroll 4
-  for (int32_t r = lo + sub; r < hi; r += ROWS) {
-    float x[8];
-    load(r, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv;
-    *reinterpret_cast<uint2*>(codes + r * D) = fp8x8<__NV_E4M3>(x);
+  for (int x = 0; x < PASSES; ++x) {
+    const int32_t r = x * ROWS + sub;
+    if (x * ROWS + ROWS <= lo || x * ROWS >= hi) continue;
+    asm volatile("" : "+r"(raw[x].x), "+r"(raw[x].y), "+r"(raw[x].z), "+r"(raw[x].w));  // (turned again: registers are scarcer)
+    float y[8];
+    value(x, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] *= inv;
+    if (r >= lo && r < hi) *reinterpret_cast<uint2*>(codes + r * D) = fp8x8<__NV_E4M3>(y);
   }
   if (lane == 0) *scale = power_of_two(exp);
 }
@@ -378,6 +511,7 @@ kvq_status launch(Kernel kern, const AppendArgs& a, int64_t grid, cudaStream_t s
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = std::max(a.tokens, a.page_ctas > 0 ? kPage : 0) * a.rot_dim * sizeof(float);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -397,23 +531,31 @@ bool append_supported(int32_t head_dim, kvq_kind kind) {
 int64_t append_grid(AppendArgs* a, int32_t sms) {
   const int32_t lanes = kThreads / (a->head_dim / 8);
   const bool pages = a->kind == KVQ_FP8_E4M3_PAGE;
-  const int32_t rows = a->num_q_heads + (pages ? 0 : a->n_kv * a->num_kv_heads);
-  const int32_t passes = (rows + lanes - 1) / lanes;
+  const int32_t kv_rows = pages ? 0 : a->n_kv * a->num_kv_heads, rows = a->num_q_heads + kv_rows;
+  const int32_t passes = (a->num_q_heads + lanes - 1) / lanes + (kv_rows + lanes - 1) / lanes;
   // a token's rows are spread over CTAs while these would not fill the GPU
   a->row_chunks = static_cast<int32_t>(
       std::max<int64_t>(1, std::min<int64_t>(passes, 4LL * sms / std::max(1, a->total))));
+  // ... and several tokens are one CTA's when there are many, which then looks for their sequences but once
+  const int64_t room = a->rot_dim > 0 ? std::max(1, 16384 / (a->rot_dim * 4)) : kTokens;  // angles in shared memory
+  a->tokens = static_cast<int32_t>(
+      std::max<int64_t>(1, std::min<int64_t>({kTokens, room, a->total / (8LL * sms), 64 / std::max(passes, 1)})));
   a->part_chunks = (2 * a->num_kv_heads + kWarps - 1) / kWarps;
   const int64_t items = pages ? (static_cast<int64_t>(a->total) + 14LL * a->batch) / kPage + a->batch : 0;
   a->page_ctas = items * a->part_chunks;
-  return a->page_ctas + (rows > 0 ? static_cast<int64_t>(a->total) * a->row_chunks : 0);
+  return a->page_ctas + (rows > 0 ? (static_cast<int64_t>(a->total) + a->tokens - 1) / a->tokens * a->row_chunks : 0);
 }
 
 kvq_status launch_append(const AppendArgs& a, int64_t grid, cudaStream_t stream) {
+  const bool shfl = a.head_dim == 64 || a.head_dim == 128 || a.head_dim == 256;  // rows lie in one warp
   switch (a.kind) {
-    case KVQ_FP8_E4M3: return launch(append_rows_kernel<KVQ_FP8_E4M3>, a, grid, stream);
-    case KVQ_Q8_0: return launch(append_rows_kernel<KVQ_Q8_0>, a, grid, stream);
-    case KVQ_FP8_E4M3_UNSCALED: return launch(append_rows_kernel<KVQ_FP8_E4M3_UNSCALED>, a, grid, stream);
-    case KVQ_FP8_E5M2_UNSCALED: return launch(append_rows_kernel<KVQ_FP8_E5M2_UNSCALED>, a, grid, stream);
+#define KVQ_APPEND_ROWS(K) \
+  case K: return shfl ? launch(append_rows_kernel<K, true>, a, grid, stream) : launch(append_rows_kernel<K, false>, a, grid, stream);
+    KVQ_APPEND_ROWS(KVQ_FP8_E4M3)
+    KVQ_APPEND_ROWS(KVQ_Q8_0)
+    KVQ_APPEND_ROWS(KVQ_FP8_E4M3_UNSCALED)
+    KVQ_APPEND_ROWS(KVQ_FP8_E5M2_UNSCALED)
+#undef KVQ_APPEND_ROWS
     case KVQ_FP8_E4M3_PAGE:
       if (a.head_dim == 64) return launch(append_pages_kernel<64>, a, grid, stream);
       if (a.head_dim == 128) return launch(append_pages_kernel<128>, a, grid, stream);

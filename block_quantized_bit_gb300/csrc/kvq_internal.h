@@ -222,6 +222,7 @@ struct AppendArgs {
   int32_t max_pages, batch, total, num_q_heads, num_kv_heads, n_kv, head_dim, page_size;
   int32_t max_position, rot_dim, rot_offset, interleaved;  // rot_dim 0: no rotation
   int32_t row_chunks, part_chunks;                         // CTAs of one token, of one page (append_grid)
+  int32_t tokens;                                          // tokens of one CTA (append_grid)
   kvq_kind kind;
 };
 // Exponents that the power of two of a KVQ_FP8_E4M3_PAGE page may have: codes from 2^-41 to 448 * 2^32.
