@@ -394,7 +394,7 @@ bool plan_tree(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
 // with it the CTAs (0: no cap).
 struct PagePlan {
   bool flash;  // the kernel for many query rows
-  int32_t grid;
+  int32_t grid, tile;
   size_t ml_offset, acc_offset, total;
 };
 
@@ -406,14 +406,14 @@ bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   // a tile of the rows kernel holds a sequence's rows of a kv head, or the flash kernel takes them
   const double rows = static_cast<double>(total_q) * (num_q_heads / L.num_kv_heads);
   pp->flash = total_q > batch && rows > static_cast<double>(kPageRowsTile) * batch;
-  const int32_t tile = pp->flash ? page_flash_rows(L.head_dim) : kPageRowsTile;
+  const int32_t tile = pp->tile = pp->flash ? page_flash_rows(L.head_dim) : rows <= 8.0 * batch ? 8 : kPageRowsTile;
   const int32_t least = pp->flash ? kPageFlashUnits : kPageMinUnits;
   const size_t slot = tile * (static_cast<size_t>(L.head_dim) + 2) * sizeof(float);
   // units of work at most: pages of tiles of 16 rows, or tiles of 64 keys or more of items (of half their rows at least)
   const double tiles = batch + rows / (pp->flash ? tile / 4 : tile) + (pp->flash ? total_q : 0);
-  const double units = tiles * L.num_kv_heads * (pp->flash ? max_pages / 4 + 1.0 : max_pages);
+  const double units = tiles * L.num_kv_heads * (pp->flash ? max_pages / 4 + 1.0 + kPageItemUnits : max_pages);
   if (units > 1e14) return false;  // (units times CTAs are counted in 64 bits)
-  int64_t grid = pp->flash ? sm_count() : page_rows_grid(L.head_dim, sm_count());
+  int64_t grid = pp->flash ? sm_count() : page_rows_grid(L.head_dim, tile, sm_count());
   if (units < static_cast<double>(grid) * least) grid = static_cast<int64_t>(units / least) + 1;
   if (max_bytes > 0) {
     if (max_bytes < kWorkspaceHeader + 1024) return false;
@@ -472,6 +472,7 @@ kvq_status page_common(const void* q, const void* pool, const void* scales, cons
   a.num_kv_heads = layout->num_kv_heads;
   a.head_dim = layout->head_dim;
   a.grid = pp.grid;
+  a.tile = pp.tile;
   a.score_scale = sm_scale * 1.4426950408889634f;  // log2(e)
   a.out_dtype = out_dtype;
   return pp.flash ? launch_page_flash(a, s) : launch_page_rows(a, s);

@@ -164,6 +164,7 @@ struct TreeArgs {
   int32_t head_dim;
   int32_t mask_words;
   int32_t grid;               // CTAs launched
+  int32_t tile;               // query rows of a unit of work
   float score_scale;          // sm_scale * log2(e)
   kvq_out_dtype out_dtype;
   kvq_kind kind;
@@ -243,20 +244,22 @@ struct PageArgs {
   uint32_t* status;
   int64_t* total;             // the call's units
   void* runs;                 // [grid] of kPageRunBytes: each CTA's first run
-  float* part_acc;            // [2 * grid][rows][head_dim], rows: kPageRowsTile or page_flash_rows()
+  float* part_acc;            // [2 * grid][rows][head_dim], rows: tile
   float* part_ml;             // [2 * grid][rows][2]
   int64_t num_pages;
   int32_t max_pages, batch, total_q, num_q_heads, num_kv_heads, head_dim;
   int32_t grid;               // CTAs launched
+  int32_t tile;               // query rows of a unit of work
   float score_scale;          // sm_scale * log2(e)
   kvq_out_dtype out_dtype;
 };
-constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel
+constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel at most (8 or 16)
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
 constexpr int kPageRunBytes = 64;
-constexpr int kPageFlashUnits = 4; // key tiles that are worth a CTA of the flash kernel
+constexpr int kPageItemUnits = 6;   // key tiles' time that an item's start and end take
+constexpr int kPageFlashUnits = 10; // units (key tiles and items' starts) that are worth a CTA of the flash kernel
 bool page_supported(int32_t head_dim);
-int32_t page_rows_grid(int32_t head_dim, int32_t sms);  // CTAs that are resident at once
+int32_t page_rows_grid(int32_t head_dim, int32_t tile, int32_t sms);  // CTAs that are resident at once
 kvq_status launch_page_rows(const PageArgs& a, cudaStream_t stream);
 int32_t page_flash_rows(int32_t head_dim);  // query rows of an item of the flash kernel
 kvq_status launch_page_flash(const PageArgs& a, cudaStream_t stream);

@@ -12,6 +12,34 @@ constexpr float kNoMax = -1e30f;  // reference of a row that has seen nothing
 constexpr float kHead = 7.0f;     // log2 of the largest p when a row's reference moves ...
 constexpr float kLimit = 15.0f;   // ... and at most (P is f16, which ends at 2^16)
 
+// Clears the status word.  The attention is its programmatic dependent: it reads what was there before this kernel, so it
+// starts at once, and touches the word only after a wait; its first CTA waits in any case, so that its end is both's.
+__global__ void page_clear_kernel(uint32_t* word) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) *word = 0;
+}
+__device__ __forceinline__ void page_cleared() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void page_report(const PageArgs& a, uint32_t code) {
+  page_cleared();
+  set_status(a.status, code);
+}
+
+// A kernel that may start before the one in front of it in the stream has ended.
+template <typename Kernel, typename... Args>
+bool launch_dependent(Kernel kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
 // One sequence's query rows and stored tokens; n = 0: nothing to do.
 struct PageSeq {
   int32_t q0, n, len;

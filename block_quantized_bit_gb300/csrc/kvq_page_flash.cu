@@ -131,14 +131,15 @@ struct Shape {
     const int64_t last = s.len - s.n + min(static_cast<int64_t>(s.n), static_cast<int64_t>(p + 1) * item_tok);
     return static_cast<int32_t>((last + Cfg::KT - 1) / Cfg::KT);
   }
-  // key tiles of the items before p (p < items: all of these have item_tok tokens)
+  // units of the items before p (p < items: all of these have item_tok tokens): their key tiles, and a start for each
   __device__ __forceinline__ int64_t before(const PageSeq& s, int32_t p) const {
-    return floor_sum(p, Cfg::KT, item_tok, static_cast<int64_t>(s.len - s.n) + item_tok + Cfg::KT - 1);
+    return floor_sum(p, Cfg::KT, item_tok, static_cast<int64_t>(s.len - s.n) + item_tok + Cfg::KT - 1) +
+           static_cast<int64_t>(p) * kPageItemUnits;
   }
   __device__ __forceinline__ int64_t per_group(const PageSeq& s) const {
     if (s.n == 0) return 0;
     const int32_t p = items(s) - 1;
-    return before(s, p) + key_tiles(s, p);
+    return before(s, p) + kPageItemUnits + key_tiles(s, p);
   }
   __device__ __forceinline__ int64_t units(const PageArgs& a, const PageSeq& s) const {
     return per_group(s) * groups * a.num_kv_heads;
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const int32_t C = sharers(U, a.grid, kPageFlashUnits);
         return cta < C && U > 0 ? first_unit(U, C, cta) : U;
       });
-  if (cta == 0 && bad) set_status(a.status, kStatusBadExtend);
+  if (cta == 0) page_cleared();
+  if (cta == 0 && bad) page_report(a, kStatusBadExtend);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     const int32_t C = sharers(place.total, a.grid, kPageFlashUnits);
     int64_t u = place.b < 0 ? 0 : first_unit(place.total, C, cta);
     const int64_t u_end = place.b < 0 ? 0 : first_unit(place.total, C, cta + 1);
-    int32_t b = place.b, group = 0, p = 0, at = 0;  // the next item, and its key tiles before the run
+    int32_t b = place.b, group = 0, p = 0, at = 0;  // the next item, and its units before the run
     PageSeq s = {0, 0, 0};
     if (u < u_end) {
       s = page_sequence(a, b, bad);
@@ -337,10 +339,10 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     uint32_t kv = 0, kc = 0, vc = 0;  // key tiles; K and V stages that hold copies
     for (uint32_t k = 0; ok; ++k) {
       Item it;
-      it.live = u < u_end;
+      it.live = u < u_end && at + (u_end - u) > kPageItemUnits;  // (a run that ends in an item's start leaves it to the next)
       int32_t g = 0;
       if (it.live) {
-        it.first = u - at;
+        it.first = u - at + kPageItemUnits;
         it.q0 = s.q0;
         it.n = s.n;
         it.len = s.len;
@@ -350,13 +352,13 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         it.heads = min(shape.heads, shape.G - part * shape.heads);
         it.tok0 = p * shape.item_tok;
         it.per_head = (65536u + it.heads - 1) / it.heads;
-        it.kt0 = at;
+        it.kt0 = max(at - kPageItemUnits, 0);
         it.all = shape.key_tiles(s, p);
-        it.kt1 = static_cast<int32_t>(min(static_cast<int64_t>(it.all), at + (u_end - u)));
+        it.kt1 = static_cast<int32_t>(min(static_cast<int64_t>(it.all), at + (u_end - u) - kPageItemUnits));
       }
       if (k == 0 && lane == 0) {
         Item x = it;
-        x.live &= at > 0;
+        x.live = it.live && it.kt0 > 0;
         static_cast<Item*>(a.runs)[cta] = x;
       }
       if (k >= ITEMS && !warp_wait_far(&bar_item_free[k % ITEMS], (k / ITEMS - 1) & 1)) { ok = false; break; }
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         if (i >= np) return -1;
         const int32_t x = __ldg(table + i);
         if (x < a.num_pages) return x;
-        set_status(a.status, kStatusBadPage);
+        page_report(a, kStatusBadPage);
         return -1;
       };
       auto scales = [&](int32_t x, float& ks, float& vs) {
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         __syncwarp();
       }
       if (!ok) break;
-      u += it.kt1 - it.kt0;
+      u += kPageItemUnits + it.kt1 - at;
       at = 0;
       if (u < u_end && ++p == shape.items(s)) {  // (a run that ends inside an item is the CTA's last)
         p = 0;
@@ -860,7 +862,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       open = true;
     }
   }
-  if (!ok) set_status(a.status, kStatusTimeout);
+  if (!ok) page_report(a, kStatusTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -924,20 +926,12 @@ kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
   if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
   auto kern = page_flash_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess) return KVQ_ECUDA;
-  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream) != cudaSuccess) return KVQ_ECUDA;
-  kern<<<a.grid, Cfg::THREADS, Cfg::SMEM, stream>>>(a, map);
+  page_clear_kernel<<<1, 32, 0, stream>>>(a.status);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
+  if (!launch_dependent(kern, dim3(a.grid), Cfg::THREADS, Cfg::SMEM, stream, a, map)) return KVQ_ECUDA;
   if (a.grid == 1) return KVQ_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid - 1, Cfg::TILES * kM / kJoinWarps);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, page_flash_join_kernel<D>, a) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  const dim3 joins(a.grid - 1, Cfg::TILES * kM / kJoinWarps);
+  return launch_dependent(page_flash_join_kernel<D>, joins, kJoinWarps * 32, 0, stream, a) ? KVQ_OK : KVQ_ECUDA;
 }
 
 }  // namespace

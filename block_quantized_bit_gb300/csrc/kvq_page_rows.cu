@@ -28,25 +28,26 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kPageRowsTile;   // query rows of a tile
-
-template <int D>
+// NT: the tile's query rows in groups of 8.
+template <int D, int NT>
 struct RCfg {
+  static constexpr int ROWS = 8 * NT;                  // query rows of a tile
+  static constexpr int WARPS = D == 256 ? 4 : 8;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int CTAS = D == 64 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2;  // resident per SM
   static constexpr int PAGE_BYTES = kPage * D;         // codes of K or V of a page
   static constexpr int STAGE = 2 * PAGE_BYTES;
-  static constexpr int STAGES = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int STAGES = D == 64 ? (NT == 1 ? 3 : 4) : NT == 1 ? 2 : 3;
   static constexpr int SLICES = D == 256 ? 2 : 1;      // 128-byte (D = 64: 64-byte) slices of a row
   static constexpr int KSTEPS = D / 16;
-  static constexpr bool Q_SHARED = D == 256;           // q fragments in shared memory (registers hold O)
-  static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int JOIN = kWarps * kRows * (D + 2) * 4;  // the warps' sums, over the ring
+  static constexpr int MT = D / 16;                    // products of 16 dims each
+  static constexpr bool Q_SHARED = D == 256 && NT == 2;  // q fragments in shared memory (registers hold O)
+  static constexpr int RING = WARPS * STAGES * STAGE;
+  static constexpr int JOIN = WARPS * ROWS * (D + 2) * 4;  // the warps' sums, over the ring
   static constexpr int DATA = RING > JOIN ? RING : JOIN;
   static constexpr int Q_OFF = (DATA + 127) / 128 * 128;
-  static constexpr int BAR_OFF = Q_OFF + (Q_SHARED ? KSTEPS * 512 : 0);
-  static constexpr int SMEM = BAR_OFF + kWarps * STAGES * 8 + 1024;  // + slack to align the base
-  static constexpr int CTAS = D == 256 ? 2 : 4;        // resident per SM
+  static constexpr int BAR_OFF = Q_OFF + (Q_SHARED ? KSTEPS * NT * 256 : 0);
+  static constexpr int SMEM = BAR_OFF + WARPS * STAGES * 8 + 1024;  // + slack to align the base
 };
 
 // A tile that a CTA went on with first, for the joining kernel.
@@ -62,11 +63,12 @@ struct Seq : PageSeq {
   int64_t units;
 };
 
+template <int ROWS>
 __device__ __forceinline__ Seq rows_sequence(const PageArgs& a, int32_t b, bool& bad) {
   Seq s;
   static_cast<PageSeq&>(s) = page_sequence(a, b, bad);
   s.pages = s.n > 0 ? (s.len + kPage - 1) / kPage : 0;
-  s.tiles = (s.n * (a.num_q_heads / a.num_kv_heads) + kRows - 1) / kRows;
+  s.tiles = (s.n * (a.num_q_heads / a.num_kv_heads) + ROWS - 1) / ROWS;
   s.units = static_cast<int64_t>(s.pages) * s.tiles * a.num_kv_heads;
   return s;
 }
@@ -78,14 +80,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
+// Lane (g8, t4) = (i / 4, i % 4) holds row g8 and columns 2 t4, 2 t4 + 1 of an 8 x 8 matrix of f16; of its transpose:
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
     page_rows_kernel(const PageArgs a, const __grid_constant__ CUtensorMap map) {
-  using Cfg = RCfg<D>;
-  constexpr int STAGES = Cfg::STAGES, SLICES = Cfg::SLICES, KSTEPS = Cfg::KSTEPS;
+  using Cfg = RCfg<D, NT>;
+  constexpr int STAGES = Cfg::STAGES, SLICES = Cfg::SLICES, KSTEPS = Cfg::KSTEPS, MT = Cfg::MT;
+  constexpr int kWarps = Cfg::WARPS, kThreads = Cfg::THREADS, kRows = Cfg::ROWS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint4* sQ = reinterpret_cast<uint4*>(smem + Cfg::Q_OFF);
+  uint2* sQ = reinterpret_cast<uint2*>(smem + Cfg::Q_OFF);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;  // of a product: row or column g8, columns 2 t4 and 2 t4 + 1
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF) + warp * STAGES;
@@ -104,12 +114,13 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
           page_store_out(a, static_cast<int64_t>(b) * a.num_q_heads * D + i * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
   }
   const Place place = page_place<kWarps>(
-      a.batch, cta == 0 ? a.total : nullptr, [&](int32_t i) { return rows_sequence(a, i, bad).units; },
+      a.batch, cta == 0 ? a.total : nullptr, [&](int32_t i) { return rows_sequence<kRows>(a, i, bad).units; },
       [&](int64_t U) {  // this CTA's first unit
         const int32_t C = sharers(U, a.grid, kPageMinUnits);
         return cta < C && U > 0 ? first_unit(U, C, cta) : U;
       });
-  if (cta == 0 && bad) set_status(a.status, kStatusBadExtend);
+  if (cta == 0) page_cleared();
+  if (cta == 0 && bad) page_report(a, kStatusBadExtend);
   if (place.b < 0) return;
   const int32_t C = sharers(place.total, a.grid, kPageMinUnits);
   int64_t u = first_unit(place.total, C, cta);
@@ -121,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
   bool ok = true;
 
   while (u < u_end) {
-    Seq s = rows_sequence(a, b, bad);
+    Seq s = rows_sequence<kRows>(a, b, bad);
     if (u >= before + s.units) {
       before += s.units;
       ++b;
@@ -138,14 +149,15 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
     if (tid == 0 && u == u_first)
       static_cast<Run*>(a.runs)[cta] = {tile_first, pg0 > 0, s.pages, s.q0, g, tile * kRows, rows};
 
-    // ---- this lane's two rows: where their q lies, how many tokens they see
-    const uint16_t* qrow[2];
-    int32_t sees[2];
+    // ---- where the q of this lane's rows g8 lies, how many tokens its rows 2 t4 and 2 t4 + 1 see
+    const uint16_t* qrow[NT];
+    int32_t sees[NT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int32_t r = min(g8 + 8 * h, rows - 1) + tile * kRows, tok = r / G;
-      qrow[h] = a.q + (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + g * G + (r - tok * G)) * D;
-      sees[h] = s.len - s.n + tok + 1;
+    for (int n = 0; n < NT; ++n) {
+      const int32_t r = min(g8 + 8 * n, rows - 1) + tile * kRows, tok = r / G;
+      qrow[n] = a.q + (static_cast<int64_t>(s.q0 + tok) * a.num_q_heads + g * G + (r - tok * G)) * D;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sees[n][e] = s.len - s.n + (min(2 * t4 + e + 8 * n, rows - 1) + tile * kRows) / G + 1;
     }
     const int32_t sees_least = s.len - s.n + tile * kRows / G + 1;
 
@@ -157,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
       if (i >= nw) return -1;
       const int32_t p = __ldg(table + i * kWarps);
       if (p < a.num_pages) return p;
-      set_status(a.status, kStatusBadPage);
+      page_report(a, kStatusBadPage);
       return -1;
     };
     auto scales = [&](int32_t p, float& ks, float& vs) {
@@ -194,61 +206,57 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
     }
 
     // ---- q as f16 fragments, the row's largest element brought to [2^14, 2^15)
-    float rowscale[2];
-    uint32_t qf[Cfg::Q_SHARED ? 1 : KSTEPS][4];
-    {
-      float top[2] = {0.0f, 0.0f};
+    float rowscale[NT][2];  // of rows 2 t4 and 2 t4 + 1
+    uint32_t qf[Cfg::Q_SHARED ? 1 : KSTEPS][NT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int n = 0; n < NT; ++n) {
+      float top = 0.0f;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow[h] + (x * 4 + t4) * 8));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int x = 0; x < D / 32; ++x) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow[n] + (x * 4 + t4) * 8));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack_bf16x2(w[k]);
-            top[h] = fmaxf(top[h], fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack_bf16x2(w[k]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
       }
-      float up[2];
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(max((__float_as_int(top) >> 23) - 127, -100), 100);
+      const float up = __int_as_float((14 - e + 127) << 23);
+      const float back = a.score_scale * __int_as_float((e - 14 + 127) << 23);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int e = min(max((__float_as_int(top[h]) >> 23) - 127, -100), 100);
-        up[h] = __int_as_float((14 - e + 127) << 23);
-        rowscale[h] = a.score_scale * __int_as_float((e - 14 + 127) << 23);
-      }
-      // k-step (x, c, i): lane t4 holds dims 128 x + 32 t4 + 16 c + 4 i ... + 3 of its rows (D = 64: 16 t4 + 4 i)
+      for (int c = 0; c < 2; ++c) rowscale[n][c] = __shfl_sync(0xffffffffu, back, (2 * t4 + c) * 4);
+      // k-step (x, c, i): lane t4 holds dims 128 x + 32 t4 + 16 c + 4 i ... + 3 of its row (D = 64: 16 t4 + 4 i)
 #pragma unroll
       for (int k = 0; k < KSTEPS; ++k) {
         const int x = k / 8, c = (k / 4) % 2, i = k % 4;
         const int d = D == 64 ? 16 * t4 + 4 * i : 128 * x + 32 * t4 + 16 * c + 4 * i;
-        uint32_t f[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(qrow[h] + d));
-          const float2 lo = unpack_bf16x2(v.x), hi = unpack_bf16x2(v.y);
-          f[h] = pack_f16x2(lo.x * up[h], lo.y * up[h]);
-          f[2 + h] = pack_f16x2(hi.x * up[h], hi.y * up[h]);
-        }
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(qrow[n] + d));
+        const float2 lo = unpack_bf16x2(v.x), hi = unpack_bf16x2(v.y);
+        const uint32_t f0 = pack_f16x2(lo.x * up, lo.y * up), f1 = pack_f16x2(hi.x * up, hi.y * up);
         if constexpr (Cfg::Q_SHARED) {
-          if (warp == k % kWarps) sQ[k * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+          if (warp == k % kWarps) sQ[(k * NT + n) * 32 + lane] = make_uint2(f0, f1);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qf[k][e] = f[e];
+          qf[k][n][0] = f0;
+          qf[k][n][1] = f1;
         }
       }
-      if constexpr (Cfg::Q_SHARED) __syncthreads();
     }
+    if constexpr (Cfg::Q_SHARED) __syncthreads();
 
-    float o[D / 8][4];
+    float o[NT][MT][4];  // of 16 dims: dims of rows g8 and g8 + 8 of the product, query rows 2 t4 and 2 t4 + 1
+    float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-    float m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][j][e] = 0.0f;
+      m[n][0] = m[n][1] = kNoMax;
+      l[n][0] = l[n][1] = 0.0f;
+    }
     int32_t landed = 0;
 
     for (int32_t i = 0; i < nw; ++i) {
@@ -268,77 +276,86 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
         const uint8_t* kc = ring + slot * Cfg::STAGE;
         const uint8_t* vc = kc + Cfg::PAGE_BYTES;
         const int32_t t0 = (pg0 + warp + i * kWarps) * kPage;  // the page's first token
-        // ---- scores of tokens 8 j + (2 t4, 2 t4 + 1)
-        float sc[2][4];
+        // ---- scores of tokens g8 and g8 + 8 with rows 2 t4, 2 t4 + 1
+        float sc[NT][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
-          const int row = 8 * j + g8;
+        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
 #pragma unroll
-          for (int q = 0; q < KSTEPS / 4; ++q) {
-            uint4 w;
+        for (int q = 0; q < KSTEPS / 4; ++q) {
+          uint32_t w[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = g8 + 8 * h;
+            uint4 v;
             if constexpr (D == 64) {
-              w = *reinterpret_cast<const uint4*>(kc + row * 64 + ((t4 ^ ((row >> 1) & 3)) << 4));
+              v = *reinterpret_cast<const uint4*>(kc + row * 64 + ((t4 ^ ((row >> 1) & 3)) << 4));
             } else {
-              w = *reinterpret_cast<const uint4*>(kc + (q / 2) * 2048 + row * 128 + (((2 * t4 + q % 2) ^ (row & 7)) << 4));
+              v = *reinterpret_cast<const uint4*>(kc + (q / 2) * 2048 + row * 128 + (((2 * t4 + q % 2) ^ (row & 7)) << 4));
             }
-            const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+            w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t b0, b1;
-              codes_to_f16x2<KVQ_FP8_E4M3>(c[e], b0, b1);
+          for (int e = 0; e < 4; ++e) {
+            uint32_t f[4];
+            codes_to_f16x2<KVQ_FP8_E4M3>(w[0][e], f[0], f[2]);
+            codes_to_f16x2<KVQ_FP8_E4M3>(w[1][e], f[1], f[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
               if constexpr (Cfg::Q_SHARED) {
-                const uint4 x = sQ[(q * 4 + e) * 32 + lane];
-                const uint32_t f[4] = {x.x, x.y, x.z, x.w};
-                mma_f16(sc[j], f, b0, b1);
+                const uint2 x = sQ[((q * 4 + e) * NT + n) * 32 + lane];
+                mma_f16(sc[n], f, x.x, x.y);
               } else {
-                mma_f16(sc[j], qf[q * 4 + e], b0, b1);
+                mma_f16(sc[n], f, qf[q * 4 + e][n][0], qf[q * 4 + e][n][1]);
               }
             }
           }
         }
         // ---- y = score + ev in the exponent; what a row does not see is -inf
         const float ev = scale_exponent(vscale), unv = scale_inverse(vscale);
-        float top[2];
         const bool whole = t0 + kPage <= sees_least;
+        bool over = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float mult = rowscale[h] * kscale;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int e = 0; e < 2; ++e) {
+            const float mult = rowscale[n][e] * kscale;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = sc[j][2 * h + e];
+            for (int h = 0; h < 2; ++h) {
+              float& x = sc[n][2 * h + e];
               x = fmaf(x, mult, ev);
-              if (!whole && t0 + 8 * j + 2 * t4 + e >= sees[h]) x = -INFINITY;
-            }
-          top[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-        }
-        if (__any_sync(0xffffffffu, top[0] > m[0] + kLimit || top[1] > m[1] + kLimit)) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = top[h];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            const float now = fmaxf(m[h], x - kHead);
-            const float alpha = ex2(m[h] - now);
-            m[h] = now;
-            l[h] *= alpha;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-              o[j][2 * h] *= alpha;
-              o[j][2 * h + 1] *= alpha;
+              if (!whole && t0 + 8 * h + g8 >= sees[n][e]) x = -INFINITY;
+              over |= x > m[n][e] + kLimit;
             }
           }
-        }
-        uint32_t pf[4];
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(sc[n][e], sc[n][2 + e]);
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              const float now = fmaxf(m[n][e], x - kHead);
+              const float alpha = ex2(m[n][e] - now);
+              m[n][e] = now;
+              l[n][e] *= alpha;
+#pragma unroll
+              for (int j = 0; j < MT; ++j) {
+                o[n][j][e] *= alpha;
+                o[n][j][2 + e] *= alpha;
+              }
+            }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(sc[j][2 * h] - m[h]), p1 = ex2(sc[j][2 * h + 1] - m[h]);
-            l[h] = fmaf(p0 + p1, unv, l[h]);
-            pf[2 * j + h] = pack_f16x2(p0, p1);
+            const float p0 = ex2(sc[n][2 * h] - m[n][0]), p1 = ex2(sc[n][2 * h + 1] - m[n][1]);
+            l[n][0] = fmaf(p0, unv, l[n][0]);
+            l[n][1] = fmaf(p1, unv, l[n][1]);
+            pf[n][h] = transposed(pack_f16x2(p0, p1));
           }
         // ---- output: dims 128 x + 16 g8 + byte (D = 64: 8 g8 + byte) of tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
         constexpr int WORDS = D == 64 ? 2 : 4;
@@ -365,11 +382,11 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const uint32_t pick = half == 0 ? 0x5140u : 0x7362u;
-              uint32_t b0[2], b1[2];
-              codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[0][k], v[1][k], pick), b0[0], b0[1]);
-              codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[2][k], v[3][k], pick), b1[0], b1[1]);
+              uint32_t f[4];
+              codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[0][k], v[1][k], pick), f[0], f[1]);
+              codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[2][k], v[3][k], pick), f[2], f[3]);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) mma_f16(o[(x * WORDS + k) * 4 + half * 2 + e], pf, b0[e], b1[e]);
+              for (int n = 0; n < NT; ++n) mma_f16(o[n][(x * WORDS + k) * 2 + half], f, pf[n][0], pf[n][1]);
             }
         }
       }
@@ -380,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
       if (j < nw) issue(j, pj);
     }
     if (!ok) {
-      set_status(a.status, kStatusTimeout);
+      page_report(a, kStatusTimeout);
       for (int32_t i = landed; i < min(nw, landed + STAGES); ++i)  // no copy may still be in flight at the end
         (void)mbar_wait_bounded(&bars[(done + i) % STAGES], ((done + i) / STAGES) & 1);
     }
@@ -388,33 +405,34 @@ __global__ void __launch_bounds__(kThreads, RCfg<D>::CTAS)
 
     // ---- the warps' sums, joined in shared memory over the ring
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
     __syncthreads();
     float2* sml = reinterpret_cast<float2*>(smem);                        // [warps][rows]
     float* sacc = reinterpret_cast<float*>(smem + kWarps * kRows * 8);    // [warps][rows][D]
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = g8 + 8 * h;
-      if (r < rows) {
-        if (t4 == 0) sml[warp * kRows + r] = make_float2(m[h], l[h]);
-        // the lane's dims: 128 x + 32 t4 ... + 31 (D = 64: 16 t4 ... + 15), first those of column 2 t4
-        constexpr int RUN = D == 64 ? 8 : 16;
-        float* dst = sacc + (warp * kRows + r) * D;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < SLICES; ++x)
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * t4 + e + 8 * n;
+        if (r < rows) {
+          if (g8 == 0) sml[warp * kRows + r] = make_float2(m[n][e], l[n][e]);
+          // the lane's dims: 128 x + 16 g8 ... + 15 (D = 64: 8 g8 ... + 7)
+          constexpr int RUN = D == 64 ? 4 : 8;  // products of them
+          float* dst = sacc + (warp * kRows + r) * D + g8 * 2 * RUN;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int x = 0; x < SLICES; ++x)
 #pragma unroll
-            for (int k = 0; k < RUN; k += 4) {
+            for (int k = 0; k < RUN; k += 2) {
               const int j = x * RUN + k;
-              *reinterpret_cast<float4*>(dst + x * 128 + (2 * t4 + e) * RUN + k) =
-                  make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e], o[j + 3][2 * h + e]);
+              *reinterpret_cast<float4*>(dst + x * 128 + 2 * k) =
+                  make_float4(o[n][j][e], o[n][j][2 + e], o[n][j + 1][e], o[n][j + 1][2 + e]);
             }
+        }
       }
-    }
     ok = __syncthreads_and(ok);
     const bool whole_tile = pg0 == 0 && pg1 == s.pages;
     const int64_t slot = part_slot(place.total, C, cta, tile_first);
@@ -474,7 +492,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
   for (int k = 0; k < V4; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int32_t i = c - 1 + warp; i <= c1; i += kJoinWarps) {
-    const int64_t at = part_slot(U, C, i, run.first) * kRows + r;
+    const int64_t at = part_slot(U, C, i, run.first) * a.tile + r;
     const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
     const float now = fmaxf(m, ml.x), f = ex2(ml.x - now), keep = ex2(m - now);
     m = now;
@@ -519,41 +537,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
   }
 }
 
-template <int D>
+template <int D, int NT>
 kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
-  using Cfg = RCfg<D>;
+  using Cfg = RCfg<D, NT>;
   CUtensorMap map;
   if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
-  auto kern = page_rows_kernel<D>;
+  auto kern = page_rows_kernel<D, NT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess) return KVQ_ECUDA;
-  if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), stream) != cudaSuccess) return KVQ_ECUDA;
-  kern<<<a.grid, kThreads, Cfg::SMEM, stream>>>(a, map);
+  page_clear_kernel<<<1, 32, 0, stream>>>(a.status);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
-  cudaLaunchConfig_t cfg = {};
+  if (!launch_dependent(kern, dim3(a.grid), Cfg::THREADS, Cfg::SMEM, stream, a, map)) return KVQ_ECUDA;
   if (a.grid == 1) return KVQ_OK;
-  cfg.gridDim = dim3(a.grid - 1, std::min<int64_t>(kRows, static_cast<int64_t>(a.total_q) * (a.num_q_heads / a.num_kv_heads)));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, page_join_kernel<D>, a) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  const int64_t rows = static_cast<int64_t>(a.total_q) * (a.num_q_heads / a.num_kv_heads);
+  const dim3 joins(a.grid - 1, std::min<int64_t>(a.tile, rows));
+  return launch_dependent(page_join_kernel<D>, joins, kJoinWarps * 32, 0, stream, a) ? KVQ_OK : KVQ_ECUDA;
 }
 
 }  // namespace
 
 bool page_supported(int32_t head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
 
-int32_t page_rows_grid(int32_t head_dim, int32_t sms) {
-  return sms * (head_dim == 64 ? RCfg<64>::CTAS : head_dim == 128 ? RCfg<128>::CTAS : RCfg<256>::CTAS);
+int32_t page_rows_grid(int32_t head_dim, int32_t tile, int32_t sms) {
+  const bool one = tile == 8;
+  return sms * (head_dim == 64    ? (one ? RCfg<64, 1>::CTAS : RCfg<64, 2>::CTAS)
+                : head_dim == 128 ? (one ? RCfg<128, 1>::CTAS : RCfg<128, 2>::CTAS)
+                                  : (one ? RCfg<256, 1>::CTAS : RCfg<256, 2>::CTAS));
 }
 
 kvq_status launch_page_rows(const PageArgs& a, cudaStream_t stream) {
-  if (a.head_dim == 64) return launch_d<64>(a, stream);
-  if (a.head_dim == 128) return launch_d<128>(a, stream);
-  return launch_d<256>(a, stream);
+  const bool one = a.tile == 8;
+  if (a.head_dim == 64) return one ? launch_d<64, 1>(a, stream) : launch_d<64, 2>(a, stream);
+  if (a.head_dim == 128) return one ? launch_d<128, 1>(a, stream) : launch_d<128, 2>(a, stream);
+  return one ? launch_d<256, 1>(a, stream) : launch_d<256, 2>(a, stream);
 }
 
 }  // namespace kvq
