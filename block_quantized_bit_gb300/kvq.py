@@ -166,7 +166,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # (current_stream() builds an object, 3 us)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -288,11 +288,11 @@ def kvq_decode(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
     else:
         raise TypeError("out must be bfloat16 or float32")
     _check_by_page(pool, scales, layout, kind)
-    o = _opts(pages_per_split, path)
+    o = ctypes.byref(_opts(pages_per_split, path)) if pages_per_split or path else None
     _check(lib().kvq_decode_ex(_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]),
                                _ptr(seq_lens), int(seq_lens.shape[0]), int(q.shape[1]), float(sm_scale), _ptr(out),
                                od, _ptr(workspace), int(workspace.numel() * workspace.element_size()),
-                               ctypes.byref(layout.c()), _kind(kind), ctypes.byref(o), _stream(stream)),
+                               _layout_info(layout)[0], _kind(kind), o, _stream(stream)),
            "kvq_decode")
 
 
@@ -405,7 +405,7 @@ def kvq_extend(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
     B = seq_lens.numel()
     args = (_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
             _ptr(q_start), int(total_q), int(B), int(Hq), float(sm_scale), _ptr(out), od, _ptr(workspace),
-            int(workspace.numel() * workspace.element_size()), ctypes.byref(layout.c()), _kind(kind))
+            int(workspace.numel() * workspace.element_size()), _layout_info(layout)[0], _kind(kind))
     opts = _extend_opts(path, precise_p)
     if opts is None:
         _check(lib().kvq_extend(*args, _stream(stream)), "kvq_extend")
@@ -506,15 +506,18 @@ def alloc_append_workspace(device="cuda"):
     return torch.empty(lib().kvq_append_workspace_bytes(), dtype=torch.uint8, device=device)
 
 
-def _check_rows(name, t, total, heads, dim, device):
+def _check_rows(name, t, shape, device):
+    """Rows [total, heads, head_dim] in bf16 whose last dimension is dense; their strides."""
+    if t.dtype is _BF16 and t.shape == shape and t.get_device() == device:
+        strides = t.stride()
+        if strides[2] == 1:
+            return strides
+        raise ValueError("the last dimension of %s must be dense" % name)
     if t.dtype is not _BF16:
         raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
-    if t.dim() != 3 or t.shape[0] != total or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError("%s must be [%d, %s, %d]" % (name, total, "heads" if heads is None else heads, dim))
-    if t.stride(2) != 1 and dim > 1:
-        raise ValueError("the last dimension of %s must be dense" % name)
-    if t.get_device() != device:
-        raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    raise ValueError("%s is on %s, not on the current CUDA device" % (name, t.device))
 
 
 def kvq_append(pool: torch.Tensor, scales: Optional[torch.Tensor], k: torch.Tensor, v: Optional[torch.Tensor],
@@ -530,44 +533,48 @@ def kvq_append(pool: torch.Tensor, scales: Optional[torch.Tensor], k: torch.Tens
     the sines) rotates elements rot_offset .. rot_offset + rot_dim - 1 of q and k, each half with the other or, when
     interleaved, neighbours; None: no rotation.  positions ([total] int32): other positions than the tokens' places.
     q, k, v and q_out may be strided between tokens and heads."""
-    total, D = k.shape[0], layout.head_dim
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("rows must be [total, heads, head_dim]")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    total, hkv, D = len(k), layout.num_kv_heads, layout.head_dim
+    batch = seq_lens.numel()
     _check_tables(block_table, seq_lens, None, layout)
-    if q_start.numel() != seq_lens.numel() + 1:
+    if q_start.numel() != batch + 1:
         raise ValueError("q_start must be [batch + 1]")
     info = _layout_info(layout)
     device = _check_args(_APPEND_NAMES, _APPEND_TYPES, block_table, seq_lens, q_start, workspace)
     code, sc = _check_pool(pool, scales, info, kind, device)
-    _check_rows("k", k, total, layout.num_kv_heads, D, device)
+    # (strides of what is absent are not read)
+    shape = (total, hkv, D)
+    ks = vs = _check_rows("k", k, shape, device)
+    dense = ks[0] == hkv * D and ks[1] == D
     if v is not None:
-        _check_rows("v", v, total, layout.num_kv_heads, D, device)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
+        vs = _check_rows("v", v, shape, device)
+        dense = dense and ks == vs
+    hq, qs, os, q_at, out_at = 0, ks, ks, None, None
     if q is not None:
-        _check_rows("q", q, total, None, D, device)
-        _check_rows("q_out", q_out, total, q.shape[1], D, device)
+        hq = q.shape[1]
+        shape = (total, hq, D)
+        qs, os = _check_rows("q", q, shape, device), _check_rows("q_out", q_out, shape, device)
+        dense = dense and qs == os and qs[0] == hq * D and qs[1] == D
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
     rope = None
     if cos_sin is not None:
         if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous float32 [max_position, rot_dim]")
         if cos_sin.get_device() != device:
             raise ValueError("cos_sin is on %s, not on the current CUDA device" % cos_sin.device)
-        rope = ctypes.byref(kvq_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], rot_offset,
-                                     1 if interleaved else 0))
+        rope = kvq_rope(cos_sin.data_ptr(), *cos_sin.shape, rot_offset, 1 if interleaved else 0)
     if positions is not None:
         if positions.numel() != total:
             raise ValueError("positions must be [total]")
         _check_args(("positions",), (_I32,), positions)
-    strides = None
-    if not (k.is_contiguous() and (v is None or v.is_contiguous()) and
-            (q is None or (q.is_contiguous() and q_out.is_contiguous()))):
-        strides = ctypes.byref(kvq_prompt_strides(*[x for t in (k if q is None else q, k, k if v is None else v,
-                                                                k if q is None else q_out) for x in t.stride()[:2]]))
-    st = lib().kvq_append(pool.data_ptr(), sc, None if q is None else q.data_ptr(), k.data_ptr(),
-                          None if v is None else v.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                          seq_lens.data_ptr(), q_start.data_ptr(), None if positions is None else positions.data_ptr(),
-                          total, seq_lens.numel(), 0 if q is None else q.shape[1],
-                          None if q is None else q_out.data_ptr(), rope, strides, workspace.data_ptr(),
-                          workspace.numel(), info[0], code, _raw_stream(stream, device))
+    strides = None if dense else kvq_prompt_strides(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
+    st = lib().kvq_append(pool.data_ptr(), sc, q_at, k.data_ptr(), None if v is None else v.data_ptr(),
+                          block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(),
+                          None if positions is None else positions.data_ptr(), total, batch, hq, out_at, rope, strides,
+                          workspace.data_ptr(), workspace.numel(), info[0], code, _raw_stream(stream, device))
     if st:
         raise KvqError(st, "kvq_append")
 
