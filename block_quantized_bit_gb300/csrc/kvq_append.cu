@@ -35,11 +35,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 8;  // tokens of a CTA at most
 
-__device__ __forceinline__ void append_report(const AppendArgs& a, uint32_t code) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the clearing kernel before this one has completed
-  set_status(a.status, code);
-}
-
 // Whether sequence b's numbers agree; q0, n and len are its first row, new tokens and stored tokens.
 __device__ __forceinline__ bool append_sequence(const AppendArgs& a, int32_t b, int32_t& q0, int32_t& n, int32_t& len) {
   q0 = __ldg(a.q_start + b);
@@ -49,12 +44,41 @@ __device__ __forceinline__ bool append_sequence(const AppendArgs& a, int32_t b, 
   return q0 >= 0 && q1 >= q0 && q1 <= a.total && n <= len && len <= static_cast<int64_t>(a.max_pages) * a.page_size;
 }
 
-// One CTA of the call reports inconsistent sequences; all of them skip these.
+// The call's first CTA reads all that the call's numbers can get wrong and writes the status word; the others only skip or
+// clamp what it finds.  With reports from all CTAs the word would have to be cleared by a launch of its own, 2 us of a small call.
 __device__ __forceinline__ void append_check(const AppendArgs& a) {
-  int32_t q0, n, len;
-  bool bad = false;
-  for (int32_t b = threadIdx.x; b < a.batch; b += kThreads) bad |= !append_sequence(a, b, q0, n, len);
-  if (bad) append_report(a, kStatusBadExtend);
+  __shared__ uint32_t s_code;
+  if (threadIdx.x == 0) s_code = 0;
+  __syncthreads();
+  constexpr int kAlone = 32;  // tokens that a thread looks through by itself; a warp shares those of longer sequences
+  const int lane = threadIdx.x & 31;
+  uint32_t code = 0;
+  auto look = [&](int32_t b, int32_t q0, int32_t n, int32_t len, int32_t from, int32_t step) {
+    const int32_t first = (len - n) / a.page_size, last = (len - 1) / a.page_size;
+    for (int32_t i = first + from; i <= last; i += step)
+      if (__ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + i) >= a.num_pages) code = max(code, kStatusBadPage);
+    if (a.rot_dim > 0 && a.positions != nullptr)
+      for (int32_t i = from; i < n; i += step)
+        if (static_cast<uint32_t>(__ldg(a.positions + q0 + i)) >= static_cast<uint32_t>(a.max_position))
+          code = max(code, kStatusBadExtend);
+    if (a.rot_dim > 0 && a.positions == nullptr && len > a.max_position) code = max(code, kStatusBadExtend);
+  };
+  for (int32_t b0 = threadIdx.x - lane; b0 < a.batch; b0 += kThreads) {
+    int32_t q0 = 0, n = 0, len = 0;
+    if (b0 + lane < a.batch && !append_sequence(a, b0 + lane, q0, n, len)) {
+      code = max(code, kStatusBadExtend);
+      n = 0;
+    }
+    if (n > 0 && n <= kAlone) look(b0 + lane, q0, n, len, 0, 1);
+    for (uint32_t more = __ballot_sync(0xffffffffu, n > kAlone); more != 0; more &= more - 1) {
+      const int from = __ffs(more) - 1;
+      look(b0 + from, __shfl_sync(0xffffffffu, q0, from), __shfl_sync(0xffffffffu, n, from),
+           __shfl_sync(0xffffffffu, len, from), lane, 32);
+    }
+  }
+  if (code != 0) atomicMax(&s_code, code);
+  __syncthreads();
+  if (threadIdx.x == 0) *a.status = s_code;
 }
 
 // The first consistent sequence for which `mine` holds, or batch: by the whole CTA.
@@ -74,20 +98,14 @@ __device__ __forceinline__ int32_t append_find(const AppendArgs& a, F mine) {
 // The page of block-table entry (b, i), or -1.
 __device__ __forceinline__ int32_t append_page(const AppendArgs& a, int32_t b, int32_t i) {
   const int32_t page = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + i);
-  if (page < a.num_pages) return page;
-  append_report(a, kStatusBadPage);
-  return -1;
+  return page < a.num_pages ? page : -1;
 }
 
 // The position to which row t, at place p of its sequence, is rotated.
 __device__ __forceinline__ int32_t append_position(const AppendArgs& a, int32_t t, int32_t p) {
   if (a.rot_dim == 0) return 0;
-  int32_t at = a.positions ? __ldg(a.positions + t) : p;
-  if (at < 0 || at >= a.max_position) {
-    append_report(a, kStatusBadExtend);
-    at = at < 0 ? 0 : a.max_position - 1;
-  }
-  return at;
+  const int32_t at = a.positions ? __ldg(a.positions + t) : p;
+  return min(max(at, 0), a.max_position - 1);
 }
 
 __device__ __forceinline__ void bf16x8(uint4 v, float (&x)[8]) {
@@ -346,14 +364,14 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int32_t t0, int
   }
 }
 
-// grid: (tokens, row chunk), row chunks fastest
+// grid: the check, then (tokens, row chunk), row chunks fastest
 template <int KIND, bool SHFL>
 __global__ void __launch_bounds__(kThreads, 4) append_rows_kernel(const AppendArgs a) {
   extern __shared__ __align__(16) float turns[];
   __shared__ Tokens tok;
-  if (blockIdx.x == 0) append_check(a);
-  const int32_t t = blockIdx.x / a.row_chunks * a.tokens;
-  append_rows<KIND, SHFL>(a, t, min(a.tokens, a.total - t), blockIdx.x % a.row_chunks, tok, turns);
+  if (blockIdx.x == 0) return append_check(a);
+  const int32_t at = blockIdx.x - 1, t = at / a.row_chunks * a.tokens;
+  append_rows<KIND, SHFL>(a, t, min(a.tokens, a.total - t), at % a.row_chunks, tok, turns);
 }
 
 // The least e with m <= 448 * 2^e (448 = 1.75 * 2^8), within the exponents that a page's scale may have.
@@ -371,7 +389,7 @@ __device__ __forceinline__ int64_t pages_before(int32_t b, int32_t q0) {
   return (static_cast<int64_t>(q0) + 14LL * b) / kPage + b;
 }
 
-// grid: (page, chunk of its 2 * heads parts) first, then (tokens, row chunk) of the queries
+// grid: the check, (page, chunk of its 2 * heads parts), then (tokens, row chunk) of the queries
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) append_pages_kernel(const AppendArgs a) {
   constexpr int PER_ROW = D / 8;               // threads of a row
@@ -379,13 +397,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) append_pages_kerne
   constexpr int PASSES = kPage / ROWS;
   extern __shared__ __align__(16) float turns[];
   __shared__ Tokens tok;
-  if (blockIdx.x == 0) append_check(a);
-  if (blockIdx.x >= a.page_ctas) {
-    const int32_t q = blockIdx.x - a.page_ctas, t = q / a.row_chunks * a.tokens;
+  if (blockIdx.x == 0) return append_check(a);
+  const int32_t at = blockIdx.x - 1;
+  if (at >= a.page_ctas) {
+    const int32_t q = static_cast<int32_t>(at - a.page_ctas), t = q / a.row_chunks * a.tokens;
     append_rows<KVQ_FP8_E4M3_PAGE, true>(a, t, min(a.tokens, a.total - t), q % a.row_chunks, tok, turns);
     return;
   }
-  const int32_t item = blockIdx.x / a.part_chunks, chunk = blockIdx.x % a.part_chunks;
+  const int32_t item = at / a.part_chunks, chunk = at % a.part_chunks;
   // the sequence among whose pages the item lies, and which of them
   const int32_t b = append_find(a, [&](int32_t s, int32_t q0, int32_t n, int32_t len) {
     if (n == 0) return false;
@@ -498,27 +517,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) append_pages_kerne
   if (lane == 0) *scale = power_of_two(exp);
 }
 
-// Clears the status word; the append is its programmatic dependent and touches the word only after a wait.
-__global__ void append_clear_kernel(uint32_t* word) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) *word = 0;
-}
-
 template <typename Kernel>
 kvq_status launch(Kernel kern, const AppendArgs& a, int64_t grid, cudaStream_t stream) {
-  append_clear_kernel<<<1, 32, 0, stream>>>(a.status);
-  if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = std::max(a.tokens, a.page_ctas > 0 ? kPage : 0) * a.rot_dim * sizeof(float);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
+  const size_t smem = std::max(a.tokens, a.page_ctas > 0 ? kPage : 0) * a.rot_dim * sizeof(float);
+  kern<<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ECUDA;
 }
 
 }  // namespace
@@ -543,7 +546,7 @@ int64_t append_grid(AppendArgs* a, int32_t sms) {
   a->part_chunks = (2 * a->num_kv_heads + kWarps - 1) / kWarps;
   const int64_t items = pages ? (static_cast<int64_t>(a->total) + 14LL * a->batch) / kPage + a->batch : 0;
   a->page_ctas = items * a->part_chunks;
-  return a->page_ctas + (rows > 0 ? (static_cast<int64_t>(a->total) + a->tokens - 1) / a->tokens * a->row_chunks : 0);
+  return 1 + a->page_ctas + (rows > 0 ? (static_cast<int64_t>(a->total) + a->tokens - 1) / a->tokens * a->row_chunks : 0);
 }
 
 kvq_status launch_append(const AppendArgs& a, int64_t grid, cudaStream_t stream) {

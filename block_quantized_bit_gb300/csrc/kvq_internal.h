@@ -243,7 +243,7 @@ struct PageArgs {
   void* out;                  // [total_q][num_q_heads][head_dim]
   uint32_t* status;
   int64_t* total;             // the call's units
-  void* runs;                 // [grid] of kPageRunBytes: each CTA's first run
+  void* runs;                 // [grid] each CTA's first run, then [grid] words: what it reports
   float* part_acc;            // [2 * grid][rows][head_dim], rows: tile
   float* part_ml;             // [2 * grid][rows][2]
   int64_t num_pages;
@@ -255,7 +255,8 @@ struct PageArgs {
 };
 constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel at most (8 or 16)
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
-constexpr int kPageRunBytes = 64;
+constexpr int kPageRunMost = 60;   // bytes of a CTA's first run, at most ...
+constexpr int kPageRunBytes = kPageRunMost + 4;  // ... and its report
 constexpr int kPageItemUnits = 6;   // key tiles' time that an item's start and end take
 constexpr int kPageFlashUnits = 10; // units (key tiles and items' starts) that are worth a CTA of the flash kernel
 bool page_supported(int32_t head_dim);

@@ -12,16 +12,25 @@ constexpr float kNoMax = -1e30f;  // reference of a row that has seen nothing
 constexpr float kHead = 7.0f;     // log2 of the largest p when a row's reference moves ...
 constexpr float kLimit = 15.0f;   // ... and at most (P is f16, which ends at 2^16)
 
-// Clears the status word.  The attention is its programmatic dependent: it reads what was there before this kernel, so it
-// starts at once, and touches the word only after a wait; its first CTA waits in any case, so that its end is both's.
-__global__ void page_clear_kernel(uint32_t* word) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) *word = 0;
+// Every CTA reports into a word of its own behind the runs, and the joining kernel, which waits for them all, collects these: a
+// status word shared by the CTAs would have to be cleared by a launch of its own (2 us of a small call).  A single CTA has the
+// status word itself.
+__device__ __forceinline__ uint32_t* page_words(const PageArgs& a) {
+  return reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.runs) + static_cast<size_t>(a.grid) * kPageRunMost);
 }
-__device__ __forceinline__ void page_cleared() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void page_report(const PageArgs& a, uint32_t code) {
-  page_cleared();
-  set_status(a.status, code);
+__device__ __forceinline__ uint32_t* page_word(const PageArgs& a) {
+  return a.grid == 1 ? a.status : page_words(a) + blockIdx.x;
+}
+__device__ __forceinline__ void page_clear(const PageArgs& a) {  // before the CTA's first barrier
+  if (threadIdx.x == 0) *page_word(a) = 0;
+}
+__device__ __forceinline__ void page_report(const PageArgs& a, uint32_t code) { set_status(page_word(a), code); }
+__device__ __forceinline__ void page_collect(const PageArgs& a) {  // by the joining kernel, once the CTAs have ended
+  if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= 32) return;
+  uint32_t code = 0;
+  for (int32_t c = threadIdx.x; c < a.grid; c += 32) code = max(code, page_words(a)[c]);
+  code = __reduce_max_sync(0xffffffffu, code);
+  if (threadIdx.x == 0) *a.status = code;
 }
 
 // A kernel that may start before the one in front of it in the stream has ended.

@@ -92,7 +92,7 @@ struct Item {
   int32_t pad;
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == all; }
 };
-static_assert(sizeof(Item) <= kPageRunBytes && kPageRunBytes == 64, "item slots");
+static_assert(sizeof(Item) <= kPageRunMost && sizeof(Item) <= 64, "item slots");
 
 // Sum over i < n of floor((a i + b) / m), a, b >= 0 (the lattice points under a line, by the Euclidean algorithm).
 __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
   bool ok = true, bad = false;
   asm volatile("griddepcontrol.launch_dependents;");  // (the joining kernel waits for this one's end)
 
+  page_clear(a);
   if (tid == 0) {
     for (int i = 0; i < KST; ++i) {
       mbar_init(&bar_k_full[i], 1);
@@ -309,7 +310,6 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const int32_t C = sharers(U, a.grid, kPageFlashUnits);
         return cta < C && U > 0 ? first_unit(U, C, cta) : U;
       });
-  if (cta == 0) page_cleared();
   if (cta == 0 && bad) page_report(a, kStatusBadExtend);
   tc_fence_before();
   __syncthreads();
@@ -880,6 +880,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_flash_join_kernel(const 
   const int32_t c = blockIdx.x + 1, lane = threadIdx.x & 31;
   const int32_t row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), w = row / kM, r = row - w * kM;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  page_collect(a);
   const int64_t U = *a.total;
   const int32_t C = sharers(U, a.grid, kPageFlashUnits);
   if (c >= C || U == 0) return;
@@ -926,9 +927,8 @@ kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
   if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
   auto kern = page_flash_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess) return KVQ_ECUDA;
-  page_clear_kernel<<<1, 32, 0, stream>>>(a.status);
+  kern<<<a.grid, Cfg::THREADS, Cfg::SMEM, stream>>>(a, map);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
-  if (!launch_dependent(kern, dim3(a.grid), Cfg::THREADS, Cfg::SMEM, stream, a, map)) return KVQ_ECUDA;
   if (a.grid == 1) return KVQ_OK;
   const dim3 joins(a.grid - 1, Cfg::TILES * kM / kJoinWarps);
   return launch_dependent(page_flash_join_kernel<D>, joins, kJoinWarps * 32, 0, stream, a) ? KVQ_OK : KVQ_ECUDA;

@@ -55,7 +55,7 @@ struct Run {
   int64_t first;                         // the tile's first unit
   int32_t live, pages, q0, g, row0, rows; // its pages; sequence's first row; kv head; first row of the group's, and how many
 };
-static_assert(sizeof(Run) <= kPageRunBytes, "run slots");
+static_assert(sizeof(Run) <= kPageRunMost, "run slots");
 
 // One sequence's rows, pages and tiles.
 struct Seq : PageSeq {
@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF) + warp * STAGES;
   uint8_t* ring = smem + warp * STAGES * Cfg::STAGE;
 
+  page_clear(a);
   if (lane < STAGES) mbar_init(&bars[lane], 1);
   fence_mbar_init();
   __syncwarp();
@@ -119,7 +120,6 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
         const int32_t C = sharers(U, a.grid, kPageMinUnits);
         return cta < C && U > 0 ? first_unit(U, C, cta) : U;
       });
-  if (cta == 0) page_cleared();
   if (cta == 0 && bad) page_report(a, kStatusBadExtend);
   if (place.b < 0) return;
   const int32_t C = sharers(place.total, a.grid, kPageMinUnits);
@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_join_kernel(const PageAr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t c = blockIdx.x + 1, r = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  page_collect(a);
   const int64_t U = *a.total;
   const int32_t C = sharers(U, a.grid, kPageMinUnits);
   if (c >= C || U == 0) return;
@@ -544,9 +545,8 @@ kvq_status launch_d(const PageArgs& a, cudaStream_t stream) {
   if (!encode_code_map(&map, a.codes, a.num_pages, a.num_kv_heads, D)) return KVQ_ECUDA;
   auto kern = page_rows_kernel<D, NT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) != cudaSuccess) return KVQ_ECUDA;
-  page_clear_kernel<<<1, 32, 0, stream>>>(a.status);
+  kern<<<a.grid, Cfg::THREADS, Cfg::SMEM, stream>>>(a, map);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ECUDA;
-  if (!launch_dependent(kern, dim3(a.grid), Cfg::THREADS, Cfg::SMEM, stream, a, map)) return KVQ_ECUDA;
   if (a.grid == 1) return KVQ_OK;
   const int64_t rows = static_cast<int64_t>(a.total_q) * (a.num_q_heads / a.num_kv_heads);
   const dim3 joins(a.grid - 1, std::min<int64_t>(a.tile, rows));
