@@ -403,9 +403,14 @@ bool plan_page(const kvq_layout& L, int32_t batch, int32_t total_q, int32_t num_
   if (batch < 0 || total_q < 0 || num_q_heads <= 0 || max_pages <= 0 || num_q_heads % L.num_kv_heads != 0) return false;
   if (L.mla || L.page_size != kPageTokens || !page_supported(L.head_dim)) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  // a tile of the rows kernel holds a sequence's rows of a kv head, or the flash kernel takes them
+  // A tile of the rows kernel holds a sequence's rows of a kv head, or the call is small for it, or the flash kernel takes
+  // it, which starts and joins more slowly but reads K and V once for 256 rows instead of 16.  Small: as the table's width has it,
+  // since lengths are not known here.  With 8 / 2 heads of 128 over 2048 tokens (rows kernel, flash kernel): 32 new
+  // tokens, 2080 units, 29 and 41 us; 128 tokens, 8700 units, 39 and 47 us; over 8192 tokens 64 and 128 new ones, 16500 and
+  // 33300 units, 47 and 49, 62 and 49 us; 32 / 8 heads over 512 tokens, 64 new ones, 4600 units, 37 and 31 us.
   const double rows = static_cast<double>(total_q) * (num_q_heads / L.num_kv_heads);
-  pp->flash = total_q > batch && rows > static_cast<double>(kPageRowsTile) * batch;
+  pp->flash = total_q > batch && rows > static_cast<double>(kPageRowsTile) * batch &&
+              rows / kPageRowsTile * L.num_kv_heads * max_pages > kPageRowsUnits;
   const int32_t tile = pp->tile = pp->flash ? page_flash_rows(L.head_dim) : rows <= 8.0 * batch ? 8 : kPageRowsTile;
   const int32_t least = pp->flash ? kPageFlashUnits : kPageMinUnits;
   const size_t slot = tile * (static_cast<size_t>(L.head_dim) + 2) * sizeof(float);

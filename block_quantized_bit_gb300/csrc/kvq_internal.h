@@ -254,6 +254,7 @@ struct PageArgs {
   kvq_out_dtype out_dtype;
 };
 constexpr int kPageRowsTile = 16;  // query rows of a tile of the rows kernel at most (8 or 16)
+constexpr double kPageRowsUnits = 4096;  // (tile, page) units up to which several tiles of a sequence stay with the rows kernel
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
 constexpr int kPageRunMost = 60;   // bytes of a CTA's first run, at most ...
 constexpr int kPageRunBytes = kPageRunMost + 4;  // ... and its report
