@@ -161,15 +161,11 @@ def _kind(kind) -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # (current_stream() builds an object, 3 us)
-    if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+    return _raw_stream(stream, None if stream is not None else torch.cuda.current_device())
 
 
 @dataclass
@@ -287,7 +283,7 @@ def kvq_decode(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
         od = KVQ_OUT_F32
     else:
         raise TypeError("out must be bfloat16 or float32")
-    _check_by_page(pool, scales, layout, kind)
+    _check_by_page(q, pool, scales, block_table, seq_lens, None, out, layout, kind)
     o = ctypes.byref(_opts(pages_per_split, path)) if pages_per_split or path else None
     _check(lib().kvq_decode_ex(_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]),
                                _ptr(seq_lens), int(seq_lens.shape[0]), int(q.shape[1]), float(sm_scale), _ptr(out),
@@ -305,7 +301,7 @@ def kvq_decode_noalloc(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor
     overlap on the GPU share it and race.
     """
     od = KVQ_OUT_BF16 if out.dtype == torch.bfloat16 else KVQ_OUT_F32
-    _check_by_page(pool, scales, layout, kind)
+    _check_by_page(q, pool, scales, block_table, seq_lens, None, out, layout, kind)
     _check(lib().kvq_decode_noalloc(_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]),
                                     _ptr(seq_lens), int(seq_lens.shape[0]), int(q.shape[1]), float(sm_scale),
                                     _ptr(out), od, ctypes.byref(layout.c()), _kind(kind), _stream(stream)),
@@ -400,7 +396,7 @@ def kvq_extend(q: torch.Tensor, pool: torch.Tensor, scales: torch.Tensor, block_
         od = KVQ_OUT_F32
     else:
         raise TypeError("out must be bfloat16 or float32")
-    _check_by_page(pool, scales, layout, kind)
+    _check_by_page(q, pool, scales, block_table, seq_lens, q_start, out, layout, kind)
     total_q, Hq = q.shape[0], q.shape[1]
     B = seq_lens.numel()
     args = (_ptr(q), _ptr(pool), _ptr(scales), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
@@ -483,10 +479,27 @@ def _check_pool(pool, scales, info, kind, device):
     return k, None if scales is None else scales.data_ptr()
 
 
-def _check_by_page(pool, scales, layout, kind):
-    """What the decode and the extend check of a pool whose scales belong to pages: they are fp32 and fewer."""
-    if _kind(kind) == KVQ_FP8_E4M3_PAGE:
-        _check_pool(pool, scales, _layout_info(layout), KVQ_FP8_E4M3_PAGE, torch.cuda.current_device())
+_BY_PAGE_NAMES, _BY_PAGE_TYPES = ("q", "block_table", "seq_lens"), (_BF16, _I32, _I32)
+
+
+def _check_by_page(q, pool, scales, block_table, seq_lens, q_start, out, layout, kind):
+    """What the decode and the extend check of a call over a pool whose scales belong to pages."""
+    if _kind(kind) != KVQ_FP8_E4M3_PAGE:
+        return
+    device = _check_args(_BY_PAGE_NAMES, _BY_PAGE_TYPES, q, block_table, seq_lens)
+    _check_pool(pool, scales, _layout_info(layout), KVQ_FP8_E4M3_PAGE, device)
+    _check_tables(block_table, seq_lens, None, layout)
+    if q.dim() != 3 or q.shape[2] != layout.head_dim or out.shape != q.shape:
+        raise ValueError("q and out must be [rows, heads, %d]" % layout.head_dim)
+    if not out.is_contiguous() or out.get_device() != device:
+        raise ValueError("out must be contiguous and on the current CUDA device")
+    if q_start is None:
+        if len(q) != seq_lens.numel():
+            raise ValueError("q must have one row per sequence")
+    else:
+        _check_args(("q_start",), (_I32,), q_start)
+        if q_start.numel() != seq_lens.numel() + 1:
+            raise ValueError("q_start must be [batch + 1]")
 
 
 def _out_dtype(out):
