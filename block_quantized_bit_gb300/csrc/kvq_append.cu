@@ -12,9 +12,9 @@
 // one warp (head_dim 64, 128, 256; otherwise from a second load).  A CTA takes up to 8 tokens, and finds their places, pages
 // and angles once, into shared memory, while its first rows are on their way; 3 or 4 rows a thread are in flight.  With
 // one row in flight and one token a CTA, four prompts of 400 to 2048 tokens with 128 heads of 576 (64 of them rotated) and
-// their latent rows took 666 us, eight turns of 500 to 4096 tokens with 32 + 2 x 8 heads of 128 197 us; now 385 us (4.9 of
-// the 6.8 TB/s that a copy reaches) and 121 us (3.8 TB/s, with the pages below).  What bounds it
-// now is the arithmetic between loads: without a rotation, 18400 x 32 heads of 128 go at 5.5 TB/s, with one at 4.2.
+// their latent rows took 666 us, eight turns of 500 to 4096 tokens with 32 + 2 x 8 heads of 128 197 us; now 374 us (5.1 of
+// the 6.8 TB/s that a copy reaches) and 114 us (4.0 TB/s, with the pages below).  The arithmetic between loads bounds it:
+// with one value at a time in place of two (mul2, add2) these took 381 and 117 us.
 // append_pages_kernel: KVQ_FP8_E4M3_PAGE.  A warp owns one (page, K or V, head): its scale is a power of two that only
 // grows, s = 2^e with the least e that lets every row stored since the page was opened fit (|x| <= 448 s), so a page that outgrows
 // its scale has its older codes multiplied by 2^(e_old - e_new): exact but for values that fall below E4M3's normal
@@ -117,6 +117,20 @@ __device__ __forceinline__ void bf16x8(uint4 v, float (&x)[8]) {
   }
 }
 
+// Products of two values, each rounded by itself, and their sums.  A packed product and sum would be contracted into one
+// rounding, also with .rn: the product is a fused one with -0, which the compiler does not know to be that (minus_zero).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b, float minus_zero) {
+  return ffma2(a, b, make_float2(minus_zero, minus_zero));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Angles of a token in shared memory, rot_dim floats in quads.  Halves that pair: a thread takes two neighbouring quads of
 // the cosines and of the sines, so the even ones come first, which lets eight neighbouring threads read 128 bytes in a row.
 __device__ __forceinline__ int32_t quad_place(const AppendArgs& a, int32_t quad) {
@@ -153,20 +167,25 @@ struct Turn {
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   }
   // x: the thread's elements, y: their partners
-  __device__ __forceinline__ void apply(float (&x)[8], const float (&y)[8]) const {
+  __device__ __forceinline__ void apply(float (&x)[8], const float (&y)[8], float minus_zero) const {
     if (!on) return;
+    // two at a time; a difference as the sum with the negative product
     if (partner == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float u = x[2 * i], v = x[2 * i + 1];
-        x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(v, s[i]));
-        x[2 * i + 1] = __fadd_rn(__fmul_rn(v, c[i]), __fmul_rn(u, s[i]));
+        const float2 z = add2(mul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(c[i], c[i]), minus_zero),
+                              mul2(make_float2(x[2 * i + 1], x[2 * i]), make_float2(-s[i], s[i]), minus_zero));
+        x[2 * i] = z.x;
+        x[2 * i + 1] = z.y;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = __fmul_rn(x[i], c[i]), q = __fmul_rn(y[i], s[i]);
-        x[i] = low ? __fsub_rn(p, q) : __fadd_rn(p, q);
+      for (int i = 0; i < 8; i += 2) {
+        const float2 q = mul2(make_float2(y[i], y[i + 1]), make_float2(s[i], s[i + 1]), minus_zero);
+        const float2 z = add2(mul2(make_float2(x[i], x[i + 1]), make_float2(c[i], c[i + 1]), minus_zero),
+                              low ? make_float2(-q.x, -q.y) : q);
+        x[i] = z.x;
+        x[i + 1] = z.y;
       }
     }
   }
@@ -314,7 +333,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int32_t t0, int
       if constexpr (SHFL) bf16x8(raw[u], y);  // (exchanged below)
       else bf16x8(other[u], y);
       turn.angles(a, turns + k * a.rot_dim, e);
-      turn.apply(x, y);
+      turn.apply(x, y, a.minus_zero);
     }
   };
   while (at.k < nt) {
@@ -466,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) append_pages_kerne
         float y[8];
         bf16x8(other, y);
         turn.angles(a, turns + r * a.rot_dim, e);
-        turn.apply(x, y);
+        turn.apply(x, y, a.minus_zero);
       }
     }
   };

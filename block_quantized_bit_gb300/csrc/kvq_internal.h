@@ -219,6 +219,7 @@ struct AppendArgs {
   uint32_t* status;
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
   int64_t num_pages;
+  float minus_zero = -0.0f;
   int64_t page_ctas;          // CTAs of the pages kernel that write pages (append_grid)
   int32_t max_pages, batch, total, num_q_heads, num_kv_heads, n_kv, head_dim, page_size;
   int32_t max_position, rot_dim, rot_offset, interleaved;  // rot_dim 0: no rotation
