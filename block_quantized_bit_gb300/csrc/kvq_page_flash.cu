@@ -19,6 +19,11 @@
 // Work: a unit is a key tile of an item (one or two tiles of a kv head).  All units lie in one order, and every CTA takes an
 // equal run of them, so that a few long contexts fill the GPU as well as many short ones.  A run that is all of an item
 // gives its output, other runs leave partial sums for a second kernel, its programmatic dependent.
+// Measured: 2048 tokens after 30000 with 32 heads of 128 over 8: 717 us, 1.44 PFLOP/s, 75% of the bf16 GEMM rate; eight turns
+// of 100 to 1024 tokens after 700 to 8192, 16 heads over 8: 226 us, 1.0 PFLOP/s (an item's start and end take the time of six
+// key tiles); four turns of 600 to 2048 tokens with 32 heads of 64 over 8: 125 us, bound by the exponentials, of which
+// head_dim 64 has twice as many per product.  The rows' scores stay in registers (128 of a row at head_dim 64 and 128): read
+// twice from tensor memory the first case took 960 us.
 // Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
 #include <cuda.h>
 

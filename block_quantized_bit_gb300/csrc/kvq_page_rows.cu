@@ -15,6 +15,8 @@
 // equal run of them, whatever the lengths.  The four warps of a CTA walk every fourth page, each with its own ring of TMA
 // boxes (swizzled: no bank conflicts), and join at the end of each tile's run.  A run that is all of a tile's pages
 // gives the output, other runs leave partial sums, which a second kernel, its programmatic dependent, joins.
+// Measured: one token each of 64 sequences over 256 to 16384 tokens, 32 heads of 128 over 8: 213 us, 5.4 of the 6.8 TB/s that a
+// copy reaches (with tiles of 16 rows, half of them empty, 256 us); of 4 over 131072 tokens, 16 heads of 256 over 2: 101 us, 5.3 TB/s.
 #include <cuda.h>
 
 #include <algorithm>
