@@ -42,6 +42,11 @@ constexpr int kM = 128;           // rows of a tile
 constexpr int kConvWarps = 2;     // that turn V's codes into f16
 constexpr int kTmemCols = 512;
 
+// What a row's factor from codes to scores is kept within, so that it is neither 0 nor infinite once a page's scale (2^-32 ..
+// 2^32) has joined it: 0 times the -inf of an unseen key would be NaN.  It changes no result: under 2^-94 every score is
+// below 2^-30 (|S| < 2^29), and from 2^65 on scores that differ at all do so by more than 2^7, which leaves the largest alone.
+constexpr float kMultLeast = 0x1p-94f, kMultMost = 0x1p65f;
+
 // What the softmax and the converting warps know of the pages of a key tile.
 template <int PAGES>
 struct alignas(16) PageInfo {
@@ -675,7 +680,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
             const int e2 = min(max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -100), 100);
             const float up = __int_as_float((7 - e2 + 127) << 23);  // the largest comes to [2^7, 2^8)
             const int of_mine = __shfl_sync(0xffffffffu, e2, lane % ROWS * PER_LINE);  // (row lane % ROWS of this step)
-            if (lane / ROWS == i0 + i) mult = a.score_scale * __int_as_float((of_mine - 7 + 127) << 23);
+            if (lane / ROWS == i0 + i)
+              mult = fminf(fmaxf(a.score_scale * __int_as_float((of_mine - 7 + 127) << 23), kMultLeast), kMultMost);
             const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
             uint32_t hi[4], lo[4];
 #pragma unroll

@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = min(max((__float_as_int(top) >> 23) - 127, -100), 100);
       const float up = __int_as_float((14 - e + 127) << 23);
-      const float back = a.score_scale * __int_as_float((e - 14 + 127) << 23);
+      // (within 2^95, so that no page's scale makes it infinite: 0 times that would be NaN.  Scores that differ there do so by
+      // 2^-33 2^95 2^-32 at least, which leaves the largest alone)
+      const float back = fminf(fmaxf(a.score_scale * __int_as_float((e - 14 + 127) << 23), -0x1p95f), 0x1p95f);
 #pragma unroll
       for (int c = 0; c < 2; ++c) rowscale[n][c] = __shfl_sync(0xffffffffu, back, (2 * t4 + c) * 4);
       // k-step (x, c, i): lane t4 holds dims 128 x + 32 t4 + 16 c + 4 i ... + 3 of its row (D = 64: 16 t4 + 4 i)
