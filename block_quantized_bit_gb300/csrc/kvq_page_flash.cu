@@ -677,7 +677,8 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));  // bf16 magnitudes sort as integers
 #pragma unroll
             for (int o = PER_LINE / 2; o > 0; o >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const int e2 = min(max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -100), 100);
+            // (-119: 2^(7 - e2) ends at 2^126; rows that lie below keep fewer bits)
+            const int e2 = max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -119);
             const float up = __int_as_float((7 - e2 + 127) << 23);  // the largest comes to [2^7, 2^8)
             const int of_mine = __shfl_sync(0xffffffffu, e2, lane % ROWS * PER_LINE);  // (row lane % ROWS of this step)
             if (lane / ROWS == i0 + i)
