@@ -679,7 +679,9 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
             for (int o = PER_LINE / 2; o > 0; o >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
             // (-119: 2^(7 - e2) ends at 2^126; rows that lie below keep fewer bits)
             const int e2 = max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -119);
-            const float up = __int_as_float((7 - e2 + 127) << 23);  // the largest comes to [2^7, 2^8)
+            // the largest comes to [2^7, 2^8); a row with an infinity becomes NaN throughout, as one with a NaN does: the conversion
+            // would make a number of it
+            const float up = __int_as_float(e2 == 128 ? 0x7FFFFFFF : (7 - e2 + 127) << 23);
             const int of_mine = __shfl_sync(0xffffffffu, e2, lane % ROWS * PER_LINE);  // (row lane % ROWS of this step)
             if (lane / ROWS == i0 + i)
               mult = fminf(fmaxf(a.score_scale * __int_as_float((of_mine - 7 + 127) << 23), kMultLeast), kMultMost);

@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = max((__float_as_int(top) >> 23) - 127, -100);  // (2^114 still brings the least bf16 to an f16)
-      const float up = __int_as_float((14 - e + 127) << 23);
+      // (a row with an infinity becomes NaN throughout: scores of -inf alone would look like a row that sees nothing)
+      const float up = __int_as_float(e == 128 ? 0x7FFFFFFF : (14 - e + 127) << 23);
       // (within 2^95, so that no page's scale makes it infinite: 0 times that would be NaN.  Scores that differ there do so by
       // 2^-33 2^95 2^-32 at least, which leaves the largest alone)
       const float back = fminf(fmaxf(a.score_scale * __int_as_float((e - 14 + 127) << 23), -0x1p95f), 0x1p95f);
