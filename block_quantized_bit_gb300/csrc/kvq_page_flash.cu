@@ -4,9 +4,12 @@
 // 4 D FLOPs per (row, key) against 2 D bytes per key for up to 256 rows: bound by the tensor pipe.
 //
 // The scales never meet a code, so K's codes go to the tensor cores as they lie in the pool: S = Q . K^T in 8 bits, with
-// each row of q, scaled by a power of two, as the sum of two E4M3 terms (bf16 has 8 significant bits, a term
-// 4; what is 2^-10 of the row's largest or less loses some, at most 2^-18 of the largest).  Two 8-bit products take the
-// time of one 16-bit one and need no conversion.  For the output P has to keep more bits than 8-bit terms give cheaply
+// each row of q, scaled by a power of two, as the sum of an E5M2 and an E4M3 term: bf16 has 8 significant bits; the first
+// takes 3 of them, and what is left of an element in [2^e, 2^(e + 1)) is a multiple of 2^(e - 7) up to 2^(e - 3), which 4 bits
+// hold.  With the row's largest element in [2^11, 2^12) (what is left of it then ends below 448), elements of 2^-13 of it and more
+// enter exactly, smaller ones are off by at most 2^-21 of it (half of E4M3's least step, 2^-10, to 2^11).  Two E4M3 terms with the
+// largest in [2^7, 2^8) were exact down to 2^-9 of it and off by up to 2^-17.  Two 8-bit products take the time of one 16-bit one
+// and need no conversion of K.  For the output P has to keep more bits than 8-bit terms give cheaply
 // (two terms would cost five instructions a probability), so V's codes become f16 instead, exactly and once for up
 // to 256 rows, and P is rounded to f16 (2^-11).
 //
@@ -170,10 +173,11 @@ struct Shape {
   }
 };
 
-// S = Q . K^T in E4M3 over a slice of STEPS k-steps of 32 bytes, both terms of q (`term` descriptor units apart) into the
-// same sums, from one elect.sync.
+// S = Q . K^T in 8 bits over a slice of STEPS k-steps of 32 bytes, both terms of q (`term` descriptor units apart, the second
+// with an instruction descriptor of its own) into the same sums, from one elect.sync.
 template <int STEPS>
-__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint64_t term, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint64_t term, uint32_t idesc, uint32_t idesc2,
+                                        uint32_t acc) {
   if constexpr (STEPS == 4) {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, c0, c1, c2, c3, b1, b2, b3;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -185,11 +189,11 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, 1;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c0, %2, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c1, b1, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c2, b2, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c3, b3, %3, 1;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "l"(term)
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c0, %2, %6, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c1, b1, %6, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c2, b2, %6, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c3, b3, %6, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "l"(term), "r"(idesc2)
         : "memory");
   } else {
     static_assert(STEPS == 2, "2 or 4 steps");
@@ -199,14 +203,15 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c0, %2, %3, 1;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c1, b1, %3, 1;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "l"(term)
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c0, %2, %6, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c1, b1, %6, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "l"(term), "r"(idesc2)
         : "memory");
   }
 }
 
-// Instruction descriptor: M = 128, N columns, fp32 sums; E4M3 x E4M3 and f16 x f16 both have code 0.
+// Instruction descriptor: M = 128, N columns, fp32 sums; E4M3 x E4M3 and f16 x f16 both have code 0, E5M2 for A adds kE5M2A.
+constexpr uint32_t kE5M2A = 1u << 7;
 __device__ __forceinline__ uint32_t page_idesc(int n, bool b_mn_major) {
   return 1u << 4 | static_cast<uint32_t>(b_mn_major) << 16 | static_cast<uint32_t>(n >> 3) << 17 |
          static_cast<uint32_t>(kM >> 4) << 24;
@@ -236,10 +241,10 @@ __device__ __forceinline__ void cp_async16(uint8_t* to, const void* from, bool t
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
-// Two values as the sum of two E4M3 terms each: codes of the nearest and of what is left.
-__device__ __forceinline__ void e4m3_terms(uint32_t f16x2, uint32_t& hi, uint32_t& lo) {
+// Two values as the sum of an E5M2 and an E4M3 term each: codes of the nearest and of what is left.
+__device__ __forceinline__ void fp8_terms(uint32_t f16x2, uint32_t& hi, uint32_t& lo) {
   asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\tsub.f16x2 d, %2, b;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 h, %2;\n\tcvt.rn.f16x2.e5m2x2 b, h;\n\tsub.f16x2 d, %2, b;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\tcvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
       : "=r"(hi), "=r"(lo)
       : "r"(f16x2));
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
 #pragma unroll
       for (int s = 0; s < SLICES; ++s)
         mma_fp8<Cfg::SLICE / 32>(tmem + buf * KT, q + ((s * kM * 128) >> 4), kk + ((s * KT * 128) >> 4), Cfg::Q_TERM >> 4,
-                                 idesc_qk, s > 0 ? 1u : 0u);
+                                 idesc_qk | kE5M2A, idesc_qk, s > 0 ? 1u : 0u);
       mma_commit(&bar_s_full[buf]);
       return true;
     };
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const int32_t rt = it.token_of(r), tok = it.tok0 + w * shape.tile_tok + rt;
         lim = rt < shape.tile_tok && tok < it.n ? it.len - it.n + tok + 1 : 0x7fffffff;
         lim_least = __reduce_min_sync(0xffffffffu, lim);
-        // as two E4M3 terms, in place: the lanes of a row find its largest element together, all read before any writes
+        // as two terms of 8 bits, in place: the lanes of a row find its largest element together, all read before any writes
         constexpr int STEPS = 32 / ROWS, AT_ONCE = 4;
 #pragma unroll 1
         for (int i0 = 0; i0 < STEPS; i0 += AT_ONCE) {
@@ -677,20 +682,20 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));  // bf16 magnitudes sort as integers
 #pragma unroll
             for (int o = PER_LINE / 2; o > 0; o >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
-            // (-119: 2^(7 - e2) ends at 2^126; rows that lie below keep fewer bits)
-            const int e2 = max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -119);
-            // the largest comes to [2^7, 2^8); a row with an infinity becomes NaN throughout, as one with a NaN does: the conversion
+            // (-115: 2^(11 - e2) ends at 2^126; rows that lie below keep fewer bits)
+            const int e2 = max(static_cast<int>(max(big >> 16, big & 0xFFFFu) >> 7) - 127, -115);
+            // the largest comes to [2^11, 2^12); a row with an infinity becomes NaN throughout, as one with a NaN does: the conversion
             // would make a number of it
-            const float up = __int_as_float(e2 == 128 ? 0x7FFFFFFF : (7 - e2 + 127) << 23);
+            const float up = __int_as_float(e2 == 128 ? 0x7FFFFFFF : (11 - e2 + 127) << 23);
             const int of_mine = __shfl_sync(0xffffffffu, e2, lane % ROWS * PER_LINE);  // (row lane % ROWS of this step)
             if (lane / ROWS == i0 + i)
-              mult = fminf(fmaxf(a.score_scale * __int_as_float((of_mine - 7 + 127) << 23), kMultLeast), kMultMost);
+              mult = fminf(fmaxf(a.score_scale * __int_as_float((of_mine - 11 + 127) << 23), kMultLeast), kMultMost);
             const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = unpack_bf16x2(x[e]);
-              e4m3_terms(pack_f16x2(f.x * up, f.y * up), hi[e], lo[e]);  // (f16 holds a scaled bf16 exactly, down to 2^-24)
+              fp8_terms(pack_f16x2(f.x * up, f.y * up), hi[e], lo[e]);  // (f16 holds a scaled bf16 exactly, down to 2^-24)
             }
             uint8_t* to = q_own + c16 % 2 * 8 +
                           (D == 64 ? rr * 64 + (((c16 / 2) ^ ((rr >> 1) & 3)) << 4)
