@@ -8,7 +8,7 @@
 namespace kvq {
 namespace {
 
-constexpr float kNoMax = -1e30f;  // reference of a row that has seen nothing
+constexpr float kNoMax = -0x1.fffffep127f;  // reference of a row that has seen nothing: below every finite score
 constexpr float kHead = 7.0f;     // log2 of the largest p when a row's reference moves ...
 constexpr float kLimit = 15.0f;   // ... and at most (P is f16, which ends at 2^16)
 

@@ -49,6 +49,10 @@ constexpr int kTmemCols = 512;
 // 2^32) has joined it: 0 times the -inf of an unseen key would be NaN.  It changes no result: under 2^-94 every score is
 // below 2^-30 (|S| < 2^29), and from 2^65 on scores that differ at all do so by more than 2^7, which leaves the largest alone.
 constexpr float kMultLeast = 0x1p-94f, kMultMost = 0x1p65f;
+// A row whose reference would pass this is given up: NaN, and a report.  Its reference is then above every score.  One fused multiply-add makes a key's exponent of its product
+// and keeps bits of that which the reference has rounded away: half a unit at most here, and from 2^24 on more than f16 has room
+// for.  To round the scores first where they are large cost 2 to 7% of the calls where none are (a branch in the softmax).
+constexpr float kFarScore = 0x1p22f, kGivenUp = 0x1.fffffep127f;
 
 // What the softmax and the converting warps know of the pages of a key tile.
 template <int PAGES>
@@ -716,7 +720,11 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         if (!warp_wait_far(&bar_pv_done[last_buf], last_use & 1)) { ok = false; break; }
         tc_fence_after();
         const Item& was = *sItem(k - 1);
-        const float inv = was.whole() ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+        if (m == kGivenUp && was_live) {
+          l = __int_as_float(0x7FFFFFFF);
+          page_report(a, kStatusBadExtend);
+        }
+        const float inv = was.whole() ? (l > 0.0f ? 1.0f / l : l) : 1.0f;  // (l: 0, or NaN)
         const int64_t slot = part_slot(place.total, sharers(place.total, a.grid, kPageFlashUnits), cta, was.first);
         const int32_t tok_w = was.tok0 + w * shape.tile_tok;
         // rows pass through the warp's 2 KB, 32 columns at a time, so that four lanes write 64 or 128 bytes of one row
@@ -831,9 +839,9 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
 #pragma unroll
         for (int p = 1; p < PAGES; ++p) top = fmaxf(top, fmaf(__uint_as_float(mx[p]), ks[p], ev[p]));
         // the reference moves when some row's largest passes it by more than 2^15; O and l are then rescaled
-        const bool moved = top > m + kLimit;
+        const bool moved = top - m > kLimit;
         if (__any_sync(0xffffffffu, moved)) {
-          const float now = moved ? top - kHead : m;
+          const float now = moved ? (fabsf(top) > kFarScore ? kGivenUp : top - kHead) : m;
           const float alpha = moved ? ex2(m - now) : 1.0f;
           m = now;
           l *= alpha;
@@ -927,7 +935,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) page_flash_join_kernel(const 
       x[k].y = fmaf(y.y, f, x[k].y * keep);
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l > 0.0f ? 1.0f / l : l;  // (0, or NaN)
   const int64_t out = (static_cast<int64_t>(it.q0 + tok) * a.num_q_heads + it.head0 + (r - rt * it.heads)) * D;
 #pragma unroll
   for (int k = 0; k < V2; ++k) {

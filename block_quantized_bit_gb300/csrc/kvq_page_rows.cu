@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
               float& x = sc[n][2 * h + e];
               x = fmaf(x, mult, ev);
               if (!whole && t0 + 8 * h + g8 >= sees[n][e]) x = -INFINITY;
-              over |= x > m[n][e] + kLimit;
             }
+            over |= fmaxf(sc[n][e], sc[n][2 + e]) - m[n][e] > kLimit;  // (m + kLimit would be rounded where m is large)
           }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
