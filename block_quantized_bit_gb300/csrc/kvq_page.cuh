@@ -159,9 +159,25 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// The exponent of a page's scale, and the scale's reciprocal.
-__device__ __forceinline__ float scale_exponent(float s) { return static_cast<float>((__float_as_int(s) >> 23) - 127); }
-__device__ __forceinline__ float scale_inverse(float s) { return __int_as_float(0x7F000000 - __float_as_int(s)); }
+// P, the f16 that meets a token's V codes, is 2^(score + ev - m).  A page whose V scale 2^e is far below that of pages before it
+// would leave P too few bits (f16 has 2^-14 to 2^15 in full), so its codes take up to 2^-14 of the scale, exactly: a code
+// is 2^-9 at the least and 4 bits wide.  `ref` is the largest e of the run so far, so the scales' part in P is within
+// 2^4 while pages' scales are within 2^18; P is then off by at most 2^-11 of itself or 2^-25 2^m, which is 2^-28 of the row's
+// largest p; further down by as much more.
+constexpr int kNearScales = 4;  // powers of two within which codes stay as they are: no product a code where scales are alike
+__device__ __forceinline__ int32_t codes_down(int32_t e, int32_t ref) {
+  return ref - e > kNearScales ? min(ref - e, 14) : 0;
+}
+__device__ __forceinline__ uint32_t f16x2_power(int32_t down) { return (15u - down) * 0x04000400u; }  // 2^-down, twice
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The exponent of a page's scale; 2^-e.
+__device__ __forceinline__ int32_t scale_exponent(float s) { return (__float_as_int(s) >> 23) - 127; }
+__device__ __forceinline__ float power_inverse(int32_t e) { return __int_as_float((127 - e) << 23); }
 
 }  // namespace
 }  // namespace kvq

@@ -11,7 +11,7 @@
 // largest in [2^7, 2^8) were exact down to 2^-9 of it and off by up to 2^-17.  Two 8-bit products take the time of one 16-bit one
 // and need no conversion of K.  For the output P has to keep more bits than 8-bit terms give cheaply
 // (two terms would cost five instructions a probability), so V's codes become f16 instead, exactly and once for up
-// to 256 rows, and P is rounded to f16 (2^-11).
+// to 256 rows, and P is rounded to f16: 2^-11, or 2^-28 of the row's largest p where V's scales are within 2^18 (codes_down).
 //
 // A tile is 128 query rows of one kv head: tokens times heads of its group (at most 128 heads; larger groups are cut).
 // Tensor memory at head_dim 64 and 128: S_A, S_B, O_A, O_B, two tiles A and B of a CTA whose softmax and MMAs alternate; at
@@ -58,9 +58,11 @@ constexpr float kFarScore = 0x1p22f, kGivenUp = 0x1.fffffep127f;
 template <int PAGES>
 struct alignas(16) PageInfo {
   float ks[PAGES];                // K's scale (1 for a masked page)
-  float ev[PAGES], unv[PAGES];    // V's exponent, and 2^-ev
+  float ev[PAGES], unv[PAGES];    // V's exponent but for what the codes take of it, and 2^-ev
   uint8_t rows[PAGES];            // rows that hold tokens; 0: masked
+  uint8_t down[PAGES];            // V's codes take 2^-down of the scale
   int32_t full;                   // every page of the tile has all its rows
+  int32_t any_down;
 };
 
 template <int D>
@@ -254,6 +256,22 @@ __device__ __forceinline__ void fp8_terms(uint32_t f16x2, uint32_t& hi, uint32_t
       : "r"(f16x2));
 }
 
+// Multiplies the f16 that a lane of a converting warp has written by what their pages' codes take of the scales; out of line, as
+// hardly any key tile needs it.
+template <int D>
+__device__ __noinline__ void take_down(uint8_t* v, const uint8_t* down, int cw, int r8, int c4) {
+  constexpr int KT = FCfg<D>::KT, PER_ROW = D / 64;
+  for (int i = cw; i < KT / 8 * PER_ROW; i += kConvWarps) {
+    const int row = i / PER_ROW * 8 + r8;
+    const uint32_t f = f16x2_power(down[row / kPage]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint4* x = reinterpret_cast<uint4*>(v + i % PER_ROW * KT * 128 + row * 128 + (((2 * c4 + k) ^ (row & 7)) << 4));
+      *x = make_uint4(mul_f16x2(x->x, f), mul_f16x2(x->y, f), mul_f16x2(x->z, f), mul_f16x2(x->w, f));
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
     page_flash_kernel(const PageArgs a, const __grid_constant__ CUtensorMap map) {
@@ -409,12 +427,22 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
       int32_t phys = fetch(0), phys_next = fetch(1);
       float ks, vs, ks_next = 1.0f, vs_next = 1.0f;
       scales(phys, ks, vs);
+      int32_t ref = -127, e = 0, down = 0;  // V's largest exponent so far; the lane's page's, and what its codes take
+      uint32_t downs = 0;                   // lanes whose page's codes take some
+      auto shares = [&] {                   // (of the 32 pages that the lanes hold)
+        e = phys >= 0 ? scale_exponent(vs) : -127;
+        ref = max(ref, __reduce_max_sync(0xffffffffu, e));
+        down = phys >= 0 ? codes_down(e, ref) : 0;
+        downs = __ballot_sync(0xffffffffu, down > 0);
+      };
+      shares();
       for (int32_t j = 0; j < it.kt1 - it.kt0; ++j, ++kv) {
         if (j > 0 && j % BATCH == 0) {
           phys = phys_next;
           ks = ks_next;
           vs = vs_next;
           phys_next = fetch(j / BATCH + 1);
+          shares();
         }
         if (j % BATCH == 1) scales(phys_next, ks_next, vs_next);
         const int32_t first = j % BATCH * PAGES;            // the lane of the tile's first page
@@ -428,10 +456,14 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const uint32_t fulls = __popc(__ballot_sync(0xffffffffu, rows == kPage));
         if (mine) {
           info.ks[x] = phys >= 0 ? ks : 1.0f;
-          info.ev[x] = phys >= 0 ? scale_exponent(vs) : 0.0f;
-          info.unv[x] = phys >= 0 ? scale_inverse(vs) : 1.0f;
+          info.ev[x] = phys >= 0 ? static_cast<float>(e + down) : 0.0f;
+          info.unv[x] = phys >= 0 ? power_inverse(e + down) : 1.0f;
           info.rows[x] = static_cast<uint8_t>(rows);
-          if (x == 0) info.full = fulls == PAGES;
+          info.down[x] = static_cast<uint8_t>(down);
+          if (x == 0) {
+            info.full = fulls == PAGES;
+            info.any_down = downs >> first & ((1u << PAGES) - 1);
+          }
         }
         __syncwarp();
         if (lane == 0) {
@@ -518,6 +550,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
           *reinterpret_cast<uint4*>(to + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4*>(to + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
+        if (info.any_down) take_down<D>(dst, info.down, cw, r8, c4);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

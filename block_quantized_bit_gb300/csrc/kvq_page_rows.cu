@@ -3,9 +3,9 @@
 //   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t:
 // the scales never meet a code.  Codes become f16 exactly, two per conversion; the products run on the warp-level tensor-core
 // instructions with f16 inputs and fp32 sums.  q enters as f16 as well, each row scaled by a power of two (exact: bf16
-// has 8 significant bits; only elements 2^31 times smaller than the row's largest lose some).  P is rounded to f16
-// (2^-11 of each), with the reference m at most 2^15 below the largest, so that what is 2^-40 of the largest
-// still counts.  2 D bytes per token and kv head are read once for up to 16 query rows: bound by HBM.
+// has 8 significant bits; only elements 2^31 times smaller than the row's largest lose some).  P is rounded to f16:
+// by 2^-11 of each, or 2^-28 of the row's largest p where V's scales are within 2^18 of one another (codes_down), since the reference m
+// is 2^7 to 2^15 below the largest.  2 D bytes per token and kv head are read once for up to 16 query rows: bound by HBM.
 //
 // A tile is 16 query rows of one kv head (heads of its group, and for kvq_extend tokens times heads), the MMA's M.  Of
 // every warp-level product m16n8k16 the tile's rows are A, 8 tokens (scores) or 8 dims (output) are B, and
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
       m[n][0] = m[n][1] = kNoMax;
       l[n][0] = l[n][1] = 0.0f;
     }
-    int32_t landed = 0;
+    int32_t landed = 0, ref = -127;  // ref: V's largest exponent so far
 
     for (int32_t i = 0; i < nw; ++i) {
       if (i > 0 && i % 32 == 0) {
@@ -316,7 +316,10 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
           }
         }
         // ---- y = score + ev in the exponent; what a row does not see is -inf
-        const float ev = scale_exponent(vscale), unv = scale_inverse(vscale);
+        const int32_t e2 = scale_exponent(vscale);
+        ref = max(ref, e2);
+        const int32_t down = codes_down(e2, ref);
+        const float ev = static_cast<float>(e2 + down), unv = power_inverse(e2 + down);
         const bool whole = t0 + kPage <= sees_least;
         bool over = false;
 #pragma unroll
@@ -390,6 +393,10 @@ __global__ void __launch_bounds__(RCfg<D, NT>::THREADS, RCfg<D, NT>::CTAS)
               uint32_t f[4];
               codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[0][k], v[1][k], pick), f[0], f[1]);
               codes_to_f16x2<KVQ_FP8_E4M3>(__byte_perm(v[2][k], v[3][k], pick), f[2], f[3]);
+              if (down > 0) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) f[y] = mul_f16x2(f[y], f16x2_power(down));
+              }
 #pragma unroll
               for (int n = 0; n < NT; ++n) mma_f16(o[n][(x * WORDS + k) * 2 + half], f, pf[n][0], pf[n][1]);
             }

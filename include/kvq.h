@@ -222,8 +222,9 @@ size_t kvq_decode_workspace_bytes_kind(const kvq_layout* layout, kvq_kind kind, 
  * kernel has a fixed cost of ~50 us); 1 otherwise; kvq_decode_path tells which.
  * KVQ_FP8_E4M3_PAGE has one kernel of its own, for every number of query heads per kv head: options must be 0 or NULL (else
  * KVQ_EUNSUPPORTED), kvq_decode_path does not speak of it, and the workspace is kvq_decode_workspace_bytes_kind's.  Its
- * products are those of the exact values code * scale, with P rounded to fp16 (error about 2^-12 of sum p|v|) and
- * fp32 sums.  A row of q that holds an infinity or a NaN gives NaN, here and in kvq_extend.
+ * products are those of the exact values code * scale, with fp32 sums and P rounded to fp16: each p is off by at most 2^-11 of
+ * itself or 2^-28 of its row's largest p, the latter times 2^(x - 18) for pages whose scale of V is 2^x, x > 18, below
+ * another's of the sequence.  A row of q that holds an infinity or a NaN gives NaN, here and in kvq_extend.
  */
 kvq_status kvq_decode(const void* q, const void* pool, const void* scales, const int32_t* block_table,
                       int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
