@@ -164,7 +164,6 @@ struct TreeArgs {
   int32_t head_dim;
   int32_t mask_words;
   int32_t grid;               // CTAs launched
-  int32_t tile;               // query rows of a unit of work
   float score_scale;          // sm_scale * log2(e)
   kvq_out_dtype out_dtype;
   kvq_kind kind;

@@ -108,7 +108,6 @@ struct Item {
   int32_t tok0;                   // first token of the item
   uint32_t per_head;              // 2^16 / heads, rounded up: r * per_head >> 16 = r / heads for r < 128
   int32_t kt0, kt1, all;          // key tiles of the run; of the item
-  int32_t pad;
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == all; }
 };
 static_assert(sizeof(Item) <= kPageRunMost && sizeof(Item) <= 64, "item slots");
