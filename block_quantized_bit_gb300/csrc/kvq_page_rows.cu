@@ -1,19 +1,20 @@
 // kvq_page_rows.cu -- attention of few query rows over a KVQ_FP8_E4M3_PAGE cache (kvq_decode, and kvq_extend's short
 // turns): K = 2^ek[page] code, V = 2^ev[page] code, one exponent per page of 16 tokens and head, so that
 //   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t:
-// the scales never meet a code.  Codes become f16 exactly, two per conversion; the products run on the warp-level tensor-core
+// the scales meet no code (but for V's on pages far below others, codes_down).  Codes become f16 exactly, two per conversion; the products run on the warp-level tensor-core
 // instructions with f16 inputs and fp32 sums.  q enters as f16 as well, each row scaled by a power of two (exact: bf16
 // has 8 significant bits; only elements 2^31 times smaller than the row's largest lose some).  P is rounded to f16:
 // by 2^-11 of each, or 2^-28 of the row's largest p where V's scales are within 2^18 of one another (codes_down), since the reference m
 // is 2^7 to 2^15 below the largest.  2 D bytes per token and kv head are read once for up to 16 query rows: bound by HBM.
 //
-// A tile is 16 query rows of one kv head (heads of its group, and for kvq_extend tokens times heads), the MMA's M.  Of
-// every warp-level product m16n8k16 the tile's rows are A, 8 tokens (scores) or 8 dims (output) are B, and
-// the scores come out in the very lanes that feed them to the output's products.  Nothing is transposed: a lane reads
-// 16 bytes of its token's K row, and of V 16 bytes of four tokens, whose codes pair up by byte permutes.
+// A tile is 8 or 16 query rows of one kv head (heads of its group, and for kvq_extend tokens times heads).  In every warp-level
+// product m16n8k16 codes are A, straight from shared memory: 16 tokens of a page (scores) or 16 dims (output) are its M, and 8 of
+// the tile's rows its N.  So a decode of a few heads leaves few columns empty, and the order of the dims within a product,
+// which does not matter, lets a lane read 16 bytes of a token's K row at a time, and of V 16 bytes of four tokens, whose codes pair
+// up by byte permutes.  Scores come out with tokens as rows; the output's products want them as columns, one movmatrix each.
 // Work: a unit is a (tile, page).  All units of the call lie in one order, sequence by sequence, and every CTA takes an
-// equal run of them, whatever the lengths.  The four warps of a CTA walk every fourth page, each with its own ring of TMA
-// boxes (swizzled: no bank conflicts), and join at the end of each tile's run.  A run that is all of a tile's pages
+// equal run of them, whatever the lengths.  The 8 warps of a CTA (4 at head_dim 256) take its pages in turn, each with its own
+// ring of TMA boxes (swizzled: no bank conflicts), and join at the end of each tile's run.  A run that is all of a tile's pages
 // gives the output, other runs leave partial sums, which a second kernel, its programmatic dependent, joins.
 // Measured: one token each of 64 sequences over 256 to 16384 tokens, 32 heads of 128 over 8: 213 us, 5.4 of the 6.8 TB/s that a
 // copy reaches (with tiles of 16 rows, half of them empty, 256 us); of 4 over 131072 tokens, 16 heads of 256 over 2: 101 us, 5.3 TB/s.
@@ -36,7 +37,8 @@ struct RCfg {
   static constexpr int ROWS = 8 * NT;                  // query rows of a tile
   static constexpr int WARPS = D == 256 ? 4 : 8;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int CTAS = D == 64 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2;  // resident per SM
+  // resident per SM: at head_dim 64 and 128 the kernels spill 16 to 124 bytes a thread for that (their caps are 64, 80 and 128 registers)
+  static constexpr int CTAS = D == 64 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2;
   static constexpr int PAGE_BYTES = kPage * D;         // codes of K or V of a page
   static constexpr int STAGE = 2 * PAGE_BYTES;
   static constexpr int STAGES = D == 64 ? (NT == 1 ? 3 : 4) : NT == 1 ? 2 : 3;
