@@ -530,6 +530,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
         const uint8_t* src = sC + s * Cfg::K_TILE;
         uint8_t* dst = sV + s * Cfg::V_TILE;
         const Info& info = sInfo[kv % INFO];
+        const int32_t some_down = *const_cast<const volatile int32_t*>(&info.any_down);  // (here, not behind the codes' loop)
         constexpr int PER_ROW = D / 64;  // steps of 64 codes in a row
 #pragma unroll 2
         for (int i = cw; i < KT / 8 * PER_ROW; i += kConvWarps) {
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(FCfg<D>::THREADS, 1)
           *reinterpret_cast<uint4*>(to + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4*>(to + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-        if (info.any_down) take_down<D>(dst, info.down, cw, r8, c4);
+        if (some_down) take_down<D>(dst, info.down, cw, r8, c4);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
