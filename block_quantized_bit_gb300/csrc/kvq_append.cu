@@ -14,7 +14,10 @@
 // one row in flight and one token a CTA, four prompts of 400 to 2048 tokens with 128 heads of 576 (64 of them rotated) and
 // their latent rows took 666 us, eight turns of 500 to 4096 tokens with 32 + 2 x 8 heads of 128 197 us; now 374 us (5.1 of
 // the 6.8 TB/s that a copy reaches) and 114 us (4.0 TB/s, with the pages below).  The arithmetic between loads bounds it:
-// with one value at a time in place of two (mul2, add2) these took 381 and 117 us.
+// with one value at a time in place of two (mul2, add2) these took 381 and 117 us.  Rows of 576 leave 40 of a CTA's 256 threads idle.
+// Further from the floor where a token has few rows: 18400 tokens with 32 + 2 x 8 heads of 128 take 119 us in KVQ_FP8_E4M3 and
+// 100 us in KVQ_FP8_E4M3_UNSCALED against 61 us, their keys and values alone 62 and 41 us against 17 us (kvq_store: 0.87 of the
+// rate).  A token is then one pass, and at most 8 of them stand behind a CTA's search for sequences, pages and angles.
 // append_pages_kernel: KVQ_FP8_E4M3_PAGE.  A warp owns one (page, K or V, head): its scale is a power of two that only
 // grows, s = 2^e with the least e that lets every row stored since the page was opened fit (|x| <= 448 s), so a page that outgrows
 // its scale has its older codes multiplied by 2^(e_old - e_new): exact but for values that fall below E4M3's normal

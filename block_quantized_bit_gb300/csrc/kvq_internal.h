@@ -258,7 +258,7 @@ constexpr double kPageRowsUnits = 4096;  // (tile, page) units up to which sever
 constexpr int kPageMinUnits = 8;   // (tile, page) units that are worth a CTA
 constexpr int kPageRunMost = 60;   // bytes of a CTA's first run, at most ...
 constexpr int kPageRunBytes = kPageRunMost + 4;  // ... and its report
-constexpr int kPageItemUnits = 6;   // key tiles' time that an item's start and end take
+constexpr int kPageItemUnits = 6;   // key tiles' time that an item's start and end take (measured at head_dim 128, used at all)
 constexpr int kPageFlashUnits = 10; // units (key tiles and items' starts) that are worth a CTA of the flash kernel
 bool page_supported(int32_t head_dim);
 int32_t page_rows_grid(int32_t head_dim, int32_t tile, int32_t sms);  // CTAs that are resident at once

@@ -1,7 +1,7 @@
 // kvq_page_flash.cu -- causal attention of many query rows over a KVQ_FP8_E4M3_PAGE cache (kvq_extend), on the tcgen05 tensor
 // cores, head_dim 64, 128 and 256, any number of query heads per kv head.  With K = 2^ek[page] code, V = 2^ev[page] code:
 //   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t.
-// 4 D FLOPs per (row, key) against 2 D bytes per key for up to 256 rows: bound by the tensor pipe.
+// 4 D FLOPs per (row, key) against 2 D bytes per key for up to 256 rows: the tensor pipe's floor.
 //
 // The scales never meet a code, so K's codes go to the tensor cores as they lie in the pool: S = Q . K^T in 8 bits, with
 // each row of q, scaled by a power of two, as the sum of an E5M2 and an E4M3 term: bf16 has 8 significant bits; the first
@@ -22,10 +22,11 @@
 // Work: a unit is a key tile of an item (one or two tiles of a kv head).  All units lie in one order, and every CTA takes an
 // equal run of them, so that a few long contexts fill the GPU as well as many short ones.  A run that is all of an item
 // gives its output, other runs leave partial sums for a second kernel, its programmatic dependent.
-// Measured: 2048 tokens after 30000 with 32 heads of 128 over 8: 717 us, 1.44 PFLOP/s, 75% of the bf16 GEMM rate; eight turns
-// of 100 to 1024 tokens after 700 to 8192, 16 heads over 8: 226 us, 1.0 PFLOP/s (an item's start and end take the time of six
-// key tiles); four turns of 600 to 2048 tokens with 32 heads of 64 over 8: 125 us, bound by the exponentials, of which
-// head_dim 64 has twice as many per product.  The rows' scores stay in registers (128 of a row at head_dim 64 and 128): read
+// Measured: 2048 tokens after 30000 with 32 heads of 128 over 8: 719 us, 1.45 PFLOP/s, 75% of the bf16 GEMM rate; eight turns
+// of 100 to 1024 tokens after 700 to 8192, 16 heads over 8: 228 us, 1.0 PFLOP/s; four turns of 600 to 2048 tokens with 32 heads of 64
+// over 8: 123 us, 0.43 PFLOP/s.  No pipe is busy in these two (tensor 51 and 24%, exponentials 25 and 24%): what is left is the way
+// from scores to P, one key tile after the other, and the items' starts, six key tiles' time each, in which the softmax warps fetch
+// q.  head_dim 256, one tile a CTA: 2048 tokens after 30000, 16 heads over 2: 1200 us, 0.87 PFLOP/s.  The rows' scores stay in registers (128 of a row at head_dim 64 and 128): read
 // twice from tensor memory the first case took 960 us.
 // Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
 #include <cuda.h>
