@@ -3,15 +3,16 @@
 //   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t.
 // 4 D FLOPs per (row, key) against 2 D bytes per key for up to 256 rows: the tensor pipe's floor.
 //
-// The scales never meet a code, so K's codes go to the tensor cores as they lie in the pool: S = Q . K^T in 8 bits, with
-// each row of q, scaled by a power of two, as the sum of an E5M2 and an E4M3 term: bf16 has 8 significant bits; the first
-// takes 3 of them, and what is left of an element in [2^e, 2^(e + 1)) is a multiple of 2^(e - 7) up to 2^(e - 3), which 4 bits
-// hold.  With the row's largest element in [2^11, 2^12) (what is left of it then ends below 448), elements of 2^-13 of it and more
-// enter exactly, smaller ones are off by at most 2^-21 of it (half of E4M3's least step, 2^-10, to 2^11).  Two E4M3 terms with the
-// largest in [2^7, 2^8) were exact down to 2^-9 of it and off by up to 2^-17.  Two 8-bit products take the time of one 16-bit one
-// and need no conversion of K.  For the output P has to keep more bits than 8-bit terms give cheaply
-// (two terms would cost five instructions a probability), so V's codes become f16 instead, exactly and once for up
-// to 256 rows, and P is rounded to f16: 2^-11, or 2^-28 of the row's largest p where V's scales are within 2^18 (codes_down).
+// K's scales never meet a code, so its codes go to the tensor cores as they lie in the pool: S = Q . K^T in 8 bits,
+// with each row of q, scaled by a power of two, as the sum of an E5M2 and an E4M3 term: bf16 has 8 significant bits;
+// the first takes 3 of them, and what is left of an element in [2^e, 2^(e + 1)) is a multiple of 2^(e - 7) up to
+// 2^(e - 3), which 4 bits hold.  With the row's largest element in [2^11, 2^12) (what is left of it then ends below 448),
+// elements of 2^-13 of it and more enter exactly, smaller ones are off by at most 2^-21 of it (half of E4M3's least
+// step, 2^-10, to 2^11).  Two E4M3 terms with the largest in [2^7, 2^8) were exact down to 2^-9 of it and off by up
+// to 2^-17.  Two 8-bit products take the time of one 16-bit one and need no conversion of K.  For the output P has to
+// keep more bits than 8-bit terms give cheaply (two terms would cost five instructions a probability), so V's codes
+// become f16 instead, exactly and once for up to 256 rows, and P is rounded to f16: 2^-11, or 2^-28 of the row's
+// largest p where V's scales are within 2^18 (codes_down).
 //
 // A tile is 128 query rows of one kv head: tokens times heads of its group (at most 128 heads; larger groups are cut).
 // Tensor memory at head_dim 64 and 128: S_A, S_B, O_A, O_B, two tiles A and B of a CTA whose softmax and MMAs alternate; at
@@ -22,12 +23,13 @@
 // Work: a unit is a key tile of an item (one or two tiles of a kv head).  All units lie in one order, and every CTA takes an
 // equal run of them, so that a few long contexts fill the GPU as well as many short ones.  A run that is all of an item
 // gives its output, other runs leave partial sums for a second kernel, its programmatic dependent.
-// Measured: 2048 tokens after 30000 with 32 heads of 128 over 8: 719 us, 1.45 PFLOP/s, 75% of the bf16 GEMM rate; eight turns
-// of 100 to 1024 tokens after 700 to 8192, 16 heads over 8: 228 us, 1.0 PFLOP/s; four turns of 600 to 2048 tokens with 32 heads of 64
-// over 8: 123 us, 0.43 PFLOP/s.  No pipe is busy in these two (tensor 51 and 24%, exponentials 25 and 24%): what is left is the way
-// from scores to P, one key tile after the other, and the items' starts, six key tiles' time each, in which the softmax warps fetch
-// q.  head_dim 256, one tile a CTA: 2048 tokens after 30000, 16 heads over 2: 1200 us, 0.87 PFLOP/s.  The rows' scores stay in registers (128 of a row at head_dim 64 and 128): read
-// twice from tensor memory the first case took 960 us.
+// Measured: 2048 tokens after 30000 with 32 heads of 128 over 8: 719 us, 1.45 PFLOP/s, 75% of the bf16 GEMM rate;
+// eight turns of 100 to 1024 tokens after 700 to 8192, 16 heads over 8: 228 us, 1.0 PFLOP/s; four turns of 600 to
+// 2048 tokens with 32 heads of 64 over 8: 123 us, 0.43 PFLOP/s.  No pipe is busy in these two (tensor 51 and 24%,
+// exponentials 25 and 24%): what is left is the way from scores to P, one key tile after the other, and the items'
+// starts, six key tiles' time each, in which the softmax warps fetch q.  head_dim 256, one tile a CTA: 2048 tokens
+// after 30000, 16 heads over 2: 1200 us, 0.87 PFLOP/s.  The rows' scores stay in registers (128 of a row at head_dim
+// 64 and 128): read twice from tensor memory the first case took 960 us.
 // Every wait is bounded (2 s) and reports a timeout in the status word instead of hanging.
 #include <cuda.h>
 
@@ -50,9 +52,10 @@ constexpr int kTmemCols = 512;
 // 2^32) has joined it: 0 times the -inf of an unseen key would be NaN.  It changes no result: under 2^-94 every score is
 // below 2^-30 (|S| < 2^29), and from 2^65 on scores that differ at all do so by more than 2^7, which leaves the largest alone.
 constexpr float kMultLeast = 0x1p-94f, kMultMost = 0x1p65f;
-// A row whose reference would pass this is given up: NaN, and a report.  Its reference is then above every score.  One fused multiply-add makes a key's exponent of its product
-// and keeps bits of that which the reference has rounded away: half a unit at most here, and from 2^24 on more than f16 has room
-// for.  To round the scores first where they are large cost 2 to 7% of the calls where none are (a branch in the softmax).
+// A row whose reference would pass this is given up: NaN, and a report.  Its reference is then above every score.
+// One fused multiply-add makes a key's exponent of its product and keeps bits of that which the reference has rounded
+// away: half a unit at most here, and from 2^24 on more than f16 has room for.  To round the scores first where they
+// are large cost 2 to 7% of the calls where none are (a branch in the softmax).
 constexpr float kFarScore = 0x1p22f, kGivenUp = 0x1.fffffep127f;
 
 // What the softmax and the converting warps know of the pages of a key tile.

@@ -1,11 +1,12 @@
 // kvq_page_rows.cu -- attention of few query rows over a KVQ_FP8_E4M3_PAGE cache (kvq_decode, and kvq_extend's short
 // turns): K = 2^ek[page] code, V = 2^ev[page] code, one exponent per page of 16 tokens and head, so that
 //   y_t = log2(e) sm_scale 2^ek q.code_t + ev,   p_t = 2^(y_t - m),   out = sum p_t code_t / sum 2^-ev p_t:
-// the scales meet no code (but for V's on pages far below others, codes_down).  Codes become f16 exactly, two per conversion; the products run on the warp-level tensor-core
-// instructions with f16 inputs and fp32 sums.  q enters as f16 as well, each row scaled by a power of two (exact: bf16
-// has 8 significant bits; only elements 2^31 times smaller than the row's largest lose some).  P is rounded to f16:
-// by 2^-11 of each, or 2^-28 of the row's largest p where V's scales are within 2^18 of one another (codes_down), since the reference m
-// is 2^7 to 2^15 below the largest.  2 D bytes per token and kv head are read once for up to 16 query rows: bound by HBM.
+// the scales meet no code (but for V's on pages far below others, codes_down).  Codes become f16 exactly, two per
+// conversion; the products run on the warp-level tensor-core instructions with f16 inputs and fp32 sums.  q enters as
+// f16 as well, each row scaled by a power of two (exact: bf16 has 8 significant bits; only elements 2^31 times
+// smaller than the row's largest lose some).  P is rounded to f16: by 2^-11 of each, or 2^-28 of the row's largest p
+// where V's scales are within 2^18 of one another (codes_down), since the reference m is 2^7 to 2^15 below the
+// largest.  2 D bytes per token and kv head are read once for up to 16 query rows: bound by HBM.
 //
 // A tile is 8 or 16 query rows of one kv head (heads of its group, and for kvq_extend tokens times heads).  In every warp-level
 // product m16n8k16 codes are A, straight from shared memory: 16 tokens of a page (scores) or 16 dims (output) are its M, and 8 of
@@ -37,7 +38,8 @@ struct RCfg {
   static constexpr int ROWS = 8 * NT;                  // query rows of a tile
   static constexpr int WARPS = D == 256 ? 4 : 8;
   static constexpr int THREADS = WARPS * 32;
-  // resident per SM: at head_dim 64 and 128 the kernels spill 16 to 124 bytes a thread for that (their caps are 64, 80 and 128 registers)
+  // Resident per SM.  At head_dim 64 and 128 the kernels spill 16 to 124 bytes a thread for that: their caps are 64, 80
+  // and 128 registers.
   static constexpr int CTAS = D == 64 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2;
   static constexpr int PAGE_BYTES = kPage * D;         // codes of K or V of a page
   static constexpr int STAGE = 2 * PAGE_BYTES;

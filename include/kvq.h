@@ -155,9 +155,10 @@ kvq_status kvq_store(void* pool, void* scales, const void* k, const void* v, con
  * max_pages_per_seq * page_size is skipped and makes kvq_workspace_status report KVQ_EINVAL, as do a block-table entry >=
  * layout->num_pages (the token is not stored) and a position outside [0, max_position) (the nearest one is taken).
  * Rows of q_out that no sequence covers are left as they are; what becomes of rows that two consistent sequences claim is
- * unspecified.  NaN and infinite inputs are outside the domain, as for kvq_store.  Supported: every layout and page size for the kinds with a
- * scale per row (head_dim up to 2048); KVQ_FP8_E4M3_PAGE as said at kvq_kind; otherwise KVQ_EUNSUPPORTED, as for more
- * than 2^31 - 1 CTAs.  Two calls that store to the same page must not run at the same time.
+ * unspecified.  NaN and infinite inputs are outside the domain, as for kvq_store.  Supported: every layout and page
+ * size for the kinds with a scale per row (head_dim up to 2048); KVQ_FP8_E4M3_PAGE as said at kvq_kind; otherwise
+ * KVQ_EUNSUPPORTED, as for more than 2^31 - 1 CTAs.  Two calls that store to the same page must not run at the same
+ * time.
  */
 typedef struct kvq_rope {
     const float* cos_sin;  /* device fp32 [max_position][rot_dim], 16-byte aligned: the cosines of a position's
@@ -328,13 +329,14 @@ kvq_status kvq_store_act_quant(void* pool, void* scales, const void* kv, const i
  * q_start and seq_lens are read on the device: a sequence with n_b < 0, n_b > seq_lens[b] or q_start[b + 1]
  * > total_q is skipped and makes kvq_workspace_status report KVQ_EINVAL, as does a block-table entry >=
  * layout->num_pages (that page is skipped).  Asynchronous on `stream`.
- * KVQ_FP8_E4M3_PAGE has two kernels of its own, for head_dim 64, 128 and 256 and any number of query heads per kv head: options must
- * be 0 or NULL (else KVQ_EUNSUPPORTED), kvq_extend_path does not speak of it, the workspace is
- * kvq_extend_workspace_bytes_kind's, and the rows of a skipped sequence are left as they are.  Calls of few rows run on
- * kvq_decode's kernel, with its precision; the others (by total_q, batch, heads and max_pages_per_seq) on one that takes q as
- * the sum of two 8-bit terms: elements of 2^-13 of their row's largest and more exactly, smaller ones to 2^-21 of it, less for
- * rows below 2^-115.  A NaN code of a stored V may reach rows before it.  That kernel gives up rows whose scores (sm_scale * q.K * log2(e)) pass 2^22: they become NaN, and
- * kvq_workspace_status reports KVQ_EINVAL.
+ * KVQ_FP8_E4M3_PAGE has two kernels of its own, for head_dim 64, 128 and 256 and any number of query heads per kv
+ * head: options must be 0 or NULL (else KVQ_EUNSUPPORTED), kvq_extend_path does not speak of it, the workspace is
+ * kvq_extend_workspace_bytes_kind's, and the rows of a skipped sequence are left as they are.  Calls of few rows run
+ * on kvq_decode's kernel, with its precision; the others (by total_q, batch, heads and max_pages_per_seq) on one that
+ * takes q as the sum of two 8-bit terms: elements of 2^-13 of their row's largest and more exactly, smaller ones to
+ * 2^-21 of it, less for rows below 2^-115.  A NaN code of a stored V may reach rows before it.  That kernel gives up
+ * rows whose scores (sm_scale * q.K * log2(e)) pass 2^22: they become NaN, and kvq_workspace_status reports
+ * KVQ_EINVAL.
  */
 typedef struct kvq_extend_options {
     int32_t path;       /* 0 = automatic; 1 = prefixes on the CUDA-core decode; 2 = flash (GQA) / tensor-core
